@@ -13,6 +13,10 @@ Entry points (names follow RFC-0025 / RFC-0026):
 * ``chunk_kda_varlen(q, k, v, g, beta, cu_seqlens=None, scale=1.0, output_final_state=True)``
 * ``chunk_kda_varlen_backward(q, k, v, g, beta, do, cu_seqlens=None, scale=1.0, ...)``
 * ``eod_to_segment_ids(tokens, eod_id)`` and ``chunk_kda_segment_ids(q, k, v, g, beta, segment_ids)``
+
+and, from ``mixers.py`` (include/pkv_mixers.h), the softmax and linear attention that stand next to
+KDA in a model and the recurrences' single-token steps: ``attn_varlen``, ``chunk_linear_attn_varlen``,
+their reverse passes, ``linear_attn_step`` and ``kda_step``.
 """
 
 import ctypes
@@ -89,6 +93,7 @@ def _load():
     lib.pkv_status_string.restype = ctypes.c_char_p
     lib.pkv_abi_version.argtypes = []
     lib.pkv_abi_version.restype = i32
+    mixers.declare(lib)
     _lib = lib
     return lib
 
@@ -413,3 +418,10 @@ def chunk_kda_varlen_backward(q, k, v, g, beta, do, cu_seqlens=None, scale=1.0, 
                                                         chunk_states.numel() * chunk_states.element_size(),
                                                         _stream(dev)))
     return KdaGrads(dq, dk, dv, dg, dbeta, dinit)
+
+
+from . import mixers  # noqa: E402  (uses the helpers above)
+from .mixers import (FLAG_BAD_SLOT, AttnGrads, LinearAttnGrads, attn_varlen,  # noqa: E402,F401
+                     attn_varlen_backward, attn_varlen_backward_workspace_size, chunk_linear_attn_varlen,
+                     chunk_linear_attn_varlen_backward, chunk_linear_attn_varlen_backward_workspace_size,
+                     chunk_linear_attn_varlen_workspace_size, kda_step, linear_attn_step)

@@ -23,6 +23,7 @@ constexpr int32_t kFlagOverflow = 1;
 constexpr int32_t kFlagLeadingPad = 2;
 constexpr int32_t kFlagBadCuSeqlens = 4;
 constexpr int32_t kFlagGateRange = 8;
+constexpr int32_t kFlagBadSlot = 16;  // include/pkv_mixers.h
 // The chunked bf16 paths split each 64-token chunk into 16-token sub-chunks
 // and put 2^{-(sum of a sub-chunk's log2 gates)} on one operand of its
 // diagonal block (the forward's query side, the reverse pass's key side).
@@ -128,5 +129,68 @@ hipError_t launch_kda_backward(const void* q, const void* k, const void* v, cons
                                const float* dfinal_state, void* dq, void* dk, void* dv, void* dg,
                                void* dbeta, float* dinitial_state, int32_t* flags,
                                hipStream_t stream);
+
+// Packed causal softmax attention (see include/pkv_mixers.h); cu may be null
+// with max_segs = 1, lse may be null.
+struct AttnArgs {
+  const void *q, *k, *v;
+  const int32_t* cu;
+  int32_t max_segs;
+  int64_t N;
+  int32_t H, Hkv, D;
+  float scale;
+  void* o;
+  float* lse;
+  int32_t* flags;
+};
+struct AttnGradArgs {
+  const void* dout;
+  float* delta;  // [H, N], in the workspace
+  void *dq, *dk, *dv;
+};
+// The largest grid of the two launchers.
+int64_t attn_simple_grid(int64_t N, int32_t max_segs, int32_t H);
+hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream);
+hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g, int32_t dtype,
+                                       hipStream_t stream);
+
+// Linear attention with one decay per head.
+struct LinearArgs {
+  const void *q, *k, *v;
+  const float* g;  // [H]
+  const int32_t* cu;
+  int32_t max_segs;
+  int64_t N;
+  int32_t H, Dk, Dv;
+  float scale;
+  const float* initial_state;
+  void* o;
+  float* final_state;
+  int32_t* flags;
+  void* workspace;
+};
+struct LinearGradArgs {
+  const void* dout;
+  const float* dfinal_state;
+  void *dq, *dk, *dv;
+  float* d_initial_state;
+};
+hipError_t launch_linear_serial(const LinearArgs& x, int32_t dtype, hipStream_t stream);
+hipError_t launch_linear_serial_backward(const LinearArgs& x, const LinearGradArgs& y, int32_t dtype,
+                                         hipStream_t stream);
+
+// Single-token steps; beta is null for linear attention.
+struct StepArgs {
+  const void *q, *k, *v, *g, *beta;
+  const int32_t* slots;
+  int64_t R;
+  int32_t S, H, Dk, Dv;
+  float scale;
+  bool qk_l2norm;
+  float* state;
+  void* o;
+  int32_t* flags;
+};
+hipError_t launch_step(const StepArgs& a, int32_t dtype, hipStream_t stream);
 
 }  // namespace pkv
