@@ -99,6 +99,8 @@ pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const in
                 {{o, qb, 16}, {lse, N * Hq * 4, 4}, {flags, 4, 4}}))
     return PKV_ERR_INVALID_ARGUMENT;
   const pkv::AttnArgs a{q, k, v, cu_seqlens, max_segs, N, Hq, Hkv, D, scale, o, lse, flags};
+  if (pkv::attn_mfma_supported(D, dtype))
+    return from_hip(pkv::launch_attn_fwd(a, static_cast<hipStream_t>(stream)));
   return from_hip(pkv::launch_attn_simple(a, dtype, static_cast<hipStream_t>(stream)));
 }
 

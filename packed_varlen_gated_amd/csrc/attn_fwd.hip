@@ -1,0 +1,309 @@
+// Packed causal softmax attention with grouped heads on the matrix cores (bf16,
+// D in {64, 128}).
+//
+//   o_t = sum_{s <= t, same segment} softmax_s(scale q_t.k_s) v_s
+//   lse_t = ln sum_s exp(scale q_t.k_s)
+//
+// A work-group of 4 waves takes 128 queries of one head (a tile aligned to its
+// segment's start, segments.h) and walks the keys in tiles of 64; a wave holds
+// 32 queries. Per tile, with the running maximum m and sum l of a row (base 2):
+//   S^T = K Q^T, P = 2^(c S - m), l += sum P, O^T += V^T P^T    (c = scale log2 e)
+// S^T has a query per lane, so the softmax needs one exchange between the
+// lanes l and l + 32, and P^T in the registers of S^T is the B operand of the
+// second product as it stands: its contraction slots are the keys
+// {4 g .. 4 g + 3, 8 + 4 g .. 8 + 4 g + 3} of a 16-key step (g = lane / 32), and
+// V^T is read through transposing LDS reads in that order.
+//
+// O and l are rescaled only when a row's maximum grew by more than 2^8 since
+// the last rescaling: weights are then at most 2^8 instead of 1, which neither
+// their bf16 rounding (relative) nor the fp32 sums see, and most tiles skip 2 D
+// multiplications per query.
+//
+// K and V tiles go from memory into LDS without passing registers, the next
+// tile while this one is used; two buffers, one barrier per tile. 16-byte chunk
+// c of row r is kept at chunk c ^ f(r) (the loads' source addresses are
+// permuted), so both the row-wise reads of K and the transposing reads of V
+// touch every bank once.
+//
+// A weight of 0 times a value that is not finite is NaN, so a later token's
+// value could reach an earlier one through a tile on the diagonal. When an
+// output is not finite the work-group walks the keys once more with such
+// values as 0 and stores the outputs of the elements that no such value
+// belongs to: with every value finite nothing is spent but the check.
+
+#include "mfma.h"
+#include "segments.h"
+
+#include <float.h>
+
+namespace pkv {
+namespace {
+
+constexpr int kBM = 128;  // queries per work-group
+constexpr int kBN = 64;   // keys per tile
+constexpr int kThreads = 256;
+constexpr int kTail = 256;        // work-groups that zero the rows no segment has
+constexpr float kGrow = 8.f;      // log2 of what a row's maximum may grow by before O is rescaled
+
+template <int D>
+struct Tile {
+  static constexpr int CH = D / 8;          // 16-byte chunks per row
+  static constexpr int BYTES = kBN * D * 2;
+  // chunk swizzles: rows read by the 16 lanes of a pass (K), or the four rows
+  // of 64 bytes that a transposing read of 32 lanes takes (V), on distinct banks
+  static __device__ __forceinline__ int k_swz(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
+  static __device__ __forceinline__ int v_swz(int row) { return D == 128 ? (row & 3) << 2 : (row & 2) << 1; }
+};
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
+    const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
+    const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
+    bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, int32_t slots) {
+  constexpr int CH = Tile<D>::CH, KS = D / 16, DT = D / 32, LD = kBN * CH / kThreads;
+  constexpr int TB = Tile<D>::BYTES;
+  __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
+  static_assert(4 * TB >= kBM * D * 2, "the outputs are staged in the tiles' buffers");
+
+  const int64_t b = blockIdx.x;
+  if (b >= int64_t(slots) * H) {
+    const int64_t j = b - int64_t(slots) * H, c = covered_tokens(cu, max_segs, N);
+    zero_tail(o, c, N, int64_t(H) * D * 2, j, kTail);
+    if (lse != nullptr)
+      for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += int64_t(kTail) * kThreads)
+        lse[(i / (N - c)) * N + c + i % (N - c)] = -INFINITY;
+    if (j == 0) check_cu(cu, max_segs, N, flags);
+    return;
+  }
+  // Consecutive work-groups run on different XCDs: the query heads of one kv
+  // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
+  const int32_t hi = int32_t(b % H), rep = H / Hkv;
+  const int32_t hk = hi % Hkv, h = hk * rep + hi / Hkv;
+  SegTile t;
+  // late tiles have the most keys: they start first
+  if (!find_tile(cu, max_segs, N, kBM, slots - 1 - int32_t(b / H), t)) return;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
+  const int32_t q0 = t.start + wave * 32;  // the wave's first query
+  const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
+  const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
+  const int n_tiles = (qend - t.a + kBN - 1) / kBN;
+
+  // c > 0: a negative scale flips the queries' signs, a scale of 0 clears them
+  // (a masked score is -inf, which a factor of 0 would turn into NaN)
+  const float c = scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
+  bf16x8 qf[KS];
+  {
+    const int32_t have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+    const auto r = buffer(q + (int64_t(rows > 0 ? q0 : t.start) * H + h) * D,
+                          have > 0 ? int64_t(have - 1) * qstride + D * 2 : 0);
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, keep = scale == 0.f ? 0u : ~0u;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      i32x4 x = __builtin_bit_cast(i32x4, load8(r, uint32_t(col) * qstride + (2 * i + half) * 16));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = int((uint32_t(x[j]) ^ flip) & keep);
+      qf[i] = __builtin_bit_cast(bf16x8, x);
+    }
+  }
+
+  uint32_t koff[LD], voff[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int ch = i * kThreads + tid, row = ch / CH, pos = ch % CH;
+    koff[i] = uint32_t(row) * kstride + (pos ^ Tile<D>::k_swz(row)) * 16;
+    voff[i] = uint32_t(row) * kstride + (pos ^ Tile<D>::v_swz(row)) * 16;
+  }
+  auto issue = [&](int it) {
+    const int32_t s0 = t.a + it * kBN;
+    const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
+    const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(have - 1) * kstride + D * 2;
+    const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);
+    char* dst = lds + (it & 1) * 2 * TB + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < LD; ++i) load_lds16(rk, koff[i], dst + i * kThreads * 16);
+#pragma unroll
+    for (int i = 0; i < LD; ++i) load_lds16(rv, voff[i], dst + TB + i * kThreads * 16);
+  };
+
+  f32x16 acc[DT];
+  float m = -FLT_MAX, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+
+  // LDS addresses of this lane's operand chunks
+  const int krow = col, kx = Tile<D>::k_swz(col);
+  const int vr = 4 * half + ((lane & 15) >> 2);              // key of the transposing read (mod 8)
+  const int vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // its chunk in a 32-channel group
+  const int vb = (lane & 1) * 8;                             // its half of the chunk
+  const int vx = Tile<D>::v_swz(vr);                         // (the swizzle has period 4)
+
+  auto walk = [&](bool clean) {
+    issue(0);
+    for (int it = 0; it < n_tiles; ++it) {
+      wait_vm();
+      bar();
+      if (it + 1 < n_tiles) issue(it + 1);
+      char* kt = lds + (it & 1) * 2 * TB;
+      char* vt = kt + TB;
+      if (clean) {
+        // values that are not finite become 0
+        for (int i = tid; i < TB / 4; i += kThreads) {
+          uint32_t x = reinterpret_cast<uint32_t*>(vt)[i];
+          if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+          if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+          reinterpret_cast<uint32_t*>(vt)[i] = x;
+        }
+        __syncthreads();
+      }
+      const int32_t s0 = t.a + it * kBN;
+      if (rows <= 0 || s0 > q0 + 31) continue;
+
+      f32x16 s[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s[j] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          const bf16x8 a = *reinterpret_cast<const bf16x8*>(kt + (32 * j + krow) * (D * 2) + (((2 * i + half) ^ kx) * 16));
+          s[j] = mfma32(a, qf[i], s[j]);
+        }
+      }
+      if (s0 + kBN - 1 > q0) {
+        const int32_t last = q0 + col - s0;  // the lane's query attends to keys 0 .. last of the tile
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[j][i] = 32 * j + 8 * (i / 4) + 4 * half + i % 4 <= last ? s[j][i] : -INFINITY;
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
+      mx = fmaxf(mx, other_half(mx)) * c;
+      if (__builtin_amdgcn_ballot_w64(mx > m + kGrow) != 0) {
+        const float mn = fmaxf(m, mx), f = ex2(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[i][j] *= f;
+      }
+      bf16x8 p[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = ex2(fmaf(s[j][i], c, -m));
+          l += x;
+          p[2 * j + i / 8][i % 8] = static_cast<bf16>(x);
+        }
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const char* a = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
+          acc[i] = mfma32(join(read_tr(a), read_tr(a + 8 * (D * 2))), p[j], acc[i]);
+        }
+    }
+  };
+  walk(false);
+
+  l += other_half(l);
+  const float inv = 1.f / l;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      acc[i][j] *= inv;
+      bad |= !finite(acc[i][j]);
+    }
+  bad = bad && col < rows;
+  if (lse != nullptr && half == 0 && col < rows) lse[int64_t(h) * N + q0 + col] = m * kLn2 + logf(l);
+
+  // outputs: rows of the wave through LDS, 16-byte stores
+  const int have = rows > 32 ? 32 : rows;
+  auto put = [&](const int32_t* first_bad) {
+    char* st = lds + wave * (32 * D * 2);
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf16x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = static_cast<bf16>(acc[i][4 * j + e]);
+        const int ch = 4 * i + j;  // channels 32 i + 8 j + 4 half ..
+        *reinterpret_cast<bf16x4*>(st + col * (D * 2) + ((ch ^ (col & (CH - 1))) * 16) + half * 8) = x;
+      }
+    // the wave's own rows: its LDS accesses are in order
+    asm volatile("" ::: "memory");
+    for (int i = lane; i < 32 * CH; i += 64) {
+      const int r = i / CH, ch = i % CH;
+      if (r >= have) continue;
+      const i32x4 x = *reinterpret_cast<const i32x4*>(st + r * (D * 2) + ((ch ^ (r & (CH - 1))) * 16));
+      bf16* dst = o + (int64_t(q0 + r) * H + h) * D + ch * 8;
+      if (first_bad == nullptr) {
+        *reinterpret_cast<i32x4*>(dst) = x;
+      } else {
+        const bf16x8 y = __builtin_bit_cast(bf16x8, x);
+        for (int e = 0; e < 8; ++e)
+          if (q0 + r < first_bad[ch * 8 + e]) dst[e] = y[e];
+      }
+    }
+  };
+  const bool again = __syncthreads_or(bad);  // (also: every wave is done with the tiles)
+  put(nullptr);
+  if (!again) return;
+
+  // Some output is not finite. first_bad[d]: the first token of the segment
+  // whose value d is not; the elements before it get outputs free of it.
+  __shared__ int32_t first_bad[D];
+  for (int d = tid; d < D; d += kThreads) first_bad[d] = 0x7fffffff;
+  __syncthreads();
+  for (int32_t s = t.a + tid / D; s < qend; s += kThreads / D)
+    if (!finite(to_f32(v[(int64_t(s) * Hkv + hk) * D + tid % D]))) {
+      atomicMin(&first_bad[tid % D], s);
+      break;
+    }
+  m = -FLT_MAX;
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+  __syncthreads();
+  walk(true);
+  l += other_half(l);
+  const float inv2 = 1.f / l;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
+  __syncthreads();
+  put(first_bad);
+}
+
+}  // namespace
+
+bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 64 || D == 128); }
+
+hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
+  const int64_t slots = tile_slots(a.N, a.max_segs, kBM);
+  const dim3 grid(uint32_t(slots * a.H + kTail)), block(kThreads);
+  const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
+  if (a.D == 64)
+    attn_fwd_kernel<64><<<grid, block, 0, stream>>>(q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
+                                                    static_cast<bf16*>(a.o), a.lse, a.flags, int32_t(slots));
+  else
+    attn_fwd_kernel<128><<<grid, block, 0, stream>>>(q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
+                                                     static_cast<bf16*>(a.o), a.lse, a.flags, int32_t(slots));
+  return hipGetLastError();
+}
+
+}  // namespace pkv

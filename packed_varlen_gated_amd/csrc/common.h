@@ -154,6 +154,10 @@ hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stre
 hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g, int32_t dtype,
                                        hipStream_t stream);
 
+// The matrix-core kernels (bf16, D in {64, 128}).
+bool attn_mfma_supported(int32_t D, int32_t dtype);
+hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
+
 // Linear attention with one decay per head.
 struct LinearArgs {
   const void *q, *k, *v;
