@@ -107,7 +107,7 @@ pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const in
 size_t pkv_attn_varlen_backward_workspace_size(int64_t N, int32_t Hq, int32_t Hkv, int32_t D,
                                                int32_t max_segs, int32_t dtype) {
   if (check_attn(nullptr, max_segs, N, Hq, Hkv, D, 1.f, dtype) != PKV_OK) return 0;
-  return size_t(N) * Hq * 4;
+  return size_t(N) * Hq * 8;
 }
 
 pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v, const void* o,
@@ -132,6 +132,8 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
   const pkv::AttnArgs a{q,   k,   v, cu_seqlens, max_segs, N, Hq, Hkv, D, scale, const_cast<void*>(o),
                         const_cast<float*>(lse), flags};
   const pkv::AttnGradArgs g{dout, static_cast<float*>(workspace), dq, dk, dv};
+  if (pkv::attn_mfma_supported(D, dtype))
+    return from_hip(pkv::launch_attn_bwd(a, g, static_cast<hipStream_t>(stream)));
   return from_hip(pkv::launch_attn_simple_backward(a, g, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -279,12 +279,12 @@ hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const T* dout = static_cast<const T*>(g.dout);
   const int64_t slots = tile_slots(a.N, a.max_segs, kT), rows = kThreads / 8;
   attn_delta<T, D><<<dim3(uint32_t((a.N * a.H + rows - 1) / rows)), dim3(kThreads), 0, stream>>>(
-      static_cast<const T*>(a.o), dout, g.delta, a.N, a.H);
+      static_cast<const T*>(a.o), dout, g.stats, a.N, a.H);
   attn_simple_dq<T, D><<<dim3(uint32_t(slots * a.H + kTail)), dim3(kThreads), 0, stream>>>(
-      q, k, v, dout, a.lse, g.delta, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dq),
+      q, k, v, dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dq),
       a.flags, slots);
   attn_simple_dkv<T, D><<<dim3(uint32_t(slots * a.Hkv + kTail)), dim3(kThreads), 0, stream>>>(
-      q, k, v, dout, a.lse, g.delta, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dk),
+      q, k, v, dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dk),
       static_cast<T*>(g.dv), slots);
   return hipGetLastError();
 }

@@ -145,7 +145,7 @@ struct AttnArgs {
 };
 struct AttnGradArgs {
   const void* dout;
-  float* delta;  // [H, N], in the workspace
+  float* stats;  // [2, H, N] in the workspace: lse log2 e, delta (the simple kernels: delta alone)
   void *dq, *dk, *dv;
 };
 // The largest grid of the two launchers.
@@ -157,6 +157,7 @@ hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g,
 // The matrix-core kernels (bf16, D in {64, 128}).
 bool attn_mfma_supported(int32_t D, int32_t dtype);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream);
 
 // Linear attention with one decay per head.
 struct LinearArgs {
