@@ -77,7 +77,15 @@ pkv_status check_linear(const int32_t* cu, int32_t& max_segs, int64_t N, int32_t
       int64_t(max_segs) * H > (int64_t(1) << 22))
     return PKV_ERR_INVALID_ARGUMENT;
   if (!known_dtype(dtype) || !supported_head_dim(Dk) || !supported_head_dim(Dv)) return PKV_ERR_UNSUPPORTED;
+  if (pkv::linear_chunk_supported(Dk, Dv, dtype) && pkv::linear_chunk_grid(N, max_segs, H) > kInt32Max)
+    return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;
+}
+
+// Of the linear-attention calls, both directions.
+size_t linear_workspace(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype) {
+  if (N < 1 || N > kInt32Max || H < 1 || H > 65536 || !pkv::linear_chunk_supported(Dk, Dv, dtype)) return 0;
+  return pkv::linear_chunk_workspace_bytes(N, H, Dk, Dv);
 }
 
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
@@ -139,7 +147,7 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
 
 size_t pkv_linear_attn_varlen_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t max_segs,
                                              int32_t dtype) {
-  return 0;
+  return linear_workspace(N, H, Dk, Dv, dtype);
 }
 
 pkv_status pkv_linear_attn_varlen(const void* q, const void* k, const void* v, const float* g,
@@ -161,12 +169,14 @@ pkv_status pkv_linear_attn_varlen(const void* q, const void* k, const void* v, c
     return PKV_ERR_INVALID_ARGUMENT;
   const pkv::LinearArgs x{q,  k,  v,     g,             cu_seqlens, max_segs,    N,     H,
                           Dk, Dv, scale, initial_state, o,          final_state, flags, workspace};
+  if (pkv::linear_chunk_supported(Dk, Dv, dtype))
+    return from_hip(pkv::launch_linear_chunk(x, static_cast<hipStream_t>(stream)));
   return from_hip(pkv::launch_linear_serial(x, dtype, static_cast<hipStream_t>(stream)));
 }
 
 size_t pkv_linear_attn_varlen_backward_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv,
                                                       int32_t max_segs, int32_t dtype) {
-  return 0;
+  return linear_workspace(N, H, Dk, Dv, dtype);
 }
 
 pkv_status pkv_linear_attn_varlen_backward(const void* q, const void* k, const void* v, const float* g,
@@ -191,6 +201,8 @@ pkv_status pkv_linear_attn_varlen_backward(const void* q, const void* k, const v
   const pkv::LinearArgs x{q,  k,  v,     g,             cu_seqlens, max_segs, N,     H,
                           Dk, Dv, scale, initial_state, nullptr,    nullptr,  flags, workspace};
   const pkv::LinearGradArgs y{dout, dfinal_state, dq, dk, dv, d_initial_state};
+  if (pkv::linear_chunk_supported(Dk, Dv, dtype))
+    return from_hip(pkv::launch_linear_chunk_backward(x, y, static_cast<hipStream_t>(stream)));
   return from_hip(pkv::launch_linear_serial_backward(x, y, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -184,6 +184,13 @@ hipError_t launch_linear_serial(const LinearArgs& x, int32_t dtype, hipStream_t 
 hipError_t launch_linear_serial_backward(const LinearArgs& x, const LinearGradArgs& y, int32_t dtype,
                                          hipStream_t stream);
 
+// The chunked matrix-core kernels (bf16, Dk and Dv in {64, 128}).
+bool linear_chunk_supported(int32_t Dk, int32_t Dv, int32_t dtype);
+size_t linear_chunk_workspace_bytes(int64_t N, int32_t H, int32_t Dk, int32_t Dv);
+int64_t linear_chunk_grid(int64_t N, int32_t max_segs, int32_t H);
+hipError_t launch_linear_chunk(const LinearArgs& x, hipStream_t stream);
+hipError_t launch_linear_chunk_backward(const LinearArgs& x, const LinearGradArgs& y, hipStream_t stream);
+
 // Single-token steps; beta is null for linear attention.
 struct StepArgs {
   const void *q, *k, *v, *g, *beta;
