@@ -21,9 +21,10 @@
 // 8-byte pieces in the order 0, 2, 1, 3): a is read in 16-byte pieces, outputs
 // are stored in 16-byte pieces.
 //
-// b and c of the next chunk go from memory into LDS while this one is used (two
-// buffers, one barrier per chunk); a goes into registers, reloaded as soon as
-// this chunk's products with it are done.
+// Tiles go from memory into LDS without passing registers. b has two buffers; a
+// and c have one each, since a is done with after the products that c is not yet
+// needed for: the next a is loaded over a's second half of a chunk, c over the
+// first. 73 KiB at 128 channels: two work-groups per compute unit.
 //
 // Segments longer than a run: a first launch walks every run but the segment's
 // last (in the walk's direction) without outputs and saves its own end state, a
@@ -91,27 +92,68 @@ struct WalkArgs {
   int32_t* flags;
 };
 
-// X of one (state, head) <-> registers.
-template <int DA, int DB, typename F>
-__device__ __forceinline__ void each_state(bool transposed, int wave, F f) {
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int r = lane & 31, e = 32 * wave + (r & 16) + ((r & 4) << 1) + ((r & 8) >> 1) + (r & 3);
+// X of one (state, head) <-> registers: register 8 v + j of tile i is row
+// 32 i + 16 v + 8 (lane / 32) + j of the lane's column. One address register;
+// the rest of an offset is an immediate or a scalar.
+template <int DA, int DB>
+struct StateAddr {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off;
+  bool transposed;
+  __device__ __forceinline__ StateAddr(const float* p, bool transposed, int wave) : transposed(transposed) {
+    const int lane = threadIdx.x & 63, l = lane & 31, half = lane >> 5;
+    const int e = 32 * wave + (l & 16) + ((l & 4) << 1) + ((l & 8) >> 1) + (l & 3);
+    r = buffer(p, int64_t(DA) * DB * 4);
+    off = 4 * (transposed ? e * DA + 8 * half : 8 * half * DB + e);
+  }
+  __device__ __forceinline__ void load(f32x16 (&X)[DA / 32]) const {
+    if (transposed) {
 #pragma unroll
-  for (int i = 0; i < DA / 32; ++i)
+      for (int i = 0; i < DA / 32; ++i)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int d = 32 * i + (j & 8) * 2 + 8 * half + (j & 7);
-      f(i, j, transposed ? e * DA + d : d * DB + e);
+        for (int j = 0; j < 16; j += 4) {
+          const auto x = __builtin_bit_cast(
+              f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * (32 * i + 2 * (j & 8) + (j & 7)), 0, 0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) X[i][j + e] = x[e];
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < DA / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          X[i][j] = __builtin_bit_cast(
+              float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 4 * DB * (32 * i + 2 * (j & 8) + (j & 7)), 0));
     }
-}
+  }
+  __device__ __forceinline__ void store(const f32x16 (&X)[DA / 32]) const {
+    if (transposed) {
+#pragma unroll
+      for (int i = 0; i < DA / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          store16(r, off + 4 * (32 * i + 2 * (j & 8) + (j & 7)),
+                  __builtin_bit_cast(i32x4, f32x4{X[i][j], X[i][j + 1], X[i][j + 2], X[i][j + 3]}));
+    } else {
+#pragma unroll
+      for (int i = 0; i < DA / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(X[i][j]), r, off,
+                                                4 * DB * (32 * i + 2 * (j & 8) + (j & 7)), 0);
+    }
+  }
+};
 
 template <int DA, int DB, bool kRev, bool kState>
 __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x) {
   constexpr int NW = DB / 32, NT = 64 * NW, KA = DA / 16, TA = DA / 32;
   constexpr int SB = Rows<DA>::BYTES, SC = Rows<DB>::BYTES;
-  // b, c of the even chunks, of the odd ones; the update's weights of each; the
+  // b of the even chunks, of the odd ones, then c and a (the state walk: c of the
+  // even chunks, of the odd ones); the update's weights of each parity; the
   // in-chunk weights of the lane
-  __shared__ __attribute__((aligned(1024))) char lds[2 * (SB + SC)];
+  constexpr int kPieces = kC * Rows<DA>::CH / NT;  // loads of a b tile per lane
+  __shared__ __attribute__((aligned(1024))) char lds[2 * SB + (kState ? 2 * SC : SC + SB)];
   __shared__ float upd[2][kC];
   __shared__ f32x4 rel[kState ? 1 : 2][kState ? 1 : 4][kState ? 1 : 64];
 
@@ -151,37 +193,38 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
   const int n_chunks = (end - t.start + kC - 1) / kC;
   auto chunk_start = [&](int i) { return t.start + (kRev ? n_chunks - 1 - i : i) * kC; };
   auto chunk_len = [&](int32_t s0) { return end - s0 < kC ? end - s0 : kC; };
-  auto issue = [&](int i) {
+  auto issue_b = [&](int i) {
     const int32_t s0 = chunk_start(i), n = chunk_len(s0);
-    char* dst = lds + (i & 1) * (SB + SC);
-    issue_tile<DA, NT>(buffer(x.b + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2), as, dst, wave);
-    issue_tile<DB, NT>(buffer(x.c + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2), cs, dst + SB, wave);
+    issue_tile<DA, NT>(buffer(x.b + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2), as,
+                       lds + (i & 1) * SB, wave);
     if (tid < kC) upd[i & 1][tid] = tid < n ? x.in_scale * ex2(g2 * (kRev ? tid + 1 : n - 1 - tid)) : 0.f;
   };
-  issue(0);
+  auto issue_c = [&](int i) {
+    const int32_t s0 = chunk_start(i), n = chunk_len(s0);
+    issue_tile<DB, NT>(buffer(x.c + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2), cs,
+                       lds + 2 * SB + (kState ? (i & 1) * SC : 0), wave);
+  };
+  auto issue_a = [&](int i) {
+    const int32_t s0 = chunk_start(i), n = chunk_len(s0);
+    issue_tile<DA, NT>(buffer(x.a + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2), as,
+                       lds + 2 * SB + SC, wave);
+  };
+  issue_b(0);
+  if constexpr (kState) issue_c(0);
+  else issue_a(0);
 
   f32x16 X[TA];
   const float* from = kState ? nullptr
                              : first ? (x.init ? x.init + (int64_t(t.seg) * x.H + h) * kState_ : nullptr)
                                      : x.saved + ((kRev ? at : at - 1) * x.H + h) * kState_;
   if (from != nullptr) {
-    each_state<DA, DB>(x.transposed, wave, [&](int i, int j, int off) { X[i][j] = from[off]; });
+    StateAddr<DA, DB>(from, x.transposed, wave).load(X);
   } else {
 #pragma unroll
     for (int i = 0; i < TA; ++i) X[i] = f32x16{};
   }
 
-  bf16x8 af[kState ? 1 : 2][KA];
-  auto load_a = [&](int i) {
-    const int32_t s0 = chunk_start(i), n = chunk_len(s0);
-    const auto r = buffer(x.a + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2);
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int j = 0; j < KA; ++j) af[u][j] = load8(r, uint32_t(32 * u + col) * as + (2 * j + half) * 16);
-  };
   if constexpr (!kState) {
-    load_a(0);
     // rel[0]: weights inside a 32 x 32 block on the diagonal, rel[1]: of the
     // block below it (s 32 .. 1 tokens further from t)
     if (wave == 0) {
@@ -207,79 +250,100 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
   for (int it = 0; it < n_chunks; ++it) {
     __builtin_amdgcn_s_waitcnt(0x0070);  // loads into LDS and LDS stores done
     bar();
-    if (it + 1 < n_chunks) issue(it + 1);
-    const char* bt = lds + (it & 1) * (SB + SC);
-    const char* ct = bt + SB;
+    if constexpr (!kState) {
+      issue_c(it);
+      // c's loads stay before the next b's: the wait for c below counts those
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (it + 1 < n_chunks) {
+      issue_b(it + 1);
+      if constexpr (kState) issue_c(it + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const char* bt = lds + (it & 1) * SB;
+    const char* ct = lds + 2 * SB + (kState ? (it & 1) * SC : 0);
+    const char* at_ = lds + 2 * SB + SC;
     const int32_t s0 = chunk_start(it), n = chunk_len(s0);
 
     bf16x8 cf[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cf[j] = tc.read(ct, wave, j);
-
     if constexpr (!kState) {
-      f32x16 o[2];
+      // In-chunk weights of a 32 x 32 block (rows s of block sb, columns t of
+      // block u) as operands; three of the four blocks have any.
+      bf16x8 wf[2][4];
+      auto weigh = [&](const f32x16& w, int u, int sb) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) o[u] = f32x16{};
-      // readout of X
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const f32x4 f = rel[sb == u ? 0 : 1][i4][lane];
 #pragma unroll
-      for (int i = 0; i < TA; ++i)
+          for (int e = 0; e < 4; ++e)
+            wf[u][2 * sb + i4 / 2][4 * (i4 % 2) + e] = static_cast<bf16>(w[4 * i4 + e] * f[e]);
+        }
+      };
+      auto row = [&](const char* t, int sb, int i) {
+        return *reinterpret_cast<const bf16x8*>(t + (32 * sb + col) * Rows<DA>::ROW + (((2 * i + half) ^ fx) * 16));
+      };
+      // Five independent products take turns: the three blocks and the readout
+      // of X for both column blocks.
+      constexpr int sFar = kRev ? 1 : 0, sOne = kRev ? 0 : 1;  // row blocks of both, of one
+      f32x16 o[2] = {};
+      {
+        f32x16 w0 = {}, w1 = {}, w2 = {};
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
+        for (int i = 0; i < KA; ++i) {
+          const bf16x8 br = row(bt, sFar, i), a0 = row(at_, 0, i), a1 = row(at_, 1, i);
           bf16x8 xs;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) xs[j] = static_cast<bf16>(X[i][8 * v + j]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) o[u] = mfma32(xs, af[u][2 * i + v], o[u]);
+          for (int j = 0; j < 8; ++j) xs[j] = static_cast<bf16>(X[i / 2][8 * (i % 2) + j]);
+          w0 = mfma32(br, a0, w0);
+          w1 = mfma32(br, a1, w1);
+          w2 = mfma32(row(bt, sOne, i), kRev ? a0 : a1, w2);
+          o[0] = mfma32(xs, a0, o[0]);
+          o[1] = mfma32(xs, a1, o[1]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        weigh(w0, 0, sFar);
+        weigh(w1, 1, sFar);
+        weigh(w2, sOne, sOne);
+      }
+      // c has come (the next b may still be on its way), a is free
+      if (it + 1 < n_chunks)
+        __builtin_amdgcn_s_waitcnt(0x0070 | kPieces);
+      else
+        __builtin_amdgcn_s_waitcnt(0x0070);
+      bar();
+      if (it + 1 < n_chunks) issue_a(it + 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cf[j] = tc.read(ct, wave, j);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int d = kRev ? n - 1 - 32 * u - col : 32 * u + col + 1;
-        const float w = x.out_scale * ex2(g2 * (d < 0 ? 0 : d));
+        const float ow = x.out_scale * ex2(g2 * (d < 0 ? 0 : d));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[u][i] *= w;
+        for (int i = 0; i < 16; ++i) o[u][i] *= ow;
       }
-      // in-chunk weights: rows s of block sb, columns t of block u
-      bf16x8 wf[2][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-          if (kRev ? sb < u : sb > u) continue;
-          f32x16 w = {};
-#pragma unroll
-          for (int i = 0; i < KA; ++i) {
-            const bf16x8 br = *reinterpret_cast<const bf16x8*>(bt + (32 * sb + col) * Rows<DA>::ROW +
-                                                               (((2 * i + half) ^ fx) * 16));
-            w = mfma32(br, af[u][i], w);
-          }
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 f = rel[sb == u ? 0 : 1][i4][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              wf[u][2 * sb + i4 / 2][4 * (i4 % 2) + e] = static_cast<bf16>(w[4 * i4 + e] * f[e]);
-          }
-        }
-      if (it + 1 < n_chunks) load_a(it + 1);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int u = 0; u < 2; ++u) {
           if (kRev ? j / 2 < u : j / 2 > u) continue;
           o[u] = mfma32(cf[j], wf[u][j], o[u]);
         }
+      // (rows past the chunk's end are out of the buffer's range)
+      const auto ro = buffer(x.out + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        if (32 * u + col < n) {
-          bf16* to = x.out + (int64_t(s0 + 32 * u + col) * x.H + h) * DB + 32 * wave + 8 * half;
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            bf16x8 y;
+        for (int v = 0; v < 2; ++v) {
+          bf16x8 y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = static_cast<bf16>(o[u][8 * v + j]);
-            *reinterpret_cast<bf16x8*>(to + 16 * v) = y;
-          }
+          for (int j = 0; j < 8; ++j) y[j] = static_cast<bf16>(o[u][8 * v + j]);
+          store16(ro, uint32_t(32 * u + col) * cs + 64 * wave + 16 * half + 32 * v, __builtin_bit_cast(i32x4, y));
         }
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cf[j] = tc.read(ct, wave, j);
     }
 
     const float carry = ex2(g2 * n);
@@ -289,7 +353,7 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
       for (int j = 0; j < 16; ++j) X[i][j] *= carry;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      bf16x8 part[3];
+      bf16x8 part[3];  // exact to 24 bits
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const f32x4 w = *reinterpret_cast<const f32x4*>(&upd[it & 1][16 * j + 8 * u + 4 * half]);
@@ -304,18 +368,20 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
           }
         }
       }
+      bf16x8 bT[TA];
 #pragma unroll
-      for (int i = 0; i < TA; ++i) {
-        const bf16x8 bT = tb.read(bt, i, j);
+      for (int i = 0; i < TA; ++i) bT[i] = tb.read(bt, i, j);
 #pragma unroll
-        for (int s = 0; s < 3; ++s) X[i] = mfma32(bT, part[s], X[i]);
-      }
+      for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int i = 0; i < TA; ++i) X[i] = mfma32(bT[i], part[s], X[i]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   float* to = kState ? x.saved + ((kRev ? at - 1 : at) * x.H + h) * kState_
                      : (last && x.fin ? x.fin + (int64_t(t.seg) * x.H + h) * kState_ : nullptr);
-  if (to != nullptr) each_state<DA, DB>(x.transposed, wave, [&](int i, int j, int off) { to[off] = X[i][j]; });
+  if (to != nullptr) StateAddr<DA, DB>(to, x.transposed, wave).store(X);
 }
 
 // The saved states, each its run's own end state, become the states that the
