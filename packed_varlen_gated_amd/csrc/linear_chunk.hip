@@ -209,8 +209,16 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
     issue_tile<DA, NT>(buffer(x.a + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2), as,
                        lds + 2 * SB + SC, wave);
   };
-  issue_b(0);
-  if constexpr (kState) issue_c(0);
+  // The state walk leaves out the chunks whose tokens decay to a weight that
+  // fp32 has only 0 for (2^-150) by the run's end.
+  int it0 = 0;
+  if constexpr (kState) {
+    const float far = g2 < 0.f ? fminf(150.f / (-kC * g2), 1e6f) : 1e6f;
+    it0 = n_chunks - 1 - int(far);
+    it0 = it0 < 0 ? 0 : it0;
+  }
+  issue_b(it0);
+  if constexpr (kState) issue_c(it0);
   else issue_a(0);
 
   f32x16 X[TA];
@@ -247,7 +255,7 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
   const Transposed<DB> tc;
   const int fx = Rows<DA>::swz(col);
 
-  for (int it = 0; it < n_chunks; ++it) {
+  for (int it = it0; it < n_chunks; ++it) {
     __builtin_amdgcn_s_waitcnt(0x0070);  // loads into LDS and LDS stores done
     bar();
     if constexpr (!kState) {
@@ -390,6 +398,7 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
 // a / run + j; a segment of m runs has m - 1, and no two share an index. A
 // work-group takes 256 x 4 elements of one head through all indices in order.
 constexpr int kScan = 256;
+constexpr int kAhead = 8;  // states whose loads are in flight at once
 
 template <bool kRev>
 __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, int32_t size, int32_t count) {
@@ -428,10 +437,10 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
       decay[tid] = d;
     }
     __syncthreads();
-    for (int32_t i0 = 0; i0 < n; i0 += 4) {
-      f32x4 own[4];
+    for (int32_t i0 = 0; i0 < n; i0 += kAhead) {
+      f32x4 own[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int32_t i = i0 + u;
         if (i < n && seg_of[i] != -2) {
           const int64_t idx = kRev ? count - 1 - (base + i) : base + i;
@@ -439,7 +448,7 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int32_t i = i0 + u;
         if (i >= n || seg_of[i] == -2) continue;
         if (seg_of[i] >= 0)
@@ -454,10 +463,16 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
   }
 }
 
-// Tokens of a run: about 512 runs over all heads, two per compute unit.
+// Tokens of a run: the smallest power of two from sqrt(1.5 N H) on, in
+// [256, 4096]. Shorter runs keep more work-groups busy but save, scan and read
+// back more states (their number times their length is N H). Measured, us at
+// runs of 512 / 1024 / 2048 / 4096: N H = 2^21 (65536 tokens, 39 segments, 32
+// heads of 128): 900 / 755 / 704 / 825; 2^19 (one segment of 32768, 16 heads):
+// 249 / 213 / 253 / 448; 2^17 (8192 tokens, forward and reverse): 282 / 398 /
+// 694 / 843 (256: 325).
 int32_t run_tokens(int64_t N, int32_t H) {
   int32_t r = 256;
-  while (r < 4096 && int64_t(r) * 512 < N * H) r *= 2;
+  while (r < 4096 && int64_t(r) * r < N * H * 3 / 2) r *= 2;
   return r;
 }
 
