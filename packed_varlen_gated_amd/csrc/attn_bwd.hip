@@ -44,21 +44,22 @@ struct Lds {
   }
 };
 
-// The lane's part in loading a 64-row tile: byte offsets of its LD chunks.
-template <int D>
+// The lane's part in loading a tile of T rows: its first chunk; the others are
+// whole multiples of 16 rows further (the swizzle's period).
+template <int D, int T, int NT>
 struct Loader {
-  static constexpr int LD = kT * Lds<D>::CH / kThreads;
-  uint32_t off[LD];
+  static constexpr int LD = T * Lds<D>::CH / NT, STEP = NT / Lds<D>::CH;
+  static_assert(STEP % 16 == 0, "the swizzle repeats");
+  uint32_t off, step;
   __device__ __forceinline__ Loader(int32_t stride) {
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int ch = i * kThreads + threadIdx.x, row = ch / Lds<D>::CH, pos = ch % Lds<D>::CH;
-      off[i] = uint32_t(row) * stride + (pos ^ Lds<D>::swz(row)) * 16;
-    }
+    const int row = threadIdx.x / Lds<D>::CH, pos = threadIdx.x % Lds<D>::CH;
+    off = uint32_t(row) * stride + (pos ^ Lds<D>::swz(row)) * 16;
+    step = uint32_t(STEP) * stride;
   }
   __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, char* dst, int wave) const {
+    const uint32_t o = fresh(off);
 #pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16(r, off[i], dst + wave * 1024 + i * kThreads * 16);
+    for (int i = 0; i < LD; ++i) load_lds16(r, o + i * step, dst + wave * 1024 + i * NT * 16);
   }
 };
 
@@ -124,25 +125,27 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[D / 32], float f,
   }
 }
 
-template <int D>
+template <int D, bool kFar>
 __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
     int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dq, float* __restrict__ stats,
-    int32_t* __restrict__ flags, int32_t slots) {
+    int32_t* __restrict__ flags, SlotGrid grid) {
   constexpr int KS = D / 16, DT = D / 32, TB = Lds<D>::BYTES;
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
 
   const int64_t b = blockIdx.x;
-  if (b >= int64_t(slots) * H) {
-    const int64_t j = b - int64_t(slots) * H;
+  if (!kFar && b >= int64_t(grid.near) * H) {
+    const int64_t j = b - int64_t(grid.near) * H;
     zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * 2, j, kTail);
     if (j == 0) check_cu(cu, max_segs, N, flags);
     return;
   }
-  const int32_t hi = int32_t(b % H), rep = H / Hkv, hk = hi % Hkv, h = hk * rep + hi / Hkv;
+  int32_t slot, h0, h1;
+  slot_of<kFar>(grid, b, H, slot, h0, h1);
   SegTile t;
-  if (!find_tile(cu, max_segs, N, kB, slots - 1 - int32_t(b / H), t)) return;
+  if (!kFar) slot = grid.near - 1 - slot;  // late tiles have the most keys: they start first
+  if (!find_tile(cu, max_segs, N, kB, slot, t)) return;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Reader<D> rd;
@@ -151,7 +154,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
   const int32_t rows = t.e - q0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
   const int32_t qend = t.start + kB < t.e ? t.start + kB : t.e;
   const int n_tiles = (qend - t.a + kT - 1) / kT;
-  const Loader<D> ld(kstride);
+  const Loader<D, kT, kThreads> ld(kstride);
+  for (int32_t hi = h0; hi < (kFar ? h1 : h0 + 1); ++hi) {
+  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;  // (as in the forward pass)
+  if (hi != h0) __syncthreads();  // the last head's outputs have left LDS
   auto issue = [&](int it) {
     const int32_t s0 = t.a + it * kT;
     const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
@@ -198,9 +204,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
       if (have == 0 || s0 + 32 * j > q0 + 31) continue;
       f32x16 s = {}, dp = {};
 #pragma unroll
-      for (int i = 0; i < KS; ++i) s = mfma32(rd.rows(kt, j, i), qf[i], s);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(vt, j, i), df[i], dp);
+      for (int i = 0; i < KS; ++i) {  // independent products take turns
+        s = mfma32(rd.rows(kt, j, i), qf[i], s);
+        dp = mfma32(rd.rows(vt, j, i), df[i], dp);
+      }
       bf16x8 ds[2];
       const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
 #pragma unroll
@@ -218,49 +225,67 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
   __syncthreads();
   if (have > 0)
     store_rows<D>(acc, scale, lds + wave * (32 * D * 2), dq + (int64_t(q0) * H + h) * D, int64_t(H) * D, have, rd);
+  }
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(
+// kQ waves share 32 keys and take the 32-query blocks of a tile in turn, their
+// sums added at the end: kQ = 1, four waves hold 128 keys; kQ = 4, eight waves
+// hold 64.
+template <int kQ>
+struct DkvShape {
+  static constexpr int NT = kQ == 4 ? 512 : 256;  // threads
+  static constexpr int KEYS = NT / 64 / kQ * 32;  // keys of a work-group
+  static constexpr int T = kQ == 4 ? 128 : 64;    // queries per tile
+};
+
+template <int D, int kQ, bool kFar>
+__global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const bf16* __restrict__ dout, const float* __restrict__ stats, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dk,
-    bf16* __restrict__ dv, int32_t slots) {
-  constexpr int KS = D / 16, DT = D / 32, TB = Lds<D>::BYTES;
+    bf16* __restrict__ dv, SlotGrid grid) {
+  constexpr int KS = D / 16, DT = D / 32;
+  constexpr int NT = DkvShape<kQ>::NT, T = DkvShape<kQ>::T, TB = T * D * 2;
   // Q, dO of the even tiles, of the odd ones; then lse log2 e and delta of each
-  __shared__ __attribute__((aligned(1024))) char lds[4 * TB + 4 * kT * 4];
+  __shared__ __attribute__((aligned(1024))) char lds[4 * TB + 4 * T * 4];
 
   const int64_t b = blockIdx.x;
-  if (b >= int64_t(slots) * Hkv) {
-    const int64_t j = b - int64_t(slots) * Hkv, cov = covered_tokens(cu, max_segs, N);
+  if (!kFar && b >= int64_t(grid.near) * Hkv) {
+    const int64_t j = b - int64_t(grid.near) * Hkv, cov = covered_tokens(cu, max_segs, N);
     zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, kTail);
     zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, kTail);
     return;
   }
-  const int32_t hk = int32_t(b % Hkv), rep = H / Hkv;
+  const int32_t rep = H / Hkv;
+  int32_t slot, h0, h1;
+  slot_of<kFar>(grid, b, Hkv, slot, h0, h1);
   SegTile t;
-  if (!find_tile(cu, max_segs, N, kB, int32_t(b / Hkv), t)) return;
+  if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Reader<D> rd;
   const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
-  const int32_t k0 = t.start + wave * 32;  // the wave's first key
+  const int32_t k0 = t.start + wave / kQ * 32;  // the wave's first key
   const int32_t rows = t.e - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-  const int per_head = (t.e - t.start + kT - 1) / kT, n_tiles = per_head * rep;
-  const Loader<D> ld(qstride);
+  const int per_head = (t.e - t.start + T - 1) / T, n_tiles = per_head * rep;
+  const Loader<D, T, NT> ld(qstride);
+  for (int32_t hk = h0; hk < (kFar ? h1 : h0 + 1); ++hk) {
+  if (hk != h0) __syncthreads();  // the last head's outputs have left LDS
   int ih = 0, iq = 0;  // head and query tile of the next load
   auto issue = [&](int it) {
-    const int32_t s0 = t.start + iq * kT, h = hk * rep + ih;
-    const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
+    const int32_t s0 = t.start + iq * T, h = hk * rep + ih;
+    const int32_t n = t.e - s0 < T ? t.e - s0 : T;
     const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
     char* dst = lds + (it & 1) * 2 * TB;
     ld.issue(buffer(q + at, bytes), dst, wave);
     ld.issue(buffer(dout + at, bytes), dst + TB, wave);
-    if (wave < 2)
+    if (wave < T / 32) {  // lse log2 e and delta, 64 queries a wave
+      const int w = wave / (T / 64), part = wave % (T / 64) * 64;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          buffer(stats + (int64_t(wave) * H + h) * N + s0, int64_t(n) * 4),
-          (__attribute__((address_space(3))) void*)(lds + 4 * TB + ((it & 1) * 2 + wave) * kT * 4), 4,
-          uint32_t(lane) * 4, 0, 0, 0);
+          buffer(stats + (int64_t(w) * H + h) * N + s0, int64_t(n) * 4),
+          (__attribute__((address_space(3))) void*)(lds + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4), 4,
+          uint32_t(part + lane) * 4, 0, 0, 0);
+    }
     if (++iq == per_head) {
       iq = 0;
       ++ih;
@@ -286,19 +311,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(
     if (it + 1 < n_tiles) issue(it + 1);
     const char* qt = lds + (it & 1) * 2 * TB;
     const char* ot = qt + TB;
-    const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * kT * 4);
-    const f32x4* dl = ls + kT / 4;
-    const int32_t s0 = t.start + cq * kT;
+    const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * T * 4);
+    const f32x4* dl = ls + T / 4;
+    const int32_t s0 = t.start + cq * T;
     if (++cq == per_head) cq = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
+#pragma unroll 1
+    for (int j = wave % kQ; j < T / 32; j += kQ) {
       const int32_t b0 = s0 + 32 * j;  // first query of the block
       if (have == 0 || b0 + 31 < k0 || b0 >= t.e) continue;
       f32x16 s = {}, dp = {};
 #pragma unroll
-      for (int i = 0; i < KS; ++i) s = mfma32(rd.rows(qt, j, i), kf[i], s);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(ot, j, i), vf[i], dp);
+      for (int i = 0; i < KS; ++i) {  // independent products take turns
+        s = mfma32(rd.rows(qt, j, i), kf[i], s);
+        dp = mfma32(rd.rows(ot, j, i), vf[i], dp);
+      }
       bf16x8 p[2], ds[2];
       // the lane's key takes part in the block's queries first .. end - 1
       const bool edge = b0 < k0 + 31 || b0 + 32 > t.e;
@@ -326,26 +352,90 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(
     }
   }
   __syncthreads();
-  if (have > 0) {
+  if constexpr (kQ > 1) {
+    // The sums of the waves that share keys: each in turn hands dk, then dv,
+    // to the first of them.
+    static_assert(NT / 64 / kQ * DT * 4096 <= int(sizeof(lds)), "sums in flight");
+    f32x4* mine = reinterpret_cast<f32x4*>(lds) + (wave / kQ) * (DT * 4 * 64) + lane;
+    auto join_sums = [&](f32x16 (&x)[DT], int from) {
+      if (wave % kQ == from) {
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mine[(4 * i + j) * 64] = f32x4{x[i][4 * j], x[i][4 * j + 1], x[i][4 * j + 2], x[i][4 * j + 3]};
+      }
+      __syncthreads();
+      if (wave % kQ == 0) {
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 y = mine[(4 * i + j) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][4 * j + e] += y[e];
+          }
+      }
+      __syncthreads();
+    };
+#pragma unroll 1
+    for (int from = 1; from < kQ; ++from) {
+      join_sums(ak, from);
+      join_sums(av, from);
+    }
+  }
+  if (have > 0 && wave % kQ == 0) {
     char* st = lds + wave * (32 * D * 2);
     const int64_t to = (int64_t(k0) * Hkv + hk) * D;
     store_rows<D>(ak, scale, st, dk + to, int64_t(Hkv) * D, have, rd);
     asm volatile("" ::: "memory");
     store_rows<D>(av, 1.f, st, dv + to, int64_t(Hkv) * D, have, rd);
   }
+  }
+}
+
+template <int D, bool kFar>
+void queries_pass(const AttnArgs& a, const AttnGradArgs& g, const SlotGrid& grid, hipStream_t stream) {
+  const int64_t blocks = kFar ? far_blocks(grid, a.H) : near_blocks(grid, a.H) + kTail;
+  attn_dq_kernel<D, kFar><<<dim3(uint32_t(blocks)), dim3(kThreads), 0, stream>>>(
+      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
+      static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
+      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, grid);
+}
+
+template <int D, int kQ, bool kFar>
+void keys_pass(const AttnArgs& a, const AttnGradArgs& g, const SlotGrid& grid, hipStream_t stream) {
+  const int64_t blocks = kFar ? far_blocks(grid, a.Hkv) : near_blocks(grid, a.Hkv) + kTail;
+  attn_dkv_kernel<D, kQ, kFar><<<dim3(uint32_t(blocks)), dim3(DkvShape<kQ>::NT), 0, stream>>>(
+      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
+      static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
+      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), grid);
+}
+
+template <int D, int kQ>
+void keys_passes(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
+  const SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
+  keys_pass<D, kQ, false>(a, g, grid, stream);
+  if (grid.slots > grid.near) keys_pass<D, kQ, true>(a, g, grid, stream);
 }
 
 template <int D>
 hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
-  const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
-  const bf16* dout = static_cast<const bf16*>(g.dout);
-  const int64_t slots = tile_slots(a.N, a.max_segs, kB);
-  attn_dq_kernel<D><<<dim3(uint32_t(slots * a.H + kTail)), dim3(kThreads), 0, stream>>>(
-      q, k, v, static_cast<const bf16*>(a.o), dout, a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-      static_cast<bf16*>(g.dq), g.stats, a.flags, int32_t(slots));
-  attn_dkv_kernel<D><<<dim3(uint32_t(slots * a.Hkv + kTail)), dim3(kThreads), 0, stream>>>(
-      q, k, v, dout, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(g.dk),
-      static_cast<bf16*>(g.dv), int32_t(slots));
+  const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
+  queries_pass<D, false>(a, g, grid, stream);
+  if (grid.slots > grid.near) queries_pass<D, true>(a, g, grid, stream);
+  // A work-group of the keys pass is a serial walk over the group's heads and the
+  // rest of the segment. Below two full rounds of the chip (1024 tiles of 128
+  // keys) the longest walk sets the time and the shared form halves the work per
+  // step; above, the other form's steps are cheaper. Whole reverse and forward
+  // pass, kQ = 4 / 1: 8192 tokens, Hkv 4 (256 tiles) 0.64 / 1.08 ms; 2048, Hkv 8
+  // (128) 0.30 / 0.58 ms; 16384, Hkv 4, D 64 (512) 0.262 / 0.267 ms; 8192,
+  // Hkv 16, D 64 (1024) 0.86 / 0.75 ms; 16384, Hkv 8 (1024) 11.2 / 10.4 ms.
+  const bool share = a.N / kB * a.Hkv < 1024;
+  if (share)
+    keys_passes<D, 4>(a, g, stream);
+  else
+    keys_passes<D, 1>(a, g, stream);
   return hipGetLastError();
 }
 

@@ -57,19 +57,19 @@ struct Tile {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
-template <int D>
+template <int D, bool kFar>
 __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
-    bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, int32_t slots) {
+    bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, SlotGrid grid) {
   constexpr int CH = Tile<D>::CH, KS = D / 16, DT = D / 32, LD = kBN * CH / kThreads;
   constexpr int TB = Tile<D>::BYTES;
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
   static_assert(4 * TB >= kBM * D * 2, "the outputs are staged in the tiles' buffers");
 
   const int64_t b = blockIdx.x;
-  if (b >= int64_t(slots) * H) {
-    const int64_t j = b - int64_t(slots) * H, c = covered_tokens(cu, max_segs, N);
+  if (!kFar && b >= int64_t(grid.near) * H) {
+    const int64_t j = b - int64_t(grid.near) * H, c = covered_tokens(cu, max_segs, N);
     zero_tail(o, c, N, int64_t(H) * D * 2, j, kTail);
     if (lse != nullptr)
       for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += int64_t(kTail) * kThreads)
@@ -77,13 +77,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     if (j == 0) check_cu(cu, max_segs, N, flags);
     return;
   }
-  // Consecutive work-groups run on different XCDs: the query heads of one kv
-  // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
-  const int32_t hi = int32_t(b % H), rep = H / Hkv;
-  const int32_t hk = hi % Hkv, h = hk * rep + hi / Hkv;
+  int32_t slot, h0, h1;
+  slot_of<kFar>(grid, b, H, slot, h0, h1);
   SegTile t;
   // late tiles have the most keys: they start first
-  if (!find_tile(cu, max_segs, N, kBM, slots - 1 - int32_t(b / H), t)) return;
+  if (!kFar) slot = grid.near - 1 - slot;
+  if (!find_tile(cu, max_segs, N, kBM, slot, t)) return;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
@@ -92,6 +91,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
   const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
   const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
   const int n_tiles = (qend - t.a + kBN - 1) / kBN;
+
+  for (int32_t hi = h0; hi < (kFar ? h1 : h0 + 1); ++hi) {
+  // Consecutive work-groups run on different XCDs: the query heads of one kv
+  // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
+  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;
+  if (hi != h0) __syncthreads();  // the last head's outputs have left LDS
 
   // c > 0: a negative scale flips the queries' signs, a scale of 0 clears them
   // (a masked score is -inf, which a factor of 0 would turn into NaN)
@@ -111,23 +116,24 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     }
   }
 
-  uint32_t koff[LD], voff[LD];
-#pragma unroll
-  for (int i = 0; i < LD; ++i) {
-    const int ch = i * kThreads + tid, row = ch / CH, pos = ch % CH;
-    koff[i] = uint32_t(row) * kstride + (pos ^ Tile<D>::k_swz(row)) * 16;
-    voff[i] = uint32_t(row) * kstride + (pos ^ Tile<D>::v_swz(row)) * 16;
-  }
+  // the lane's first chunk of a tile; the others are whole multiples of 16 rows
+  // further (the swizzles' period)
+  constexpr int STEP = kThreads / CH;
+  static_assert(STEP % 16 == 0, "the swizzles repeat");
+  const int lrow = tid / CH, lpos = tid % CH;
+  const uint32_t koff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::k_swz(lrow)) * 16;
+  const uint32_t voff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::v_swz(lrow)) * 16;
   auto issue = [&](int it) {
     const int32_t s0 = t.a + it * kBN;
     const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
     const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(have - 1) * kstride + D * 2;
     const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);
     char* dst = lds + (it & 1) * 2 * TB + wave * 1024;
+    const uint32_t ko = fresh(koff), vo = fresh(voff);
 #pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16(rk, koff[i], dst + i * kThreads * 16);
+    for (int i = 0; i < LD; ++i) load_lds16(rk, ko + i * STEP * kstride, dst + i * kThreads * 16);
 #pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16(rv, voff[i], dst + TB + i * kThreads * 16);
+    for (int i = 0; i < LD; ++i) load_lds16(rv, vo + i * STEP * kstride, dst + TB + i * kThreads * 16);
   };
 
   f32x16 acc[DT];
@@ -261,7 +267,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
   };
   const bool again = __syncthreads_or(bad);  // (also: every wave is done with the tiles)
   put(nullptr);
-  if (!again) return;
+  if (!again) continue;
 
   // Some output is not finite. first_bad[d]: the first token of the segment
   // whose value d is not; the elements before it get outputs free of it.
@@ -287,23 +293,29 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
   __syncthreads();
   put(first_bad);
+  }
 }
 
 }  // namespace
 
 bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 64 || D == 128); }
 
-hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
-  const int64_t slots = tile_slots(a.N, a.max_segs, kBM);
-  const dim3 grid(uint32_t(slots * a.H + kTail)), block(kThreads);
+namespace {
+template <int D>
+hipError_t run(const AttnArgs& a, hipStream_t stream) {
+  const SlotGrid g = slot_grid(a.N, a.max_segs, kBM);
   const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
-  if (a.D == 64)
-    attn_fwd_kernel<64><<<grid, block, 0, stream>>>(q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-                                                    static_cast<bf16*>(a.o), a.lse, a.flags, int32_t(slots));
-  else
-    attn_fwd_kernel<128><<<grid, block, 0, stream>>>(q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-                                                     static_cast<bf16*>(a.o), a.lse, a.flags, int32_t(slots));
+  attn_fwd_kernel<D, false><<<dim3(uint32_t(near_blocks(g, a.H) + kTail)), dim3(kThreads), 0, stream>>>(
+      q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
+  if (g.slots > g.near)
+    attn_fwd_kernel<D, true><<<dim3(uint32_t(far_blocks(g, a.H))), dim3(kThreads), 0, stream>>>(
+        q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
+  return a.D == 64 ? run<64>(a, stream) : run<128>(a, stream);
 }
 
 }  // namespace pkv

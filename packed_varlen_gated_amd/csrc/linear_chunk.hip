@@ -50,10 +50,12 @@ struct Rows {  // an LDS tile of 64 rows of D channels
 
 template <int D, int NT>
 __device__ __forceinline__ void issue_tile(__amdgpu_buffer_rsrc_t r, int32_t stride, char* dst, int wave) {
+  constexpr int STEP = NT / Rows<D>::CH;
+  const int row = fresh(threadIdx.x) / Rows<D>::CH, pos = threadIdx.x % Rows<D>::CH;
 #pragma unroll
-  for (int i = 0; i < kC * Rows<D>::CH / NT; ++i) {
-    const int ch = i * NT + threadIdx.x, row = ch / Rows<D>::CH, pos = ch % Rows<D>::CH;
-    load_lds16(r, uint32_t(row) * stride + (pos ^ Rows<D>::swz(row)) * 16, dst + wave * 1024 + i * NT * 16);
+  for (int i = 0; i < kC / STEP; ++i) {
+    const int s = STEP % 16 == 0 ? Rows<D>::swz(row) : Rows<D>::swz(row + i * STEP);
+    load_lds16(r, uint32_t(row + i * STEP) * stride + (pos ^ s) * 16, dst + wave * 1024 + i * NT * 16);
   }
 }
 
@@ -82,7 +84,8 @@ struct WalkArgs {
   const int32_t* cu;
   int32_t max_segs;
   int64_t N;
-  int32_t H, run, slots;
+  int32_t H, run;
+  SlotGrid grid;
   float in_scale, out_scale;
   bool transposed;    // states are [DB][DA] in memory
   const float* init;  // [max_segs, H, ..] or null
@@ -145,6 +148,25 @@ struct StateAddr {
   }
 };
 
+// Saved state j of a segment whose first token is a has index a / run + j: a
+// segment of m runs has m - 1, and no two share an index. Forward it is the
+// state after run j, backward after run j + 1. The segment is the last one with
+// cu[i] / run <= index: those before it with the same quotient are shorter than
+// a run.
+template <bool kRev>
+__device__ __forceinline__ bool find_saved(const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t run,
+                                           int32_t idx, SegTile& t) {
+  t.seg = 0;
+  t.a = 0;
+  t.e = int32_t(N);
+  if (cu != nullptr && !find_segment(cu, max_segs, run, 0, idx, t.seg, t.a, t.e)) return false;
+  if (!segment_ok(t.seg, t.a, t.e, N)) return false;
+  const int64_t j = idx - t.a / run, m = (int64_t(t.e) - t.a + run - 1) / run;
+  if (j < 0 || j >= m - 1) return false;
+  t.start = int32_t(t.a + (kRev ? j + 1 : j) * run);
+  return true;
+}
+
 template <int DA, int DB, bool kRev, bool kState>
 __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x) {
   constexpr int NW = DB / 32, NT = 64 * NW, KA = DA / 16, TA = DA / 32;
@@ -159,8 +181,8 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t blk = blockIdx.x;
-  if (!kState && blk >= int64_t(x.slots) * x.H) {
-    const int64_t j = blk - int64_t(x.slots) * x.H;
+  if (!kState && blk >= int64_t(x.grid.near) * x.H) {
+    const int64_t j = blk - int64_t(x.grid.near) * x.H;
     zero_tail(x.out, covered_tokens(x.cu, x.max_segs, x.N), x.N, int64_t(x.H) * DB * 2, j, kTail);
     if (j == 0) check_cu(x.cu, x.max_segs, x.N, x.flags);
     if (x.fin != nullptr && x.cu != nullptr) {
@@ -177,11 +199,16 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
   }
   const int32_t h = int32_t(blk % x.H);
   SegTile t;
-  if (!find_tile(x.cu, x.max_segs, x.N, x.run, int32_t(blk / x.H), t)) return;
+  if constexpr (kState) {
+    // the run that ends in saved state blk / H
+    const int32_t idx = int32_t(blk / x.H);
+    if (!find_saved<kRev>(x.cu, x.max_segs, x.N, x.run, idx, t)) return;
+  } else {
+    if (!find_tile(x.cu, x.max_segs, x.N, x.run, int32_t(blk / x.H), t)) return;
+  }
   const int32_t end = t.e - t.start > x.run ? t.start + x.run : t.e;
   const bool first = kRev ? end == t.e : t.start == t.a;  // in the walk's direction
   const bool last = kRev ? t.start == t.a : end == t.e;
-  if (kState && last) return;
   // the saved state that this run starts from is at - 1 (backward: at), and the
   // one it ends in is at (backward: at - 1)
   const int64_t at = int64_t(t.a / x.run) + (t.start - t.a) / x.run;
@@ -394,9 +421,8 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
 
 // The saved states, each its run's own end state, become the states that the
 // walk has there: X <- own + lam^(run's tokens) X, X = init before a segment's
-// first run. Saved state j of a segment whose first token is a has index
-// a / run + j; a segment of m runs has m - 1, and no two share an index. A
-// work-group takes 256 x 4 elements of one head through all indices in order.
+// first run. A work-group takes 256 x 4 elements of one head through all indices
+// in order.
 constexpr int kScan = 256;
 constexpr int kAhead = 8;  // states whose loads are in flight at once
 
@@ -488,7 +514,7 @@ void walk(WalkArgs x, const void* a, const void* b, const void* c, bool transpos
   x.init = init;
   x.out = static_cast<bf16*>(out);
   x.fin = fin;
-  const int64_t grid = int64_t(x.slots) * x.H + (kState ? 0 : kTail);
+  const int64_t grid = kState ? x.N / x.run * x.H : int64_t(x.grid.near) * x.H + kTail;
   linear_walk_kernel<DA, DB, kRev, kState><<<dim3(uint32_t(grid)), dim3(2 * DB), 0, stream>>>(x);
 }
 
@@ -507,7 +533,8 @@ WalkArgs common(const LinearArgs& y) {
   x.N = y.N;
   x.H = y.H;
   x.run = run_tokens(y.N, y.H);
-  x.slots = int32_t(tile_slots(y.N, y.max_segs, x.run));
+  x.grid = slot_grid(y.N, y.max_segs, x.run);
+  x.grid.near = x.grid.slots;
   x.saved = static_cast<float*>(y.workspace);
   x.flags = y.flags;
   return x;

@@ -46,7 +46,14 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t off, 
 // 16 bytes per lane from a buffer straight into LDS, at `lds` (the same in
 // every lane) + 16 lane; out-of-range reads write 0.
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t off, void* lds) {
+  // (a scalar offset would not take part in the range check)
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+}
+// x, recomputed from here on: what is derived from it in a loop is not kept in
+// registers across the loop.
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
 // Transposing LDS read: within each group of 16 lanes, lane k points at 4

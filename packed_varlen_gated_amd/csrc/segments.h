@@ -14,6 +14,39 @@
 
 namespace pkv {
 
+// The work-groups of a call. Most slots of a batch with many empty segment slots
+// have no tile, and 30000 work-groups that only find that out take 40 us. So the
+// first `near` slots get a work-group per head, and the ones behind them (real
+// when most segments are short or few slots are empty) a second launch with one
+// for kFarHeads heads.
+constexpr int kFarHeads = 4;
+struct SlotGrid {
+  int32_t slots, near;
+};
+inline SlotGrid slot_grid(int64_t N, int64_t max_segs, int64_t bm) {
+  const int64_t few = N / bm / 2 < 64 ? 64 : N / bm / 2;
+  return {int32_t(N / bm + max_segs), int32_t(N / bm + (max_segs < few + few / 2 ? max_segs : few))};
+}
+inline int64_t near_blocks(const SlotGrid& g, int32_t heads) { return int64_t(g.near) * heads; }
+inline int64_t far_blocks(const SlotGrid& g, int32_t heads) {
+  return int64_t(g.slots - g.near) * ((heads + kFarHeads - 1) / kFarHeads);
+}
+// The slot and heads [h0, h1) of work-group b of a launch.
+template <bool kFar>
+__device__ __forceinline__ void slot_of(const SlotGrid& g, int64_t b, int32_t heads, int32_t& slot, int32_t& h0,
+                                        int32_t& h1) {
+  if (!kFar) {
+    slot = int32_t(b / heads);
+    h0 = int32_t(b % heads);
+    h1 = h0 + 1;
+  } else {
+    const int32_t per = (heads + kFarHeads - 1) / kFarHeads;
+    slot = g.near + int32_t(b / per);
+    h0 = int32_t(b % per) * kFarHeads;
+    h1 = h0 + kFarHeads < heads ? h0 + kFarHeads : heads;
+  }
+}
+
 struct SegTile {
   int32_t seg;    // segment slot
   int32_t start;  // first token of the tile
@@ -25,6 +58,35 @@ inline int64_t tile_slots(int64_t N, int64_t max_segs, int64_t bm) { return N / 
 // Whether cu[i], cu[i+1] bound a segment inside [0, N).
 __device__ __forceinline__ bool segment_ok(int32_t i, int64_t a, int64_t e, int64_t N) {
   return a >= 0 && e >= a && e <= N && (i != 0 || a == 0);
+}
+
+// The last segment i < max_segs with floor(cu[i] / bm) + inc * i <= key, and its
+// bounds; false when there is none. Every lane of the wave takes part (64 probes
+// a round, so 2 rounds up to 4096 segments) and gets the same answer. A
+// malformed cu gives some segment.
+__device__ __forceinline__ bool find_segment(const int32_t* __restrict__ cu, int32_t max_segs, int32_t bm,
+                                             int32_t inc, int32_t key, int32_t& seg, int32_t& a, int32_t& e) {
+  const int lane = threadIdx.x & 63;
+  int32_t lo = 0, hi = max_segs;  // the segment is in [lo, hi)
+  for (;;) {
+    const int32_t step = (hi - lo + 63) >> 6;
+    const int64_t i = int64_t(lo) + int64_t(lane) * step;
+    const int32_t c = cu[i < hi ? i : hi];  // (cu holds max_segs + 1)
+    const bool le = i < hi && int64_t(c < 0 ? 0 : c / bm) + inc * i <= key;
+    const uint64_t m = ~__builtin_amdgcn_ballot_w64(le);
+    const int n = m == 0 ? 64 : __builtin_ctzll(m);
+    if (n == 0) return false;
+    lo = lo + (n - 1) * step;
+    if (step == 1) {
+      seg = __builtin_amdgcn_readfirstlane(lo);
+      a = __builtin_amdgcn_readlane(c, n - 1);
+      // the probe after it holds its end (or, past lane 63, memory does)
+      e = n < 64 ? __builtin_amdgcn_readlane(c, n) : cu[seg + 1];
+      e = __builtin_amdgcn_readfirstlane(e);
+      return true;
+    }
+    if (hi - lo > step) hi = lo + step;
+  }
 }
 
 // The tile of a slot; false when the slot has none. Every lane of the wave
@@ -41,23 +103,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ cu, int32_
     t.e = int32_t(N);
     return true;
   }
-  const int lane = threadIdx.x & 63;
-  int32_t lo = 0, hi = max_segs;  // the segment is in [lo, hi)
-  for (;;) {
-    const int32_t step = (hi - lo + 63) >> 6;
-    const int64_t i = int64_t(lo) + int64_t(lane) * step;
-    const bool in = i < hi;
-    const int32_t c = in ? cu[i] : 0;
-    const bool le = in && int64_t(c < 0 ? 0 : c / bm) + i <= slot;
-    const uint64_t m = ~__builtin_amdgcn_ballot_w64(le);
-    const int n = m == 0 ? 64 : __builtin_ctzll(m);
-    if (n == 0) return false;
-    lo = lo + (n - 1) * step;
-    if (hi - lo > step) hi = lo + step;
-    if (step == 1) break;
-  }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  const int32_t a = cu[lo], e = cu[lo + 1];
+  int32_t lo, a, e;
+  if (!find_segment(cu, max_segs, bm, 1, slot, lo, a, e)) return false;
   if (!segment_ok(lo, a, e, N)) return false;
   const int64_t s = a + (int64_t(slot) - (a / bm + lo)) * bm;
   if (s < a || s >= e) return false;
