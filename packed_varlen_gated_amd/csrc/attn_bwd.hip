@@ -51,8 +51,8 @@ struct Loader {
   static constexpr int LD = T * Lds<D>::CH / NT, STEP = NT / Lds<D>::CH;
   static_assert(STEP % 16 == 0, "the swizzle repeats");
   uint32_t off, step;
-  __device__ __forceinline__ Loader(int32_t stride) {
-    const int row = threadIdx.x / Lds<D>::CH, pos = threadIdx.x % Lds<D>::CH;
+  __device__ __forceinline__ Loader(int32_t stride, int tid) {
+    const int row = tid / Lds<D>::CH, pos = tid % Lds<D>::CH;
     off = uint32_t(row) * stride + (pos ^ Lds<D>::swz(row)) * 16;
     step = uint32_t(STEP) * stride;
   }
@@ -63,32 +63,30 @@ struct Loader {
   }
 };
 
-// Operand reads from a tile: rows 32 j + lane % 32 (contraction over channels,
-// step i of 16), and transposed: channels 32 i + lane % 32 (contraction over
-// the rows of 16-row step j, in the order of a product's result registers).
+// Operand reads from a tile (of 1024-byte alignment): rows 32 j + lane % 32
+// (contraction over channels, step i of 16), and transposed: channels
+// 32 i + lane % 32 (contraction over the rows of 16-row step j, in the order of
+// a product's result registers). The swizzle is an XOR of address bits that the
+// step only flips: an address register per read kind, not one per step.
 template <int D>
 struct Reader {
-  int col, half, fx;
-  int tr[2];   // row and half-chunk bytes of the two transposing reads
-  int tc[2];   // swizzled chunk before the 32-channel group is added
-  __device__ __forceinline__ Reader() {
-    const int lane = threadIdx.x & 63;
+  int col, half;
+  uint32_t row0, tr0, tr1;
+  __device__ __forceinline__ Reader(int tid) {
+    const int lane = tid & 63;
     half = lane >> 5;
     col = lane & 31;
-    fx = Lds<D>::swz(col);
+    row0 = col * Lds<D>::ROW + (half ^ Lds<D>::swz(col)) * 16;
     const int r = 4 * half + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      tr[u] = (r + 8 * u) * Lds<D>::ROW + (lane & 1) * 8;
-      tc[u] = c ^ Lds<D>::swz(r + 8 * u);
-    }
+    tr0 = r * Lds<D>::ROW + (lane & 1) * 8 + (c ^ Lds<D>::swz(r)) * 16;
+    tr1 = (r + 8) * Lds<D>::ROW + (lane & 1) * 8 + (c ^ Lds<D>::swz(r + 8)) * 16;
   }
-  __device__ __forceinline__ bf16x8 rows(const char* t, int j, int i) const {
-    return *reinterpret_cast<const bf16x8*>(t + (32 * j + col) * Lds<D>::ROW + (((2 * i + half) ^ fx) * 16));
+  __device__ __forceinline__ bf16x8 rows(uint32_t t, int j, int i) const {
+    return read_lds8(((t + row0) ^ (32 * i)) + 32 * j * Lds<D>::ROW);
   }
-  __device__ __forceinline__ bf16x8 channels(const char* t, int i, int j) const {
-    const char* p = t + 16 * j * Lds<D>::ROW;
-    return join(read_tr(p + tr[0] + ((4 * i) ^ tc[0]) * 16), read_tr(p + tr[1] + ((4 * i) ^ tc[1]) * 16));
+  __device__ __forceinline__ bf16x8 channels(uint32_t t, int i, int j) const {
+    return join(read_tr(((t + tr0) ^ (64 * i)) + 16 * j * Lds<D>::ROW),
+                read_tr(((t + tr1) ^ (64 * i)) + 16 * j * Lds<D>::ROW));
   }
 };
 
@@ -117,7 +115,7 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[D / 32], float f,
       *reinterpret_cast<bf16x4*>(st + rd.col * ROW + (((4 * i + j) ^ (rd.col & (CH - 1))) * 16) + rd.half * 8) = x;
     }
   asm volatile("" ::: "memory");  // the wave's own rows: its LDS accesses are in order
-  for (int i = threadIdx.x & 63; i < 32 * CH; i += 64) {
+  for (int i = rd.half * 32 + rd.col; i < 32 * CH; i += 64) {
     const int r = i / CH, ch = i % CH;
     if (r < have)
       *reinterpret_cast<i32x4*>(dst + r * stride + ch * 8) =
@@ -125,7 +123,7 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[D / 32], float f,
   }
 }
 
-template <int D, bool kFar>
+template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
@@ -135,29 +133,31 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
 
   const int64_t b = blockIdx.x;
-  if (!kFar && b >= int64_t(grid.near) * H) {
-    const int64_t j = b - int64_t(grid.near) * H;
+  const int64_t blocks = slot_blocks(grid, H);
+  if (b >= blocks) {
+    const int64_t j = b - blocks;
     zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * 2, j, kTail);
     if (j == 0) check_cu(cu, max_segs, N, flags);
     return;
   }
   int32_t slot, h0, h1;
-  slot_of<kFar>(grid, b, H, slot, h0, h1);
+  slot_of(grid, b, H, slot, h0, h1);
   SegTile t;
-  if (!kFar) slot = grid.near - 1 - slot;  // late tiles have the most keys: they start first
+  // late tiles have the most keys: they start first
+  if (slot < grid.near) slot = grid.near - 1 - slot;
   if (!find_tile(cu, max_segs, N, kB, slot, t)) return;
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Reader<D> rd;
+  for (int32_t hi = h0; hi < h1; ++hi) {
+  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;  // (as in the forward pass)
+  // (nothing that goes by the lane is kept from one head to the next)
+  const int tid = fresh(threadIdx.x), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Reader<D> rd(tid);
   const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
   const int32_t q0 = t.start + wave * 32;
   const int32_t rows = t.e - q0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
   const int32_t qend = t.start + kB < t.e ? t.start + kB : t.e;
   const int n_tiles = (qend - t.a + kT - 1) / kT;
-  const Loader<D, kT, kThreads> ld(kstride);
-  for (int32_t hi = h0; hi < (kFar ? h1 : h0 + 1); ++hi) {
-  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;  // (as in the forward pass)
-  if (hi != h0) __syncthreads();  // the last head's outputs have left LDS
+  const Loader<D, kT, kThreads> ld(kstride, tid);
   auto issue = [&](int it) {
     const int32_t s0 = t.a + it * kT;
     const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
@@ -196,8 +196,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
     wait_vm();
     bar();
     if (it + 1 < n_tiles) issue(it + 1);
-    const char* kt = lds + (it & 1) * 2 * TB;
-    const char* vt = kt + TB;
+    const uint32_t kt = lds_addr(lds) + (it & 1) * 2 * TB, vt = kt + TB;
     const int32_t s0 = t.a + it * kT;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -225,6 +224,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
   __syncthreads();
   if (have > 0)
     store_rows<D>(acc, scale, lds + wave * (32 * D * 2), dq + (int64_t(q0) * H + h) * D, int64_t(H) * D, have, rd);
+  if (hi + 1 < h1) __syncthreads();  // the outputs have left LDS
   }
 }
 
@@ -238,7 +238,7 @@ struct DkvShape {
   static constexpr int T = kQ == 4 ? 128 : 64;    // queries per tile
 };
 
-template <int D, int kQ, bool kFar>
+template <int D, int kQ>
 __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const bf16* __restrict__ dout, const float* __restrict__ stats, const int32_t* __restrict__ cu,
@@ -250,30 +250,32 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB + 4 * T * 4];
 
   const int64_t b = blockIdx.x;
-  if (!kFar && b >= int64_t(grid.near) * Hkv) {
-    const int64_t j = b - int64_t(grid.near) * Hkv, cov = covered_tokens(cu, max_segs, N);
+  const int64_t blocks = slot_blocks(grid, Hkv);
+  if (b >= blocks) {
+    const int64_t j = b - blocks, cov = covered_tokens(cu, max_segs, N);
     zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, kTail);
     zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, kTail);
     return;
   }
   const int32_t rep = H / Hkv;
   int32_t slot, h0, h1;
-  slot_of<kFar>(grid, b, Hkv, slot, h0, h1);
+  slot_of(grid, b, Hkv, slot, h0, h1);
   SegTile t;
   if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Reader<D> rd;
+  for (int32_t hk = h0; hk < (kQ == 1 ? h1 : h0 + 1); ++hk) {
+  // (nothing that goes by the lane is kept from one head to the next)
+  const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Reader<D> rd(tid);
   const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
   const int32_t k0 = t.start + wave / kQ * 32;  // the wave's first key
   const int32_t rows = t.e - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
   const int per_head = (t.e - t.start + T - 1) / T, n_tiles = per_head * rep;
-  const Loader<D, T, NT> ld(qstride);
-  for (int32_t hk = h0; hk < (kFar ? h1 : h0 + 1); ++hk) {
-  if (hk != h0) __syncthreads();  // the last head's outputs have left LDS
-  int ih = 0, iq = 0;  // head and query tile of the next load
+  const Loader<D, T, NT> ld(qstride, tid);
+  int ih = hk * rep, iq = 0;  // query head and tile of the next load
+  // Q, dO and the statistics of the next tile
   auto issue = [&](int it) {
-    const int32_t s0 = t.start + iq * T, h = hk * rep + ih;
+    const int32_t s0 = t.start + iq * T, h = ih;
     const int32_t n = t.e - s0 < T ? t.e - s0 : T;
     const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
     char* dst = lds + (it & 1) * 2 * TB;
@@ -292,7 +294,6 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
     }
   };
   issue(0);
-
   const int64_t at = (int64_t(have > 0 ? k0 : t.start) * Hkv + hk) * D;
   bf16x8 kf[KS], vf[KS];
   load_rows<D>(kf, k + at, have, kstride, rd);
@@ -309,8 +310,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
     wait_vm();
     bar();
     if (it + 1 < n_tiles) issue(it + 1);
-    const char* qt = lds + (it & 1) * 2 * TB;
-    const char* ot = qt + TB;
+    const uint32_t qt0 = lds_addr(lds) + (it & 1) * 2 * TB;
     const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * T * 4);
     const f32x4* dl = ls + T / 4;
     const int32_t s0 = t.start + cq * T;
@@ -318,36 +318,52 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
 #pragma unroll 1
     for (int j = wave % kQ; j < T / 32; j += kQ) {
       const int32_t b0 = s0 + 32 * j;  // first query of the block
+      // (addresses are formed per block: one register each instead of one per read)
+      const uint32_t qt = fresh_uniform(qt0 + 32 * j * Lds<D>::ROW), ot = qt + TB;
       if (have == 0 || b0 + 31 < k0 || b0 >= t.e) continue;
-      f32x16 s = {}, dp = {};
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {  // independent products take turns
-        s = mfma32(rd.rows(qt, j, i), kf[i], s);
-        dp = mfma32(rd.rows(ot, j, i), vf[i], dp);
-      }
+      // Registers are full at D = 128 (k, v, dk and dv take 192): the weights are
+      // done with before dP is begun, and nothing of a phase starts early. The
+      // other wave of the SIMD fills the gaps.
       bf16x8 p[2], ds[2];
+      f32x16 x = {};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) x = mfma32(rd.rows(qt, 0, i), kf[i], x);
+      if (D == 128) __builtin_amdgcn_sched_barrier(0);
       // the lane's key takes part in the block's queries first .. end - 1
       const bool edge = b0 < k0 + 31 || b0 + 32 > t.e;
       const int32_t first = edge ? k0 + rd.col - b0 - 4 * rd.half : -64;
       const int32_t end = edge ? t.e - b0 - 4 * rd.half : 64;
 #pragma unroll
       for (int i4 = 0; i4 < 4; ++i4) {
-        const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half], d4 = dl[8 * j + 2 * i4 + rd.half];
+        const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 4 * i4 + e, r = 8 * i4 + e;
-          float x = ex2(fmaf(s[i], c, -l4[e]));
-          x = r >= first && r < end ? x : 0.f;
-          p[i / 8][i % 8] = static_cast<bf16>(x);
-          ds[i / 8][i % 8] = static_cast<bf16>(x * (dp[i] - d4[e]));
+          const float y = ex2(fmaf(x[i], c, -l4[e]));
+          x[i] = r >= first && r < end ? y : 0.f;
+          p[i / 8][i % 8] = static_cast<bf16>(x[i]);
+        }
+      }
+      if (D == 128) __builtin_amdgcn_sched_barrier(0);
+      f32x16 dp = {};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(ot, 0, i), vf[i], dp);
+      if (D == 128) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const f32x4 d4 = dl[8 * j + 2 * i4 + rd.half];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * i4 + e;
+          ds[i / 8][i % 8] = static_cast<bf16>(x[i] * (dp[i] - d4[e]));
         }
       }
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          av[i] = mfma32(rd.channels(ot, i, 2 * j + u), p[u], av[i]);
-          ak[i] = mfma32(rd.channels(qt, i, 2 * j + u), ds[u], ak[i]);
+          av[i] = mfma32(rd.channels(ot, i, u), p[u], av[i]);
+          ak[i] = mfma32(rd.channels(qt, i, u), ds[u], ak[i]);
         }
     }
   }
@@ -355,7 +371,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
   if constexpr (kQ > 1) {
     // The sums of the waves that share keys: each in turn hands dk, then dv,
     // to the first of them.
-    static_assert(NT / 64 / kQ * DT * 4096 <= int(sizeof(lds)), "sums in flight");
+    static_assert(NT / 64 / kQ * DT * 4096 <= 4 * TB, "sums in flight");
     f32x4* mine = reinterpret_cast<f32x4*>(lds) + (wave / kQ) * (DT * 4 * 64) + lane;
     auto join_sums = [&](f32x16 (&x)[DT], int from) {
       if (wave % kQ == from) {
@@ -385,45 +401,33 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
     }
   }
   if (have > 0 && wave % kQ == 0) {
-    char* st = lds + wave * (32 * D * 2);
+    char* st = lds + wave / kQ * (32 * D * 2);
     const int64_t to = (int64_t(k0) * Hkv + hk) * D;
     store_rows<D>(ak, scale, st, dk + to, int64_t(Hkv) * D, have, rd);
     asm volatile("" ::: "memory");
     store_rows<D>(av, 1.f, st, dv + to, int64_t(Hkv) * D, have, rd);
   }
+  if (kQ == 1 && hk + 1 < h1) __syncthreads();  // the outputs have left LDS
   }
 }
 
-template <int D, bool kFar>
-void queries_pass(const AttnArgs& a, const AttnGradArgs& g, const SlotGrid& grid, hipStream_t stream) {
-  const int64_t blocks = kFar ? far_blocks(grid, a.H) : near_blocks(grid, a.H) + kTail;
-  attn_dq_kernel<D, kFar><<<dim3(uint32_t(blocks)), dim3(kThreads), 0, stream>>>(
-      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
-      static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
-      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, grid);
-}
-
-template <int D, int kQ, bool kFar>
-void keys_pass(const AttnArgs& a, const AttnGradArgs& g, const SlotGrid& grid, hipStream_t stream) {
-  const int64_t blocks = kFar ? far_blocks(grid, a.Hkv) : near_blocks(grid, a.Hkv) + kTail;
-  attn_dkv_kernel<D, kQ, kFar><<<dim3(uint32_t(blocks)), dim3(DkvShape<kQ>::NT), 0, stream>>>(
+template <int D, int kQ>
+void keys_pass(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
+  SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
+  if (kQ > 1) grid.near = grid.slots;  // (small calls: a work-group per head)
+  attn_dkv_kernel<D, kQ><<<dim3(uint32_t(slot_blocks(grid, a.Hkv) + kTail)), dim3(DkvShape<kQ>::NT), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
       static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), grid);
 }
 
-template <int D, int kQ>
-void keys_passes(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
-  const SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
-  keys_pass<D, kQ, false>(a, g, grid, stream);
-  if (grid.slots > grid.near) keys_pass<D, kQ, true>(a, g, grid, stream);
-}
-
 template <int D>
 hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
-  queries_pass<D, false>(a, g, grid, stream);
-  if (grid.slots > grid.near) queries_pass<D, true>(a, g, grid, stream);
+  attn_dq_kernel<D><<<dim3(uint32_t(slot_blocks(grid, a.H) + kTail)), dim3(kThreads), 0, stream>>>(
+      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
+      static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
+      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, grid);
   // A work-group of the keys pass is a serial walk over the group's heads and the
   // rest of the segment. Below two full rounds of the chip (1024 tiles of 128
   // keys) the longest walk sets the time and the shared form halves the work per
@@ -433,9 +437,9 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   // Hkv 16, D 64 (1024) 0.86 / 0.75 ms; 16384, Hkv 8 (1024) 11.2 / 10.4 ms.
   const bool share = a.N / kB * a.Hkv < 1024;
   if (share)
-    keys_passes<D, 4>(a, g, stream);
+    keys_pass<D, 4>(a, g, stream);
   else
-    keys_passes<D, 1>(a, g, stream);
+    keys_pass<D, 1>(a, g, stream);
   return hipGetLastError();
 }
 

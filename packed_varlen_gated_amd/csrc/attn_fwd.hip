@@ -57,7 +57,7 @@ struct Tile {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
-template <int D, bool kFar>
+template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
@@ -68,8 +68,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
   static_assert(4 * TB >= kBM * D * 2, "the outputs are staged in the tiles' buffers");
 
   const int64_t b = blockIdx.x;
-  if (!kFar && b >= int64_t(grid.near) * H) {
-    const int64_t j = b - int64_t(grid.near) * H, c = covered_tokens(cu, max_segs, N);
+  const int64_t blocks = slot_blocks(grid, H);
+  if (b >= blocks) {
+    const int64_t j = b - blocks, c = covered_tokens(cu, max_segs, N);
     zero_tail(o, c, N, int64_t(H) * D * 2, j, kTail);
     if (lse != nullptr)
       for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += int64_t(kTail) * kThreads)
@@ -78,43 +79,24 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     return;
   }
   int32_t slot, h0, h1;
-  slot_of<kFar>(grid, b, H, slot, h0, h1);
+  slot_of(grid, b, H, slot, h0, h1);
   SegTile t;
   // late tiles have the most keys: they start first
-  if (!kFar) slot = grid.near - 1 - slot;
+  if (slot < grid.near) slot = grid.near - 1 - slot;
   if (!find_tile(cu, max_segs, N, kBM, slot, t)) return;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int32_t hi = h0; hi < h1; ++hi) {
+  // Consecutive work-groups run on different XCDs: the query heads of one kv
+  // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
+  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;
+  // (nothing that goes by the lane is kept from one head to the next)
+  const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
   const int32_t q0 = t.start + wave * 32;  // the wave's first query
   const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
   const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
   const int n_tiles = (qend - t.a + kBN - 1) / kBN;
-
-  for (int32_t hi = h0; hi < (kFar ? h1 : h0 + 1); ++hi) {
-  // Consecutive work-groups run on different XCDs: the query heads of one kv
-  // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
-  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;
-  if (hi != h0) __syncthreads();  // the last head's outputs have left LDS
-
-  // c > 0: a negative scale flips the queries' signs, a scale of 0 clears them
-  // (a masked score is -inf, which a factor of 0 would turn into NaN)
-  const float c = scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
-  bf16x8 qf[KS];
-  {
-    const int32_t have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-    const auto r = buffer(q + (int64_t(rows > 0 ? q0 : t.start) * H + h) * D,
-                          have > 0 ? int64_t(have - 1) * qstride + D * 2 : 0);
-    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, keep = scale == 0.f ? 0u : ~0u;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      i32x4 x = __builtin_bit_cast(i32x4, load8(r, uint32_t(col) * qstride + (2 * i + half) * 16));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = int((uint32_t(x[j]) ^ flip) & keep);
-      qf[i] = __builtin_bit_cast(bf16x8, x);
-    }
-  }
 
   // the lane's first chunk of a tile; the others are whole multiples of 16 rows
   // further (the swizzles' period)
@@ -135,6 +117,24 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
 #pragma unroll
     for (int i = 0; i < LD; ++i) load_lds16(rv, vo + i * STEP * kstride, dst + TB + i * kThreads * 16);
   };
+
+  // c > 0: a negative scale flips the queries' signs, a scale of 0 clears them
+  // (a masked score is -inf, which a factor of 0 would turn into NaN)
+  const float c = scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
+  bf16x8 qf[KS];
+  {
+    const int32_t have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+    const auto r = buffer(q + (int64_t(rows > 0 ? q0 : t.start) * H + h) * D,
+                          have > 0 ? int64_t(have - 1) * qstride + D * 2 : 0);
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, keep = scale == 0.f ? 0u : ~0u;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      i32x4 x = __builtin_bit_cast(i32x4, load8(r, uint32_t(col) * qstride + (2 * i + half) * 16));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = int((uint32_t(x[j]) ^ flip) & keep);
+      qf[i] = __builtin_bit_cast(bf16x8, x);
+    }
+  }
 
   f32x16 acc[DT];
   float m = -FLT_MAX, l = 0.f;
@@ -267,7 +267,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
   };
   const bool again = __syncthreads_or(bad);  // (also: every wave is done with the tiles)
   put(nullptr);
-  if (!again) continue;
+  if (!again) {
+    if (hi + 1 < h1) __syncthreads();  // the outputs have left LDS
+    continue;
+  }
 
   // Some output is not finite. first_bad[d]: the first token of the segment
   // whose value d is not; the elements before it get outputs free of it.
@@ -293,6 +296,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
     for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
   __syncthreads();
   put(first_bad);
+  __syncthreads();
   }
 }
 
@@ -300,22 +304,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
 
 bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 64 || D == 128); }
 
-namespace {
-template <int D>
-hipError_t run(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
   const SlotGrid g = slot_grid(a.N, a.max_segs, kBM);
   const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
-  attn_fwd_kernel<D, false><<<dim3(uint32_t(near_blocks(g, a.H) + kTail)), dim3(kThreads), 0, stream>>>(
+  (a.D == 64 ? attn_fwd_kernel<64> : attn_fwd_kernel<128>)<<<dim3(uint32_t(slot_blocks(g, a.H) + kTail)),
+                                                             dim3(kThreads), 0, stream>>>(
       q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
-  if (g.slots > g.near)
-    attn_fwd_kernel<D, true><<<dim3(uint32_t(far_blocks(g, a.H))), dim3(kThreads), 0, stream>>>(
-        q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
   return hipGetLastError();
-}
-}  // namespace
-
-hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
-  return a.D == 64 ? run<64>(a, stream) : run<128>(a, stream);
 }
 
 }  // namespace pkv

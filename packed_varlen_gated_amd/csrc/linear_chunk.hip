@@ -84,8 +84,7 @@ struct WalkArgs {
   const int32_t* cu;
   int32_t max_segs;
   int64_t N;
-  int32_t H, run;
-  SlotGrid grid;
+  int32_t H, run, slots;
   float in_scale, out_scale;
   bool transposed;    // states are [DB][DA] in memory
   const float* init;  // [max_segs, H, ..] or null
@@ -181,8 +180,8 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t blk = blockIdx.x;
-  if (!kState && blk >= int64_t(x.grid.near) * x.H) {
-    const int64_t j = blk - int64_t(x.grid.near) * x.H;
+  if (!kState && blk >= int64_t(x.slots) * x.H) {
+    const int64_t j = blk - int64_t(x.slots) * x.H;
     zero_tail(x.out, covered_tokens(x.cu, x.max_segs, x.N), x.N, int64_t(x.H) * DB * 2, j, kTail);
     if (j == 0) check_cu(x.cu, x.max_segs, x.N, x.flags);
     if (x.fin != nullptr && x.cu != nullptr) {
@@ -514,7 +513,7 @@ void walk(WalkArgs x, const void* a, const void* b, const void* c, bool transpos
   x.init = init;
   x.out = static_cast<bf16*>(out);
   x.fin = fin;
-  const int64_t grid = kState ? x.N / x.run * x.H : int64_t(x.grid.near) * x.H + kTail;
+  const int64_t grid = kState ? x.N / x.run * x.H : int64_t(x.slots) * x.H + kTail;
   linear_walk_kernel<DA, DB, kRev, kState><<<dim3(uint32_t(grid)), dim3(2 * DB), 0, stream>>>(x);
 }
 
@@ -533,8 +532,7 @@ WalkArgs common(const LinearArgs& y) {
   x.N = y.N;
   x.H = y.H;
   x.run = run_tokens(y.N, y.H);
-  x.grid = slot_grid(y.N, y.max_segs, x.run);
-  x.grid.near = x.grid.slots;
+  x.slots = int32_t(tile_slots(y.N, y.max_segs, x.run));
   x.saved = static_cast<float*>(y.workspace);
   x.flags = y.flags;
   return x;

@@ -56,13 +56,29 @@ __device__ __forceinline__ uint32_t fresh(uint32_t x) {
   return x;
 }
 
+__device__ __forceinline__ uint32_t fresh_uniform(uint32_t x) {
+  x = __builtin_amdgcn_readfirstlane(x);
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
+// LDS by byte address.
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((const lds_char*)(p)));
+}
+__device__ __forceinline__ bf16x8 read_lds8(uint32_t a) {
+  typedef const __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+  return *(lds_bf16x8*)(uintptr_t(a));
+}
 // Transposing LDS read: within each group of 16 lanes, lane k points at 4
 // consecutive bf16; with lane k at row r0 + k / 4, column c0 + 4 (k % 4) of a
 // tile, lane j gets column c0 + j of rows r0 .. r0 + 3.
-__device__ __forceinline__ s16x4 read_tr(const void* p) {
+__device__ __forceinline__ s16x4 read_tr(uint32_t a) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t(a)));
 }
+__device__ __forceinline__ s16x4 read_tr(const void* p) { return read_tr(lds_addr(p)); }
 __device__ __forceinline__ bf16x8 join(s16x4 lo, s16x4 hi) {
   return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }

@@ -14,33 +14,33 @@
 
 namespace pkv {
 
-// The work-groups of a call. Most slots of a batch with many empty segment slots
-// have no tile, and 30000 work-groups that only find that out take 40 us. So the
-// first `near` slots get a work-group per head, and the ones behind them (real
-// when most segments are short or few slots are empty) a second launch with one
-// for kFarHeads heads.
-constexpr int kFarHeads = 4;
+// The work-groups of a call. A batch with many empty segment slots has many slots
+// without a tile, and a work-group that only finds that out still costs its
+// dispatch (30000 of them 40 us). The first `near` slots, enough for segments of
+// a tile's length on average, get a work-group per head; the ones behind them,
+// real only when most segments are shorter, one for kFarHeads heads.
+constexpr int kFarHeads = 8;
 struct SlotGrid {
   int32_t slots, near;
 };
 inline SlotGrid slot_grid(int64_t N, int64_t max_segs, int64_t bm) {
-  const int64_t few = N / bm / 2 < 64 ? 64 : N / bm / 2;
-  return {int32_t(N / bm + max_segs), int32_t(N / bm + (max_segs < few + few / 2 ? max_segs : few))};
+  const int64_t few = N / bm < 64 ? 64 : N / bm;
+  return {int32_t(N / bm + max_segs), int32_t(N / bm + (max_segs < few ? max_segs : few))};
 }
-inline int64_t near_blocks(const SlotGrid& g, int32_t heads) { return int64_t(g.near) * heads; }
-inline int64_t far_blocks(const SlotGrid& g, int32_t heads) {
-  return int64_t(g.slots - g.near) * ((heads + kFarHeads - 1) / kFarHeads);
+__host__ __device__ inline int64_t slot_blocks(const SlotGrid& g, int32_t heads) {
+  return int64_t(g.near) * heads + int64_t(g.slots - g.near) * ((heads + kFarHeads - 1) / kFarHeads);
 }
-// The slot and heads [h0, h1) of work-group b of a launch.
-template <bool kFar>
+// The slot and heads [h0, h1) of work-group b.
 __device__ __forceinline__ void slot_of(const SlotGrid& g, int64_t b, int32_t heads, int32_t& slot, int32_t& h0,
                                         int32_t& h1) {
-  if (!kFar) {
-    slot = int32_t(b / heads);
-    h0 = int32_t(b % heads);
+  // (those of several heads start first)
+  const int32_t per = (heads + kFarHeads - 1) / kFarHeads;
+  const int64_t far = int64_t(g.slots - g.near) * per;
+  if (b >= far) {
+    slot = int32_t((b - far) / heads);
+    h0 = int32_t((b - far) % heads);
     h1 = h0 + 1;
   } else {
-    const int32_t per = (heads + kFarHeads - 1) / kFarHeads;
     slot = g.near + int32_t(b / per);
     h0 = int32_t(b % per) * kFarHeads;
     h1 = h0 + kFarHeads < heads ? h0 + kFarHeads : heads;

@@ -190,6 +190,29 @@ def test_many_empty_slots():
     linear_case(lens, 5, 2, 64, 64, "bf16", states=False)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_short_segments_many_heads(D):
+    """Enough slots and heads that a work-group takes several heads of its tile (10 heads: groups of 4, 4, 2)."""
+    rng = np.random.default_rng(17)
+    lens = []
+    while sum(lens) < 13300:
+        lens.append(int(rng.integers(1, 260)))
+    lens[3:3] = [0] * 600
+    attn_case(lens, 21, 10, 10, D, "bf16", seed=18)
+    N, cu = lay(lens, 21)
+    q, k, v, do = attn_inputs(19, N, 10, 10, D, "bf16")
+    ref = attn_run(q, k, v, do, cu_gpu(cu))
+    for t in (q, k, v, do):
+        t[0, cu[605] + 1:cu[606]] = float("nan")     # a segment's later tokens
+    got = attn_run(q, k, v, do, cu_gpu(cu))
+    keep = torch.ones(N, dtype=torch.bool, device=dev())
+    keep[cu[605] + 1:cu[606]] = False
+    assert torch.equal(got["o"][0][keep], ref["o"][0][keep])
+    keep[cu[605]:cu[606]] = False
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(got[n][0][keep], ref[n][0][keep]), n
+
+
 # ------------------------------------------------------- linear attention
 
 def linear_run(q, k, v, do, g, S0, dF, cud, scale=1.0):
