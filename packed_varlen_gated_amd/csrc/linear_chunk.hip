@@ -63,8 +63,8 @@ __device__ __forceinline__ void issue_tile(__amdgpu_buffer_rsrc_t r, int32_t str
 template <int D>
 struct Transposed {
   int at[2], ch[2];
-  __device__ __forceinline__ Transposed() {
-    const int lane = threadIdx.x & 63, r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+  __device__ __forceinline__ Transposed(int lane) {
+    const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
     const int c = ((lane >> 4) & 1) * 2 + (lane & 1);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -84,7 +84,8 @@ struct WalkArgs {
   const int32_t* cu;
   int32_t max_segs;
   int64_t N;
-  int32_t H, run, slots;
+  int32_t H, run;
+  SlotGrid grid;
   float in_scale, out_scale;
   bool transposed;    // states are [DB][DA] in memory
   const float* init;  // [max_segs, H, ..] or null
@@ -102,9 +103,9 @@ struct StateAddr {
   __amdgpu_buffer_rsrc_t r;
   uint32_t off;
   bool transposed;
-  __device__ __forceinline__ StateAddr(const float* p, bool transposed, int wave) : transposed(transposed) {
-    const int lane = threadIdx.x & 63, l = lane & 31, half = lane >> 5;
-    const int e = 32 * wave + (l & 16) + ((l & 4) << 1) + ((l & 8) >> 1) + (l & 3);
+  __device__ __forceinline__ StateAddr(const float* p, bool transposed, int tid) : transposed(transposed) {
+    const int l = tid & 31, half = (tid >> 5) & 1;
+    const int e = 32 * (tid >> 6) + (l & 16) + ((l & 4) << 1) + ((l & 8) >> 1) + (l & 3);
     r = buffer(p, int64_t(DA) * DB * 4);
     off = 4 * (transposed ? e * DA + 8 * half : 8 * half * DB + e);
   }
@@ -178,10 +179,10 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
   __shared__ float upd[2][kC];
   __shared__ f32x4 rel[kState ? 1 : 2][kState ? 1 : 4][kState ? 1 : 64];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t blk = blockIdx.x;
-  if (!kState && blk >= int64_t(x.slots) * x.H) {
-    const int64_t j = blk - int64_t(x.slots) * x.H;
+  if (!kState && blk >= slot_blocks(x.grid, x.H)) {
+    const int tid = threadIdx.x;
+    const int64_t j = blk - slot_blocks(x.grid, x.H);
     zero_tail(x.out, covered_tokens(x.cu, x.max_segs, x.N), x.N, int64_t(x.H) * DB * 2, j, kTail);
     if (j == 0) check_cu(x.cu, x.max_segs, x.N, x.flags);
     if (x.fin != nullptr && x.cu != nullptr) {
@@ -196,14 +197,16 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
     }
     return;
   }
-  const int32_t h = int32_t(blk % x.H);
+  int32_t slot, h0, h1;
   SegTile t;
   if constexpr (kState) {
     // the run that ends in saved state blk / H
-    const int32_t idx = int32_t(blk / x.H);
-    if (!find_saved<kRev>(x.cu, x.max_segs, x.N, x.run, idx, t)) return;
+    h0 = int32_t(blk % x.H);
+    h1 = h0 + 1;
+    if (!find_saved<kRev>(x.cu, x.max_segs, x.N, x.run, int32_t(blk / x.H), t)) return;
   } else {
-    if (!find_tile(x.cu, x.max_segs, x.N, x.run, int32_t(blk / x.H), t)) return;
+    slot_of(x.grid, blk, x.H, slot, h0, h1);
+    if (!find_tile(x.cu, x.max_segs, x.N, x.run, slot, t)) return;
   }
   const int32_t end = t.e - t.start > x.run ? t.start + x.run : t.e;
   const bool first = kRev ? end == t.e : t.start == t.a;  // in the walk's direction
@@ -213,6 +216,10 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
   const int64_t at = int64_t(t.a / x.run) + (t.start - t.a) / x.run;
   constexpr int64_t kState_ = int64_t(DA) * DB;
 
+  for (int32_t h = h0; h < (kState ? h0 + 1 : h1); ++h) {
+  // (nothing that goes by the lane is kept from one head to the next)
+  const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (!kState && h != h0) __syncthreads();  // the last head is done with LDS
   const float g2 = x.g[h] * kLog2e;
   const int half = lane >> 5, col = lane & 31;
   const int32_t as = x.H * DA * 2, cs = x.H * DB * 2;
@@ -252,7 +259,7 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
                              : first ? (x.init ? x.init + (int64_t(t.seg) * x.H + h) * kState_ : nullptr)
                                      : x.saved + ((kRev ? at : at - 1) * x.H + h) * kState_;
   if (from != nullptr) {
-    StateAddr<DA, DB>(from, x.transposed, wave).load(X);
+    StateAddr<DA, DB>(from, x.transposed, tid).load(X);
   } else {
 #pragma unroll
     for (int i = 0; i < TA; ++i) X[i] = f32x16{};
@@ -277,8 +284,8 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
       }
     }
   }
-  const Transposed<DA> tb;
-  const Transposed<DB> tc;
+  const Transposed<DA> tb(lane);
+  const Transposed<DB> tc(lane);
   const int fx = Rows<DA>::swz(col);
 
   for (int it = it0; it < n_chunks; ++it) {
@@ -415,7 +422,8 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
 
   float* to = kState ? x.saved + ((kRev ? at - 1 : at) * x.H + h) * kState_
                      : (last && x.fin ? x.fin + (int64_t(t.seg) * x.H + h) * kState_ : nullptr);
-  if (to != nullptr) StateAddr<DA, DB>(to, x.transposed, wave).store(X);
+  if (to != nullptr) StateAddr<DA, DB>(to, x.transposed, tid).store(X);
+  }
 }
 
 // The saved states, each its run's own end state, become the states that the
@@ -513,7 +521,7 @@ void walk(WalkArgs x, const void* a, const void* b, const void* c, bool transpos
   x.init = init;
   x.out = static_cast<bf16*>(out);
   x.fin = fin;
-  const int64_t grid = kState ? x.N / x.run * x.H : int64_t(x.slots) * x.H + kTail;
+  const int64_t grid = kState ? x.N / x.run * x.H : slot_blocks(x.grid, x.H) + kTail;
   linear_walk_kernel<DA, DB, kRev, kState><<<dim3(uint32_t(grid)), dim3(2 * DB), 0, stream>>>(x);
 }
 
@@ -532,7 +540,7 @@ WalkArgs common(const LinearArgs& y) {
   x.N = y.N;
   x.H = y.H;
   x.run = run_tokens(y.N, y.H);
-  x.slots = int32_t(tile_slots(y.N, y.max_segs, x.run));
+  x.grid = slot_grid(y.N, y.max_segs, x.run);
   x.saved = static_cast<float*>(y.workspace);
   x.flags = y.flags;
   return x;
