@@ -82,10 +82,9 @@ pkv_status check_linear(const int32_t* cu, int32_t& max_segs, int64_t N, int32_t
   return PKV_OK;
 }
 
-// Of the linear-attention calls, both directions.
-size_t linear_workspace(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype) {
+size_t linear_workspace(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, bool reverse) {
   if (N < 1 || N > kInt32Max || H < 1 || H > 65536 || !pkv::linear_chunk_supported(Dk, Dv, dtype)) return 0;
-  return pkv::linear_chunk_workspace_bytes(N, H, Dk, Dv);
+  return pkv::linear_chunk_workspace_bytes(N, H, Dk, Dv, reverse);
 }
 
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
@@ -147,7 +146,7 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
 
 size_t pkv_linear_attn_varlen_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t max_segs,
                                              int32_t dtype) {
-  return linear_workspace(N, H, Dk, Dv, dtype);
+  return linear_workspace(N, H, Dk, Dv, dtype, false);
 }
 
 pkv_status pkv_linear_attn_varlen(const void* q, const void* k, const void* v, const float* g,
@@ -176,7 +175,7 @@ pkv_status pkv_linear_attn_varlen(const void* q, const void* k, const void* v, c
 
 size_t pkv_linear_attn_varlen_backward_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv,
                                                       int32_t max_segs, int32_t dtype) {
-  return linear_workspace(N, H, Dk, Dv, dtype);
+  return linear_workspace(N, H, Dk, Dv, dtype, true);
 }
 
 pkv_status pkv_linear_attn_varlen_backward(const void* q, const void* k, const void* v, const float* g,

@@ -186,7 +186,7 @@ hipError_t launch_linear_serial_backward(const LinearArgs& x, const LinearGradAr
 
 // The chunked matrix-core kernels (bf16, Dk and Dv in {64, 128}).
 bool linear_chunk_supported(int32_t Dk, int32_t Dv, int32_t dtype);
-size_t linear_chunk_workspace_bytes(int64_t N, int32_t H, int32_t Dk, int32_t Dv);
+size_t linear_chunk_workspace_bytes(int64_t N, int32_t H, int32_t Dk, int32_t Dv, bool reverse);
 int64_t linear_chunk_grid(int64_t N, int32_t max_segs, int32_t H);
 hipError_t launch_linear_chunk(const LinearArgs& x, hipStream_t stream);
 hipError_t launch_linear_chunk_backward(const LinearArgs& x, const LinearGradArgs& y, hipStream_t stream);

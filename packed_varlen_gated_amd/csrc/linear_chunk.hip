@@ -8,13 +8,13 @@
 // (backward: the two powers change places and the mask is s >= t):
 //   out_t = sum_{s <= t} lam^(t - s) (a_t.b_s) c_s + lam^(t + 1) X^T a_t
 //   X <- lam^n X + sum_s lam^(n - 1 - s) b_s c_s^T
-// A work-group takes one run (up to `run` tokens of a segment) of one head; a
-// wave owns 32 columns of X, in fp32 registers, and of the output. The in-chunk
-// weights are formed by every wave: b rows from LDS against a in registers, and
-// their result is, register for register, an operand of the product with c.
-// X is rounded to bf16 once, as the operand of the readout; the update's decayed
-// c is split into three bf16 parts (24 bits), so X itself sees no bf16 rounding:
-// its products would cost less with one part, but final states are fp32 results.
+// A team of DB / 32 waves takes one run (up to `run` tokens of a segment) of one
+// head; a wave owns 32 columns of X, in fp32 registers, and of the output. The
+// in-chunk weights are formed in 16-token blocks, a block of columns per wave,
+// and shared through LDS as bf16. X is rounded to bf16 once, as the operand of
+// the readout; the update's decayed c is split into bf16 parts so that X itself
+// sees no bf16 rounding: three (24 bits) where final states, which are fp32
+// results, are asked for, two (2^-17) where X only feeds outputs.
 //
 // Rows and columns of X are dealt to the registers so that 8 consecutive ones
 // are 8 consecutive registers of a lane (the transposing LDS reads take their
@@ -24,12 +24,15 @@
 // Tiles go from memory into LDS without passing registers. b has two buffers; a
 // and c have one each, since a is done with after the products that c is not yet
 // needed for: the next a is loaded over a's second half of a chunk, c over the
-// first. 73 KiB at 128 channels: two work-groups per compute unit.
+// first. 74 KiB at 128 channels: two work-groups per compute unit. Backward, dk
+// and dv walk together where Dk = Dv: two teams in a work-group, q and do (b of
+// one, c of the other) loaded once.
 //
 // Segments longer than a run: a first launch walks every run but the segment's
 // last (in the walk's direction) without outputs and saves its own end state, a
 // second one turns these into the states before each run, and the walk starts
-// from those. A run's length depends on the call's sizes only.
+// from those; the reverse pass does both directions in one launch each. A run's
+// length depends on the call's sizes only.
 
 #include "mfma.h"
 #include "segments.h"
@@ -78,20 +81,23 @@ struct Transposed {
   }
 };
 
-struct WalkArgs {
+struct Role {
   const bf16 *a, *b, *c;
+  bf16* out;
+  const float* init;  // [max_segs, H, ..] or null
+  float* saved;       // [N / run, H, ..]: states between runs
+  float* fin;         // [max_segs, H, ..] or null
+  float in_scale, out_scale;
+  bool transposed;  // states are [DB][DA] in memory
+};
+struct WalkArgs {
+  Role r[2];
   const float* g;
   const int32_t* cu;
   int32_t max_segs;
   int64_t N;
   int32_t H, run;
   SlotGrid grid;
-  float in_scale, out_scale;
-  bool transposed;    // states are [DB][DA] in memory
-  const float* init;  // [max_segs, H, ..] or null
-  float* saved;       // [N / run, H, ..]: states between runs
-  bf16* out;
-  float* fin;  // [max_segs, H, ..] or null
   int32_t* flags;
 };
 
@@ -167,199 +173,297 @@ __device__ __forceinline__ bool find_saved(const int32_t* __restrict__ cu, int32
   return true;
 }
 
-template <int DA, int DB, bool kRev, bool kState>
-__global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x) {
-  constexpr int NW = DB / 32, NT = 64 * NW, KA = DA / 16, TA = DA / 32;
+// The update: X <- carry X + sum_s w_s b_s c_s^T from a chunk's tiles.
+template <int DA, int kParts>
+__device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const bf16x8 (&cf)[4], const float* w, int half,
+                                       const Transposed<DA>& tb, const char* bt) {
+  constexpr int TA = DA / 32;
+#pragma unroll
+  for (int i = 0; i < TA; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) X[i][j] *= carry;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    bf16x8 part[kParts];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const f32x4 ws = *reinterpret_cast<const f32x4*>(w + 16 * j + 8 * u + 4 * half);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y = to_f32(cf[j][4 * u + e]) * ws[e];
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+          const bf16 r = static_cast<bf16>(y);
+          part[s][4 * u + e] = r;
+          y -= to_f32(r);
+        }
+      }
+    }
+    bf16x8 bT[TA];
+#pragma unroll
+    for (int i = 0; i < TA; ++i) bT[i] = tb.read(bt, i, j);
+#pragma unroll
+    for (int s = 0; s < kParts; ++s)
+#pragma unroll
+      for (int i = 0; i < TA; ++i) X[i] = mfma32(bT[i], part[s], X[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// What a team knows of its run.
+template <bool kRev>
+struct Run {
+  int32_t start, end;
+  int n_chunks;
+  __device__ __forceinline__ int32_t chunk(int i) const { return start + (kRev ? n_chunks - 1 - i : i) * kC; }
+  __device__ __forceinline__ int32_t len(int32_t s0) const { return end - s0 < kC ? end - s0 : kC; }
+};
+
+// A tile of a chunk's rows [s0, s0 + n) of head h, into dst.
+template <int D, int NT>
+__device__ __forceinline__ void issue_rows(const bf16* p, int32_t s0, int32_t n, int32_t H, int32_t h, char* dst,
+                                           int wave) {
+  const int32_t stride = H * D * 2;
+  issue_tile<D, NT>(buffer(p + (int64_t(s0) * H + h) * D, int64_t(n - 1) * stride + D * 2), stride, dst, wave);
+}
+
+template <bool kRev>
+__device__ __forceinline__ float update_weight(float scale, float g2, int s, int32_t n) {
+  return s < n ? scale * ex2(g2 * (kRev ? s + 1 : n - 1 - s)) : 0.f;
+}
+
+// The state walk of one run: block blk of saved states x heads.
+template <int DA, int DB, bool kRev, int kParts>
+__device__ __forceinline__ void state_walk(const WalkArgs& x, const Role& R, int64_t blk, char* lds, float* upd) {
+  constexpr int NT = 2 * DB, TA = DA / 32, SB = Rows<DA>::BYTES, SC = Rows<DB>::BYTES;
+  const int32_t h = int32_t(blk % x.H), idx = int32_t(blk / x.H);
+  SegTile t;
+  if (!find_saved<kRev>(x.cu, x.max_segs, x.N, x.run, idx, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  Run<kRev> run;
+  run.start = t.start;
+  run.end = t.e - t.start > x.run ? t.start + x.run : t.e;
+  run.n_chunks = (run.end - run.start + kC - 1) / kC;
+  const float g2 = x.g[h] * kLog2e;
+  auto issue = [&](int i) {
+    const int32_t s0 = run.chunk(i), n = run.len(s0);
+    char* dst = lds + (i & 1) * (SB + SC);
+    issue_rows<DA, NT>(R.b, s0, n, x.H, h, dst, wave);
+    issue_rows<DB, NT>(R.c, s0, n, x.H, h, dst + SB, wave);
+    if (tid < kC) upd[(i & 1) * kC + tid] = update_weight<kRev>(R.in_scale, g2, tid, n);
+  };
+  // chunks whose tokens decay to a weight that fp32 has only 0 for (2^-150) by
+  // the run's end are left out
+  const float far = g2 < 0.f ? fminf(150.f / (-kC * g2), 1e6f) : 1e6f;
+  int it = run.n_chunks - 1 - int(far);
+  it = it < 0 ? 0 : it;
+  issue(it);
+  f32x16 X[TA];
+#pragma unroll
+  for (int i = 0; i < TA; ++i) X[i] = f32x16{};
+  const Transposed<DA> tb(lane);
+  const Transposed<DB> tc(lane);
+  for (; it < run.n_chunks; ++it) {
+    wait_all();
+    bar();
+    if (it + 1 < run.n_chunks) issue(it + 1);
+    const char* bt = lds + (it & 1) * (SB + SC);
+    bf16x8 cf[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cf[j] = tc.read(bt + SB, wave, j);
+    update<DA, kParts>(X, ex2(g2 * run.len(run.chunk(it))), cf, upd + (it & 1) * kC, lane >> 5, tb, bt);
+  }
+  StateAddr<DA, DB>(R.saved + (int64_t(idx) * x.H + h) * DA * DB, R.transposed, tid).store(X);
+}
+
+// Role 0 forward and, with kBoth, role 1 backward.
+template <int DA, int DB, int kParts, bool kBoth>
+__global__ __launch_bounds__(2 * DB, 2) void linear_state_kernel(const WalkArgs x) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * (Rows<DA>::BYTES + Rows<DB>::BYTES)];
+  __shared__ __attribute__((aligned(16))) float upd[2 * kC];
+  const int64_t n = x.N / x.run * x.H, blk = blockIdx.x;
+  if (!kBoth || blk < n)
+    state_walk<DA, DB, false, kParts>(x, x.r[0], blk, lds, upd);
+  else
+    state_walk<DA, DB, true, kParts>(x, x.r[1], blk - n, lds, upd);
+}
+
+template <int DA, int DB, bool kRev, int kParts, bool kPair>
+__global__ __launch_bounds__((kPair ? 4 : 2) * DB, 2) void linear_walk_kernel(const WalkArgs x) {
+  constexpr int NW = DB / 32, NT = (kPair ? 2 : 1) * 64 * NW, KA = DA / 16, TA = DA / 32;
   constexpr int SB = Rows<DA>::BYTES, SC = Rows<DB>::BYTES;
-  // b of the even chunks, of the odd ones, then c and a (the state walk: c of the
-  // even chunks, of the odd ones); the update's weights of each parity; the
-  // in-chunk weights of the lane
+  static_assert(!kPair || DA == DB, "a team's b is the other one's c");
+  // one team: b of the even chunks, of the odd ones, c, a; two: the first team's
+  // b of the even and odd chunks, the second's, and the a of each
+  constexpr int kA = kPair ? 4 * SB : 2 * SB + SC;
   constexpr int kPieces = kC * Rows<DA>::CH / NT;  // loads of a b tile per lane
-  __shared__ __attribute__((aligned(1024))) char lds[2 * SB + (kState ? 2 * SC : SC + SB)];
-  __shared__ float upd[2][kC];
-  __shared__ f32x4 rel[kState ? 1 : 2][kState ? 1 : 4][kState ? 1 : 64];
+  __shared__ __attribute__((aligned(1024))) char lds[kA + (kPair ? 2 : 1) * SB];
+  constexpr int WP = kC + 8;  // row of the in-chunk weights [t][s]
+  __shared__ __attribute__((aligned(16))) bf16 wts[kPair ? 2 : 1][kC][WP];
+  __shared__ __attribute__((aligned(16))) float upd[2][kC];
 
   const int64_t blk = blockIdx.x;
-  if (!kState && blk >= slot_blocks(x.grid, x.H)) {
-    const int tid = threadIdx.x;
+  if (blk >= slot_blocks(x.grid, x.H)) {
     const int64_t j = blk - slot_blocks(x.grid, x.H);
-    zero_tail(x.out, covered_tokens(x.cu, x.max_segs, x.N), x.N, int64_t(x.H) * DB * 2, j, kTail);
+    const int64_t cov = covered_tokens(x.cu, x.max_segs, x.N);
+#pragma unroll
+    for (int i = 0; i < (kPair ? 2 : 1); ++i) zero_tail(x.r[i].out, cov, x.N, int64_t(x.H) * DB * 2, j, kTail);
     if (j == 0) check_cu(x.cu, x.max_segs, x.N, x.flags);
-    if (x.fin != nullptr && x.cu != nullptr) {
+    if (x.r[0].fin != nullptr && x.cu != nullptr) {
       // empty slots keep their initial state (or 0)
       const int64_t n = int64_t(x.H) * DA * DB / 4;
       for (int64_t s = j; s < x.max_segs; s += kTail) {
         if (x.cu[s] != x.cu[s + 1]) continue;
-        f32x4* to = reinterpret_cast<f32x4*>(x.fin) + s * n;
-        const f32x4* from = x.init ? reinterpret_cast<const f32x4*>(x.init) + s * n : nullptr;
-        for (int64_t i = tid; i < n; i += NT) to[i] = from ? from[i] : f32x4{0.f, 0.f, 0.f, 0.f};
+        f32x4* to = reinterpret_cast<f32x4*>(x.r[0].fin) + s * n;
+        const f32x4* from = x.r[0].init ? reinterpret_cast<const f32x4*>(x.r[0].init) + s * n : nullptr;
+        for (int64_t i = threadIdx.x; i < n; i += NT) to[i] = from ? from[i] : f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
     return;
   }
   int32_t slot, h0, h1;
   SegTile t;
-  if constexpr (kState) {
-    // the run that ends in saved state blk / H
-    h0 = int32_t(blk % x.H);
-    h1 = h0 + 1;
-    if (!find_saved<kRev>(x.cu, x.max_segs, x.N, x.run, int32_t(blk / x.H), t)) return;
-  } else {
-    slot_of(x.grid, blk, x.H, slot, h0, h1);
-    if (!find_tile(x.cu, x.max_segs, x.N, x.run, slot, t)) return;
-  }
-  const int32_t end = t.e - t.start > x.run ? t.start + x.run : t.e;
-  const bool first = kRev ? end == t.e : t.start == t.a;  // in the walk's direction
-  const bool last = kRev ? t.start == t.a : end == t.e;
-  // the saved state that this run starts from is at - 1 (backward: at), and the
-  // one it ends in is at (backward: at - 1)
-  const int64_t at = int64_t(t.a / x.run) + (t.start - t.a) / x.run;
-  constexpr int64_t kState_ = int64_t(DA) * DB;
+  slot_of(x.grid, blk, x.H, slot, h0, h1);
+  if (!find_tile(x.cu, x.max_segs, x.N, x.run, slot, t)) return;
+  Run<kRev> run;
+  run.start = t.start;
+  run.end = t.e - t.start > x.run ? t.start + x.run : t.e;
+  run.n_chunks = (run.end - run.start + kC - 1) / kC;
+  const bool first = kRev ? run.end == t.e : t.start == t.a;  // in the walk's direction
+  const bool last = kRev ? t.start == t.a : run.end == t.e;
+  // the saved state that this run starts from
+  const int64_t at = int64_t(t.a / x.run) + (t.start - t.a) / x.run - (kRev ? 0 : 1);
 
-  for (int32_t h = h0; h < (kState ? h0 + 1 : h1); ++h) {
-  // (nothing that goes by the lane is kept from one head to the next)
-  const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (!kState && h != h0) __syncthreads();  // the last head is done with LDS
-  const float g2 = x.g[h] * kLog2e;
-  const int half = lane >> 5, col = lane & 31;
-  const int32_t as = x.H * DA * 2, cs = x.H * DB * 2;
-  const int n_chunks = (end - t.start + kC - 1) / kC;
-  auto chunk_start = [&](int i) { return t.start + (kRev ? n_chunks - 1 - i : i) * kC; };
-  auto chunk_len = [&](int32_t s0) { return end - s0 < kC ? end - s0 : kC; };
-  auto issue_b = [&](int i) {
-    const int32_t s0 = chunk_start(i), n = chunk_len(s0);
-    issue_tile<DA, NT>(buffer(x.b + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2), as,
-                       lds + (i & 1) * SB, wave);
-    if (tid < kC) upd[i & 1][tid] = tid < n ? x.in_scale * ex2(g2 * (kRev ? tid + 1 : n - 1 - tid)) : 0.f;
-  };
-  auto issue_c = [&](int i) {
-    const int32_t s0 = chunk_start(i), n = chunk_len(s0);
-    issue_tile<DB, NT>(buffer(x.c + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2), cs,
-                       lds + 2 * SB + (kState ? (i & 1) * SC : 0), wave);
-  };
-  auto issue_a = [&](int i) {
-    const int32_t s0 = chunk_start(i), n = chunk_len(s0);
-    issue_tile<DA, NT>(buffer(x.a + (int64_t(s0) * x.H + h) * DA, int64_t(n - 1) * as + DA * 2), as,
-                       lds + 2 * SB + SC, wave);
-  };
-  // The state walk leaves out the chunks whose tokens decay to a weight that
-  // fp32 has only 0 for (2^-150) by the run's end.
-  int it0 = 0;
-  if constexpr (kState) {
-    const float far = g2 < 0.f ? fminf(150.f / (-kC * g2), 1e6f) : 1e6f;
-    it0 = n_chunks - 1 - int(far);
-    it0 = it0 < 0 ? 0 : it0;
-  }
-  issue_b(it0);
-  if constexpr (kState) issue_c(it0);
-  else issue_a(0);
+  for (int32_t h = h0; h < h1; ++h) {
+    // (nothing that goes by the lane is kept from one head to the next)
+    const int tid = fresh(threadIdx.x), lane = tid & 63, wave_ = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int team = kPair ? wave_ / NW : 0, wave = kPair ? wave_ % NW : wave_;
+    const Role& R = x.r[team];
+    if (h != h0) __syncthreads();  // the last head is done with LDS
+    const float g2 = x.g[h] * kLog2e;
+    const int half = lane >> 5, col = lane & 31;
+    const int32_t cs = x.H * DB * 2;
+    auto issue_b = [&](int i) {
+      const int32_t s0 = run.chunk(i), n = run.len(s0);
+      issue_rows<DA, NT>(x.r[0].b, s0, n, x.H, h, lds + (i & 1) * SB, wave_);
+      if constexpr (kPair) issue_rows<DA, NT>(x.r[1].b, s0, n, x.H, h, lds + (2 + (i & 1)) * SB, wave_);
+      if (tid < kC) upd[i & 1][tid] = update_weight<kRev>(x.r[0].in_scale, g2, tid, n);
+    };
+    auto issue_a = [&](int i) {
+      const int32_t s0 = run.chunk(i), n = run.len(s0);
+      issue_rows<DA, NT>(x.r[0].a, s0, n, x.H, h, lds + kA, wave_);
+      if constexpr (kPair) issue_rows<DA, NT>(x.r[1].a, s0, n, x.H, h, lds + kA + SB, wave_);
+    };
+    issue_b(0);
+    issue_a(0);
 
-  f32x16 X[TA];
-  const float* from = kState ? nullptr
-                             : first ? (x.init ? x.init + (int64_t(t.seg) * x.H + h) * kState_ : nullptr)
-                                     : x.saved + ((kRev ? at : at - 1) * x.H + h) * kState_;
-  if (from != nullptr) {
-    StateAddr<DA, DB>(from, x.transposed, tid).load(X);
-  } else {
+    f32x16 X[TA];
+    const float* from = first ? (R.init ? R.init + (int64_t(t.seg) * x.H + h) * DA * DB : nullptr)
+                              : R.saved + (at * x.H + h) * DA * DB;
+    if (from != nullptr) {
+      StateAddr<DA, DB>(from, R.transposed, tid - team * 64 * NW).load(X);
+    } else {
 #pragma unroll
-    for (int i = 0; i < TA; ++i) X[i] = f32x16{};
-  }
-
-  if constexpr (!kState) {
-    // rel[0]: weights inside a 32 x 32 block on the diagonal, rel[1]: of the
-    // block below it (s 32 .. 1 tokens further from t)
-    if (wave == 0) {
-      const float f = x.in_scale * x.out_scale;
-#pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        f32x4 w0, w1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int s = 8 * i4 + 4 * half + e, d = kRev ? s - col : col - s;
-          w0[e] = d >= 0 ? f * ex2(g2 * d) : 0.f;
-          w1[e] = f * ex2(g2 * (d + 32));
-        }
-        rel[0][i4][lane] = w0;
-        rel[1][i4][lane] = w1;
-      }
+      for (int i = 0; i < TA; ++i) X[i] = f32x16{};
     }
-  }
-  const Transposed<DA> tb(lane);
-  const Transposed<DB> tc(lane);
-  const int fx = Rows<DA>::swz(col);
 
-  for (int it = it0; it < n_chunks; ++it) {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // loads into LDS and LDS stores done
-    bar();
-    if constexpr (!kState) {
-      issue_c(it);
-      // c's loads stay before the next b's: the wait for c below counts those
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
+    // In-chunk weights of the lane: column t = lane % 16 of a 16-token block,
+    // rows s = 4 (lane / 16) + e. near: of the block on the diagonal, next: of
+    // the block 16 tokens off it (every further one a power of `apart` more).
+    // The columns a wave forms: block `wave` of 4, or blocks `wave`, 3 - wave.
+    const int c16 = lane & 15, r16 = lane >> 4;
+    f32x4 near, next;
+    const float apart = ex2(g2 * 16.f), both = R.in_scale * R.out_scale;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = kRev ? 4 * r16 + e - c16 : c16 - 4 * r16 - e;
+      near[e] = d >= 0 ? both * ex2(g2 * d) : 0.f;
+      next[e] = both * ex2(g2 * (d + 16));
     }
-    if (it + 1 < n_chunks) {
-      issue_b(it + 1);
-      if constexpr (kState) issue_c(it + 1);
+    bf16* wt = &wts[team][0][0];
+    // blocks that the 32-row steps of the second product read beside the
+    // diagonal ones and that never have any
+    if (wave < 2) {
+      const int cb = 2 * wave + (kRev ? 1 : 0), sb = 2 * wave + (kRev ? 0 : 1);
+      *reinterpret_cast<uint64_t*>(wt + (16 * cb + c16) * WP + 16 * sb + 4 * r16) = 0;
     }
-    __builtin_amdgcn_sched_barrier(0);
-    const char* bt = lds + (it & 1) * SB;
-    const char* ct = lds + 2 * SB + (kState ? (it & 1) * SC : 0);
-    const char* at_ = lds + 2 * SB + SC;
-    const int32_t s0 = chunk_start(it), n = chunk_len(s0);
+    const Transposed<DA> tb(lane);
+    const Transposed<DB> tc(lane);
 
-    bf16x8 cf[4];
-    if constexpr (!kState) {
-      // In-chunk weights of a 32 x 32 block (rows s of block sb, columns t of
-      // block u) as operands; three of the four blocks have any.
-      bf16x8 wf[2][4];
-      auto weigh = [&](const f32x16& w, int u, int sb) {
-#pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const f32x4 f = rel[sb == u ? 0 : 1][i4][lane];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            wf[u][2 * sb + i4 / 2][4 * (i4 % 2) + e] = static_cast<bf16>(w[4 * i4 + e] * f[e]);
-        }
-      };
-      auto row = [&](const char* t, int sb, int i) {
-        return *reinterpret_cast<const bf16x8*>(t + (32 * sb + col) * Rows<DA>::ROW + (((2 * i + half) ^ fx) * 16));
-      };
-      // Five independent products take turns: the three blocks and the readout
-      // of X for both column blocks.
-      constexpr int sFar = kRev ? 1 : 0, sOne = kRev ? 0 : 1;  // row blocks of both, of one
-      f32x16 o[2] = {};
-      {
-        f32x16 w0 = {}, w1 = {}, w2 = {};
-#pragma unroll
-        for (int i = 0; i < KA; ++i) {
-          const bf16x8 br = row(bt, sFar, i), a0 = row(at_, 0, i), a1 = row(at_, 1, i);
-          bf16x8 xs;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) xs[j] = static_cast<bf16>(X[i / 2][8 * (i % 2) + j]);
-          w0 = mfma32(br, a0, w0);
-          w1 = mfma32(br, a1, w1);
-          w2 = mfma32(row(bt, sOne, i), kRev ? a0 : a1, w2);
-          o[0] = mfma32(xs, a0, o[0]);
-          o[1] = mfma32(xs, a1, o[1]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        weigh(w0, 0, sFar);
-        weigh(w1, 1, sFar);
-        weigh(w2, sOne, sOne);
-      }
-      // c has come (the next b may still be on its way), a is free
-      if (it + 1 < n_chunks)
-        __builtin_amdgcn_s_waitcnt(0x0070 | kPieces);
-      else
-        __builtin_amdgcn_s_waitcnt(0x0070);
+    for (int it = 0; it < run.n_chunks; ++it) {
+      wait_all();
       bar();
-      if (it + 1 < n_chunks) issue_a(it + 1);
+      if constexpr (!kPair) {
+        const int32_t s0 = run.chunk(it);
+        issue_rows<DB, NT>(x.r[0].c, s0, run.len(s0), x.H, h, lds + 2 * SB, wave_);
+        // c's loads stay before the next b's: the wait for c below counts those
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (it + 1 < run.n_chunks) issue_b(it + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const char* bt = lds + ((it & 1) + 2 * team) * SB;
+      const char* ct = kPair ? lds + ((it & 1) + 2 * (1 - team)) * SB : lds + 2 * SB;
+      const char* at_ = lds + kA + team * SB;
+      const int32_t s0 = run.chunk(it), n = run.len(s0);
+
+      // in-chunk weights, a block of 16 columns at a time
+#pragma unroll
+      for (int v = 0; v < 4 / NW; ++v) {
+        const int cb = v == 0 ? wave : 3 - wave;
+        f32x4 w[4] = {};
+#pragma unroll
+        for (int i = 0; i < DA / 32; ++i) {
+          auto row = [&](const char* tile, int blk16) {
+            return *reinterpret_cast<const bf16x8*>(tile + (16 * blk16 + c16) * Rows<DA>::ROW +
+                                                    (((4 * i + r16) ^ Rows<DA>::swz(c16)) * 16));
+          };
+          const bf16x8 a = row(at_, cb);
+#pragma unroll
+          for (int sb = 0; sb < 4; ++sb)
+            if (kRev ? sb >= cb : sb <= cb) w[sb] = mfma16(row(bt, sb), a, w[sb]);
+        }
+#pragma unroll
+        for (int sb = 0; sb < 4; ++sb) {
+          const int off = kRev ? sb - cb : cb - sb;
+          if (off < 0) continue;
+          const float more = off < 2 ? 1.f : (off == 2 ? apart : apart * apart);
+          bf16x4 y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = static_cast<bf16>(w[sb][e] * (off == 0 ? near[e] : next[e] * more));
+          *reinterpret_cast<bf16x4*>(wt + (16 * cb + c16) * WP + 16 * sb + 4 * r16) = y;
+        }
+      }
+      // readout of X
+      f32x16 o[2] = {};
+#pragma unroll
+      for (int i = 0; i < KA; ++i) {
+        bf16x8 xs;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xs[j] = static_cast<bf16>(X[i / 2][8 * (i % 2) + j]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          o[u] = mfma32(xs, *reinterpret_cast<const bf16x8*>(at_ + (32 * u + col) * Rows<DA>::ROW +
+                                                             (((2 * i + half) ^ Rows<DA>::swz(col)) * 16)),
+                        o[u]);
+      }
+      // c has come (the next b may still be on its way), the weights are in LDS,
+      // a is free
+      if (!kPair && it + 1 < run.n_chunks)
+        __builtin_amdgcn_s_waitcnt(0x0070 | kPieces);
+      else if (!kPair)
+        wait_all();
+      else
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS stores alone
+      bar();
+      if (it + 1 < run.n_chunks) issue_a(it + 1);
+      bf16x8 cf[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) cf[j] = tc.read(ct, wave, j);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int d = kRev ? n - 1 - 32 * u - col : 32 * u + col + 1;
-        const float ow = x.out_scale * ex2(g2 * (d < 0 ? 0 : d));
+        const float ow = R.out_scale * ex2(g2 * (d < 0 ? 0 : d));
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[u][i] *= ow;
       }
@@ -368,10 +472,12 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           if (kRev ? j / 2 < u : j / 2 > u) continue;
-          o[u] = mfma32(cf[j], wf[u][j], o[u]);
+          const bf16* p = wt + (32 * u + col) * WP + 16 * j + 4 * half;
+          const s16x4 lo = *reinterpret_cast<const s16x4*>(p), hi = *reinterpret_cast<const s16x4*>(p + 8);
+          o[u] = mfma32(cf[j], join(lo, hi), o[u]);
         }
       // (rows past the chunk's end are out of the buffer's range)
-      const auto ro = buffer(x.out + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2);
+      const auto ro = buffer(R.out + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -382,47 +488,11 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_walk_kernel(const WalkArgs x
           store16(ro, uint32_t(32 * u + col) * cs + 64 * wave + 16 * half + 32 * v, __builtin_bit_cast(i32x4, y));
         }
       __builtin_amdgcn_sched_barrier(0);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) cf[j] = tc.read(ct, wave, j);
+      update<DA, kParts>(X, ex2(g2 * n), cf, upd[it & 1], half, tb, bt);
     }
 
-    const float carry = ex2(g2 * n);
-#pragma unroll
-    for (int i = 0; i < TA; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) X[i][j] *= carry;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bf16x8 part[3];  // exact to 24 bits
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f32x4 w = *reinterpret_cast<const f32x4*>(&upd[it & 1][16 * j + 8 * u + 4 * half]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y = to_f32(cf[j][4 * u + e]) * w[e];
-#pragma unroll
-          for (int s = 0; s < 3; ++s) {
-            const bf16 r = static_cast<bf16>(y);
-            part[s][4 * u + e] = r;
-            y -= to_f32(r);
-          }
-        }
-      }
-      bf16x8 bT[TA];
-#pragma unroll
-      for (int i = 0; i < TA; ++i) bT[i] = tb.read(bt, i, j);
-#pragma unroll
-      for (int s = 0; s < 3; ++s)
-#pragma unroll
-        for (int i = 0; i < TA; ++i) X[i] = mfma32(bT[i], part[s], X[i]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
-  float* to = kState ? x.saved + ((kRev ? at - 1 : at) * x.H + h) * kState_
-                     : (last && x.fin ? x.fin + (int64_t(t.seg) * x.H + h) * kState_ : nullptr);
-  if (to != nullptr) StateAddr<DA, DB>(to, x.transposed, tid).store(X);
+    if (last && R.fin != nullptr)
+      StateAddr<DA, DB>(R.fin + (int64_t(t.seg) * x.H + h) * DA * DB, R.transposed, tid - team * 64 * NW).store(X);
   }
 }
 
@@ -434,12 +504,12 @@ constexpr int kScan = 256;
 constexpr int kAhead = 8;  // states whose loads are in flight at once
 
 template <bool kRev>
-__global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, int32_t size, int32_t count) {
-  __shared__ int32_t seg_of[kScan];  // segment of the index if it starts the walk there, -1 if it goes on, -2 if unused
-  __shared__ float decay[kScan];
+__device__ __forceinline__ void scan(const WalkArgs& x, const Role& R, int32_t blk, int32_t size, int32_t count,
+                                     int32_t* seg_of, float* decay) {
+  // seg_of: segment of the index if it starts the walk there, -1 if it goes on, -2 if unused
   const int tid = threadIdx.x;
-  const int32_t parts = size / (4 * kScan), h = blockIdx.x / parts;
-  const int64_t elem = (int64_t(blockIdx.x % parts) * kScan + tid) * 4;
+  const int32_t parts = size / (4 * kScan), h = blk / parts;
+  const int64_t elem = (int64_t(blk % parts) * kScan + tid) * 4;
   const float g2 = x.g[h] * kLog2e;
   f32x4 X = {0.f, 0.f, 0.f, 0.f};
   for (int32_t base = 0; base < count; base += kScan) {
@@ -477,7 +547,7 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
         const int32_t i = i0 + u;
         if (i < n && seg_of[i] != -2) {
           const int64_t idx = kRev ? count - 1 - (base + i) : base + i;
-          own[u] = *reinterpret_cast<const f32x4*>(x.saved + (idx * x.H + h) * size + elem);
+          own[u] = *reinterpret_cast<const f32x4*>(R.saved + (idx * x.H + h) * size + elem);
         }
       }
 #pragma unroll
@@ -485,15 +555,26 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
         const int32_t i = i0 + u;
         if (i >= n || seg_of[i] == -2) continue;
         if (seg_of[i] >= 0)
-          X = x.init ? *reinterpret_cast<const f32x4*>(x.init + (int64_t(seg_of[i]) * x.H + h) * size + elem)
+          X = R.init ? *reinterpret_cast<const f32x4*>(R.init + (int64_t(seg_of[i]) * x.H + h) * size + elem)
                      : f32x4{0.f, 0.f, 0.f, 0.f};
         const int64_t idx = kRev ? count - 1 - (base + i) : base + i;
 #pragma unroll
         for (int e = 0; e < 4; ++e) X[e] = own[u][e] + decay[i] * X[e];
-        *reinterpret_cast<f32x4*>(x.saved + (idx * x.H + h) * size + elem) = X;
+        *reinterpret_cast<f32x4*>(R.saved + (idx * x.H + h) * size + elem) = X;
       }
     }
   }
+}
+
+// Role 0 forward and, behind its work-groups, role 1 backward.
+__global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, int32_t size, int32_t count) {
+  __shared__ int32_t seg_of[kScan];
+  __shared__ float decay[kScan];
+  const int32_t n = x.H * (size / (4 * kScan)), blk = blockIdx.x;
+  if (blk < n)
+    scan<false>(x, x.r[0], blk, size, count, seg_of, decay);
+  else
+    scan<true>(x, x.r[1], blk - n, size, count, seg_of, decay);
 }
 
 // Tokens of a run: the smallest power of two from sqrt(1.5 N H) on, in
@@ -509,27 +590,26 @@ int32_t run_tokens(int64_t N, int32_t H) {
   return r;
 }
 
-template <int DA, int DB, bool kRev, bool kState>
-void walk(WalkArgs x, const void* a, const void* b, const void* c, bool transposed, float in_scale, float out_scale,
-          const float* init, void* out, float* fin, hipStream_t stream) {
-  x.a = static_cast<const bf16*>(a);
-  x.b = static_cast<const bf16*>(b);
-  x.c = static_cast<const bf16*>(c);
-  x.transposed = transposed;
-  x.in_scale = in_scale;
-  x.out_scale = out_scale;
-  x.init = init;
-  x.out = static_cast<bf16*>(out);
-  x.fin = fin;
-  const int64_t grid = kState ? x.N / x.run * x.H : slot_blocks(x.grid, x.H) + kTail;
-  linear_walk_kernel<DA, DB, kRev, kState><<<dim3(uint32_t(grid)), dim3(2 * DB), 0, stream>>>(x);
+Role role(const void* a, const void* b, const void* c, void* out, const float* init, float* saved, float* fin,
+          float in_scale, float out_scale, bool transposed) {
+  return {static_cast<const bf16*>(a), static_cast<const bf16*>(b), static_cast<const bf16*>(c),
+          static_cast<bf16*>(out), init, saved, fin, in_scale, out_scale, transposed};
 }
 
-template <bool kRev>
-void scan(WalkArgs x, int32_t size, const float* init, hipStream_t stream) {
-  x.init = init;
-  linear_scan_kernel<kRev><<<dim3(uint32_t(x.H * (size / (4 * kScan)))), dim3(kScan), 0, stream>>>(
-      x, size, int32_t(x.N / x.run));
+// Own end states of the runs, then the states before them, of one or both roles.
+template <int DA, int DB, int kParts, bool kBoth>
+void states(const WalkArgs& x, hipStream_t stream) {
+  const int32_t count = int32_t(x.N / x.run), size = DA * DB;
+  linear_state_kernel<DA, DB, kParts, kBoth><<<dim3(uint32_t(int64_t(count) * x.H * (kBoth ? 2 : 1))), dim3(2 * DB), 0,
+                                               stream>>>(x);
+  linear_scan_kernel<<<dim3(uint32_t(x.H * (size / (4 * kScan)) * (kBoth ? 2 : 1))), dim3(kScan), 0, stream>>>(x, size,
+                                                                                                               count);
+}
+
+template <int DA, int DB, bool kRev, int kParts, bool kPair>
+void walk(const WalkArgs& x, hipStream_t stream) {
+  linear_walk_kernel<DA, DB, kRev, kParts, kPair>
+      <<<dim3(uint32_t(slot_blocks(x.grid, x.H) + kTail)), dim3((kPair ? 4 : 2) * DB), 0, stream>>>(x);
 }
 
 WalkArgs common(const LinearArgs& y) {
@@ -541,37 +621,53 @@ WalkArgs common(const LinearArgs& y) {
   x.H = y.H;
   x.run = run_tokens(y.N, y.H);
   x.grid = slot_grid(y.N, y.max_segs, x.run);
-  x.saved = static_cast<float*>(y.workspace);
   x.flags = y.flags;
   return x;
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int kParts>
 hipError_t fwd(const LinearArgs& y, hipStream_t s) {
-  const WalkArgs x = common(y);
+  WalkArgs x = common(y);
+  x.r[0] = role(y.q, y.k, y.v, y.o, y.initial_state, static_cast<float*>(y.workspace), y.final_state, 1.f, y.scale, false);
+  if (y.N > x.run) states<DK, DV, kParts, false>(x, s);
+  walk<DK, DV, false, kParts, false>(x, s);
+  return hipGetLastError();
+}
+
+template <int DK, int DV, int kParts>
+hipError_t bwd(const LinearArgs& y, const LinearGradArgs& z, hipStream_t s) {
+  WalkArgs x = common(y);
+  float* saved = static_cast<float*>(y.workspace);
+  float* adjoint = saved + y.N / x.run * y.H * DK * DV;
   if (y.N > x.run) {
-    walk<DK, DV, false, true>(x, nullptr, y.k, y.v, false, 1.f, 1.f, nullptr, nullptr, nullptr, s);
-    scan<false>(x, DK * DV, y.initial_state, s);
+    x.r[0] = role(nullptr, y.k, y.v, nullptr, y.initial_state, saved, nullptr, 1.f, 1.f, false);
+    x.r[1] = role(nullptr, y.q, z.dout, nullptr, z.dfinal_state, adjoint, nullptr, y.scale, 1.f, false);
+    states<DK, DV, kParts, true>(x, s);
   }
-  walk<DK, DV, false, false>(x, y.q, y.k, y.v, false, 1.f, y.scale, y.initial_state, y.o, y.final_state, s);
+  const Role dq = role(z.dout, y.v, y.k, z.dq, y.initial_state, saved, nullptr, 1.f, y.scale, true);
+  const Role dv = role(y.k, y.q, z.dout, z.dv, z.dfinal_state, adjoint, z.d_initial_state, y.scale, 1.f, false);
+  const Role dk = role(y.v, z.dout, y.q, z.dk, z.dfinal_state, adjoint, nullptr, y.scale, 1.f, true);
+  x.r[0] = dq;
+  walk<DV, DK, false, 2, false>(x, s);
+  x.r[0] = dv;
+  if constexpr (DK == DV) {
+    x.r[1] = dk;
+    walk<DK, DV, true, kParts, true>(x, s);
+  } else {
+    walk<DK, DV, true, kParts, false>(x, s);
+    x.r[0] = dk;
+    walk<DV, DK, true, 2, false>(x, s);
+  }
   return hipGetLastError();
 }
 
 template <int DK, int DV>
+hipError_t fwd(const LinearArgs& y, hipStream_t s) {
+  return y.final_state ? fwd<DK, DV, 3>(y, s) : fwd<DK, DV, 2>(y, s);
+}
+template <int DK, int DV>
 hipError_t bwd(const LinearArgs& y, const LinearGradArgs& z, hipStream_t s) {
-  const WalkArgs x = common(y);
-  if (y.N > x.run) {
-    walk<DK, DV, false, true>(x, nullptr, y.k, y.v, false, 1.f, 1.f, nullptr, nullptr, nullptr, s);
-    scan<false>(x, DK * DV, y.initial_state, s);
-  }
-  walk<DV, DK, false, false>(x, z.dout, y.v, y.k, true, 1.f, y.scale, y.initial_state, z.dq, nullptr, s);
-  if (y.N > x.run) {
-    walk<DK, DV, true, true>(x, nullptr, y.q, z.dout, false, y.scale, 1.f, nullptr, nullptr, nullptr, s);
-    scan<true>(x, DK * DV, z.dfinal_state, s);
-  }
-  walk<DV, DK, true, false>(x, y.v, z.dout, y.q, true, y.scale, 1.f, z.dfinal_state, z.dk, nullptr, s);
-  walk<DK, DV, true, false>(x, y.k, y.q, z.dout, false, y.scale, 1.f, z.dfinal_state, z.dv, z.d_initial_state, s);
-  return hipGetLastError();
+  return z.d_initial_state ? bwd<DK, DV, 3>(y, z, s) : bwd<DK, DV, 2>(y, z, s);
 }
 
 }  // namespace
@@ -580,9 +676,9 @@ bool linear_chunk_supported(int32_t Dk, int32_t Dv, int32_t dtype) {
   return dtype == 0 && (Dk == 64 || Dk == 128) && (Dv == 64 || Dv == 128);
 }
 
-size_t linear_chunk_workspace_bytes(int64_t N, int32_t H, int32_t Dk, int32_t Dv) {
+size_t linear_chunk_workspace_bytes(int64_t N, int32_t H, int32_t Dk, int32_t Dv, bool reverse) {
   const int32_t run = run_tokens(N, H);
-  return N > run ? size_t(N / run) * H * Dk * Dv * 4 : 0;
+  return N > run ? size_t(N / run) * H * Dk * Dv * 4 * (reverse ? 2 : 1) : 0;
 }
 
 int64_t linear_chunk_grid(int64_t N, int32_t max_segs, int32_t H) {

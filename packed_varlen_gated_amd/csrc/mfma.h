@@ -93,6 +93,8 @@ __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x)
 
 // All of this wave's vector-memory operations (loads into LDS among them) done.
 __device__ __forceinline__ void wait_vm() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// ... and its LDS operations.
+__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x0070); }
 // A work-group barrier that waits for nothing but the other waves.
 __device__ __forceinline__ void bar() {
   asm volatile("" ::: "memory");
