@@ -1,4 +1,4 @@
-// Packed linear attention with one decay per head in chunks of 64 tokens on the
+// Packed linear attention with one decay per head in chunks of 32 tokens on the
 // matrix cores (bf16, head dimensions 64 and 128).
 //
 //   S_t = lam S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t,  lam = e^{g_h}
@@ -21,12 +21,12 @@
 // 8-byte pieces in the order 0, 2, 1, 3): a is read in 16-byte pieces, outputs
 // are stored in 16-byte pieces.
 //
-// Tiles go from memory into LDS without passing registers. b has two buffers; a
-// and c have one each, since a is done with after the products that c is not yet
-// needed for: the next a is loaded over a's second half of a chunk, c over the
-// first. 74 KiB at 128 channels: two work-groups per compute unit. Backward, dk
-// and dv walk together where Dk = Dv: two teams in a work-group, q and do (b of
-// one, c of the other) loaded once.
+// Tiles go from memory into LDS without passing registers, the next chunk's while
+// this one is used. A chunk is a chain of dependent steps (LDS reads, products,
+// a barrier, products, the update), so what counts is how many work-groups take
+// turns: two stages of 24 KiB at 128 channels and at most 168 registers, three
+// work-groups per compute unit. Backward, dk and dv walk together where Dk = Dv:
+// two teams in a work-group, q and do (b of one, c of the other) loaded once.
 //
 // Segments longer than a run: a first launch walks every run but the segment's
 // last (in the walk's direction) without outputs and saves its own end state, a
@@ -40,23 +40,24 @@
 namespace pkv {
 namespace {
 
-constexpr int kC = 64;      // tokens per chunk
+constexpr int kC = 32;       // tokens per chunk of a walk
+constexpr int kCState = 64;  // ... of a state walk
 constexpr int kTail = 256;  // work-groups for the rows no segment has and empty slots
 
 template <int D>
-struct Rows {  // an LDS tile of 64 rows of D channels
-  static constexpr int CH = D / 8, ROW = D * 2, BYTES = kC * ROW;
+struct Rows {  // an LDS tile of a chunk's rows of D channels
+  static constexpr int CH = D / 8, ROW = D * 2;
   static __device__ __forceinline__ int swz(int row) {
     return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
   }
 };
 
-template <int D, int NT>
+template <int D, int C, int NT>
 __device__ __forceinline__ void issue_tile(__amdgpu_buffer_rsrc_t r, int32_t stride, char* dst, int wave) {
   constexpr int STEP = NT / Rows<D>::CH;
   const int row = fresh(threadIdx.x) / Rows<D>::CH, pos = threadIdx.x % Rows<D>::CH;
 #pragma unroll
-  for (int i = 0; i < kC / STEP; ++i) {
+  for (int i = 0; i < C / STEP; ++i) {
     const int s = STEP % 16 == 0 ? Rows<D>::swz(row) : Rows<D>::swz(row + i * STEP);
     load_lds16(r, uint32_t(row + i * STEP) * stride + (pos ^ s) * 16, dst + wave * 1024 + i * NT * 16);
   }
@@ -174,8 +175,8 @@ __device__ __forceinline__ bool find_saved(const int32_t* __restrict__ cu, int32
 }
 
 // The update: X <- carry X + sum_s w_s b_s c_s^T from a chunk's tiles.
-template <int DA, int kParts>
-__device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const bf16x8 (&cf)[4], const float* w, int half,
+template <int DA, int C, int kParts>
+__device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const bf16x8 (&cf)[C / 16], const float* w, int half,
                                        const Transposed<DA>& tb, const char* bt) {
   constexpr int TA = DA / 32;
 #pragma unroll
@@ -183,7 +184,7 @@ __device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const 
 #pragma unroll
     for (int j = 0; j < 16; ++j) X[i][j] *= carry;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < C / 16; ++j) {
     bf16x8 part[kParts];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -211,20 +212,20 @@ __device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const 
 }
 
 // What a team knows of its run.
-template <bool kRev>
+template <int C, bool kRev>
 struct Run {
   int32_t start, end;
   int n_chunks;
-  __device__ __forceinline__ int32_t chunk(int i) const { return start + (kRev ? n_chunks - 1 - i : i) * kC; }
-  __device__ __forceinline__ int32_t len(int32_t s0) const { return end - s0 < kC ? end - s0 : kC; }
+  __device__ __forceinline__ int32_t chunk(int i) const { return start + (kRev ? n_chunks - 1 - i : i) * C; }
+  __device__ __forceinline__ int32_t len(int32_t s0) const { return end - s0 < C ? end - s0 : C; }
 };
 
 // A tile of a chunk's rows [s0, s0 + n) of head h, into dst.
-template <int D, int NT>
+template <int D, int C, int NT>
 __device__ __forceinline__ void issue_rows(const bf16* p, int32_t s0, int32_t n, int32_t H, int32_t h, char* dst,
                                            int wave) {
   const int32_t stride = H * D * 2;
-  issue_tile<D, NT>(buffer(p + (int64_t(s0) * H + h) * D, int64_t(n - 1) * stride + D * 2), stride, dst, wave);
+  issue_tile<D, C, NT>(buffer(p + (int64_t(s0) * H + h) * D, int64_t(n - 1) * stride + D * 2), stride, dst, wave);
 }
 
 template <bool kRev>
@@ -235,26 +236,26 @@ __device__ __forceinline__ float update_weight(float scale, float g2, int s, int
 // The state walk of one run: block blk of saved states x heads.
 template <int DA, int DB, bool kRev, int kParts>
 __device__ __forceinline__ void state_walk(const WalkArgs& x, const Role& R, int64_t blk, char* lds, float* upd) {
-  constexpr int NT = 2 * DB, TA = DA / 32, SB = Rows<DA>::BYTES, SC = Rows<DB>::BYTES;
+  constexpr int C = kCState, NT = 2 * DB, TA = DA / 32, SB = C * DA * 2, SC = C * DB * 2;
   const int32_t h = int32_t(blk % x.H), idx = int32_t(blk / x.H);
   SegTile t;
   if (!find_saved<kRev>(x.cu, x.max_segs, x.N, x.run, idx, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  Run<kRev> run;
+  Run<C, kRev> run;
   run.start = t.start;
   run.end = t.e - t.start > x.run ? t.start + x.run : t.e;
-  run.n_chunks = (run.end - run.start + kC - 1) / kC;
+  run.n_chunks = (run.end - run.start + C - 1) / C;
   const float g2 = x.g[h] * kLog2e;
   auto issue = [&](int i) {
-    const int32_t s0 = run.chunk(i), n = run.len(s0);
-    char* dst = lds + (i & 1) * (SB + SC);
-    issue_rows<DA, NT>(R.b, s0, n, x.H, h, dst, wave);
-    issue_rows<DB, NT>(R.c, s0, n, x.H, h, dst + SB, wave);
-    if (tid < kC) upd[(i & 1) * kC + tid] = update_weight<kRev>(R.in_scale, g2, tid, n);
+    const int32_t s0 = run.chunk(i), n = run.len(s0), stage = i & 1;
+    char* dst = lds + stage * (SB + SC);
+    issue_rows<DA, C, NT>(R.b, s0, n, x.H, h, dst, wave);
+    issue_rows<DB, C, NT>(R.c, s0, n, x.H, h, dst + SB, wave);
+    if (tid < C) upd[stage * C + tid] = update_weight<kRev>(R.in_scale, g2, tid, n);
   };
   // chunks whose tokens decay to a weight that fp32 has only 0 for (2^-150) by
   // the run's end are left out
-  const float far = g2 < 0.f ? fminf(150.f / (-kC * g2), 1e6f) : 1e6f;
+  const float far = g2 < 0.f ? fminf(150.f / (-C * g2), 1e6f) : 1e6f;
   int it = run.n_chunks - 1 - int(far);
   it = it < 0 ? 0 : it;
   issue(it);
@@ -268,19 +269,19 @@ __device__ __forceinline__ void state_walk(const WalkArgs& x, const Role& R, int
     bar();
     if (it + 1 < run.n_chunks) issue(it + 1);
     const char* bt = lds + (it & 1) * (SB + SC);
-    bf16x8 cf[4];
+    bf16x8 cf[C / 16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cf[j] = tc.read(bt + SB, wave, j);
-    update<DA, kParts>(X, ex2(g2 * run.len(run.chunk(it))), cf, upd + (it & 1) * kC, lane >> 5, tb, bt);
+    for (int j = 0; j < C / 16; ++j) cf[j] = tc.read(bt + SB, wave, j);
+    update<DA, C, kParts>(X, ex2(g2 * run.len(run.chunk(it))), cf, upd + (it & 1) * C, lane >> 5, tb, bt);
   }
   StateAddr<DA, DB>(R.saved + (int64_t(idx) * x.H + h) * DA * DB, R.transposed, tid).store(X);
 }
 
 // Role 0 forward and, with kBoth, role 1 backward.
 template <int DA, int DB, int kParts, bool kBoth>
-__global__ __launch_bounds__(2 * DB, 2) void linear_state_kernel(const WalkArgs x) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * (Rows<DA>::BYTES + Rows<DB>::BYTES)];
-  __shared__ __attribute__((aligned(16))) float upd[2 * kC];
+__global__ __launch_bounds__(2 * DB, 3) void linear_state_kernel(const WalkArgs x) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kCState * (DA + DB) * 2];
+  __shared__ __attribute__((aligned(16))) float upd[2 * kCState];
   const int64_t n = x.N / x.run * x.H, blk = blockIdx.x;
   if (!kBoth || blk < n)
     state_walk<DA, DB, false, kParts>(x, x.r[0], blk, lds, upd);
@@ -289,15 +290,15 @@ __global__ __launch_bounds__(2 * DB, 2) void linear_state_kernel(const WalkArgs 
 }
 
 template <int DA, int DB, bool kRev, int kParts, bool kPair>
-__global__ __launch_bounds__((kPair ? 4 : 2) * DB, 2) void linear_walk_kernel(const WalkArgs x) {
+__global__ __launch_bounds__((kPair ? 4 : 2) * DB, kPair ? 2 : 3) void linear_walk_kernel(const WalkArgs x) {
   constexpr int NW = DB / 32, NT = (kPair ? 2 : 1) * 64 * NW, KA = DA / 16, TA = DA / 32;
-  constexpr int SB = Rows<DA>::BYTES, SC = Rows<DB>::BYTES;
+  constexpr int SB = kC * DA * 2, SC = kC * DB * 2;
   static_assert(!kPair || DA == DB, "a team's b is the other one's c");
-  // one team: b of the even chunks, of the odd ones, c, a; two: the first team's
-  // b of the even and odd chunks, the second's, and the a of each
-  constexpr int kA = kPair ? 4 * SB : 2 * SB + SC;
-  constexpr int kPieces = kC * Rows<DA>::CH / NT;  // loads of a b tile per lane
-  __shared__ __attribute__((aligned(1024))) char lds[kA + (kPair ? 2 : 1) * SB];
+  // a stage: a, b and c of a team; of two, a and b of each (a team's c is the
+  // other one's b)
+  constexpr int kStage = kPair ? 4 * SB : 2 * SB + SC;
+  constexpr int kStores = 2;  // of a chunk's outputs, per lane
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
   constexpr int WP = kC + 8;  // row of the in-chunk weights [t][s]
   __shared__ __attribute__((aligned(16))) bf16 wts[kPair ? 2 : 1][kC][WP];
   __shared__ __attribute__((aligned(16))) float upd[2][kC];
@@ -325,7 +326,7 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, 2) void linear_walk_kernel(co
   SegTile t;
   slot_of(x.grid, blk, x.H, slot, h0, h1);
   if (!find_tile(x.cu, x.max_segs, x.N, x.run, slot, t)) return;
-  Run<kRev> run;
+  Run<kC, kRev> run;
   run.start = t.start;
   run.end = t.e - t.start > x.run ? t.start + x.run : t.e;
   run.n_chunks = (run.end - run.start + kC - 1) / kC;
@@ -343,19 +344,20 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, 2) void linear_walk_kernel(co
     const float g2 = x.g[h] * kLog2e;
     const int half = lane >> 5, col = lane & 31;
     const int32_t cs = x.H * DB * 2;
-    auto issue_b = [&](int i) {
-      const int32_t s0 = run.chunk(i), n = run.len(s0);
-      issue_rows<DA, NT>(x.r[0].b, s0, n, x.H, h, lds + (i & 1) * SB, wave_);
-      if constexpr (kPair) issue_rows<DA, NT>(x.r[1].b, s0, n, x.H, h, lds + (2 + (i & 1)) * SB, wave_);
-      if (tid < kC) upd[i & 1][tid] = update_weight<kRev>(x.r[0].in_scale, g2, tid, n);
+    auto issue = [&](int i) {
+      const int32_t s0 = run.chunk(i), n = run.len(s0), stage = i & 1;
+      char* dst = lds + stage * kStage;
+      issue_rows<DA, kC, NT>(x.r[0].a, s0, n, x.H, h, dst, wave_);
+      issue_rows<DA, kC, NT>(x.r[0].b, s0, n, x.H, h, dst + SB, wave_);
+      if constexpr (kPair) {
+        issue_rows<DA, kC, NT>(x.r[1].a, s0, n, x.H, h, dst + 2 * SB, wave_);
+        issue_rows<DA, kC, NT>(x.r[1].b, s0, n, x.H, h, dst + 3 * SB, wave_);
+      } else {
+        issue_rows<DB, kC, NT>(x.r[0].c, s0, n, x.H, h, dst + 2 * SB, wave_);
+      }
+      if (tid < kC) upd[stage][tid] = update_weight<kRev>(x.r[0].in_scale, g2, tid, n);
     };
-    auto issue_a = [&](int i) {
-      const int32_t s0 = run.chunk(i), n = run.len(s0);
-      issue_rows<DA, NT>(x.r[0].a, s0, n, x.H, h, lds + kA, wave_);
-      if constexpr (kPair) issue_rows<DA, NT>(x.r[1].a, s0, n, x.H, h, lds + kA + SB, wave_);
-    };
-    issue_b(0);
-    issue_a(0);
+    issue(0);
 
     f32x16 X[TA];
     const float* from = first ? (R.init ? R.init + (int64_t(t.seg) * x.H + h) * DA * DB : nullptr)
@@ -368,12 +370,11 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, 2) void linear_walk_kernel(co
     }
 
     // In-chunk weights of the lane: column t = lane % 16 of a 16-token block,
-    // rows s = 4 (lane / 16) + e. near: of the block on the diagonal, next: of
-    // the block 16 tokens off it (every further one a power of `apart` more).
-    // The columns a wave forms: block `wave` of 4, or blocks `wave`, 3 - wave.
+    // rows s = 4 (lane / 16) + e; near: of a block on the diagonal, next: of the
+    // block beside it.
     const int c16 = lane & 15, r16 = lane >> 4;
     f32x4 near, next;
-    const float apart = ex2(g2 * 16.f), both = R.in_scale * R.out_scale;
+    const float both = R.in_scale * R.out_scale;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int d = kRev ? 4 * r16 + e - c16 : c16 - 4 * r16 - e;
@@ -381,114 +382,88 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, 2) void linear_walk_kernel(co
       next[e] = both * ex2(g2 * (d + 16));
     }
     bf16* wt = &wts[team][0][0];
-    // blocks that the 32-row steps of the second product read beside the
-    // diagonal ones and that never have any
-    if (wave < 2) {
-      const int cb = 2 * wave + (kRev ? 1 : 0), sb = 2 * wave + (kRev ? 0 : 1);
-      *reinterpret_cast<uint64_t*>(wt + (16 * cb + c16) * WP + 16 * sb + 4 * r16) = 0;
-    }
+    // the block that never has any
+    if (wave == NW - 1)
+      *reinterpret_cast<uint64_t*>(wt + (16 * (kRev ? 1 : 0) + c16) * WP + 16 * (kRev ? 0 : 1) + 4 * r16) = 0;
     const Transposed<DA> tb(lane);
     const Transposed<DB> tc(lane);
 
     for (int it = 0; it < run.n_chunks; ++it) {
-      wait_all();
+      // This chunk has come; the last chunk's outputs, stored after it was asked
+      // for, may be on their way (the counter is in order).
+      if (it == 0)
+        wait_all();
+      else
+        wait_loads<kStores>();
       bar();
-      if constexpr (!kPair) {
-        const int32_t s0 = run.chunk(it);
-        issue_rows<DB, NT>(x.r[0].c, s0, run.len(s0), x.H, h, lds + 2 * SB, wave_);
-        // c's loads stay before the next b's: the wait for c below counts those
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (it + 1 < run.n_chunks) issue_b(it + 1);
+      if (it + 1 < run.n_chunks) issue(it + 1);
+      asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      const char* bt = lds + ((it & 1) + 2 * team) * SB;
-      const char* ct = kPair ? lds + ((it & 1) + 2 * (1 - team)) * SB : lds + 2 * SB;
-      const char* at_ = lds + kA + team * SB;
+      const char* st = lds + (it & 1) * kStage;
+      const char* at_ = st + (kPair ? 2 * team * SB : 0);
+      const char* bt = at_ + SB;
+      const char* ct = st + (kPair ? (3 - 2 * team) * SB : 2 * SB);
       const int32_t s0 = run.chunk(it), n = run.len(s0);
 
-      // in-chunk weights, a block of 16 columns at a time
+      // in-chunk weights: three blocks of 16 x 16, one or two a wave
 #pragma unroll
-      for (int v = 0; v < 4 / NW; ++v) {
-        const int cb = v == 0 ? wave : 3 - wave;
-        f32x4 w[4] = {};
+      for (int v = 0; v < (3 + NW - 1) / NW; ++v) {
+        const int blk16 = wave + v * NW;  // 0, 1: on the diagonal, 2: beside it
+        if (blk16 > 2) continue;
+        const int cb = blk16 < 2 ? blk16 : (kRev ? 0 : 1), sb = blk16 < 2 ? blk16 : (kRev ? 1 : 0);
+        f32x4 w = {};
 #pragma unroll
         for (int i = 0; i < DA / 32; ++i) {
-          auto row = [&](const char* tile, int blk16) {
-            return *reinterpret_cast<const bf16x8*>(tile + (16 * blk16 + c16) * Rows<DA>::ROW +
+          auto row = [&](const char* tile, int b16) {
+            return *reinterpret_cast<const bf16x8*>(tile + (16 * b16 + c16) * Rows<DA>::ROW +
                                                     (((4 * i + r16) ^ Rows<DA>::swz(c16)) * 16));
           };
-          const bf16x8 a = row(at_, cb);
-#pragma unroll
-          for (int sb = 0; sb < 4; ++sb)
-            if (kRev ? sb >= cb : sb <= cb) w[sb] = mfma16(row(bt, sb), a, w[sb]);
+          w = mfma16(row(bt, sb), row(at_, cb), w);
         }
+        bf16x4 y;
 #pragma unroll
-        for (int sb = 0; sb < 4; ++sb) {
-          const int off = kRev ? sb - cb : cb - sb;
-          if (off < 0) continue;
-          const float more = off < 2 ? 1.f : (off == 2 ? apart : apart * apart);
-          bf16x4 y;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = static_cast<bf16>(w[sb][e] * (off == 0 ? near[e] : next[e] * more));
-          *reinterpret_cast<bf16x4*>(wt + (16 * cb + c16) * WP + 16 * sb + 4 * r16) = y;
-        }
+        for (int e = 0; e < 4; ++e) y[e] = static_cast<bf16>(w[e] * (blk16 < 2 ? near[e] : next[e]));
+        *reinterpret_cast<bf16x4*>(wt + (16 * cb + c16) * WP + 16 * sb + 4 * r16) = y;
       }
-      // readout of X
-      f32x16 o[2] = {};
+      // readout of X, in two chains
+      f32x16 o = {}, o2 = {};
 #pragma unroll
       for (int i = 0; i < KA; ++i) {
         bf16x8 xs;
 #pragma unroll
         for (int j = 0; j < 8; ++j) xs[j] = static_cast<bf16>(X[i / 2][8 * (i % 2) + j]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          o[u] = mfma32(xs, *reinterpret_cast<const bf16x8*>(at_ + (32 * u + col) * Rows<DA>::ROW +
-                                                             (((2 * i + half) ^ Rows<DA>::swz(col)) * 16)),
-                        o[u]);
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(at_ + col * Rows<DA>::ROW +
+                                                          (((2 * i + half) ^ Rows<DA>::swz(col)) * 16));
+        if (i % 2 == 0)
+          o = mfma32(xs, a, o);
+        else
+          o2 = mfma32(xs, a, o2);
       }
-      // c has come (the next b may still be on its way), the weights are in LDS,
-      // a is free
-      if (!kPair && it + 1 < run.n_chunks)
-        __builtin_amdgcn_s_waitcnt(0x0070 | kPieces);
-      else if (!kPair)
-        wait_all();
-      else
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS stores alone
-      bar();
-      if (it + 1 < run.n_chunks) issue_a(it + 1);
-      bf16x8 cf[4];
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS stores
+      bar();                               // the weights are in LDS
+      bf16x8 cf[kC / 16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cf[j] = tc.read(ct, wave, j);
+      for (int j = 0; j < kC / 16; ++j) cf[j] = tc.read(ct, wave, j);
+      const int d = kRev ? n - 1 - col : col + 1;
+      const float ow = R.out_scale * ex2(g2 * (d < 0 ? 0 : d));
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int d = kRev ? n - 1 - 32 * u - col : 32 * u + col + 1;
-        const float ow = R.out_scale * ex2(g2 * (d < 0 ? 0 : d));
+      for (int i = 0; i < 16; ++i) o[i] = (o[i] + o2[i]) * ow;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[u][i] *= ow;
+      for (int j = 0; j < kC / 16; ++j) {
+        const bf16* p = wt + col * WP + 16 * j + 4 * half;
+        o = mfma32(cf[j], join(*reinterpret_cast<const s16x4*>(p), *reinterpret_cast<const s16x4*>(p + 8)), o);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (kRev ? j / 2 < u : j / 2 > u) continue;
-          const bf16* p = wt + (32 * u + col) * WP + 16 * j + 4 * half;
-          const s16x4 lo = *reinterpret_cast<const s16x4*>(p), hi = *reinterpret_cast<const s16x4*>(p + 8);
-          o[u] = mfma32(cf[j], join(lo, hi), o[u]);
-        }
       // (rows past the chunk's end are out of the buffer's range)
       const auto ro = buffer(R.out + (int64_t(s0) * x.H + h) * DB, int64_t(n - 1) * cs + DB * 2);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int v = 0; v < kStores; ++v) {
+        bf16x8 y;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          bf16x8 y;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = static_cast<bf16>(o[u][8 * v + j]);
-          store16(ro, uint32_t(32 * u + col) * cs + 64 * wave + 16 * half + 32 * v, __builtin_bit_cast(i32x4, y));
-        }
+        for (int j = 0; j < 8; ++j) y[j] = static_cast<bf16>(o[8 * v + j]);
+        store16(ro, uint32_t(col) * cs + 64 * wave + 16 * half + 32 * v, __builtin_bit_cast(i32x4, y));
+      }
       __builtin_amdgcn_sched_barrier(0);
-      update<DA, kParts>(X, ex2(g2 * n), cf, upd[it & 1], half, tb, bt);
+      update<DA, kC, kParts>(X, ex2(g2 * n), cf, upd[(it & 1)], half, tb, bt);
     }
 
     if (last && R.fin != nullptr)
@@ -580,10 +555,9 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
 // Tokens of a run: the smallest power of two from sqrt(1.5 N H) on, in
 // [256, 4096]. Shorter runs keep more work-groups busy but save, scan and read
 // back more states (their number times their length is N H). Measured, us at
-// runs of 512 / 1024 / 2048 / 4096: N H = 2^21 (65536 tokens, 39 segments, 32
-// heads of 128): 900 / 755 / 704 / 825; 2^19 (one segment of 32768, 16 heads):
-// 249 / 213 / 253 / 448; 2^17 (8192 tokens, forward and reverse): 282 / 398 /
-// 694 / 843 (256: 325).
+// runs of 512 / 1024 / 2048: N H = 2^21 (65536 tokens, 39 segments, 32 heads of
+// 128): 867 / 721 / 661; 2^19 (one segment of 32768, 16 heads): 248 / 210 / 289;
+// 2^17 (8192 tokens, forward and reverse): 248 / 334 / 603 (256: 263).
 int32_t run_tokens(int64_t N, int32_t H) {
   int32_t r = 256;
   while (r < 4096 && int64_t(r) * r < N * H * 3 / 2) r *= 2;

@@ -95,6 +95,13 @@ __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x)
 __device__ __forceinline__ void wait_vm() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 // ... and its LDS operations.
 __device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x0070); }
+// All LDS operations done, and all vector-memory operations but the last n (they
+// complete in order).
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(n >= 0 && n < 64, "a 6-bit counter");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);
+}
 // A work-group barrier that waits for nothing but the other waves.
 __device__ __forceinline__ void bar() {
   asm volatile("" ::: "memory");
