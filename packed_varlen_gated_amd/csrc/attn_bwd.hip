@@ -124,7 +124,7 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[D / 32], float f,
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
     int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dq, float* __restrict__ stats,
@@ -239,7 +239,7 @@ struct DkvShape {
 };
 
 template <int D, int kQ>
-__global__ __launch_bounds__(DkvShape<kQ>::NT, 2) void attn_dkv_kernel(
+__global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void attn_dkv_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const bf16* __restrict__ dout, const float* __restrict__ stats, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dk,

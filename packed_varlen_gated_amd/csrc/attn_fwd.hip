@@ -58,7 +58,7 @@ struct Tile {
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_fwd_kernel(
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
     bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, SlotGrid grid) {
