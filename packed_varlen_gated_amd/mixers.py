@@ -12,20 +12,15 @@ computation runs in the library's HIP kernels on torch's current stream.
 * ``kda_step(q, k, v, g, beta, state, slots=None, scale=1.0)``
 """
 
-import contextlib
 import ctypes
 import math
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_check, _dtype_code, _load, _need, _need_shape, _ptr, _stream, _workspace,
-               OPT_QK_L2NORM)
+from . import _check, _dtype_code, _load, _need, _need_shape, _workspace, OPT_QK_L2NORM, PKV_BF16
 
 FLAG_BAD_SLOT = 16
-
-_NOTHING = contextlib.nullcontext()
-
 
 def declare(lib):
     """Argument types of the calls (once, when the library is loaded)."""
@@ -46,37 +41,88 @@ def declare(lib):
         fn.restype = res
 
 
-def _on(device):
-    """The call's device as the current one while it launches."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, expected a GPU")
-    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+# A decoding step's kernel takes a few microseconds, so the checks of a call that
+# passes them are kept short: _fit asks everything of several tensors at once, and
+# only where it says no does _need find out what is wrong.
+def _fit(index, dtype, ndim, *tensors):
+    try:
+        for t in tensors:
+            if t.get_device() != index or t.dtype is not dtype or t.dim() != ndim or not t.is_contiguous():
+                return False
+        return True
+    except AttributeError:
+        return False
+
+
+def _tensors(device, dtype, ndim, **tensors):
+    if not _fit(device, dtype, ndim, *tensors.values()):
+        dev = next((t.device for t in tensors.values() if isinstance(t, torch.Tensor) and t.get_device() == device),
+                   torch.device("cuda", device) if device >= 0 else torch.device("cpu"))
+        for name, t in tensors.items():
+            _need(t, name, dev, dtype, ndim)
+
+
+def _shape(t, name, shape):
+    if t.shape != shape:
+        _need_shape(t, name, shape)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(fn, device, *args):
+    """The call on the device's current stream, with the device as the current one."""
+    if device < 0:
+        raise ValueError("the tensors are on the CPU, expected a GPU")
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        _check(status)
+
+
+def _code(dtype):
+    return PKV_BF16 if dtype is torch.bfloat16 else _dtype_code(dtype)
+
+
+def _flags_of(flags, device):
+    if flags is not None:
+        _tensors(device, torch.int32, 1, flags=flags)
+        _shape(flags, "flags", (1,))
 
 
 def _slots_of(cu_seqlens, device):
     if cu_seqlens is None:
         return 1
-    _need(cu_seqlens, "cu_seqlens", device, torch.int32, 1)
+    _tensors(device, torch.int32, 1, cu_seqlens=cu_seqlens)
     if cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must hold max_segs + 1 >= 2 entries")
     return cu_seqlens.shape[0] - 1
 
 
+def _scratch(workspace, need, q):
+    if need <= 0:
+        return None, 0
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=q.device), need
+    return _workspace(workspace, need, q.device)
+
+
 def _attn_shapes(q, k, v, cu_seqlens, scale, flags):
-    dev, dt = q.device, q.dtype
-    code = _dtype_code(dt)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, dev, dt, 4)
+    dev, dt = q.get_device(), q.dtype
+    code = _code(dt)
+    _tensors(dev, dt, 4, q=q, k=k, v=v)
     B, T, Hq, D = q.shape
-    if tuple(k.shape[:2]) != (B, T) or k.shape[3] != D or tuple(v.shape) != tuple(k.shape):
+    kb, kt, Hkv, kd = k.shape
+    if kb != B or kt != T or kd != D or v.shape != k.shape:
         raise ValueError("k and v must be [.., N, Hkv, D] with q's N and D")
-    Hkv = k.shape[2]
     if Hkv < 1 or Hq % Hkv != 0:
         raise ValueError(f"q has {Hq} heads, not a multiple of the {Hkv} of k and v")
     segs = _slots_of(cu_seqlens, dev)
-    if flags is not None:
-        _need(flags, "flags", dev, torch.int32, 1)
-        _need_shape(flags, "flags", (1,))
+    _flags_of(flags, dev)
     return dev, code, B * T, Hq, Hkv, D, segs, 1.0 / math.sqrt(D) if scale is None else float(scale)
 
 
@@ -91,14 +137,15 @@ def attn_varlen(q, k, v, cu_seqlens=None, scale=None, output_lse=True, flags=Non
     """
     lib = _load()
     dev, code, N, Hq, Hkv, D, segs, scale = _attn_shapes(q, k, v, cu_seqlens, scale, flags)
-    o = torch.empty_like(q) if out is None else out
-    _need(o, "out", dev, q.dtype, 4)
-    _need_shape(o, "out", q.shape)
-    lse = torch.empty(Hq, N, dtype=torch.float32, device=dev) if output_lse else None
-    with _on(dev):
-        _check(lib.pkv_attn_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), segs, N, Hq, Hkv, D, scale, code,
-                                   _ptr(o), _ptr(lse), _ptr(flags), _stream(dev)))
-    return o, lse
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _tensors(dev, q.dtype, 4, out=out)
+        _shape(out, "out", q.shape)
+    lse = torch.empty(Hq, N, dtype=torch.float32, device=q.device) if output_lse else None
+    _run(lib.pkv_attn_varlen, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cu_seqlens), segs, N, Hq, Hkv, D,
+         scale, code, out.data_ptr(), _ptr(lse), _ptr(flags))
+    return out, lse
 
 
 class AttnGrads(NamedTuple):
@@ -116,42 +163,37 @@ def attn_varlen_backward(q, k, v, o, lse, do, cu_seqlens=None, scale=None, flags
     do = dL/do. Returns AttnGrads; dk and dv are summed over the query heads of their kv head."""
     lib = _load()
     dev, code, N, Hq, Hkv, D, segs, scale = _attn_shapes(q, k, v, cu_seqlens, scale, flags)
-    for name, t in (("o", o), ("do", do)):
-        _need(t, name, dev, q.dtype, 4)
-        _need_shape(t, name, q.shape)
-    _need(lse, "lse", dev, torch.float32, 2)
-    _need_shape(lse, "lse", (Hq, N))
+    _tensors(dev, q.dtype, 4, o=o, do=do)
+    _shape(o, "o", q.shape)
+    _shape(do, "do", q.shape)
+    _tensors(dev, torch.float32, 2, lse=lse)
+    _shape(lse, "lse", (Hq, N))
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    need = int(lib.pkv_attn_varlen_backward_workspace_size(N, Hq, Hkv, D, segs, code))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    with _on(dev):
-        _check(lib.pkv_attn_varlen_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do),
-                                            _ptr(cu_seqlens), segs, N, Hq, Hkv, D, scale, code, _ptr(dq), _ptr(dk),
-                                            _ptr(dv), _ptr(flags), _ptr(workspace), ws_bytes, _stream(dev)))
+    workspace, ws_bytes = _scratch(workspace, lib.pkv_attn_varlen_backward_workspace_size(N, Hq, Hkv, D, segs, code), q)
+    _run(lib.pkv_attn_varlen_backward, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+         do.data_ptr(), _ptr(cu_seqlens), segs, N, Hq, Hkv, D, scale, code, dq.data_ptr(), dk.data_ptr(),
+         dv.data_ptr(), _ptr(flags), _ptr(workspace), ws_bytes)
     return AttnGrads(dq, dk, dv)
 
 
 def _linear_shapes(q, k, v, g, cu_seqlens, states, flags):
-    dev, dt = q.device, q.dtype
-    code = _dtype_code(dt)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, dev, dt, 4)
+    dev, dt = q.get_device(), q.dtype
+    code = _code(dt)
+    _tensors(dev, dt, 4, q=q, k=k, v=v)
     B, T, H, Dk = q.shape
-    Dv = v.shape[3]
-    if tuple(k.shape) != tuple(q.shape):
+    vb, vt, vh, Dv = v.shape
+    if k.shape != q.shape:
         raise ValueError("q and k must have the same shape")
-    if tuple(v.shape[:3]) != (B, T, H):
+    if vb != B or vt != T or vh != H:
         raise ValueError("v must be [.., N, H, Dv]")
-    _need(g, "g", dev, torch.float32, 1)
-    _need_shape(g, "g", (H,))
+    _tensors(dev, torch.float32, 1, g=g)
+    _shape(g, "g", (H,))
     segs = _slots_of(cu_seqlens, dev)
-    for name, t in states:
+    for name, t in states.items():
         if t is not None:
-            _need(t, name, dev, torch.float32, 4)
-            _need_shape(t, name, (segs, H, Dk, Dv))
-    if flags is not None:
-        _need(flags, "flags", dev, torch.int32, 1)
-        _need_shape(flags, "flags", (1,))
+            _tensors(dev, torch.float32, 4, **{name: t})
+            _shape(t, name, (segs, H, Dk, Dv))
+    _flags_of(flags, dev)
     return dev, code, B * T, H, Dk, Dv, segs
 
 
@@ -170,18 +212,18 @@ def chunk_linear_attn_varlen(q, k, v, g, cu_seqlens=None, scale=1.0, output_fina
     Returns (o like v, final_state fp32 [max_segs, H, Dk, Dv] or None).
     """
     lib = _load()
-    dev, code, N, H, Dk, Dv, segs = _linear_shapes(q, k, v, g, cu_seqlens, [("initial_state", initial_state)], flags)
-    o = torch.empty_like(v) if out is None else out
-    _need(o, "out", dev, v.dtype, 4)
-    _need_shape(o, "out", v.shape)
-    fs = torch.empty(segs, H, Dk, Dv, dtype=torch.float32, device=dev) if output_final_state else None
-    need = int(lib.pkv_linear_attn_varlen_workspace_size(N, H, Dk, Dv, segs, code))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    with _on(dev):
-        _check(lib.pkv_linear_attn_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), segs, N, H, Dk, Dv,
-                                          float(scale), code, _ptr(initial_state), _ptr(o), _ptr(fs), _ptr(flags),
-                                          _ptr(workspace), ws_bytes, _stream(dev)))
-    return o, fs
+    dev, code, N, H, Dk, Dv, segs = _linear_shapes(q, k, v, g, cu_seqlens, dict(initial_state=initial_state), flags)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _tensors(dev, v.dtype, 4, out=out)
+        _shape(out, "out", v.shape)
+    fs = torch.empty(segs, H, Dk, Dv, dtype=torch.float32, device=q.device) if output_final_state else None
+    workspace, ws_bytes = _scratch(workspace, lib.pkv_linear_attn_varlen_workspace_size(N, H, Dk, Dv, segs, code), q)
+    _run(lib.pkv_linear_attn_varlen, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(cu_seqlens),
+         segs, N, H, Dk, Dv, float(scale), code, _ptr(initial_state), out.data_ptr(), _ptr(fs), _ptr(flags),
+         _ptr(workspace), ws_bytes)
+    return out, fs
 
 
 class LinearAttnGrads(NamedTuple):
@@ -205,49 +247,49 @@ def chunk_linear_attn_varlen_backward(q, k, v, g, do, cu_seqlens=None, scale=1.0
     """
     lib = _load()
     dev, code, N, H, Dk, Dv, segs = _linear_shapes(
-        q, k, v, g, cu_seqlens, [("initial_state", initial_state), ("dfinal_state", dfinal_state)], flags)
-    _need(do, "do", dev, v.dtype, 4)
-    _need_shape(do, "do", v.shape)
+        q, k, v, g, cu_seqlens, dict(initial_state=initial_state, dfinal_state=dfinal_state), flags)
+    _tensors(dev, v.dtype, 4, do=do)
+    _shape(do, "do", v.shape)
     if output_d_initial_state is None:
         output_d_initial_state = initial_state is not None
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dinit = torch.empty(segs, H, Dk, Dv, dtype=torch.float32, device=dev) if output_d_initial_state else None
-    need = int(lib.pkv_linear_attn_varlen_backward_workspace_size(N, H, Dk, Dv, segs, code))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    with _on(dev):
-        _check(lib.pkv_linear_attn_varlen_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), segs, N, H, Dk, Dv, float(scale), code,
-            _ptr(initial_state), _ptr(do), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinit),
-            _ptr(flags), _ptr(workspace), ws_bytes, _stream(dev)))
+    dinit = torch.empty(segs, H, Dk, Dv, dtype=torch.float32, device=q.device) if output_d_initial_state else None
+    workspace, ws_bytes = _scratch(
+        workspace, lib.pkv_linear_attn_varlen_backward_workspace_size(N, H, Dk, Dv, segs, code), q)
+    _run(lib.pkv_linear_attn_varlen_backward, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+         _ptr(cu_seqlens), segs, N, H, Dk, Dv, float(scale), code, _ptr(initial_state), do.data_ptr(),
+         _ptr(dfinal_state), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dinit), _ptr(flags), _ptr(workspace),
+         ws_bytes)
     return LinearAttnGrads(dq, dk, dv, dinit)
 
 
 def _step_shapes(q, k, v, state, slots, out, flags):
-    dev, dt = q.device, q.dtype
-    code = _dtype_code(dt)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, dev, dt, 3)
+    dev, dt = q.get_device(), q.dtype
+    code = _code(dt)
+    _tensors(dev, dt, 3, q=q, k=k, v=v)
     R, H, Dk = q.shape
-    Dv = v.shape[2]
-    if tuple(k.shape) != tuple(q.shape):
+    vr, vh, Dv = v.shape
+    if k.shape != q.shape:
         raise ValueError("q and k must have the same shape")
-    if tuple(v.shape[:2]) != (R, H):
+    if vr != R or vh != H:
         raise ValueError("v must be [R, H, Dv]")
-    _need(state, "state", dev, torch.float32, 4)
-    S = state.shape[0]
-    _need_shape(state, "state", (S, H, Dk, Dv))
+    _tensors(dev, torch.float32, 4, state=state)
+    S, sh, sk, sv = state.shape
+    if sh != H or sk != Dk or sv != Dv:
+        _need_shape(state, "state", (S, H, Dk, Dv))
     if slots is not None:
-        _need(slots, "slots", dev, torch.int32, 1)
-        _need_shape(slots, "slots", (R,))
+        _tensors(dev, torch.int32, 1, slots=slots)
+        if slots.shape[0] != R:
+            _need_shape(slots, "slots", (R,))
     elif R > S:
         raise ValueError(f"{R} rows for {S} state slots")
-    o = torch.empty_like(v) if out is None else out
-    _need(o, "out", dev, dt, 3)
-    _need_shape(o, "out", v.shape)
-    if flags is not None:
-        _need(flags, "flags", dev, torch.int32, 1)
-        _need_shape(flags, "flags", (1,))
-    return dev, code, R, S, H, Dk, Dv, o
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _tensors(dev, dt, 3, out=out)
+        _shape(out, "out", v.shape)
+    _flags_of(flags, dev)
+    return dev, code, R, S, H, Dk, Dv, out
 
 
 def linear_attn_step(q, k, v, g, state, slots=None, scale=1.0, out=None, flags=None):
@@ -261,11 +303,11 @@ def linear_attn_step(q, k, v, g, state, slots=None, scale=1.0, out=None, flags=N
     """
     lib = _load()
     dev, code, R, S, H, Dk, Dv, o = _step_shapes(q, k, v, state, slots, out, flags)
-    _need(g, "g", dev, torch.float32, 1)
-    _need_shape(g, "g", (H,))
-    with _on(dev):
-        _check(lib.pkv_linear_attn_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(slots), R, S, H, Dk, Dv,
-                                        float(scale), code, _ptr(state), _ptr(o), _ptr(flags), _stream(dev)))
+    _tensors(dev, torch.float32, 1, g=g)
+    if g.shape[0] != H:
+        _need_shape(g, "g", (H,))
+    _run(lib.pkv_linear_attn_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(slots), R, S, H,
+         Dk, Dv, float(scale), code, state.data_ptr(), o.data_ptr(), _ptr(flags))
     return o
 
 
@@ -277,12 +319,11 @@ def kda_step(q, k, v, g, beta, state, slots=None, scale=1.0, out=None, flags=Non
     """
     lib = _load()
     dev, code, R, S, H, Dk, Dv, o = _step_shapes(q, k, v, state, slots, out, flags)
-    _need(g, "g", dev, q.dtype, 3)
-    _need_shape(g, "g", q.shape)
-    _need(beta, "beta", dev, q.dtype, 2)
-    _need_shape(beta, "beta", (R, H))
-    with _on(dev):
-        _check(lib.pkv_kda_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(slots), R, S, H, Dk, Dv,
-                                float(scale), code, OPT_QK_L2NORM if use_qk_l2norm_in_kernel else 0, _ptr(state),
-                                _ptr(o), _ptr(flags), _stream(dev)))
+    _tensors(dev, q.dtype, 3, g=g)
+    _shape(g, "g", q.shape)
+    _tensors(dev, q.dtype, 2, beta=beta)
+    _shape(beta, "beta", (R, H))
+    _run(lib.pkv_kda_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(slots),
+         R, S, H, Dk, Dv, float(scale), code, OPT_QK_L2NORM if use_qk_l2norm_in_kernel else 0, state.data_ptr(),
+         o.data_ptr(), _ptr(flags))
     return o
