@@ -13,10 +13,11 @@
 //
 // A work-group of 256 threads takes 32 rows (queries, or keys in the dk/dv
 // pass) of one head and walks the other side in tiles of 32 staged in LDS as
-// fp32. Thread (r, c) = (tid / 8, tid % 8) holds row r's scores of columns
-// c + 8 j and its output channels c + 8 j; the softmax runs in one pass with a
-// running maximum and sum. These shapes serve fp32 batches that models are
-// debugged on; the MFMA kernels serve bf16 at D = 64 and 128.
+// fp32, the next tile's values on their way in registers. Thread (r, c) =
+// (tid / 8, tid % 8) holds row r's scores of columns c + 8 j and its channels
+// 4 (c + 8 j) .. + 3; LDS is read 16 bytes at a time. The softmax runs in one pass
+// with a running maximum and sum. These shapes serve fp32 batches that models are
+// debugged on, where latency counts; the MFMA kernels serve bf16 at D = 64 and 128.
 
 #include "segments.h"
 
@@ -27,13 +28,79 @@ constexpr int kT = 32;        // tokens per tile, both sides
 constexpr int kThreads = 256;
 constexpr int kTail = 64;     // work-groups that zero the rows no segment has
 
-// 32 rows of a [N, H, D] tensor from `row` on, fp32, zero past `end`.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <int D>
+struct alignas(16) Tile {
+  float x[kT][D + 4];  // (rows 16 bytes apart modulo the banks)
+  __device__ __forceinline__ f32x4 at(int r, int d) const { return *reinterpret_cast<const f32x4*>(&x[r][d]); }
+};
+struct alignas(16) Weights {
+  float x[kT][kT + 4];
+  __device__ __forceinline__ f32x4 at(int r, int s) const { return *reinterpret_cast<const f32x4*>(&x[r][s]); }
+};
+
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load4(const bf16* p) {
+  typedef bf16 b16x4 __attribute__((ext_vector_type(4)));
+  const b16x4 x = *reinterpret_cast<const b16x4*>(p);
+  return f32x4{to_f32(x[0]), to_f32(x[1]), to_f32(x[2]), to_f32(x[3])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
+__device__ __forceinline__ void store4(bf16* p, f32x4 x) {
+  typedef bf16 b16x4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<b16x4*>(p) = b16x4{from_f32<bf16>(x[0]), from_f32<bf16>(x[1]), from_f32<bf16>(x[2]), from_f32<bf16>(x[3])};
+}
+
+// The thread's part of 32 rows of a [N, H, D] tensor from `row` on, zero past `end`.
 template <typename T, int D>
-__device__ __forceinline__ void stage(float (&dst)[kT][D + 1], const T* __restrict__ src, int64_t row,
-                                      int64_t end, int32_t H, int32_t h) {
-  for (int i = threadIdx.x; i < kT * D; i += kThreads) {
-    const int r = i / D, d = i % D;
-    dst[r][d] = row + r < end ? to_f32(src[((row + r) * H + h) * D + d]) : 0.f;
+struct Stage {
+  f32x4 v[D / 32];
+  __device__ __forceinline__ void load(const T* __restrict__ src, int64_t row, int64_t end, int32_t H, int32_t h) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int at = (i * kThreads + threadIdx.x) * 4, r = at / D, d = at % D;
+      v[i] = row + r < end ? load4(src + ((row + r) * H + h) * D + d) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+  __device__ __forceinline__ void put(Tile<D>& t) const {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int at = (i * kThreads + threadIdx.x) * 4;
+      *reinterpret_cast<f32x4*>(&t.x[at / D][at % D]) = v[i];
+    }
+  }
+};
+
+// Products of row r of a with rows c + 8 j of b, added to x.
+template <int D>
+__device__ __forceinline__ void dots(float (&x)[kT / 8], const Tile<D>& a, int r, const Tile<D>& b, int c) {
+#pragma unroll 8
+  for (int d = 0; d < D; d += 4) {
+    const f32x4 y = a.at(r, d);
+#pragma unroll
+    for (int j = 0; j < kT / 8; ++j) {
+      const f32x4 z = b.at(c + 8 * j, d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[j] += y[e] * z[e];
+    }
+  }
+}
+
+// acc += sum over s in [first, end) of w[r][s] t[s][the thread's channels]; the
+// rows of t outside take no part, whatever they hold.
+template <int D>
+__device__ __forceinline__ void combine(f32x4 (&acc)[D / 32], const Weights& w, int r, const Tile<D>& t, int c, int first,
+                                        int end) {
+#pragma unroll 2
+  for (int s4 = first & ~3; s4 < end; s4 += 4) {
+    const f32x4 p = w.at(r, s4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (s4 + e < first || s4 + e >= end) continue;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) acc[j] += p[e] * t.at(s4 + e, 4 * (c + 8 * j));
+    }
   }
 }
 
@@ -52,7 +119,8 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
     T* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, int64_t slots) {
-  __shared__ float sq[kT][D + 1], sk[kT][D + 1], sv[kT][D + 1], sp[kT][kT + 1];
+  __shared__ Tile<D> sq, sk, sv;
+  __shared__ Weights sp;
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
     const int64_t j = b - slots * H, c = covered_tokens(cu, max_segs, N);
@@ -70,19 +138,22 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
   const int r = threadIdx.x / 8, c = threadIdx.x % 8;
   const int64_t row = int64_t(t.start) + r;
 
-  stage<T, D>(sq, q, t.start, t.e, H, h);
-  float m = -INFINITY, l = 0.f, acc[D / 8] = {};
+  Stage<T, D> gq, gk, gv;
+  gq.load(q, t.start, t.e, H, h);
+  gk.load(k, t.a, t.e, Hkv, hk);
+  gv.load(v, t.a, t.e, Hkv, hk);
+  gq.put(sq);
+  float m = -INFINITY, l = 0.f;
+  f32x4 acc[D / 32] = {};
   for (int64_t s0 = t.a; s0 < t.start + kT && s0 < t.e; s0 += kT) {
     __syncthreads();
-    stage<T, D>(sk, k, s0, t.e, Hkv, hk);
-    stage<T, D>(sv, v, s0, t.e, Hkv, hk);
+    gk.put(sk);
+    gv.put(sv);
     __syncthreads();
+    gk.load(k, s0 + kT, t.e, Hkv, hk);
+    gv.load(v, s0 + kT, t.e, Hkv, hk);
     float x[kT / 8] = {};
-    for (int d = 0; d < D; ++d) {
-      const float y = sq[r][d];
-#pragma unroll
-      for (int j = 0; j < kT / 8; ++j) x[j] += y * sk[c + 8 * j][d];
-    }
+    dots<D>(x, sq, r, sk, c);
     float mt = m;
 #pragma unroll
     for (int j = 0; j < kT / 8; ++j) {
@@ -98,49 +169,32 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     for (int j = 0; j < kT / 8; ++j) {
       const float p = expf(x[j] - ms);
       lt += p;
-      sp[r][c + 8 * j] = p;
+      sp.x[r][c + 8 * j] = p;
     }
     l = l * f + row_sum(lt);
     m = mt;
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) acc[j] *= f;
-    __syncthreads();
-    // only the keys the row attends to: a later key's value takes no part,
-    // whatever it holds
-    const int64_t last = row - s0 < kT - 1 ? row - s0 : kT - 1;
-    for (int s = 0; s <= last; ++s) {
-      const float p = sp[r][s];
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) acc[j] += p * sv[s][c + 8 * j];
-    }
+    for (int j = 0; j < D / 32; ++j) acc[j] *= f;
+    // (a row's weights are written and read by the same 8 lanes of a wave)
+    asm volatile("" ::: "memory");
+    combine<D>(acc, sp, r, sv, c, 0, row - s0 < kT ? int(row - s0) + 1 : kT);
   }
   if (row >= t.e) return;
   const float inv = 1.f / l;
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) o[(row * H + h) * D + c + 8 * j] = from_f32<T>(acc[j] * inv);
+  for (int j = 0; j < D / 32; ++j) store4(o + (row * H + h) * D + 4 * (c + 8 * j), acc[j] * inv);
   if (lse != nullptr && c == 0) lse[int64_t(h) * N + row] = m + logf(l);
-}
-
-// delta_t = do_t.o_t, fp32 [H, N].
-template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_delta(const T* __restrict__ o, const T* __restrict__ dout,
-                                                       float* __restrict__ delta, int64_t N, int32_t H) {
-  const int64_t i = int64_t(blockIdx.x) * (kThreads / 8) + threadIdx.x / 8;  // token * H + head
-  const int c = threadIdx.x % 8;
-  float x = 0.f;
-  if (i < N * H)
-    for (int d = c; d < D; d += 8) x += to_f32(o[i * D + d]) * to_f32(dout[i * D + d]);
-  x = row_sum(x);
-  if (i < N * H && c == 0) delta[(i % H) * N + i / H] = x;
 }
 
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_simple_dq(
-    const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ dout,
-    const float* __restrict__ lse, const float* __restrict__ delta, const int32_t* __restrict__ cu,
-    int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, T* __restrict__ dq,
+    const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ o,
+    const T* __restrict__ dout, const float* __restrict__ lse, float* __restrict__ delta,
+    const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
+    T* __restrict__ dq,
     int32_t* __restrict__ flags, int64_t slots) {
-  __shared__ float sq[kT][D + 1], sdo[kT][D + 1], sk[kT][D + 1], sv[kT][D + 1], sp[kT][kT + 1];
+  __shared__ Tile<D> sq, sdo, sk, sv;
+  __shared__ Weights sp;
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
     zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * sizeof(T), b - slots * H, kTail);
@@ -154,39 +208,47 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
   const int r = threadIdx.x / 8, c = threadIdx.x % 8;
   const int64_t row = int64_t(t.start) + r;
   const bool real = row < t.e;
-  const float ls = real ? lse[int64_t(h) * N + row] : INFINITY;
-  const float dl = real ? delta[int64_t(h) * N + row] : 0.f;
 
-  stage<T, D>(sq, q, t.start, t.e, H, h);
-  stage<T, D>(sdo, dout, t.start, t.e, H, h);
-  float acc[D / 8] = {};
+  Stage<T, D> gq, gdo, gk, gv;
+  gq.load(q, t.start, t.e, H, h);
+  gdo.load(dout, t.start, t.e, H, h);
+  gk.load(k, t.a, t.e, Hkv, hk);
+  gv.load(v, t.a, t.e, Hkv, hk);
+  const float ls = real ? lse[int64_t(h) * N + row] : INFINITY;
+  // delta_t, which the keys pass reads
+  float dl = 0.f;
+  if (real)
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const int64_t at = (row * H + h) * D + 4 * (c + 8 * j);
+      const f32x4 x = load4(o + at), y = load4(dout + at);
+      dl += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
+    }
+  dl = row_sum(dl);
+  if (real && c == 0) delta[int64_t(h) * N + row] = dl;
+  gq.put(sq);
+  gdo.put(sdo);
+  f32x4 acc[D / 32] = {};
   for (int64_t s0 = t.a; s0 < t.start + kT && s0 < t.e; s0 += kT) {
     __syncthreads();
-    stage<T, D>(sk, k, s0, t.e, Hkv, hk);
-    stage<T, D>(sv, v, s0, t.e, Hkv, hk);
+    gk.put(sk);
+    gv.put(sv);
     __syncthreads();
+    gk.load(k, s0 + kT, t.e, Hkv, hk);
+    gv.load(v, s0 + kT, t.e, Hkv, hk);
     float x[kT / 8] = {}, y[kT / 8] = {};
-    for (int d = 0; d < D; ++d) {
-#pragma unroll
-      for (int j = 0; j < kT / 8; ++j) {
-        x[j] += sq[r][d] * sk[c + 8 * j][d];
-        y[j] += sdo[r][d] * sv[c + 8 * j][d];
-      }
-    }
+    dots<D>(x, sq, r, sk, c);
+    dots<D>(y, sdo, r, sv, c);
 #pragma unroll
     for (int j = 0; j < kT / 8; ++j)
-      sp[r][c + 8 * j] = s0 + c + 8 * j <= row ? expf(x[j] * scale - ls) * (y[j] - dl) : 0.f;
-    __syncthreads();
-    const int64_t last = row - s0 < kT - 1 ? row - s0 : kT - 1;
-    for (int s = 0; s <= last; ++s) {
-      const float p = sp[r][s];
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) acc[j] += p * sk[s][c + 8 * j];
-    }
+      sp.x[r][c + 8 * j] = s0 + c + 8 * j <= row ? expf(x[j] * scale - ls) * (y[j] - dl) : 0.f;
+    // (a row's weights are written and read by the same 8 lanes of a wave)
+    asm volatile("" ::: "memory");
+    combine<D>(acc, sp, r, sk, c, 0, row - s0 < kT ? int(row - s0) + 1 : kT);
   }
   if (!real) return;
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) dq[(row * H + h) * D + c + 8 * j] = from_f32<T>(acc[j] * scale);
+  for (int j = 0; j < D / 32; ++j) store4(dq + (row * H + h) * D + 4 * (c + 8 * j), acc[j] * scale);
 }
 
 template <typename T, int D>
@@ -195,9 +257,9 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
     const float* __restrict__ lse, const float* __restrict__ delta, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, T* __restrict__ dk,
     T* __restrict__ dv, int64_t slots) {
-  // x of row r (a key) and column s (a query)
-  __shared__ float sq[kT][D + 1], sdo[kT][D + 1], sk[kT][D + 1], sv[kT][D + 1];
-  __shared__ float sp[kT][kT + 1], sd[kT][kT + 1], sl[kT], sdl[kT];
+  __shared__ Tile<D> sq, sdo, sk, sv;
+  __shared__ Weights sp, sd;  // of row r (a key) and column s (a query)
+  __shared__ float sl[kT], sdl[kT];
   const int64_t b = blockIdx.x;
   if (b >= slots * Hkv) {
     const int64_t j = b - slots * Hkv, cov = covered_tokens(cu, max_segs, N);
@@ -212,55 +274,60 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
   const int r = threadIdx.x / 8, c = threadIdx.x % 8;
   const int64_t row = int64_t(t.start) + r;
 
-  stage<T, D>(sk, k, t.start, t.e, Hkv, hk);
-  stage<T, D>(sv, v, t.start, t.e, Hkv, hk);
-  float ak[D / 8] = {}, av[D / 8] = {};
+  Stage<T, D> gq, gdo;
+  float gs = 0.f;
+  auto load = [&](int32_t h, int64_t s0) {
+    gq.load(q, s0, t.e, H, h);
+    gdo.load(dout, s0, t.e, H, h);
+    if (threadIdx.x < 2 * kT) {
+      const int64_t s = s0 + threadIdx.x % kT;
+      const bool first = threadIdx.x < kT;
+      gs = s < t.e ? (first ? lse : delta)[int64_t(h) * N + s] : (first ? INFINITY : 0.f);
+    }
+  };
+  {
+    Stage<T, D> gk, gv;
+    gk.load(k, t.start, t.e, Hkv, hk);
+    gv.load(v, t.start, t.e, Hkv, hk);
+    load(hk * rep, t.start);
+    gk.put(sk);
+    gv.put(sv);
+  }
+  f32x4 ak[D / 32] = {}, av[D / 32] = {};
   for (int32_t h = hk * rep; h < (hk + 1) * rep; ++h) {
     for (int64_t s0 = t.start; s0 < t.e; s0 += kT) {
       __syncthreads();
-      stage<T, D>(sq, q, s0, t.e, H, h);
-      stage<T, D>(sdo, dout, s0, t.e, H, h);
-      if (threadIdx.x < kT) {
-        const int64_t s = s0 + threadIdx.x;
-        sl[threadIdx.x] = s < t.e ? lse[int64_t(h) * N + s] : INFINITY;
-        sdl[threadIdx.x] = s < t.e ? delta[int64_t(h) * N + s] : 0.f;
-      }
+      gq.put(sq);
+      gdo.put(sdo);
+      if (threadIdx.x < 2 * kT) (threadIdx.x < kT ? sl : sdl)[threadIdx.x % kT] = gs;
       __syncthreads();
+      if (s0 + kT < t.e)
+        load(h, s0 + kT);
+      else if (h + 1 < (hk + 1) * rep)
+        load(h + 1, t.start);
       float x[kT / 8] = {}, y[kT / 8] = {};
-      for (int d = 0; d < D; ++d) {
-#pragma unroll
-        for (int j = 0; j < kT / 8; ++j) {
-          x[j] += sk[r][d] * sq[c + 8 * j][d];
-          y[j] += sv[r][d] * sdo[c + 8 * j][d];
-        }
-      }
+      dots<D>(x, sk, r, sq, c);
+      dots<D>(y, sv, r, sdo, c);
 #pragma unroll
       for (int j = 0; j < kT / 8; ++j) {
         const int s = c + 8 * j;
         const float p = expf(x[j] * scale - sl[s]);
-        sp[r][s] = p;
-        sd[r][s] = p * (y[j] - sdl[s]);
+        sp.x[r][s] = p;
+        sd.x[r][s] = p * (y[j] - sdl[s]);
       }
-      __syncthreads();
-      // only the queries that attend to the row
-      const int first = row > s0 ? int(row - s0) : 0;
-      const int end = t.e - s0 < kT ? int(t.e - s0) : kT;
-      for (int s = first; s < end; ++s) {
-        const float p = sp[r][s], d = sd[r][s];
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          av[j] += p * sdo[s][c + 8 * j];
-          ak[j] += d * sq[s][c + 8 * j];
-        }
-      }
+      // (a row's weights are written and read by the same 8 lanes of a wave)
+      asm volatile("" ::: "memory");
+      const int first = row > s0 ? int(row - s0) : 0, end = t.e - s0 < kT ? int(t.e - s0) : kT;
+      combine<D>(av, sp, r, sdo, c, first, end);
+      combine<D>(ak, sd, r, sq, c, first, end);
     }
   }
   if (row >= t.e) return;
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    const int64_t i = (row * Hkv + hk) * D + c + 8 * j;
-    dk[i] = from_f32<T>(ak[j] * scale);
-    dv[i] = from_f32<T>(av[j]);
+  for (int j = 0; j < D / 32; ++j) {
+    const int64_t i = (row * Hkv + hk) * D + 4 * (c + 8 * j);
+    store4(dk + i, ak[j] * scale);
+    store4(dv + i, av[j]);
   }
 }
 
@@ -277,12 +344,10 @@ template <typename T, int D>
 hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
   const T* dout = static_cast<const T*>(g.dout);
-  const int64_t slots = tile_slots(a.N, a.max_segs, kT), rows = kThreads / 8;
-  attn_delta<T, D><<<dim3(uint32_t((a.N * a.H + rows - 1) / rows)), dim3(kThreads), 0, stream>>>(
-      static_cast<const T*>(a.o), dout, g.stats, a.N, a.H);
+  const int64_t slots = tile_slots(a.N, a.max_segs, kT);
   attn_simple_dq<T, D><<<dim3(uint32_t(slots * a.H + kTail)), dim3(kThreads), 0, stream>>>(
-      q, k, v, dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dq),
-      a.flags, slots);
+      q, k, v, static_cast<const T*>(a.o), dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
+      static_cast<T*>(g.dq), a.flags, slots);
   attn_simple_dkv<T, D><<<dim3(uint32_t(slots * a.Hkv + kTail)), dim3(kThreads), 0, stream>>>(
       q, k, v, dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dk),
       static_cast<T*>(g.dv), slots);
@@ -292,8 +357,7 @@ hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 }  // namespace
 
 int64_t attn_simple_grid(int64_t N, int32_t max_segs, int32_t H) {
-  const int64_t tiles = tile_slots(N, max_segs, kT) * H + kTail, delta = (N * H + 31) / 32;
-  return tiles > delta ? tiles : delta;
+  return tile_slots(N, max_segs, kT) * H + kTail;
 }
 
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream) {
