@@ -207,7 +207,6 @@ __device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const 
     for (int s = 0; s < kParts; ++s)
 #pragma unroll
       for (int i = 0; i < TA; ++i) X[i] = mfma32(bT[i], part[s], X[i]);
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
