@@ -183,12 +183,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
   load_rows<D>(qf, q + at, have, qstride, rd);
   const int64_t row = int64_t(h) * N + q0 + rd.col;
   const float lse2 = rd.col < have ? lse[row] * kLog2e : 0.f;
-  if (rd.half == 0 && rd.col < have) {
-    stats[row] = lse2;
-    stats[int64_t(H) * N + row] = delta;
-  }
 
   const float c = scale * kLog2e;
+  float rest = 0.f;  // sum_s dS_ts
   f32x16 acc[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
@@ -212,14 +209,22 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float p = ex2(fmaf(s[i], c, -lse2));
-        const float x = p * (dp[i] - delta);
-        ds[i / 8][i % 8] = static_cast<bf16>(8 * (i / 4) + i % 4 <= last ? x : 0.f);
+        const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
+        rest += x;
+        ds[i / 8][i % 8] = static_cast<bf16>(x);
       }
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) acc[i] = mfma32(rd.channels(kt, i, 2 * j + u), ds[u], acc[i]);
     }
+  }
+  // The sum of a row's dS is 0; what it is short of that is delta's error, which
+  // stems from the rounding of o. The keys pass gets delta without it.
+  rest += other_half(rest);
+  if (rd.half == 0 && rd.col < have) {
+    stats[row] = lse2;
+    stats[int64_t(H) * N + row] = delta + rest;
   }
   __syncthreads();
   if (have > 0)
