@@ -1,5 +1,5 @@
-// Packed causal softmax attention with grouped heads, and its reverse pass, on
-// the vector units in fp32: fp32 tensors, and bf16 tensors at D = 32.
+// Packed causal softmax attention with grouped heads, and its reverse pass, in
+// fp32 on the matrix cores: fp32 tensors, and bf16 tensors at D = 32.
 //
 // Token t of a segment attends to the tokens s <= t of the same segment
 // ("Drill: Sequence Packing from scratch", The math: doc(s) = doc(t), s <= t):
@@ -11,13 +11,18 @@
 //   share the kv head, in a fixed order (no atomics).
 // Query head h reads kv head h / (Hq / Hkv).
 //
-// A work-group of 256 threads takes 32 rows (queries, or keys in the dk/dv
-// pass) of one head and walks the other side in tiles of 32 staged in LDS as
-// fp32, the next tile's values on their way in registers. Thread (r, c) =
-// (tid / 8, tid % 8) holds row r's scores of columns c + 8 j and its channels
-// 4 (c + 8 j) .. + 3; LDS is read 16 bytes at a time. The softmax runs in one pass
-// with a running maximum and sum. These shapes serve fp32 batches that models are
-// debugged on, where latency counts; the MFMA kernels serve bf16 at D = 64 and 128.
+// A work-group takes 32 rows (queries, or keys in the dk/dv pass) of one head. Its
+// four waves take the tiles of 32 of the other side in turn, each in LDS of its
+// own (no barrier inside a walk), and their sums are joined at the end, the
+// softmax's by their maxima: these shapes serve the small fp32 batches that models
+// are debugged on, where the length of a chain counts and not the rate.
+//
+// v_mfma_f32_32x32x2_f32: lane l holds row (or column) l % 32 and contraction slot
+// l / 32 of an operand, and the result's column l % 32, rows
+// 8 (i / 4) + 4 (l / 32) + i % 4. Over channels, step (p, e) pairs channels 8 p + e
+// and 8 p + 4 + e: a lane reads its operand 16 bytes at a time. Over rows of a
+// tile, step i pairs the rows of result register i of the two half-waves: a
+// product's result is the next one's operand as it stands.
 
 #include "segments.h"
 
@@ -25,19 +30,18 @@ namespace pkv {
 namespace {
 
 constexpr int kT = 32;        // tokens per tile, both sides
-constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
 constexpr int kTail = 64;     // work-groups that zero the rows no segment has
+constexpr float kFinite = 3.4028234663852886e38f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <int D>
-struct alignas(16) Tile {
-  float x[kT][D + 4];  // (rows 16 bytes apart modulo the banks)
+struct alignas(16) Tile {  // of one wave
+  float x[kT][D + 4];      // (rows 4 banks apart)
   __device__ __forceinline__ f32x4 at(int r, int d) const { return *reinterpret_cast<const f32x4*>(&x[r][d]); }
-};
-struct alignas(16) Weights {
-  float x[kT][kT + 4];
-  __device__ __forceinline__ f32x4 at(int r, int s) const { return *reinterpret_cast<const f32x4*>(&x[r][s]); }
 };
 
 __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -52,66 +56,88 @@ __device__ __forceinline__ void store4(bf16* p, f32x4 x) {
   *reinterpret_cast<b16x4*>(p) = b16x4{from_f32<bf16>(x[0]), from_f32<bf16>(x[1]), from_f32<bf16>(x[2]), from_f32<bf16>(x[3])};
 }
 
-// The thread's part of 32 rows of a [N, H, D] tensor from `row` on, zero past `end`.
+// The wave's LDS accesses are in order; nothing is moved across.
+__device__ __forceinline__ void wave_fence() { asm volatile("" ::: "memory"); }
+
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+__device__ __forceinline__ int row_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
+
+// 32 rows of a [N, H, D] tensor from `row` on into a wave's tile, zero past `end`;
+// whether the lane's values are all finite.
 template <typename T, int D>
-struct Stage {
-  f32x4 v[D / 32];
-  __device__ __forceinline__ void load(const T* __restrict__ src, int64_t row, int64_t end, int32_t H, int32_t h) {
+__device__ __forceinline__ bool fill(Tile<D>& t, const T* __restrict__ src, int64_t row, int64_t end, int32_t H, int32_t h,
+                                     int lane) {
+  f32x4 v[D / 8];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int at = (i * kThreads + threadIdx.x) * 4, r = at / D, d = at % D;
-      v[i] = row + r < end ? load4(src + ((row + r) * H + h) * D + d) : f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+  for (int i = 0; i < D / 8; ++i) {
+    const int at = (i * 64 + lane) * 4, r = at / D, d = at % D;
+    v[i] = row + r < end ? load4(src + ((row + r) * H + h) * D + d) : f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  __device__ __forceinline__ void put(Tile<D>& t) const {
+  bool ok = true;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int at = (i * kThreads + threadIdx.x) * 4;
-      *reinterpret_cast<f32x4*>(&t.x[at / D][at % D]) = v[i];
-    }
+  for (int i = 0; i < D / 8; ++i) {
+    const int at = (i * 64 + lane) * 4;
+    *reinterpret_cast<f32x4*>(&t.x[at / D][at % D]) = v[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ok &= fabsf(v[i][e]) <= kFinite;
   }
-};
-
-// Products of row r of a with rows c + 8 j of b, added to x.
-template <int D>
-__device__ __forceinline__ void dots(float (&x)[kT / 8], const Tile<D>& a, int r, const Tile<D>& b, int c) {
-#pragma unroll 8
-  for (int d = 0; d < D; d += 4) {
-    const f32x4 y = a.at(r, d);
-#pragma unroll
-    for (int j = 0; j < kT / 8; ++j) {
-      const f32x4 z = b.at(c + 8 * j, d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[j] += y[e] * z[e];
-    }
-  }
+  return ok;
 }
 
-// acc += sum over s in [first, end) of w[r][s] t[s][the thread's channels]; the
-// rows of t outside take no part, whatever they hold.
-template <int D>
-__device__ __forceinline__ void combine(f32x4 (&acc)[D / 32], const Weights& w, int r, const Tile<D>& t, int c, int first,
-                                        int end) {
-#pragma unroll 2
-  for (int s4 = first & ~3; s4 < end; s4 += 4) {
-    const f32x4 p = w.at(r, s4);
+// The lane's part of row `row` (zero if not real) as an operand.
+template <typename T, int D>
+__device__ __forceinline__ void load_row(f32x4 (&f)[D / 8], const T* __restrict__ src, int64_t row, bool real, int32_t H,
+                                         int32_t h, int half) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (s4 + e < first || s4 + e >= end) continue;
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) acc[j] += p[e] * t.at(s4 + e, 4 * (c + 8 * j));
-    }
-  }
+  for (int p = 0; p < D / 8; ++p)
+    f[p] = real ? load4(src + (row * H + h) * D + 8 * p + 4 * half) : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// Over the 8 threads of a row.
-__device__ __forceinline__ float row_max(float x) {
-  for (int d = 4; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 8));
+// Products of the tile's rows with the operand f.
+template <int D>
+__device__ __forceinline__ f32x16 over_channels(const Tile<D>& t, const f32x4 (&f)[D / 8], int col, int half) {
+  f32x16 x = {};
+#pragma unroll
+  for (int p = 0; p < D / 8; ++p) {
+    const f32x4 a = t.at(col, 8 * p + 4 * half);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], f[p][e], x, 0, 0, 0);
+  }
   return x;
 }
-__device__ __forceinline__ float row_sum(float x) {
-  for (int d = 4; d; d >>= 1) x += __shfl_xor(x, d, 8);
-  return x;
+
+// acc[channel][column of w] += sum over the tile's rows of t[row][channel] w[row].
+template <int D>
+__device__ __forceinline__ void over_rows(f32x16 (&acc)[D / 32], const Tile<D>& t, const f32x16& w, int col, int half) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      acc[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(t.x[row_of(i, half)][32 * j + col], w[i], acc[j], 0, 0, 0);
+}
+
+// A wave's sums into its tile, a row per column of the sums.
+template <int D>
+__device__ __forceinline__ void put_sums(Tile<D>& t, const f32x16 (&acc)[D / 32], int col, int half) {
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<f32x4*>(&t.x[col][32 * j + row_of(i, half)]) =
+          f32x4{acc[j][i], acc[j][i + 1], acc[j][i + 2], acc[j][i + 3]};
+}
+
+// The sum of the waves' tiles (tile 2 w of wave w) times f, rows [0, rows), to out.
+template <typename T, int D>
+__device__ __forceinline__ void store_sums(const Tile<D>* t, float f, T* out, int64_t stride, int32_t rows) {
+  for (int i = threadIdx.x; i < kT * D / 4; i += kThreads) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    if (r >= rows) continue;
+    f32x4 x = t[0].at(r, d);
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) x += t[2 * w].at(r, d);
+    store4(out + r * stride + d, x * f);
+  }
 }
 
 template <typename T, int D>
@@ -119,8 +145,8 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
     T* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, int64_t slots) {
-  __shared__ Tile<D> sq, sk, sv;
-  __shared__ Weights sp;
+  __shared__ Tile<D> tiles[2 * kWaves];
+  __shared__ float sm[kWaves][kT], sl[kWaves][kT];
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
     const int64_t j = b - slots * H, c = covered_tokens(cu, max_segs, N);
@@ -135,55 +161,98 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
   SegTile t;
   if (!find_tile(cu, max_segs, N, kT, int32_t(b / H), t)) return;
   const int32_t hk = h / (H / Hkv);
-  const int r = threadIdx.x / 8, c = threadIdx.x % 8;
-  const int64_t row = int64_t(t.start) + r;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+  const int64_t row = int64_t(t.start) + col;
+  Tile<D>&tk = tiles[2 * wave], &tv = tiles[2 * wave + 1];
 
-  Stage<T, D> gq, gk, gv;
-  gq.load(q, t.start, t.e, H, h);
-  gk.load(k, t.a, t.e, Hkv, hk);
-  gv.load(v, t.a, t.e, Hkv, hk);
-  gq.put(sq);
+  f32x4 qf[D / 8];
+  load_row<T, D>(qf, q, row, row < t.e, H, h, half);
   float m = -INFINITY, l = 0.f;
-  f32x4 acc[D / 32] = {};
-  for (int64_t s0 = t.a; s0 < t.start + kT && s0 < t.e; s0 += kT) {
-    __syncthreads();
-    gk.put(sk);
-    gv.put(sv);
-    __syncthreads();
-    gk.load(k, s0 + kT, t.e, Hkv, hk);
-    gv.load(v, s0 + kT, t.e, Hkv, hk);
-    float x[kT / 8] = {};
-    dots<D>(x, sq, r, sk, c);
+  f32x16 acc[D / 32] = {};
+  for (int64_t s0 = t.a + wave * kT; s0 <= t.start; s0 += kWaves * kT) {
+    wave_fence();
+    fill<T, D>(tk, k, s0, t.e, Hkv, hk, lane);
+    const bool ok = fill<T, D>(tv, v, s0, t.e, Hkv, hk, lane);
+    wave_fence();
+    f32x16 x = over_channels<D>(tk, qf, col, half);
     float mt = m;
 #pragma unroll
-    for (int j = 0; j < kT / 8; ++j) {
-      x[j] = s0 + c + 8 * j <= row ? x[j] * scale : -INFINITY;
-      mt = fmaxf(mt, x[j]);
+    for (int i = 0; i < 16; ++i) {
+      x[i] = s0 + row_of(i, half) <= row ? x[i] * scale : -INFINITY;
+      mt = fmaxf(mt, x[i]);
     }
-    mt = row_max(mt);
+    mt = fmaxf(mt, other_half(mt));
     // a row whose scores so far are all -inf has no maximum to subtract
     const float ms = mt == -INFINITY ? 0.f : mt;
     const float f = expf(m - ms);
-    float lt = 0.f;
-#pragma unroll
-    for (int j = 0; j < kT / 8; ++j) {
-      const float p = expf(x[j] - ms);
-      lt += p;
-      sp.x[r][c + 8 * j] = p;
-    }
-    l = l * f + row_sum(lt);
     m = mt;
+    l *= f;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) acc[j] *= f;
-    // (a row's weights are written and read by the same 8 lanes of a wave)
-    asm volatile("" ::: "memory");
-    combine<D>(acc, sp, r, sv, c, 0, row - s0 < kT ? int(row - s0) + 1 : kT);
+    for (int i = 0; i < 16; ++i) {
+      x[i] = expf(x[i] - ms);
+      l += x[i];
+    }
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[j][i] *= f;
+    if (s0 < t.start || __all(ok)) {
+      over_rows<D>(acc, tv, x, col, half);
+    } else {
+      // The tile on the diagonal holds a value that is not finite: a weight of 0
+      // times it is NaN, so such values are 0 in the product and are added for the
+      // rows that attend to them alone. The other rows keep their bits.
+      wave_fence();
+      for (int i = lane; i < kT * D; i += 64) {
+        const float y = tv.x[i / D][i % D];
+        tk.x[i / D][i % D] = fabsf(y) <= kFinite ? y : 0.f;
+      }
+      wave_fence();
+      over_rows<D>(acc, tk, x, col, half);
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) tk.x[row_of(i, half)][col] = x[i];
+      wave_fence();
+      for (int s = 0; s < kT && s0 + s <= row && s0 + s < t.e; ++s) {
+        const float p = tk.x[s][col];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float y = tv.x[s][32 * j + row_of(i, half)];
+            if (!(fabsf(y) <= kFinite)) acc[j][i] += p * y;
+          }
+      }
+    }
   }
-  if (row >= t.e) return;
-  const float inv = 1.f / l;
+  l += other_half(l);
+  wave_fence();
+  put_sums<D>(tk, acc, col, half);
+  if (half == 0) {
+    sm[wave][col] = m;
+    sl[wave][col] = l;
+  }
+  __syncthreads();
+  const int32_t rows = t.e - t.start;
+  for (int i = threadIdx.x; i < kT * D / 4; i += kThreads) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    if (r >= rows) continue;
+    float top = sm[0][r];
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) store4(o + (row * H + h) * D + 4 * (c + 8 * j), acc[j] * inv);
-  if (lse != nullptr && c == 0) lse[int64_t(h) * N + row] = m + logf(l);
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][r]);
+    const float ms = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (t.a + w * kT > t.start) continue;  // (had no tile)
+      const float f = expf(sm[w][r] - ms);
+      sum += f * sl[w][r];
+      x += f * tiles[2 * w].at(r, d);
+    }
+    store4(o + ((int64_t(t.start) + r) * H + h) * D + d, x * (1.f / sum));
+    if (lse != nullptr && d == 0) lse[int64_t(h) * N + t.start + r] = top + logf(sum);
+  }
 }
 
 template <typename T, int D>
@@ -191,10 +260,8 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ o,
     const T* __restrict__ dout, const float* __restrict__ lse, float* __restrict__ delta,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
-    T* __restrict__ dq,
-    int32_t* __restrict__ flags, int64_t slots) {
-  __shared__ Tile<D> sq, sdo, sk, sv;
-  __shared__ Weights sp;
+    T* __restrict__ dq, int32_t* __restrict__ flags, int64_t slots) {
+  __shared__ Tile<D> tiles[2 * kWaves];
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
     zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * sizeof(T), b - slots * H, kTail);
@@ -205,50 +272,40 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
   SegTile t;
   if (!find_tile(cu, max_segs, N, kT, int32_t(b / H), t)) return;
   const int32_t hk = h / (H / Hkv);
-  const int r = threadIdx.x / 8, c = threadIdx.x % 8;
-  const int64_t row = int64_t(t.start) + r;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+  const int64_t row = int64_t(t.start) + col;
   const bool real = row < t.e;
+  Tile<D>&tk = tiles[2 * wave], &tv = tiles[2 * wave + 1];
 
-  Stage<T, D> gq, gdo, gk, gv;
-  gq.load(q, t.start, t.e, H, h);
-  gdo.load(dout, t.start, t.e, H, h);
-  gk.load(k, t.a, t.e, Hkv, hk);
-  gv.load(v, t.a, t.e, Hkv, hk);
-  const float ls = real ? lse[int64_t(h) * N + row] : INFINITY;
-  // delta_t, which the keys pass reads
+  f32x4 qf[D / 8], df[D / 8];
+  load_row<T, D>(qf, o, row, real, H, h, half);
+  load_row<T, D>(df, dout, row, real, H, h, half);
   float dl = 0.f;
-  if (real)
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const int64_t at = (row * H + h) * D + 4 * (c + 8 * j);
-      const f32x4 x = load4(o + at), y = load4(dout + at);
-      dl += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-    }
-  dl = row_sum(dl);
-  if (real && c == 0) delta[int64_t(h) * N + row] = dl;
-  gq.put(sq);
-  gdo.put(sdo);
-  f32x4 acc[D / 32] = {};
-  for (int64_t s0 = t.a; s0 < t.start + kT && s0 < t.e; s0 += kT) {
-    __syncthreads();
-    gk.put(sk);
-    gv.put(sv);
-    __syncthreads();
-    gk.load(k, s0 + kT, t.e, Hkv, hk);
-    gv.load(v, s0 + kT, t.e, Hkv, hk);
-    float x[kT / 8] = {}, y[kT / 8] = {};
-    dots<D>(x, sq, r, sk, c);
-    dots<D>(y, sdo, r, sv, c);
+  for (int p = 0; p < D / 8; ++p)
 #pragma unroll
-    for (int j = 0; j < kT / 8; ++j)
-      sp.x[r][c + 8 * j] = s0 + c + 8 * j <= row ? expf(x[j] * scale - ls) * (y[j] - dl) : 0.f;
-    // (a row's weights are written and read by the same 8 lanes of a wave)
-    asm volatile("" ::: "memory");
-    combine<D>(acc, sp, r, sk, c, 0, row - s0 < kT ? int(row - s0) + 1 : kT);
+    for (int e = 0; e < 4; ++e) dl += qf[p][e] * df[p][e];
+  dl += other_half(dl);
+  load_row<T, D>(qf, q, row, real, H, h, half);
+  const float ls = real ? lse[int64_t(h) * N + row] : INFINITY;
+  if (real && wave == 0 && half == 0) delta[int64_t(h) * N + row] = dl;  // for the keys pass
+  f32x16 acc[D / 32] = {};
+  for (int64_t s0 = t.a + wave * kT; s0 <= t.start; s0 += kWaves * kT) {
+    wave_fence();
+    fill<T, D>(tk, k, s0, t.e, Hkv, hk, lane);
+    fill<T, D>(tv, v, s0, t.e, Hkv, hk, lane);
+    wave_fence();
+    f32x16 x = over_channels<D>(tk, qf, col, half);
+    const f32x16 y = over_channels<D>(tv, df, col, half);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      x[i] = s0 + row_of(i, half) <= row ? expf(x[i] * scale - ls) * (y[i] - dl) : 0.f;
+    over_rows<D>(acc, tk, x, col, half);
   }
-  if (!real) return;
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) store4(dq + (row * H + h) * D + 4 * (c + 8 * j), acc[j] * scale);
+  wave_fence();
+  put_sums<D>(tk, acc, col, half);
+  __syncthreads();
+  store_sums<T, D>(tiles, scale, dq + (int64_t(t.start) * H + h) * D, int64_t(H) * D, t.e - t.start);
 }
 
 template <typename T, int D>
@@ -257,9 +314,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
     const float* __restrict__ lse, const float* __restrict__ delta, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, T* __restrict__ dk,
     T* __restrict__ dv, int64_t slots) {
-  __shared__ Tile<D> sq, sdo, sk, sv;
-  __shared__ Weights sp, sd;  // of row r (a key) and column s (a query)
-  __shared__ float sl[kT], sdl[kT];
+  __shared__ Tile<D> tiles[2 * kWaves];
   const int64_t b = blockIdx.x;
   if (b >= slots * Hkv) {
     const int64_t j = b - slots * Hkv, cov = covered_tokens(cu, max_segs, N);
@@ -271,64 +326,50 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
   SegTile t;
   if (!find_tile(cu, max_segs, N, kT, int32_t(b / Hkv), t)) return;
   const int32_t rep = H / Hkv;
-  const int r = threadIdx.x / 8, c = threadIdx.x % 8;
-  const int64_t row = int64_t(t.start) + r;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+  const int64_t row = int64_t(t.start) + col;  // the lane's key
+  Tile<D>&tq = tiles[2 * wave], &to = tiles[2 * wave + 1];
 
-  Stage<T, D> gq, gdo;
-  float gs = 0.f;
-  auto load = [&](int32_t h, int64_t s0) {
-    gq.load(q, s0, t.e, H, h);
-    gdo.load(dout, s0, t.e, H, h);
-    if (threadIdx.x < 2 * kT) {
-      const int64_t s = s0 + threadIdx.x % kT;
-      const bool first = threadIdx.x < kT;
-      gs = s < t.e ? (first ? lse : delta)[int64_t(h) * N + s] : (first ? INFINITY : 0.f);
-    }
-  };
-  {
-    Stage<T, D> gk, gv;
-    gk.load(k, t.start, t.e, Hkv, hk);
-    gv.load(v, t.start, t.e, Hkv, hk);
-    load(hk * rep, t.start);
-    gk.put(sk);
-    gv.put(sv);
-  }
-  f32x4 ak[D / 32] = {}, av[D / 32] = {};
-  for (int32_t h = hk * rep; h < (hk + 1) * rep; ++h) {
-    for (int64_t s0 = t.start; s0 < t.e; s0 += kT) {
-      __syncthreads();
-      gq.put(sq);
-      gdo.put(sdo);
-      if (threadIdx.x < 2 * kT) (threadIdx.x < kT ? sl : sdl)[threadIdx.x % kT] = gs;
-      __syncthreads();
-      if (s0 + kT < t.e)
-        load(h, s0 + kT);
-      else if (h + 1 < (hk + 1) * rep)
-        load(h + 1, t.start);
-      float x[kT / 8] = {}, y[kT / 8] = {};
-      dots<D>(x, sk, r, sq, c);
-      dots<D>(y, sv, r, sdo, c);
+  f32x4 kf[D / 8], vf[D / 8];
+  load_row<T, D>(kf, k, row, row < t.e, Hkv, hk, half);
+  load_row<T, D>(vf, v, row, row < t.e, Hkv, hk, half);
+  f32x16 ak[D / 32] = {}, av[D / 32] = {};
+  // (query head, query tile) pairs, dealt to the waves in turn
+  const int64_t per = (int64_t(t.e) - t.start + kT - 1) / kT;
+  for (int64_t it = wave; it < per * rep; it += kWaves) {
+    const int32_t h = hk * rep + int32_t(it / per);
+    const int64_t s0 = t.start + it % per * kT;
+    wave_fence();
+    fill<T, D>(tq, q, s0, t.e, H, h, lane);
+    fill<T, D>(to, dout, s0, t.e, H, h, lane);
+    float ls[16], dl[16];
 #pragma unroll
-      for (int j = 0; j < kT / 8; ++j) {
-        const int s = c + 8 * j;
-        const float p = expf(x[j] * scale - sl[s]);
-        sp.x[r][s] = p;
-        sd.x[r][s] = p * (y[j] - sdl[s]);
-      }
-      // (a row's weights are written and read by the same 8 lanes of a wave)
-      asm volatile("" ::: "memory");
-      const int first = row > s0 ? int(row - s0) : 0, end = t.e - s0 < kT ? int(t.e - s0) : kT;
-      combine<D>(av, sp, r, sdo, c, first, end);
-      combine<D>(ak, sd, r, sq, c, first, end);
+    for (int i = 0; i < 16; ++i) {
+      const int64_t s = s0 + row_of(i, half);
+      ls[i] = s < t.e ? lse[int64_t(h) * N + s] : INFINITY;
+      dl[i] = s < t.e ? delta[int64_t(h) * N + s] : 0.f;
     }
-  }
-  if (row >= t.e) return;
+    wave_fence();
+    f32x16 x = over_channels<D>(tq, kf, col, half);
+    f32x16 y = over_channels<D>(to, vf, col, half);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) {
-    const int64_t i = (row * Hkv + hk) * D + 4 * (c + 8 * j);
-    store4(dk + i, ak[j] * scale);
-    store4(dv + i, av[j]);
+    for (int i = 0; i < 16; ++i) {
+      const int64_t s = s0 + row_of(i, half);
+      x[i] = s >= row && s < t.e ? expf(x[i] * scale - ls[i]) : 0.f;
+      y[i] = x[i] * (y[i] - dl[i]);
+    }
+    over_rows<D>(av, to, x, col, half);
+    over_rows<D>(ak, tq, y, col, half);
   }
+  const int64_t to_ = (int64_t(t.start) * Hkv + hk) * D;
+  wave_fence();
+  put_sums<D>(tq, ak, col, half);
+  __syncthreads();
+  store_sums<T, D>(tiles, scale, dk + to_, int64_t(Hkv) * D, t.e - t.start);
+  __syncthreads();
+  put_sums<D>(tq, av, col, half);
+  __syncthreads();
+  store_sums<T, D>(tiles, 1.f, dv + to_, int64_t(Hkv) * D, t.e - t.start);
 }
 
 template <typename T, int D>
