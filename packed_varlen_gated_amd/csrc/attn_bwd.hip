@@ -34,7 +34,6 @@ namespace {
 constexpr int kB = 128;   // queries, or keys, that a work-group owns
 constexpr int kT = 64;    // tokens of a tile of the other side
 constexpr int kThreads = 256;
-constexpr int kTail = 256;
 
 template <int D>
 struct Lds {
@@ -135,8 +134,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
   const int64_t b = blockIdx.x;
   const int64_t blocks = slot_blocks(grid, H);
   if (b >= blocks) {
-    const int64_t j = b - blocks;
-    zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * 2, j, kTail);
+    const int64_t j = b - blocks, groups = gridDim.x - blocks;
+    zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * 2, j, groups);
     if (j == 0) check_cu(cu, max_segs, N, flags);
     return;
   }
@@ -257,9 +256,9 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   const int64_t b = blockIdx.x;
   const int64_t blocks = slot_blocks(grid, Hkv);
   if (b >= blocks) {
-    const int64_t j = b - blocks, cov = covered_tokens(cu, max_segs, N);
-    zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, kTail);
-    zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, kTail);
+    const int64_t j = b - blocks, groups = gridDim.x - blocks, cov = covered_tokens(cu, max_segs, N);
+    zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, groups);
+    zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, groups);
     return;
   }
   const int32_t rep = H / Hkv;
@@ -420,7 +419,7 @@ template <int D, int kQ>
 void keys_pass(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
   if (kQ > 1) grid.near = grid.slots;  // (small calls: a work-group per head)
-  attn_dkv_kernel<D, kQ><<<dim3(uint32_t(slot_blocks(grid, a.Hkv) + kTail)), dim3(DkvShape<kQ>::NT), 0, stream>>>(
+  attn_dkv_kernel<D, kQ><<<dim3(uint32_t(slot_blocks(grid, a.Hkv) + tail_groups(a.N * a.Hkv * D * 2))), dim3(DkvShape<kQ>::NT), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
       static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), grid);
@@ -429,7 +428,7 @@ void keys_pass(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 template <int D>
 hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
-  attn_dq_kernel<D><<<dim3(uint32_t(slot_blocks(grid, a.H) + kTail)), dim3(kThreads), 0, stream>>>(
+  attn_dq_kernel<D><<<dim3(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2))), dim3(kThreads), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
       a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, grid);

@@ -42,7 +42,6 @@ namespace {
 constexpr int kBM = 128;  // queries per work-group
 constexpr int kBN = 64;   // keys per tile
 constexpr int kThreads = 256;
-constexpr int kTail = 256;        // work-groups that zero the rows no segment has
 constexpr float kGrow = 8.f;      // log2 of what a row's maximum may grow by before O is rescaled
 
 template <int D>
@@ -70,10 +69,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
   const int64_t b = blockIdx.x;
   const int64_t blocks = slot_blocks(grid, H);
   if (b >= blocks) {
-    const int64_t j = b - blocks, c = covered_tokens(cu, max_segs, N);
-    zero_tail(o, c, N, int64_t(H) * D * 2, j, kTail);
+    const int64_t j = b - blocks, groups = gridDim.x - blocks, c = covered_tokens(cu, max_segs, N);
+    zero_tail(o, c, N, int64_t(H) * D * 2, j, groups);
     if (lse != nullptr)
-      for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += int64_t(kTail) * kThreads)
+      for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += groups * kThreads)
         lse[(i / (N - c)) * N + c + i % (N - c)] = -INFINITY;
     if (j == 0) check_cu(cu, max_segs, N, flags);
     return;
@@ -307,7 +306,7 @@ bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
   const SlotGrid g = slot_grid(a.N, a.max_segs, kBM);
   const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
-  (a.D == 64 ? attn_fwd_kernel<64> : attn_fwd_kernel<128>)<<<dim3(uint32_t(slot_blocks(g, a.H) + kTail)),
+  (a.D == 64 ? attn_fwd_kernel<64> : attn_fwd_kernel<128>)<<<dim3(uint32_t(slot_blocks(g, a.H) + tail_groups(a.N * a.H * a.D * 2))),
                                                              dim3(kThreads), 0, stream>>>(
       q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
   return hipGetLastError();

@@ -32,7 +32,6 @@ namespace {
 constexpr int kT = 32;        // tokens per tile, both sides
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kTail = 64;     // work-groups that zero the rows no segment has
 constexpr float kFinite = 3.4028234663852886e38f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -149,10 +148,10 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
   __shared__ float sm[kWaves][kT], sl[kWaves][kT];
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
-    const int64_t j = b - slots * H, c = covered_tokens(cu, max_segs, N);
-    zero_tail(o, c, N, int64_t(H) * D * sizeof(T), j, kTail);
+    const int64_t j = b - slots * H, groups = gridDim.x - slots * H, c = covered_tokens(cu, max_segs, N);
+    zero_tail(o, c, N, int64_t(H) * D * sizeof(T), j, groups);
     if (lse != nullptr)
-      for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += int64_t(kTail) * kThreads)
+      for (int64_t i = j * kThreads + threadIdx.x; i < (N - c) * H; i += groups * kThreads)
         lse[(i / (N - c)) * N + c + i % (N - c)] = -INFINITY;
     if (j == 0) check_cu(cu, max_segs, N, flags);
     return;
@@ -264,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
   __shared__ Tile<D> tiles[2 * kWaves];
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
-    zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * sizeof(T), b - slots * H, kTail);
+    zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * sizeof(T), b - slots * H, gridDim.x - slots * H);
     if (b == slots * H) check_cu(cu, max_segs, N, flags);
     return;
   }
@@ -317,9 +316,9 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
   __shared__ Tile<D> tiles[2 * kWaves];
   const int64_t b = blockIdx.x;
   if (b >= slots * Hkv) {
-    const int64_t j = b - slots * Hkv, cov = covered_tokens(cu, max_segs, N);
-    zero_tail(dk, cov, N, int64_t(Hkv) * D * sizeof(T), j, kTail);
-    zero_tail(dv, cov, N, int64_t(Hkv) * D * sizeof(T), j, kTail);
+    const int64_t j = b - slots * Hkv, groups = gridDim.x - slots * Hkv, cov = covered_tokens(cu, max_segs, N);
+    zero_tail(dk, cov, N, int64_t(Hkv) * D * sizeof(T), j, groups);
+    zero_tail(dv, cov, N, int64_t(Hkv) * D * sizeof(T), j, groups);
     return;
   }
   const int32_t hk = int32_t(b % Hkv);
@@ -374,7 +373,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
 
 template <typename T, int D>
 hipError_t fwd(const AttnArgs& a, hipStream_t stream) {
-  const int64_t slots = tile_slots(a.N, a.max_segs, kT), grid = slots * a.H + kTail;
+  const int64_t slots = tile_slots(a.N, a.max_segs, kT), grid = slots * a.H + tail_groups(a.N * a.H * D * sizeof(T));
   attn_simple_fwd<T, D><<<dim3(uint32_t(grid)), dim3(kThreads), 0, stream>>>(
       static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.cu, a.max_segs,
       a.N, a.H, a.Hkv, a.scale, static_cast<T*>(a.o), a.lse, a.flags, slots);
@@ -386,10 +385,10 @@ hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
   const T* dout = static_cast<const T*>(g.dout);
   const int64_t slots = tile_slots(a.N, a.max_segs, kT);
-  attn_simple_dq<T, D><<<dim3(uint32_t(slots * a.H + kTail)), dim3(kThreads), 0, stream>>>(
+  attn_simple_dq<T, D><<<dim3(uint32_t(slots * a.H + tail_groups(a.N * a.H * D * sizeof(T)))), dim3(kThreads), 0, stream>>>(
       q, k, v, static_cast<const T*>(a.o), dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
       static_cast<T*>(g.dq), a.flags, slots);
-  attn_simple_dkv<T, D><<<dim3(uint32_t(slots * a.Hkv + kTail)), dim3(kThreads), 0, stream>>>(
+  attn_simple_dkv<T, D><<<dim3(uint32_t(slots * a.Hkv + tail_groups(a.N * a.Hkv * D * sizeof(T)))), dim3(kThreads), 0, stream>>>(
       q, k, v, dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dk),
       static_cast<T*>(g.dv), slots);
   return hipGetLastError();
@@ -398,7 +397,7 @@ hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 }  // namespace
 
 int64_t attn_simple_grid(int64_t N, int32_t max_segs, int32_t H) {
-  return tile_slots(N, max_segs, kT) * H + kTail;
+  return tile_slots(N, max_segs, kT) * H + 256;
 }
 
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream) {

@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kC = 32;       // tokens per chunk of a walk
 constexpr int kCState = 64;  // ... of a state walk
-constexpr int kTail = 256;  // work-groups for the rows no segment has and empty slots
 
 template <int D>
 struct Rows {  // an LDS tile of a chunk's rows of D channels
@@ -304,15 +303,15 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, kPair ? 2 : 3) void linear_wa
 
   const int64_t blk = blockIdx.x;
   if (blk >= slot_blocks(x.grid, x.H)) {
-    const int64_t j = blk - slot_blocks(x.grid, x.H);
+    const int64_t j = blk - slot_blocks(x.grid, x.H), groups = gridDim.x - slot_blocks(x.grid, x.H);
     const int64_t cov = covered_tokens(x.cu, x.max_segs, x.N);
 #pragma unroll
-    for (int i = 0; i < (kPair ? 2 : 1); ++i) zero_tail(x.r[i].out, cov, x.N, int64_t(x.H) * DB * 2, j, kTail);
+    for (int i = 0; i < (kPair ? 2 : 1); ++i) zero_tail(x.r[i].out, cov, x.N, int64_t(x.H) * DB * 2, j, groups);
     if (j == 0) check_cu(x.cu, x.max_segs, x.N, x.flags);
     if (x.r[0].fin != nullptr && x.cu != nullptr) {
       // empty slots keep their initial state (or 0)
       const int64_t n = int64_t(x.H) * DA * DB / 4;
-      for (int64_t s = j; s < x.max_segs; s += kTail) {
+      for (int64_t s = j; s < x.max_segs; s += groups) {
         if (x.cu[s] != x.cu[s + 1]) continue;
         f32x4* to = reinterpret_cast<f32x4*>(x.r[0].fin) + s * n;
         const f32x4* from = x.r[0].init ? reinterpret_cast<const f32x4*>(x.r[0].init) + s * n : nullptr;
@@ -581,8 +580,9 @@ void states(const WalkArgs& x, hipStream_t stream) {
 
 template <int DA, int DB, bool kRev, int kParts, bool kPair>
 void walk(const WalkArgs& x, hipStream_t stream) {
+  const int64_t tail = x.N * x.H * DB * 2 + (x.r[0].fin ? int64_t(x.max_segs) * x.H * DA * DB * 4 : 0);
   linear_walk_kernel<DA, DB, kRev, kParts, kPair>
-      <<<dim3(uint32_t(slot_blocks(x.grid, x.H) + kTail)), dim3((kPair ? 4 : 2) * DB), 0, stream>>>(x);
+      <<<dim3(uint32_t(slot_blocks(x.grid, x.H) + tail_groups(tail))), dim3((kPair ? 4 : 2) * DB), 0, stream>>>(x);
 }
 
 WalkArgs common(const LinearArgs& y) {
@@ -655,7 +655,7 @@ size_t linear_chunk_workspace_bytes(int64_t N, int32_t H, int32_t Dk, int32_t Dv
 }
 
 int64_t linear_chunk_grid(int64_t N, int32_t max_segs, int32_t H) {
-  return tile_slots(N, max_segs, run_tokens(N, H)) * H + kTail;
+  return tile_slots(N, max_segs, run_tokens(N, H)) * H + 256;
 }
 
 hipError_t launch_linear_chunk(const LinearArgs& x, hipStream_t s) {

@@ -123,6 +123,11 @@ __device__ __forceinline__ int64_t covered_tokens(const int32_t* __restrict__ cu
   return c < 0 ? 0 : (c > N ? N : c);
 }
 
+// Work-groups behind those of the slots, which zero the rows that no segment has
+// (and copy the states of empty slots): one per 64 KiB that there may be to write,
+// at most 256, so that a small call does not wait for them.
+inline int64_t tail_groups(int64_t bytes) { return bytes >> 16 < 255 ? (bytes >> 16) + 1 : 256; }
+
 // One work-group's check of the whole cu: sets kFlagBadCuSeqlens.
 __device__ __forceinline__ void check_cu(const int32_t* __restrict__ cu, int32_t max_segs, int64_t N,
                                          int32_t* __restrict__ flags) {
