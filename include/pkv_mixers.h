@@ -56,9 +56,9 @@ extern "C" {
  * the weights are rounded to bf16 for the product with v.
  * Supported: D in {32, 64, 128}. Errors: PKV_ERR_INVALID_ARGUMENT for a NULL
  * tensor, N < 1, N > INT32_MAX, Hq or Hkv < 1 or > 65536, Hq not a multiple of
- * Hkv, max_segs < 1 (with cu_seqlens), more than 2^31 - 1 work-groups
- * ((N / 32 + max_segs) Hq), a misaligned or overlapping tensor, a scale that is
- * not finite; PKV_ERR_UNSUPPORTED for another D or dtype.
+ * Hkv, max_segs < 1 (with cu_seqlens), (N / 32 + max_segs) Hq >= 2^23, a
+ * misaligned or overlapping tensor, a scale that is not finite;
+ * PKV_ERR_UNSUPPORTED for another D or dtype.
  */
 pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
                            int32_t max_segs, int64_t N, int32_t Hq, int32_t Hkv, int32_t D,
@@ -96,17 +96,17 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
  * empty slot).
  *
  * q, k   [1, N, H, Dk]; v, o [1, N, H, Dv], in `dtype`.
- * g      float32 [H]: log decays (<= 0). A constant of the layer: the reverse
+ * g      float32 [H]: log decays (<= 0; -inf keeps nothing). A constant of the layer: the reverse
  *        pass has no gradient for it. Above 0 the state grows; up to
  *        64 g = 80 ln 2 the weights inside a chunk stay finite.
  * initial_state, final_state  float32 [max_segs, H, Dk, Dv] or NULL.
  * workspace  at least pkv_linear_attn_varlen_workspace_size() bytes, 256-byte
  *        aligned (NULL where that is 0); scratch: calls that share it must be
  *        ordered on one stream.
- * With bf16 and Dk, Dv in {64, 128} the call works in chunks of 64 tokens:
+ * With bf16 and Dk, Dv in {64, 128} the call works in chunks of 32 tokens:
  * states and sums are fp32, the in-chunk weights and, for the readout, the
  * state are rounded to bf16; NaN and infinities reach no other segment, but
- * may reach earlier tokens of their own chunk.
+ * may reach earlier tokens of their own chunk. Weights below 2^-150 are 0.
  * Supported: Dk, Dv in {32, 64, 128}. Errors: as pkv_attn_varlen with H in
  * place of the heads, max_segs * H > 2^22; PKV_ERR_WORKSPACE.
  */

@@ -14,6 +14,9 @@
 namespace {
 
 constexpr int64_t kInt32Max = 2147483647;
+// Work-groups of a launch: a grid holds less than 2^32 work-items, of at most 512
+// a group.
+constexpr int64_t kMaxGroups = int64_t(1) << 23;
 
 bool supported_head_dim(int32_t d) { return d == 32 || d == 64 || d == 128; }
 bool known_dtype(int32_t dt) { return dt == PKV_BF16 || dt == PKV_F32; }
@@ -67,7 +70,7 @@ pkv_status check_attn(const int32_t* cu, int32_t& max_segs, int64_t N, int32_t H
       Hq % Hkv != 0)
     return PKV_ERR_INVALID_ARGUMENT;
   if (!known_dtype(dtype) || !supported_head_dim(D)) return PKV_ERR_UNSUPPORTED;
-  if (pkv::attn_simple_grid(N, max_segs, Hq) > kInt32Max) return PKV_ERR_INVALID_ARGUMENT;
+  if ((N / 32 + max_segs) * Hq >= kMaxGroups) return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;
 }
 
@@ -77,7 +80,7 @@ pkv_status check_linear(const int32_t* cu, int32_t& max_segs, int64_t N, int32_t
       int64_t(max_segs) * H > (int64_t(1) << 22))
     return PKV_ERR_INVALID_ARGUMENT;
   if (!known_dtype(dtype) || !supported_head_dim(Dk) || !supported_head_dim(Dv)) return PKV_ERR_UNSUPPORTED;
-  if (pkv::linear_chunk_supported(Dk, Dv, dtype) && pkv::linear_chunk_grid(N, max_segs, H) > kInt32Max)
+  if (pkv::linear_chunk_supported(Dk, Dv, dtype) && pkv::linear_chunk_grid(N, max_segs, H) >= kMaxGroups)
     return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;
 }

@@ -396,10 +396,6 @@ hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attn_simple_grid(int64_t N, int32_t max_segs, int32_t H) {
-  return tile_slots(N, max_segs, kT) * H + 256;
-}
-
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream) {
   if (dtype == 1) {
     if (a.D == 32) return fwd<float, 32>(a, stream);

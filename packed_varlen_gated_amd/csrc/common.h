@@ -148,8 +148,6 @@ struct AttnGradArgs {
   float* stats;  // [2, H, N] in the workspace: lse log2 e, delta (the simple kernels: delta alone)
   void *dq, *dk, *dv;
 };
-// The largest grid of the two launchers.
-int64_t attn_simple_grid(int64_t N, int32_t max_segs, int32_t H);
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream);
 hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g, int32_t dtype,
                                        hipStream_t stream);

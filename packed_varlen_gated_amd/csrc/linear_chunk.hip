@@ -101,6 +101,13 @@ struct WalkArgs {
   int32_t* flags;
 };
 
+// The log decay in base 2; one of -inf (nothing is kept) stays finite, since it is
+// multiplied by distances of 0.
+__device__ __forceinline__ float log2_decay(float g) {
+  const float x = g * kLog2e;
+  return x < -1e30f ? -1e30f : x;
+}
+
 // X of one (state, head) <-> registers: register 8 v + j of tile i is row
 // 32 i + 16 v + 8 (lane / 32) + j of the lane's column. One address register;
 // the rest of an offset is an immediate or a scalar.
@@ -243,7 +250,7 @@ __device__ __forceinline__ void state_walk(const WalkArgs& x, const Role& R, int
   run.start = t.start;
   run.end = t.e - t.start > x.run ? t.start + x.run : t.e;
   run.n_chunks = (run.end - run.start + C - 1) / C;
-  const float g2 = x.g[h] * kLog2e;
+  const float g2 = log2_decay(x.g[h]);
   auto issue = [&](int i) {
     const int32_t s0 = run.chunk(i), n = run.len(s0), stage = i & 1;
     char* dst = lds + stage * (SB + SC);
@@ -339,7 +346,7 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, kPair ? 2 : 3) void linear_wa
     const int team = kPair ? wave_ / NW : 0, wave = kPair ? wave_ % NW : wave_;
     const Role& R = x.r[team];
     if (h != h0) __syncthreads();  // the last head is done with LDS
-    const float g2 = x.g[h] * kLog2e;
+    const float g2 = log2_decay(x.g[h]);
     const int half = lane >> 5, col = lane & 31;
     const int32_t cs = x.H * DB * 2;
     auto issue = [&](int i) {
@@ -483,7 +490,7 @@ __device__ __forceinline__ void scan(const WalkArgs& x, const Role& R, int32_t b
   const int tid = threadIdx.x;
   const int32_t parts = size / (4 * kScan), h = blk / parts;
   const int64_t elem = (int64_t(blk % parts) * kScan + tid) * 4;
-  const float g2 = x.g[h] * kLog2e;
+  const float g2 = log2_decay(x.g[h]);
   f32x4 X = {0.f, 0.f, 0.f, 0.f};
   for (int32_t base = 0; base < count; base += kScan) {
     const int32_t n = count - base < kScan ? count - base : kScan;

@@ -258,6 +258,19 @@ def test_linear_one_segment_and_decays(dtype, D):
     linear_case([150], 0, 1, D, D, dtype, False, g=[-200.0])                          # e^g is 0 in fp32
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+def test_linear_decay_of_minus_infinity_keeps_nothing(dtype, D):
+    N, cu = lay([700, 33], 0)
+    q, k, v, do, _, _, _ = linear_inputs(23, N, 2, D, D, dtype)
+    g = torch.full((2,), -float("inf"), device=dev())
+    got = linear_run(q, k, v, do, g, None, None, cu_gpu(cu))
+    one = linear_run(q, k, v, do, g, None, None, cu_gpu(np.arange(N + 1)))    # every token alone
+    for n in ("o", "dq", "dk", "dv"):
+        x, y = host(got[n]), host(one[n])
+        # the same products, in another place of a chunk: fp32 sums of D terms, rounded once
+        assert np.isfinite(x).all() and np.abs(x - y).max() <= 2 * half_step(dtype) * np.abs(y).max() + gamma(D) * 30
+
+
 @pytest.mark.parametrize("states", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
 def test_linear_many_chunks(D, states):

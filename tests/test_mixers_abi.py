@@ -49,7 +49,8 @@ ATTN_BAD = [
     (dict(q=NUL), 1), (dict(k=NUL), 1), (dict(v=NUL), 1), (dict(o=NUL), 1), (dict(N=0), 1), (dict(N=1 << 31), 1),
     (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hkv=3), 1), (dict(Hq=1 << 17), 1), (dict(max_segs=0), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(D=48), 2), (dict(D=256), 2),
-    (dict(dtype=2), 2), (dict(N=(1 << 31) - 1, Hq=64, Hkv=64), 1), (dict(q=A(1, 2)), 1), (dict(k=A(2, 8)), 1),
+    (dict(dtype=2), 2), (dict(N=(1 << 31) - 1, Hq=64, Hkv=64), 1),
+    (dict(max_segs=1 << 21), 1), (dict(q=A(1, 2)), 1), (dict(k=A(2, 8)), 1),
 ]
 
 
