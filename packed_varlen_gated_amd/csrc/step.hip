@@ -42,25 +42,33 @@ __global__ __launch_bounds__(kThreads) void step_kernel(
   const int64_t slot = slots == nullptr ? r : slots[r];
   const int64_t row = r * H + h;
 
-  bool bad = false;
-  if (slots != nullptr && slot >= 0) {
-    bad = slot >= S;
-    for (int64_t i = tid; i < r; i += kThreads) bad |= slots[i] == slot;
+  bool bad = slots != nullptr && slot >= S;
+  const bool live = !bad && slot >= 0;
+  const int rg = tid / TC, c = c0 + tid % TC * 4;
+  float* p = state + ((slot * H + h) * DK + rg * R) * DV + c;
+  f32x4 x[R];
+  if (live && tid < USED) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const f32x4*>(p + i * DV);
+  }
+  if (live && slots != nullptr) {
+    // while the state comes: the earlier rows' slots, 16 bytes a load
+    typedef int32_t i32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+    const int64_t quads = r / 4;
+#pragma unroll 4
+    for (int64_t i = tid; i < quads; i += kThreads) {
+      const i32x4_a4 y = *reinterpret_cast<const i32x4_a4*>(slots + 4 * i);
+      bad |= (y[0] == slot) | (y[1] == slot) | (y[2] == slot) | (y[3] == slot);
+    }
+    if (tid < r % 4) bad |= slots[4 * quads + tid] == slot;
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0 && h == 0 && c0 == 0 && flags != nullptr) atomicOr(flags, kFlagBadSlot);
-  if (bad || slot < 0) {
+  if (bad || !live) {
     if (tid < CW) o[row * DV + c0 + tid] = from_f32<T>(0.f);
     return;
   }
 
-  const int rg = tid / TC, c = c0 + tid % TC * 4;
-  float* p = state + ((slot * H + h) * DK + rg * R) * DV + c;
-  f32x4 x[R];
-  if (tid < USED) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const f32x4*>(p + i * DV);
-  }
   if (tid < DK) {
     sq[tid] = to_f32(q[row * DK + tid]);
     const float kk = to_f32(k[row * DK + tid]);
