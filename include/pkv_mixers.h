@@ -71,7 +71,8 @@ pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const in
  *   delta_t = do_t.o_t,  dS_ts = P_ts (do_t.v_s - delta_t)
  *   dq_t = scale sum_s dS_ts k_s
  *   dk_s = scale sum_t dS_ts q_t,  dv_s = sum_t P_ts do_t,
- * dk and dv summed over the query heads of their kv head (in a fixed order).
+ * dk and dv summed over the query heads of their kv head, in an order that the
+ * sizes and the segments' lengths fix.
  * A segment with NaN or infinities may have them anywhere in its gradients.
  * workspace  at least pkv_attn_varlen_backward_workspace_size() bytes, 256-byte
  *            aligned; scratch.

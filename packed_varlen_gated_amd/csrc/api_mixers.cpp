@@ -117,7 +117,7 @@ pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const in
 size_t pkv_attn_varlen_backward_workspace_size(int64_t N, int32_t Hq, int32_t Hkv, int32_t D,
                                                int32_t max_segs, int32_t dtype) {
   if (check_attn(nullptr, max_segs, N, Hq, Hkv, D, 1.f, dtype) != PKV_OK) return 0;
-  return size_t(N) * Hq * 8;
+  return size_t(N) * Hq * 8 + 16;  // two numbers per row; the form of the keys pass
 }
 
 pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v, const void* o,

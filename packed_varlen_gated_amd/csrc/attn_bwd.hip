@@ -28,6 +28,8 @@
 #include "mfma.h"
 #include "segments.h"
 
+#include <cmath>
+
 namespace pkv {
 namespace {
 
@@ -122,12 +124,51 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[D / 32], float f,
   }
 }
 
+// A work-group of the keys pass is a serial walk over the queries of the group's
+// heads. If the walk of the longest segment outlasts what all walks come to when
+// dealt to the chip (512 work-groups of 128 keys at a time), it sets the time, and
+// the form with kQ = 4 halves it; else the other form's steps are cheaper, and so
+// is what its walks cost beside them. In queries: rep Lmax > 768 + 2 (rep Hkv sum L^2 / 2^17).
+// Forward and reverse pass, kQ = 4 / 1 (rep Lmax, rep Hkv sum L^2 / 2^17):
+//   one of 512 tokens, H 16, Hkv 4, D 128 (2048, 32)             89 / 147 us
+//   one of 1024, H 8, Hkv 8, D 64 (1024, 64)                     63 / 84 us
+//   one of 4096, H 16, Hkv 16, D 128 (4096, 2048)               480 / 496 us
+//   8192, median 800, H 16, Hkv 4, D 128 (13636, 2579)          611 / 963 us
+//   16384, median 800, H 32, Hkv 8, D 128 (13636, 7089)        1458 / 1461 us
+//   16384 in docs of about 200, H 16, Hkv 4, D 128 (1580, 542)  335 / 271 us
+//   32768, median 800, H 16, Hkv 16, D 128 (8192, 13547)       2775 / 2272 us
+//   one of 32768, H 32, Hkv 8, D 128 (131072, 262144)          42.9 / 38.3 ms
+__host__ __device__ inline bool shared_form(uint64_t longest, uint64_t squares, int32_t H, int32_t Hkv) {
+  const double rep = H / Hkv;
+  return rep * double(longest) > 768. + rep * Hkv * double(squares) * (1. / 65536);
+}
+
+// By one work-group, for the next launches.
+__device__ __forceinline__ void choose_form(const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H,
+                                            int32_t Hkv, int32_t* __restrict__ form, char* lds) {
+  unsigned long long* sums = reinterpret_cast<unsigned long long*>(lds);  // the longest, the squares' sum
+  if (threadIdx.x < 2) sums[threadIdx.x] = 0;
+  __syncthreads();
+  unsigned long long longest = 0, squares = 0;
+  for (int64_t i = threadIdx.x; i < max_segs; i += kThreads) {
+    const int64_t a = cu[i], e = cu[i + 1];
+    if (!segment_ok(int32_t(i), a, e, N)) continue;
+    const unsigned long long n = e - a;
+    longest = n > longest ? n : longest;
+    squares += n * n;
+  }
+  atomicMax(&sums[0], longest);
+  atomicAdd(&sums[1], squares);
+  __syncthreads();
+  if (threadIdx.x == 0) *form = shared_form(sums[0], sums[1], H, Hkv) ? 4 : 1;
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
     int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dq, float* __restrict__ stats,
-    int32_t* __restrict__ flags, SlotGrid grid) {
+    int32_t* __restrict__ flags, int32_t* __restrict__ form, SlotGrid grid) {
   constexpr int KS = D / 16, DT = D / 32, TB = Lds<D>::BYTES;
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
 
@@ -137,6 +178,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const int64_t j = b - blocks, groups = gridDim.x - blocks;
     zero_tail(dq, covered_tokens(cu, max_segs, N), N, int64_t(H) * D * 2, j, groups);
     if (j == 0) check_cu(cu, max_segs, N, flags);
+    if (j == 0 && form != nullptr) choose_form(cu, max_segs, N, H, Hkv, form, lds);
     return;
   }
   int32_t slot, h0, h1;
@@ -247,7 +289,8 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const bf16* __restrict__ dout, const float* __restrict__ stats, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dk,
-    bf16* __restrict__ dv, SlotGrid grid) {
+    bf16* __restrict__ dv, const int32_t* __restrict__ form, SlotGrid grid) {
+  if (form != nullptr && *form != kQ) return;
   constexpr int KS = D / 16, DT = D / 32;
   constexpr int NT = DkvShape<kQ>::NT, T = DkvShape<kQ>::T, TB = T * D * 2;
   // Q, dO of the even tiles, of the odd ones; then lse log2 e and delta of each
@@ -267,7 +310,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   SegTile t;
   if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
 
-  for (int32_t hk = h0; hk < (kQ == 1 ? h1 : h0 + 1); ++hk) {
+  for (int32_t hk = h0; hk < h1; ++hk) {
   // (nothing that goes by the lane is kept from one head to the next)
   const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Reader<D> rd(tid);
@@ -411,39 +454,36 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
     asm volatile("" ::: "memory");
     store_rows<D>(av, 1.f, st, dv + to, int64_t(Hkv) * D, have, rd);
   }
-  if (kQ == 1 && hk + 1 < h1) __syncthreads();  // the outputs have left LDS
+  if (hk + 1 < h1) __syncthreads();  // the outputs have left LDS
   }
 }
 
 template <int D, int kQ>
-void keys_pass(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
-  SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
-  if (kQ > 1) grid.near = grid.slots;  // (small calls: a work-group per head)
+void keys_pass(const AttnArgs& a, const AttnGradArgs& g, const int32_t* form, hipStream_t stream) {
+  const SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
   attn_dkv_kernel<D, kQ><<<dim3(uint32_t(slot_blocks(grid, a.Hkv) + tail_groups(a.N * a.Hkv * D * 2))), dim3(DkvShape<kQ>::NT), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), grid);
+      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), form, grid);
 }
 
 template <int D>
 hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
+  // Whether any lengths make the shared form the better one: of one segment of L
+  // tokens, 1 > Hkv L / 2^16 + 768 / (rep L), the least at the L of equal terms.
+  const double rep = a.H / a.Hkv, equal = sqrt(768. * 65536. / (rep * a.Hkv)), L = equal < double(a.N) ? equal : double(a.N);
+  const bool may = shared_form(uint64_t(L), uint64_t(L * L), a.H, a.Hkv);
+  int32_t* form = may && a.cu != nullptr ? reinterpret_cast<int32_t*>(g.stats + 2 * a.N * a.H) : nullptr;
   attn_dq_kernel<D><<<dim3(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2))), dim3(kThreads), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
-      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, grid);
-  // A work-group of the keys pass is a serial walk over the group's heads and the
-  // rest of the segment. Below two full rounds of the chip (1024 tiles of 128
-  // keys) the longest walk sets the time and the shared form halves the work per
-  // step; above, the other form's steps are cheaper. Whole reverse and forward
-  // pass, kQ = 4 / 1: 8192 tokens, Hkv 4 (256 tiles) 0.64 / 1.08 ms; 2048, Hkv 8
-  // (128) 0.30 / 0.58 ms; 16384, Hkv 4, D 64 (512) 0.262 / 0.267 ms; 8192,
-  // Hkv 16, D 64 (1024) 0.86 / 0.75 ms; 16384, Hkv 8 (1024) 11.2 / 10.4 ms.
-  const bool share = a.N / kB * a.Hkv < 1024;
-  if (share)
-    keys_pass<D, 4>(a, g, stream);
-  else
-    keys_pass<D, 1>(a, g, stream);
+      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, form, grid);
+  // With cu the lengths are on the device: both forms are launched, and the one
+  // that was not chosen ends at once.
+  const bool share = a.cu == nullptr && shared_form(a.N, uint64_t(a.N) * a.N, a.H, a.Hkv);
+  if (form != nullptr || share) keys_pass<D, 4>(a, g, form, stream);
+  if (!share) keys_pass<D, 1>(a, g, form, stream);
   return hipGetLastError();
 }
 

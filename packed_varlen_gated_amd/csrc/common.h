@@ -145,7 +145,9 @@ struct AttnArgs {
 };
 struct AttnGradArgs {
   const void* dout;
-  float* stats;  // [2, H, N] in the workspace: lse log2 e, delta (the simple kernels: delta alone)
+  // [2, H, N] in the workspace: lse log2 e, delta (the simple kernels: delta alone);
+  // behind it the form of the keys pass
+  float* stats;
   void *dq, *dk, *dv;
 };
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream);

@@ -107,6 +107,47 @@ def test_attn_many_tiles(D):
     attn_case([1500, 300, 2], 7, 2, 1, D, "bf16", seed=5)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (6, 1), (4, 2), (20, 10)])
+def test_attn_one_long_segment_among_short_ones(Hq, Hkv, D):
+    """The keys pass whose waves share keys is chosen by the longest segment; the short ones go through it too."""
+    attn_case([33, 0, 1100, 1, 63, 64, 65, 0, 129, 31], 40, Hq, Hkv, D, "bf16", seed=Hq + D)
+    attn_case([3] * 70 + [1000] + [0] * 200, 0, Hq, Hkv, D, "bf16", seed=D)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_none_is_one_segment(D):
+    """Without cu_seqlens the form of the keys pass is chosen on the host, with it on the device: the same one."""
+    for N in (100, 700, 1300):
+        q, k, v, do = attn_inputs(N, N, 2, 1, D, "bf16")
+        a, b = attn_run(q, k, v, do, None), attn_run(q, k, v, do, cu_gpu([0, N]))
+        assert all(torch.equal(a[n], b[n]) for n in a), N
+
+
+def test_attn_captured_with_changing_lengths():
+    """A captured reverse pass goes by the lengths that cu_seqlens holds at the replay."""
+    N, D = 1300, 64
+    q, k, v, do = attn_inputs(23, N, 4, 2, D, "bf16")
+    lays = [[0, 1300, 1300, 1300, 1300], [0, 200, 500, 800, 1100], [0, 1, 1290, 1290, 1295], [0, 0, 0, 0, 0]]
+    want = [attn_run(q, k, v, do, cu_gpu(c)) for c in lays]
+    cud = cu_gpu(lays[1])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        o, lse = pkv.attn_varlen(q, k, v, cud)
+        pkv.attn_varlen_backward(q, k, v, o, lse, do, cud)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = pkv.attn_varlen(q, k, v, cud)
+        gr = pkv.attn_varlen_backward(q, k, v, o, lse, do, cud)
+    for i in (0, 1, 2, 3, 1, 0):
+        cud.copy_(cu_gpu(lays[i]))
+        g.replay()
+        torch.cuda.synchronize()
+        for n, x in dict(o=o, lse=lse, dq=gr.dq, dk=gr.dk, dv=gr.dv).items():
+            assert torch.equal(x, want[i][n]), (i, n)
+
+
 @pytest.mark.parametrize("dtype,D", [("f32", 32), ("bf16", 64), ("bf16", 128)])
 def test_attn_segments_are_isolated(dtype, D):
     """NaN and infinities in one segment and behind the last reach no other: the bits stay."""
