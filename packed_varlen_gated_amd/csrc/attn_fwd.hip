@@ -30,6 +30,15 @@
 // output is not finite the work-group walks the keys once more with such
 // values as 0 and stores the outputs of the elements that no such value
 // belongs to: with every value finite nothing is spent but the check.
+//
+// Bound by the matrix and the vector units' turns: 46 % of the cycles have a
+// matrix instruction, the softmax's vector work takes about as many, and two
+// work-groups per compute unit (the sums and Q take 192 registers at D 128) do not
+// hide all of one under the other. 65536 tokens in documents of up to 8192, H 32,
+// Hkv 8, D 128: 2.11-2.17 ms, 885-910 TFLOP/s of causal products (a large matrix
+// product reaches 1220 here, 1.57 ms); 16384 in one document 787 TFLOP/s forward and
+// reverse; 77 tokens, H 16: 8.8 us. A raised wave priority around the products made
+// the first 2.31 ms.
 
 #include "mfma.h"
 #include "segments.h"

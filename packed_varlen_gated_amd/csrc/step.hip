@@ -9,7 +9,9 @@
 // against 4 Dk Dv operations. A work-group takes a slice of the value columns
 // of one (request, head); a thread reads 16 bytes of a row at a time, all its
 // rows before the first use, and the readout is summed over the row groups
-// through LDS.
+// through LDS. 123 rows, H 32, 128 x 128: 107 us for 516 MB (4.8 TB/s; a copy
+// reaches 5.2); KDA with 48 rows: 39.6 us (5.1 TB/s); one row, H 16: 3.8 us, a
+// launch. A slice is 32 columns, so that one row of 16 heads has 64 work-groups.
 //
 // A row whose slot is negative is idle: o = 0 and no state is touched. A slot
 // past the last one, or one that an earlier row of the call names too, is
