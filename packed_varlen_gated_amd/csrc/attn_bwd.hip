@@ -196,88 +196,88 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
   if (!find_tile(cu, max_segs, N, kB, slot, t)) return;
 
   for (int32_t hi = h0; hi < h1; ++hi) {
-  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;  // (as in the forward pass)
-  // (nothing that goes by the lane is kept from one head to the next)
-  const int tid = fresh(threadIdx.x), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Reader<D> rd(tid);
-  const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
-  const int32_t q0 = t.start + wave * 32;
-  const int32_t rows = t.e - q0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-  const int32_t qend = t.start + kB < t.e ? t.start + kB : t.e;
-  const int n_tiles = (qend - t.a + kT - 1) / kT;
-  const Loader<D, kT, kThreads> ld(kstride, tid);
-  auto issue = [&](int it) {
-    const int32_t s0 = t.a + it * kT;
-    const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
-    const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(n - 1) * kstride + D * 2;
-    char* dst = lds + (it & 1) * 2 * TB;
-    ld.issue(buffer(k + at, bytes), dst, wave);
-    ld.issue(buffer(v + at, bytes), dst + TB, wave);
-  };
-  issue(0);
+    const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;  // (as in the forward pass)
+    // (nothing that goes by the lane is kept from one head to the next)
+    const int tid = fresh(threadIdx.x), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Reader<D> rd(tid);
+    const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
+    const int32_t q0 = t.start + wave * 32;
+    const int32_t rows = t.e - q0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+    const int32_t qend = t.start + kB < t.e ? t.start + kB : t.e;
+    const int n_tiles = (qend - t.a + kT - 1) / kT;
+    const Loader<D, kT, kThreads> ld(kstride, tid);
+    auto issue = [&](int it) {
+      const int32_t s0 = t.a + it * kT;
+      const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
+      const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(n - 1) * kstride + D * 2;
+      char* dst = lds + (it & 1) * 2 * TB;
+      ld.issue(buffer(k + at, bytes), dst, wave);
+      ld.issue(buffer(v + at, bytes), dst + TB, wave);
+    };
+    issue(0);
 
-  const int64_t at = (int64_t(have > 0 ? q0 : t.start) * H + h) * D;
-  bf16x8 qf[KS], df[KS];
-  load_rows<D>(df, dout + at, have, qstride, rd);
-  float delta = 0.f;
-  {
-    load_rows<D>(qf, o + at, have, qstride, rd);
+    const int64_t at = (int64_t(have > 0 ? q0 : t.start) * H + h) * D;
+    bf16x8 qf[KS], df[KS];
+    load_rows<D>(df, dout + at, have, qstride, rd);
+    float delta = 0.f;
+    {
+      load_rows<D>(qf, o + at, have, qstride, rd);
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) delta += to_f32(df[i][j]) * to_f32(qf[i][j]);
-    delta += other_half(delta);
-  }
-  load_rows<D>(qf, q + at, have, qstride, rd);
-  const int64_t row = int64_t(h) * N + q0 + rd.col;
-  const float lse2 = rd.col < have ? lse[row] * kLog2e : 0.f;
-
-  const float c = scale * kLog2e;
-  float rest = 0.f;  // sum_s dS_ts
-  f32x16 acc[DT];
-#pragma unroll
-  for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
-  for (int it = 0; it < n_tiles; ++it) {
-    wait_vm();
-    bar();
-    if (it + 1 < n_tiles) issue(it + 1);
-    const uint32_t kt = lds_addr(lds) + (it & 1) * 2 * TB, vt = kt + TB;
-    const int32_t s0 = t.a + it * kT;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (have == 0 || s0 + 32 * j > q0 + 31) continue;
-      f32x16 s = {}, dp = {};
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {  // independent products take turns
-        s = mfma32(rd.rows(kt, j, i), qf[i], s);
-        dp = mfma32(rd.rows(vt, j, i), df[i], dp);
-      }
-      bf16x8 ds[2];
-      const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p = ex2(fmaf(s[i], c, -lse2));
-        const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
-        rest += x;
-        ds[i / 8][i % 8] = static_cast<bf16>(x);
-      }
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) acc[i] = mfma32(rd.channels(kt, i, 2 * j + u), ds[u], acc[i]);
+        for (int j = 0; j < 8; ++j) delta += to_f32(df[i][j]) * to_f32(qf[i][j]);
+      delta += other_half(delta);
     }
-  }
-  // The sum of a row's dS is 0; what it is short of that is delta's error, which
-  // stems from the rounding of o. The keys pass gets delta without it.
-  rest += other_half(rest);
-  if (rd.half == 0 && rd.col < have) {
-    stats[row] = lse2;
-    stats[int64_t(H) * N + row] = delta + rest;
-  }
-  __syncthreads();
-  if (have > 0)
-    store_rows<D>(acc, scale, lds + wave * (32 * D * 2), dq + (int64_t(q0) * H + h) * D, int64_t(H) * D, have, rd);
-  if (hi + 1 < h1) __syncthreads();  // the outputs have left LDS
+    load_rows<D>(qf, q + at, have, qstride, rd);
+    const int64_t row = int64_t(h) * N + q0 + rd.col;
+    const float lse2 = rd.col < have ? lse[row] * kLog2e : 0.f;
+
+    const float c = scale * kLog2e;
+    float rest = 0.f;  // sum_s dS_ts
+    f32x16 acc[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+    for (int it = 0; it < n_tiles; ++it) {
+      wait_vm();
+      bar();
+      if (it + 1 < n_tiles) issue(it + 1);
+      const uint32_t kt = lds_addr(lds) + (it & 1) * 2 * TB, vt = kt + TB;
+      const int32_t s0 = t.a + it * kT;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (have == 0 || s0 + 32 * j > q0 + 31) continue;
+        f32x16 s = {}, dp = {};
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {  // independent products take turns
+          s = mfma32(rd.rows(kt, j, i), qf[i], s);
+          dp = mfma32(rd.rows(vt, j, i), df[i], dp);
+        }
+        bf16x8 ds[2];
+        const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = ex2(fmaf(s[i], c, -lse2));
+          const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
+          rest += x;
+          ds[i / 8][i % 8] = static_cast<bf16>(x);
+        }
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) acc[i] = mfma32(rd.channels(kt, i, 2 * j + u), ds[u], acc[i]);
+      }
+    }
+    // The sum of a row's dS is 0; what it is short of that is delta's error, which
+    // stems from the rounding of o. The keys pass gets delta without it.
+    rest += other_half(rest);
+    if (rd.half == 0 && rd.col < have) {
+      stats[row] = lse2;
+      stats[int64_t(H) * N + row] = delta + rest;
+    }
+    __syncthreads();
+    if (have > 0)
+      store_rows<D>(acc, scale, lds + wave * (32 * D * 2), dq + (int64_t(q0) * H + h) * D, int64_t(H) * D, have, rd);
+    if (hi + 1 < h1) __syncthreads();  // the outputs have left LDS
   }
 }
 
@@ -318,157 +318,158 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
 
   for (int32_t hk = h0; hk < h1; ++hk) {
-  // (nothing that goes by the lane is kept from one head to the next)
-  const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Reader<D> rd(tid);
-  const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
-  const int32_t k0 = t.start + wave / kQ * 32;  // the wave's first key
-  const int32_t rows = t.e - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-  const int per_head = (t.e - t.start + T - 1) / T, n_tiles = per_head * rep;
-  const Loader<D, T, NT> ld(qstride, tid);
-  int ih = hk * rep, iq = 0;  // query head and tile of the next load
-  // Q, dO and the statistics of the next tile
-  auto issue = [&](int it) {
-    const int32_t s0 = t.start + iq * T, h = ih;
-    const int32_t n = t.e - s0 < T ? t.e - s0 : T;
-    const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
-    char* dst = lds + (it & 1) * 2 * TB;
-    ld.issue(buffer(q + at, bytes), dst, wave);
-    ld.issue(buffer(dout + at, bytes), dst + TB, wave);
-    if (wave < T / 32) {  // lse log2 e and delta, 64 queries a wave
-      const int w = wave / (T / 64), part = wave % (T / 64) * 64;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          buffer(stats + (int64_t(w) * H + h) * N + s0, int64_t(n) * 4),
-          (__attribute__((address_space(3))) void*)(lds + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4), 4,
-          uint32_t(part + lane) * 4, 0, 0, 0);
-    }
-    if (++iq == per_head) {
-      iq = 0;
-      ++ih;
-    }
-  };
-  issue(0);
-  const int64_t at = (int64_t(have > 0 ? k0 : t.start) * Hkv + hk) * D;
-  bf16x8 kf[KS], vf[KS];
-  load_rows<D>(kf, k + at, have, kstride, rd);
-  load_rows<D>(vf, v + at, have, kstride, rd);
-  const float c = scale * kLog2e;
-  f32x16 ak[DT], av[DT];
+    // (nothing that goes by the lane is kept from one head to the next)
+    const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Reader<D> rd(tid);
+    const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
+    const int32_t k0 = t.start + wave / kQ * 32;  // the wave's first key
+    const int32_t rows = t.e - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+    const int per_head = (t.e - t.start + T - 1) / T, n_tiles = per_head * rep;
+    const Loader<D, T, NT> ld(qstride, tid);
+    int ih = hk * rep, iq = 0;  // query head and tile of the next load
+    // Q, dO and the statistics of the next tile
+    auto issue = [&](int it) {
+      const int32_t s0 = t.start + iq * T, h = ih;
+      const int32_t n = t.e - s0 < T ? t.e - s0 : T;
+      const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
+      char* dst = lds + (it & 1) * 2 * TB;
+      ld.issue(buffer(q + at, bytes), dst, wave);
+      ld.issue(buffer(dout + at, bytes), dst + TB, wave);
+      if (wave < T / 32) {  // lse log2 e and delta, 64 queries a wave
+        const int w = wave / (T / 64), part = wave % (T / 64) * 64;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            buffer(stats + (int64_t(w) * H + h) * N + s0, int64_t(n) * 4),
+            (__attribute__((address_space(3))) void*)(lds + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4), 4,
+            uint32_t(part + lane) * 4, 0, 0, 0);
+      }
+      if (++iq == per_head) {
+        iq = 0;
+        ++ih;
+      }
+    };
+    issue(0);
+    const int64_t at = (int64_t(have > 0 ? k0 : t.start) * Hkv + hk) * D;
+    bf16x8 kf[KS], vf[KS];
+    load_rows<D>(kf, k + at, have, kstride, rd);
+    load_rows<D>(vf, v + at, have, kstride, rd);
+    const float c = scale * kLog2e;
+    f32x16 ak[DT], av[DT];
 #pragma unroll
-  for (int i = 0; i < DT; ++i) {
-    ak[i] = f32x16{};
-    av[i] = f32x16{};
-  }
-  int cq = 0;  // query tile in use
-  for (int it = 0; it < n_tiles; ++it) {
-    wait_vm();
-    bar();
-    if (it + 1 < n_tiles) issue(it + 1);
-    const uint32_t qt0 = lds_addr(lds) + (it & 1) * 2 * TB;
-    const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * T * 4);
-    const f32x4* dl = ls + T / 4;
-    const int32_t s0 = t.start + cq * T;
-    if (++cq == per_head) cq = 0;
+    for (int i = 0; i < DT; ++i) {
+      ak[i] = f32x16{};
+      av[i] = f32x16{};
+    }
+    int cq = 0;  // query tile in use
+    for (int it = 0; it < n_tiles; ++it) {
+      wait_vm();
+      bar();
+      if (it + 1 < n_tiles) issue(it + 1);
+      const uint32_t qt0 = lds_addr(lds) + (it & 1) * 2 * TB;
+      const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * T * 4);
+      const f32x4* dl = ls + T / 4;
+      const int32_t s0 = t.start + cq * T;
+      if (++cq == per_head) cq = 0;
 #pragma unroll 1
-    for (int j = wave % kQ; j < T / 32; j += kQ) {
-      const int32_t b0 = s0 + 32 * j;  // first query of the block
-      // (addresses are formed per block: one register each instead of one per read)
-      const uint32_t qt = fresh_uniform(qt0 + 32 * j * Lds<D>::ROW), ot = qt + TB;
-      if (have == 0 || b0 + 31 < k0 || b0 >= t.e) continue;
-      // Registers are full at D = 128 (k, v, dk and dv take 192): the weights are
-      // done with before dP is begun, and nothing of a phase starts early. The
-      // other wave of the SIMD fills the gaps.
-      bf16x8 p[2], ds[2];
-      f32x16 x = {};
+      for (int j = wave % kQ; j < T / 32; j += kQ) {
+        const int32_t b0 = s0 + 32 * j;  // first query of the block
+        // (addresses are formed per block: one register each instead of one per read)
+        const uint32_t qt = fresh_uniform(qt0 + 32 * j * Lds<D>::ROW), ot = qt + TB;
+        if (have == 0 || b0 + 31 < k0 || b0 >= t.e) continue;
+        // Registers are full at D = 128 (k, v, dk and dv take 192): the weights are
+        // done with before dP is begun, and nothing of a phase starts early. The
+        // other wave of the SIMD fills the gaps.
+        bf16x8 p[2], ds[2];
+        f32x16 x = {};
 #pragma unroll
-      for (int i = 0; i < KS; ++i) x = mfma32(rd.rows(qt, 0, i), kf[i], x);
-      if (D == 128) __builtin_amdgcn_sched_barrier(0);
-      // the lane's key takes part in the block's queries first .. end - 1
-      const bool edge = b0 < k0 + 31 || b0 + 32 > t.e;
-      const int32_t first = edge ? k0 + rd.col - b0 - 4 * rd.half : -64;
-      const int32_t end = edge ? t.e - b0 - 4 * rd.half : 64;
+        for (int i = 0; i < KS; ++i) x = mfma32(rd.rows(qt, 0, i), kf[i], x);
+        if (D == 128) __builtin_amdgcn_sched_barrier(0);
+        // the lane's key takes part in the block's queries first .. end - 1
+        const bool edge = b0 < k0 + 31 || b0 + 32 > t.e;
+        const int32_t first = edge ? k0 + rd.col - b0 - 4 * rd.half : -64;
+        const int32_t end = edge ? t.e - b0 - 4 * rd.half : 64;
 #pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * i4 + e, r = 8 * i4 + e;
-          const float y = ex2(fmaf(x[i], c, -l4[e]));
-          x[i] = r >= first && r < end ? y : 0.f;
-          p[i / 8][i % 8] = static_cast<bf16>(x[i]);
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * i4 + e, r = 8 * i4 + e;
+            const float y = ex2(fmaf(x[i], c, -l4[e]));
+            x[i] = r >= first && r < end ? y : 0.f;
+            p[i / 8][i % 8] = static_cast<bf16>(x[i]);
+          }
         }
-      }
-      if (D == 128) __builtin_amdgcn_sched_barrier(0);
-      f32x16 dp = {};
+        if (D == 128) __builtin_amdgcn_sched_barrier(0);
+        f32x16 dp = {};
 #pragma unroll
-      for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(ot, 0, i), vf[i], dp);
-      if (D == 128) __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(ot, 0, i), vf[i], dp);
+        if (D == 128) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const f32x4 d4 = dl[8 * j + 2 * i4 + rd.half];
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const f32x4 d4 = dl[8 * j + 2 * i4 + rd.half];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * i4 + e;
-          ds[i / 8][i % 8] = static_cast<bf16>(x[i] * (dp[i] - d4[e]));
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * i4 + e;
+            ds[i / 8][i % 8] = static_cast<bf16>(x[i] * (dp[i] - d4[e]));
+          }
         }
-      }
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          av[i] = mfma32(rd.channels(ot, i, u), p[u], av[i]);
-          ak[i] = mfma32(rd.channels(qt, i, u), ds[u], ak[i]);
-        }
-    }
-  }
-  __syncthreads();
-  if constexpr (kQ > 1) {
-    // The sums of the waves that share keys: each in turn hands dk, then dv,
-    // to the first of them.
-    static_assert(NT / 64 / kQ * DT * 4096 <= 4 * TB, "sums in flight");
-    f32x4* mine = reinterpret_cast<f32x4*>(lds) + (wave / kQ) * (DT * 4 * 64) + lane;
-    auto join_sums = [&](f32x16 (&x)[DT], int from) {
-      if (wave % kQ == from) {
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mine[(4 * i + j) * 64] = f32x4{x[i][4 * j], x[i][4 * j + 1], x[i][4 * j + 2], x[i][4 * j + 3]};
-      }
-      __syncthreads();
-      if (wave % kQ == 0) {
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 y = mine[(4 * i + j) * 64];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][4 * j + e] += y[e];
+          for (int u = 0; u < 2; ++u) {
+            av[i] = mfma32(rd.channels(ot, i, u), p[u], av[i]);
+            ak[i] = mfma32(rd.channels(qt, i, u), ds[u], ak[i]);
           }
       }
-      __syncthreads();
-    };
-#pragma unroll 1
-    for (int from = 1; from < kQ; ++from) {
-      join_sums(ak, from);
-      join_sums(av, from);
     }
-  }
-  if (have > 0 && wave % kQ == 0) {
-    char* st = lds + wave / kQ * (32 * D * 2);
-    const int64_t to = (int64_t(k0) * Hkv + hk) * D;
-    store_rows<D>(ak, scale, st, dk + to, int64_t(Hkv) * D, have, rd);
-    asm volatile("" ::: "memory");
-    store_rows<D>(av, 1.f, st, dv + to, int64_t(Hkv) * D, have, rd);
-  }
-  if (hk + 1 < h1) __syncthreads();  // the outputs have left LDS
+    __syncthreads();
+    if constexpr (kQ > 1) {
+      // The sums of the waves that share keys: each in turn hands dk, then dv,
+      // to the first of them.
+      static_assert(NT / 64 / kQ * DT * 4096 <= 4 * TB, "sums in flight");
+      f32x4* mine = reinterpret_cast<f32x4*>(lds) + (wave / kQ) * (DT * 4 * 64) + lane;
+      auto join_sums = [&](f32x16 (&x)[DT], int from) {
+        if (wave % kQ == from) {
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mine[(4 * i + j) * 64] = f32x4{x[i][4 * j], x[i][4 * j + 1], x[i][4 * j + 2], x[i][4 * j + 3]};
+        }
+        __syncthreads();
+        if (wave % kQ == 0) {
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const f32x4 y = mine[(4 * i + j) * 64];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][4 * j + e] += y[e];
+            }
+        }
+        __syncthreads();
+      };
+#pragma unroll 1
+      for (int from = 1; from < kQ; ++from) {
+        join_sums(ak, from);
+        join_sums(av, from);
+      }
+    }
+    if (have > 0 && wave % kQ == 0) {
+      char* st = lds + wave / kQ * (32 * D * 2);
+      const int64_t to = (int64_t(k0) * Hkv + hk) * D;
+      store_rows<D>(ak, scale, st, dk + to, int64_t(Hkv) * D, have, rd);
+      asm volatile("" ::: "memory");
+      store_rows<D>(av, 1.f, st, dv + to, int64_t(Hkv) * D, have, rd);
+    }
+    if (hk + 1 < h1) __syncthreads();  // the outputs have left LDS
   }
 }
 
 template <int D, int kQ>
 void keys_pass(const AttnArgs& a, const AttnGradArgs& g, const int32_t* form, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
-  attn_dkv_kernel<D, kQ><<<dim3(uint32_t(slot_blocks(grid, a.Hkv) + tail_groups(a.N * a.Hkv * D * 2))), dim3(DkvShape<kQ>::NT), 0, stream>>>(
+  const dim3 blocks(uint32_t(slot_blocks(grid, a.Hkv) + tail_groups(a.N * a.Hkv * D * 2)));
+  attn_dkv_kernel<D, kQ><<<blocks, dim3(DkvShape<kQ>::NT), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
       static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), form, grid);
@@ -479,10 +480,12 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
   // Whether any lengths make the shared form the better one: of one segment of L
   // tokens, 1 > Hkv L / 2^16 + 768 / (rep L), the least at the L of equal terms.
-  const double rep = a.H / a.Hkv, equal = sqrt(768. * 65536. / (rep * a.Hkv)), L = equal < double(a.N) ? equal : double(a.N);
+  const double rep = a.H / a.Hkv, equal = sqrt(768. * 65536. / (rep * a.Hkv));
+  const double L = equal < double(a.N) ? equal : double(a.N);
   const bool may = shared_form(uint64_t(L), uint64_t(L * L), a.H, a.Hkv);
   int32_t* form = may && a.cu != nullptr ? reinterpret_cast<int32_t*>(g.stats + 2 * a.N * a.H) : nullptr;
-  attn_dq_kernel<D><<<dim3(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2))), dim3(kThreads), 0, stream>>>(
+  const dim3 blocks(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2)));
+  attn_dq_kernel<D><<<blocks, dim3(kThreads), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
       a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, form, grid);

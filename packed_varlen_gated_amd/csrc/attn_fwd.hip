@@ -94,217 +94,218 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
   if (!find_tile(cu, max_segs, N, kBM, slot, t)) return;
 
   for (int32_t hi = h0; hi < h1; ++hi) {
-  // Consecutive work-groups run on different XCDs: the query heads of one kv
-  // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
-  const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;
-  // (nothing that goes by the lane is kept from one head to the next)
-  const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5, col = lane & 31;
-  const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
-  const int32_t q0 = t.start + wave * 32;  // the wave's first query
-  const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
-  const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
-  const int n_tiles = (qend - t.a + kBN - 1) / kBN;
+    // Consecutive work-groups run on different XCDs: the query heads of one kv
+    // head are Hkv apart, so with Hkv a multiple of 8 they share an L2.
+    const int32_t hk = hi % Hkv, h = hk * (H / Hkv) + hi / Hkv;
+    // (nothing that goes by the lane is kept from one head to the next)
+    const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
+    const int32_t q0 = t.start + wave * 32;  // the wave's first query
+    const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
+    const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
+    const int n_tiles = (qend - t.a + kBN - 1) / kBN;
 
-  // the lane's first chunk of a tile; the others are whole multiples of 16 rows
-  // further (the swizzles' period)
-  constexpr int STEP = kThreads / CH;
-  static_assert(STEP % 16 == 0, "the swizzles repeat");
-  const int lrow = tid / CH, lpos = tid % CH;
-  const uint32_t koff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::k_swz(lrow)) * 16;
-  const uint32_t voff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::v_swz(lrow)) * 16;
-  auto issue = [&](int it) {
-    const int32_t s0 = t.a + it * kBN;
-    const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
-    const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(have - 1) * kstride + D * 2;
-    const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);
-    char* dst = lds + (it & 1) * 2 * TB + wave * 1024;
-    const uint32_t ko = fresh(koff), vo = fresh(voff);
-#pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16(rk, ko + i * STEP * kstride, dst + i * kThreads * 16);
-#pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16(rv, vo + i * STEP * kstride, dst + TB + i * kThreads * 16);
-  };
-
-  // c > 0: a negative scale flips the queries' signs, a scale of 0 clears them
-  // (a masked score is -inf, which a factor of 0 would turn into NaN)
-  const float c = scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
-  bf16x8 qf[KS];
-  {
-    const int32_t have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-    const auto r = buffer(q + (int64_t(rows > 0 ? q0 : t.start) * H + h) * D,
-                          have > 0 ? int64_t(have - 1) * qstride + D * 2 : 0);
-    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, keep = scale == 0.f ? 0u : ~0u;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      i32x4 x = __builtin_bit_cast(i32x4, load8(r, uint32_t(col) * qstride + (2 * i + half) * 16));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = int((uint32_t(x[j]) ^ flip) & keep);
-      qf[i] = __builtin_bit_cast(bf16x8, x);
-    }
-  }
-
-  f32x16 acc[DT];
-  float m = -FLT_MAX, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
-
-  // LDS addresses of this lane's operand chunks
-  const int krow = col, kx = Tile<D>::k_swz(col);
-  const int vr = 4 * half + ((lane & 15) >> 2);              // key of the transposing read (mod 8)
-  const int vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // its chunk in a 32-channel group
-  const int vb = (lane & 1) * 8;                             // its half of the chunk
-  const int vx = Tile<D>::v_swz(vr);                         // (the swizzle has period 4)
-
-  auto walk = [&](bool clean) {
-    issue(0);
-    for (int it = 0; it < n_tiles; ++it) {
-      wait_vm();
-      bar();
-      if (it + 1 < n_tiles) issue(it + 1);
-      char* kt = lds + (it & 1) * 2 * TB;
-      char* vt = kt + TB;
-      if (clean) {
-        // values that are not finite become 0
-        for (int i = tid; i < TB / 4; i += kThreads) {
-          uint32_t x = reinterpret_cast<uint32_t*>(vt)[i];
-          if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
-          if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
-          reinterpret_cast<uint32_t*>(vt)[i] = x;
-        }
-        __syncthreads();
-      }
+    // the lane's first chunk of a tile; the others are whole multiples of 16 rows
+    // further (the swizzles' period)
+    constexpr int STEP = kThreads / CH;
+    static_assert(STEP % 16 == 0, "the swizzles repeat");
+    const int lrow = tid / CH, lpos = tid % CH;
+    const uint32_t koff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::k_swz(lrow)) * 16;
+    const uint32_t voff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::v_swz(lrow)) * 16;
+    auto issue = [&](int it) {
       const int32_t s0 = t.a + it * kBN;
-      if (rows <= 0 || s0 > q0 + 31) continue;
+      const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
+      const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(have - 1) * kstride + D * 2;
+      const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);
+      char* dst = lds + (it & 1) * 2 * TB + wave * 1024;
+      const uint32_t ko = fresh(koff), vo = fresh(voff);
+#pragma unroll
+      for (int i = 0; i < LD; ++i) load_lds16(rk, ko + i * STEP * kstride, dst + i * kThreads * 16);
+#pragma unroll
+      for (int i = 0; i < LD; ++i) load_lds16(rv, vo + i * STEP * kstride, dst + TB + i * kThreads * 16);
+    };
 
-      f32x16 s[2];
+    // c > 0: a negative scale flips the queries' signs, a scale of 0 clears them
+    // (a masked score is -inf, which a factor of 0 would turn into NaN)
+    const float c = scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
+    bf16x8 qf[KS];
+    {
+      const int32_t have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+      const auto r = buffer(q + (int64_t(rows > 0 ? q0 : t.start) * H + h) * D,
+                            have > 0 ? int64_t(have - 1) * qstride + D * 2 : 0);
+      const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, keep = scale == 0.f ? 0u : ~0u;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        s[j] = f32x16{};
+      for (int i = 0; i < KS; ++i) {
+        i32x4 x = __builtin_bit_cast(i32x4, load8(r, uint32_t(col) * qstride + (2 * i + half) * 16));
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const bf16x8 a = *reinterpret_cast<const bf16x8*>(kt + (32 * j + krow) * (D * 2) + (((2 * i + half) ^ kx) * 16));
-          s[j] = mfma32(a, qf[i], s[j]);
-        }
+        for (int j = 0; j < 4; ++j) x[j] = int((uint32_t(x[j]) ^ flip) & keep);
+        qf[i] = __builtin_bit_cast(bf16x8, x);
       }
-      if (s0 + kBN - 1 > q0) {
-        const int32_t last = q0 + col - s0;  // the lane's query attends to keys 0 .. last of the tile
+    }
+
+    f32x16 acc[DT];
+    float m = -FLT_MAX, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+
+    // LDS addresses of this lane's operand chunks
+    const int krow = col, kx = Tile<D>::k_swz(col);
+    const int vr = 4 * half + ((lane & 15) >> 2);              // key of the transposing read (mod 8)
+    const int vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // its chunk in a 32-channel group
+    const int vb = (lane & 1) * 8;                             // its half of the chunk
+    const int vx = Tile<D>::v_swz(vr);                         // (the swizzle has period 4)
+
+    auto walk = [&](bool clean) {
+      issue(0);
+      for (int it = 0; it < n_tiles; ++it) {
+        wait_vm();
+        bar();
+        if (it + 1 < n_tiles) issue(it + 1);
+        char* kt = lds + (it & 1) * 2 * TB;
+        char* vt = kt + TB;
+        if (clean) {
+          // values that are not finite become 0
+          for (int i = tid; i < TB / 4; i += kThreads) {
+            uint32_t x = reinterpret_cast<uint32_t*>(vt)[i];
+            if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+            if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+            reinterpret_cast<uint32_t*>(vt)[i] = x;
+          }
+          __syncthreads();
+        }
+        const int32_t s0 = t.a + it * kBN;
+        if (rows <= 0 || s0 > q0 + 31) continue;
+
+        f32x16 s[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[j] = f32x16{};
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            const char* at = kt + (32 * j + krow) * (D * 2) + (((2 * i + half) ^ kx) * 16);
+            const bf16x8 a = *reinterpret_cast<const bf16x8*>(at);
+            s[j] = mfma32(a, qf[i], s[j]);
+          }
+        }
+        if (s0 + kBN - 1 > q0) {
+          const int32_t last = q0 + col - s0;  // the lane's query attends to keys 0 .. last of the tile
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              s[j][i] = 32 * j + 8 * (i / 4) + 4 * half + i % 4 <= last ? s[j][i] : -INFINITY;
+        }
+        float mx = s[0][0];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[j][i] = 32 * j + 8 * (i / 4) + 4 * half + i % 4 <= last ? s[j][i] : -INFINITY;
-      }
-      float mx = s[0][0];
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
+        mx = fmaxf(mx, other_half(mx)) * c;
+        if (__builtin_amdgcn_ballot_w64(mx > m + kGrow) != 0) {
+          const float mn = fmaxf(m, mx), f = ex2(m - mn);
+          m = mn;
+          l *= f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+          for (int i = 0; i < DT; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
-      mx = fmaxf(mx, other_half(mx)) * c;
-      if (__builtin_amdgcn_ballot_w64(mx > m + kGrow) != 0) {
-        const float mn = fmaxf(m, mx), f = ex2(m - mn);
-        m = mn;
-        l *= f;
+            for (int j = 0; j < 16; ++j) acc[i][j] *= f;
+        }
+        bf16x8 p[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = ex2(fmaf(s[j][i], c, -m));
+            l += x;
+            p[2 * j + i / 8][i % 8] = static_cast<bf16>(x);
+          }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[i][j] *= f;
+          for (int j = 0; j < 4; ++j) {
+            const char* a = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
+            acc[i] = mfma32(join(read_tr(a), read_tr(a + 8 * (D * 2))), p[j], acc[i]);
+          }
       }
-      bf16x8 p[4];
+    };
+    walk(false);
+
+    l += other_half(l);
+    const float inv = 1.f / l;
+    bool bad = false;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < DT; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float x = ex2(fmaf(s[j][i], c, -m));
-          l += x;
-          p[2 * j + i / 8][i % 8] = static_cast<bf16>(x);
-        }
+      for (int j = 0; j < 16; ++j) {
+        acc[i][j] *= inv;
+        bad |= !finite(acc[i][j]);
+      }
+    bad = bad && col < rows;
+    if (lse != nullptr && half == 0 && col < rows) lse[int64_t(h) * N + q0 + col] = m * kLn2 + logf(l);
+
+    // outputs: rows of the wave through LDS, 16-byte stores
+    const int have = rows > 32 ? 32 : rows;
+    auto put = [&](const int32_t* first_bad) {
+      char* st = lds + wave * (32 * D * 2);
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const char* a = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
-          acc[i] = mfma32(join(read_tr(a), read_tr(a + 8 * (D * 2))), p[j], acc[i]);
+          bf16x4 x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = static_cast<bf16>(acc[i][4 * j + e]);
+          const int ch = 4 * i + j;  // channels 32 i + 8 j + 4 half ..
+          *reinterpret_cast<bf16x4*>(st + col * (D * 2) + ((ch ^ (col & (CH - 1))) * 16) + half * 8) = x;
         }
+      // the wave's own rows: its LDS accesses are in order
+      asm volatile("" ::: "memory");
+      for (int i = lane; i < 32 * CH; i += 64) {
+        const int r = i / CH, ch = i % CH;
+        if (r >= have) continue;
+        const i32x4 x = *reinterpret_cast<const i32x4*>(st + r * (D * 2) + ((ch ^ (r & (CH - 1))) * 16));
+        bf16* dst = o + (int64_t(q0 + r) * H + h) * D + ch * 8;
+        if (first_bad == nullptr) {
+          *reinterpret_cast<i32x4*>(dst) = x;
+        } else {
+          const bf16x8 y = __builtin_bit_cast(bf16x8, x);
+          for (int e = 0; e < 8; ++e)
+            if (q0 + r < first_bad[ch * 8 + e]) dst[e] = y[e];
+        }
+      }
+    };
+    const bool again = __syncthreads_or(bad);  // (also: every wave is done with the tiles)
+    put(nullptr);
+    if (!again) {
+      if (hi + 1 < h1) __syncthreads();  // the outputs have left LDS
+      continue;
     }
-  };
-  walk(false);
 
-  l += other_half(l);
-  const float inv = 1.f / l;
-  bool bad = false;
+    // Some output is not finite. first_bad[d]: the first token of the segment
+    // whose value d is not; the elements before it get outputs free of it.
+    __shared__ int32_t first_bad[D];
+    for (int d = tid; d < D; d += kThreads) first_bad[d] = 0x7fffffff;
+    __syncthreads();
+    for (int32_t s = t.a + tid / D; s < qend; s += kThreads / D)
+      if (!finite(to_f32(v[(int64_t(s) * Hkv + hk) * D + tid % D]))) {
+        atomicMin(&first_bad[tid % D], s);
+        break;
+      }
+    m = -FLT_MAX;
+    l = 0.f;
 #pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      acc[i][j] *= inv;
-      bad |= !finite(acc[i][j]);
-    }
-  bad = bad && col < rows;
-  if (lse != nullptr && half == 0 && col < rows) lse[int64_t(h) * N + q0 + col] = m * kLn2 + logf(l);
-
-  // outputs: rows of the wave through LDS, 16-byte stores
-  const int have = rows > 32 ? 32 : rows;
-  auto put = [&](const int32_t* first_bad) {
-    char* st = lds + wave * (32 * D * 2);
+    for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+    __syncthreads();
+    walk(true);
+    l += other_half(l);
+    const float inv2 = 1.f / l;
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x4 x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = static_cast<bf16>(acc[i][4 * j + e]);
-        const int ch = 4 * i + j;  // channels 32 i + 8 j + 4 half ..
-        *reinterpret_cast<bf16x4*>(st + col * (D * 2) + ((ch ^ (col & (CH - 1))) * 16) + half * 8) = x;
-      }
-    // the wave's own rows: its LDS accesses are in order
-    asm volatile("" ::: "memory");
-    for (int i = lane; i < 32 * CH; i += 64) {
-      const int r = i / CH, ch = i % CH;
-      if (r >= have) continue;
-      const i32x4 x = *reinterpret_cast<const i32x4*>(st + r * (D * 2) + ((ch ^ (r & (CH - 1))) * 16));
-      bf16* dst = o + (int64_t(q0 + r) * H + h) * D + ch * 8;
-      if (first_bad == nullptr) {
-        *reinterpret_cast<i32x4*>(dst) = x;
-      } else {
-        const bf16x8 y = __builtin_bit_cast(bf16x8, x);
-        for (int e = 0; e < 8; ++e)
-          if (q0 + r < first_bad[ch * 8 + e]) dst[e] = y[e];
-      }
-    }
-  };
-  const bool again = __syncthreads_or(bad);  // (also: every wave is done with the tiles)
-  put(nullptr);
-  if (!again) {
-    if (hi + 1 < h1) __syncthreads();  // the outputs have left LDS
-    continue;
-  }
-
-  // Some output is not finite. first_bad[d]: the first token of the segment
-  // whose value d is not; the elements before it get outputs free of it.
-  __shared__ int32_t first_bad[D];
-  for (int d = tid; d < D; d += kThreads) first_bad[d] = 0x7fffffff;
-  __syncthreads();
-  for (int32_t s = t.a + tid / D; s < qend; s += kThreads / D)
-    if (!finite(to_f32(v[(int64_t(s) * Hkv + hk) * D + tid % D]))) {
-      atomicMin(&first_bad[tid % D], s);
-      break;
-    }
-  m = -FLT_MAX;
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
-  __syncthreads();
-  walk(true);
-  l += other_half(l);
-  const float inv2 = 1.f / l;
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
-  __syncthreads();
-  put(first_bad);
-  __syncthreads();
+      for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
+    __syncthreads();
+    put(first_bad);
+    __syncthreads();
   }
 }
 
@@ -315,8 +316,8 @@ bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
   const SlotGrid g = slot_grid(a.N, a.max_segs, kBM);
   const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
-  (a.D == 64 ? attn_fwd_kernel<64> : attn_fwd_kernel<128>)<<<dim3(uint32_t(slot_blocks(g, a.H) + tail_groups(a.N * a.H * a.D * 2))),
-                                                             dim3(kThreads), 0, stream>>>(
+  const dim3 blocks(uint32_t(slot_blocks(g, a.H) + tail_groups(a.N * a.H * a.D * 2)));
+  (a.D == 64 ? attn_fwd_kernel<64> : attn_fwd_kernel<128>)<<<blocks, dim3(kThreads), 0, stream>>>(
       q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
   return hipGetLastError();
 }
