@@ -40,7 +40,7 @@
 // 64-token chunks the walk took 682 us, with three stages and two work-groups per
 // compute unit 622, with the update before the middle barrier 578 instead of 562.
 // 32768 tokens in one segment, H 16, with states: 73 + 23 + 130 us. 8192 tokens,
-// H 16, forward and reverse: 0.248 ms in eight launches. 32768 tokens in documents
+// H 16, forward and reverse: 0.248 ms in seven launches. 32768 tokens in documents
 // of about 104, H 32, D 64: walks of 160, 160 and 205 us.
 
 #include "mfma.h"
