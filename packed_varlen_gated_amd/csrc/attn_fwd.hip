@@ -48,12 +48,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kBM = 128;  // queries per work-group
-constexpr int kBN = 64;   // keys per tile
 constexpr int kThreads = 256;
+// kS waves share 32 queries, each with 64 keys of a tile, their sums joined at the
+// end: kS = 1, a work-group has 128 queries; kS = 2, 64 and tiles of 128 keys.
+template <int kS>
+struct Shape {
+  static constexpr int BM = 128 / kS, BN = 64 * kS;  // queries of a work-group, keys of a tile
+};
 constexpr float kGrow = 8.f;      // log2 of what a row's maximum may grow by before O is rescaled
 
-template <int D>
+template <int D, int kBN>
 struct Tile {
   static constexpr int CH = D / 8;          // 16-byte chunks per row
   static constexpr int BYTES = kBN * D * 2;
@@ -65,13 +69,15 @@ struct Tile {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
+template <int D, int kS>
+__global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
     bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, SlotGrid grid) {
-  constexpr int CH = Tile<D>::CH, KS = D / 16, DT = D / 32, LD = kBN * CH / kThreads;
-  constexpr int TB = Tile<D>::BYTES;
+  constexpr int kBM = Shape<kS>::BM, kBN = Shape<kS>::BN;
+  using TileD = Tile<D, kBN>;
+  constexpr int CH = TileD::CH, KS = D / 16, DT = D / 32, LD = kBN * CH / kThreads;
+  constexpr int TB = TileD::BYTES;
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
   static_assert(4 * TB >= kBM * D * 2, "the outputs are staged in the tiles' buffers");
 
@@ -101,7 +107,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
     const int tid = fresh(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
     const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
-    const int32_t q0 = t.start + wave * 32;  // the wave's first query
+    const int part = wave % kS;                    // of the keys
+    const int32_t q0 = t.start + wave / kS * 32;  // the wave's first query
     const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
     const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
     const int n_tiles = (qend - t.a + kBN - 1) / kBN;
@@ -111,8 +118,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
     constexpr int STEP = kThreads / CH;
     static_assert(STEP % 16 == 0, "the swizzles repeat");
     const int lrow = tid / CH, lpos = tid % CH;
-    const uint32_t koff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::k_swz(lrow)) * 16;
-    const uint32_t voff = uint32_t(lrow) * kstride + (lpos ^ Tile<D>::v_swz(lrow)) * 16;
+    const uint32_t koff = uint32_t(lrow) * kstride + (lpos ^ TileD::k_swz(lrow)) * 16;
+    const uint32_t voff = uint32_t(lrow) * kstride + (lpos ^ TileD::v_swz(lrow)) * 16;
     auto issue = [&](int it) {
       const int32_t s0 = t.a + it * kBN;
       const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
@@ -150,11 +157,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
     for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
 
     // LDS addresses of this lane's operand chunks
-    const int krow = col, kx = Tile<D>::k_swz(col);
+    const int krow = col, kx = TileD::k_swz(col);
     const int vr = 4 * half + ((lane & 15) >> 2);              // key of the transposing read (mod 8)
     const int vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // its chunk in a 32-channel group
     const int vb = (lane & 1) * 8;                             // its half of the chunk
-    const int vx = Tile<D>::v_swz(vr);                         // (the swizzle has period 4)
+    const int vx = TileD::v_swz(vr);                         // (the swizzle has period 4)
 
     auto walk = [&](bool clean) {
       issue(0);
@@ -174,8 +181,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
           }
           __syncthreads();
         }
-        const int32_t s0 = t.a + it * kBN;
+        const int32_t s0 = t.a + it * kBN + part * 64;  // the wave's first key
         if (rows <= 0 || s0 > q0 + 31) continue;
+        kt += part * (64 * D * 2);
+        vt += part * (64 * D * 2);
 
         f32x16 s[2];
 #pragma unroll
@@ -188,7 +197,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
             s[j] = mfma32(a, qf[i], s[j]);
           }
         }
-        if (s0 + kBN - 1 > q0) {
+        if (s0 + 63 > q0) {
           const int32_t last = q0 + col - s0;  // the lane's query attends to keys 0 .. last of the tile
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -229,8 +238,39 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
           }
       }
     };
+    // the shares' sums, by their maxima
+    auto join_parts = [&] {
+      if constexpr (kS > 1) {
+        __syncthreads();  // every wave is done with the tiles
+        f32x4* at = reinterpret_cast<f32x4*>(lds) + wave / kS * (DT * 4 * 64 + 64) + lane;
+        if (part == 1) {
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              at[(4 * i + j) * 64] = f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+          at[DT * 4 * 64] = f32x4{m, l, 0.f, 0.f};
+        }
+        __syncthreads();
+        if (part == 0) {
+          const f32x4 y = at[DT * 4 * 64];
+          const float mn = fmaxf(m, y[0]), f0 = ex2(m - mn), f1 = ex2(y[0] - mn);
+          m = mn;
+          l = l * f0 + y[1] * f1;
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const f32x4 x = at[(4 * i + j) * 64];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][4 * j + e] = acc[i][4 * j + e] * f0 + x[e] * f1;
+            }
+        }
+      }
+    };
     walk(false);
 
+    join_parts();
     l += other_half(l);
     const float inv = 1.f / l;
     bool bad = false;
@@ -241,11 +281,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
         acc[i][j] *= inv;
         bad |= !finite(acc[i][j]);
       }
-    bad = bad && col < rows;
-    if (lse != nullptr && half == 0 && col < rows) lse[int64_t(h) * N + q0 + col] = m * kLn2 + logf(l);
+    bad = bad && col < rows && part == 0;
+    if (lse != nullptr && half == 0 && col < rows && part == 0) lse[int64_t(h) * N + q0 + col] = m * kLn2 + logf(l);
 
     // outputs: rows of the wave through LDS, 16-byte stores
-    const int have = rows > 32 ? 32 : rows;
+    const int have = part != 0 ? 0 : rows > 32 ? 32 : rows;
     auto put = [&](const int32_t* first_bad) {
       char* st = lds + wave * (32 * D * 2);
 #pragma unroll
@@ -297,6 +337,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
     for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
     __syncthreads();
     walk(true);
+    join_parts();
     l += other_half(l);
     const float inv2 = 1.f / l;
 #pragma unroll
@@ -313,12 +354,30 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_fwd_kernel(
 
 bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 64 || D == 128); }
 
+template <int D, int kS>
+void run(const AttnArgs& a, hipStream_t stream) {
+  const SlotGrid g = slot_grid(a.N, a.max_segs, Shape<kS>::BM);
+  const dim3 blocks(uint32_t(slot_blocks(g, a.H) + tail_groups(a.N * a.H * D * 2)));
+  attn_fwd_kernel<D, kS><<<blocks, dim3(kThreads), 0, stream>>>(
+      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v), a.cu, a.max_segs,
+      a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
+}
+
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
-  const SlotGrid g = slot_grid(a.N, a.max_segs, kBM);
-  const auto *q = static_cast<const bf16*>(a.q), *k = static_cast<const bf16*>(a.k), *v = static_cast<const bf16*>(a.v);
-  const dim3 blocks(uint32_t(slot_blocks(g, a.H) + tail_groups(a.N * a.H * a.D * 2)));
-  (a.D == 64 ? attn_fwd_kernel<64> : attn_fwd_kernel<128>)<<<blocks, dim3(kThreads), 0, stream>>>(
-      q, k, v, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
+  // With few work-groups the longest walk over the keys sets the time, and waves that
+  // share queries make it shorter; with many, or with many short walks, their joins
+  // cost more than they save. Only a single segment's length is known here. kS = 2 / 1,
+  // one segment, D 64: 1024 tokens, H 8 (64 tiles) 13.9 / 19.6 us; 4096, H 8 (256)
+  // 40.6 / 66.5; 8192, H 8 (512) 103 / 132; 8192, H 16 (1024) 190 / 176; 512, H 8
+  // 12.3 / 12.2. D 128 (one work-group per compute unit): 1024, H 8 (64) 21.4 / 26.3;
+  // 4096, H 4 (128) 62.7 / 86.1; 1024, H 32 (256) 31.4 / 28.9; 77 tokens 14.4 / 10.6.
+  // 4096 tokens in 20 segments, H 8, D 128: 27.8 / 15.1 us.
+  const int64_t tiles = a.N / 128 * a.H;
+  const bool share = a.max_segs == 1 && a.N >= 1024 && (a.D == 64 ? tiles <= 512 : tiles < 256);
+  if (a.D == 64)
+    share ? run<64, 2>(a, stream) : run<64, 1>(a, stream);
+  else
+    share ? run<128, 2>(a, stream) : run<128, 1>(a, stream);
   return hipGetLastError();
 }
 

@@ -116,6 +116,23 @@ def test_attn_one_long_segment_among_short_ones(Hq, Hkv, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,tail", [(1024, 0), (1087, 0), (1050, 130)])
+def test_attn_one_segment_of_many_tiles(N, tail, D):
+    """A single segment with few heads: waves share queries in the forward pass, 64 keys each."""
+    attn_case([N - 63 * (tail > 0)], tail, 4, 2, D, "bf16", seed=N + D)
+    attn_case([N], 0, 2, 2, D, "bf16", seed=N, scale=-0.2, amp=3.0, none=True)
+    # a later token's values reach no earlier row
+    q, k, v, do = attn_inputs(N, N, 2, 1, D, "bf16")
+    o, lse = pkv.attn_varlen(q, k, v)
+    for a in (N - 1, 700, 64):
+        x = [t.clone() for t in (q, k, v)]
+        for t in x:
+            t[0, a:a + 9] = float("nan")
+        y, z = pkv.attn_varlen(*x)
+        assert torch.equal(y[0, :a], o[0, :a]) and torch.equal(z[:, :a], lse[:, :a]), a
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_attn_none_is_one_segment(D):
     """Without cu_seqlens the form of the keys pass is chosen on the host, with it on the device: the same one."""
     for N in (100, 700, 1300):
