@@ -211,9 +211,11 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
 #pragma unroll
           for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
         mx = fmaxf(mx, other_half(mx)) * c;
-        if (__builtin_amdgcn_ballot_w64(mx > m + kGrow) != 0) {
-          const float mn = fmaxf(m, mx), f = ex2(m - mn);
-          m = mn;
+        const bool grew = mx > m + kGrow;
+        if (__builtin_amdgcn_ballot_w64(grew) != 0) {
+          // (a row that did not grow keeps its bits, whatever the wave's other rows hold)
+          const float f = grew ? ex2(m - mx) : 1.f;
+          m = grew ? mx : m;
           l *= f;
 #pragma unroll
           for (int i = 0; i < DT; ++i)
