@@ -28,8 +28,9 @@
 // A weight of 0 times a value that is not finite is NaN, so a later token's
 // value could reach an earlier one through a tile on the diagonal. When an
 // output is not finite the work-group walks the keys once more with such
-// values as 0 and stores the outputs of the elements that no such value
-// belongs to: with every value finite nothing is spent but the check.
+// values as 0, and adds to each row the infinity or NaN of its own past (the
+// weight of a finite score is above 0): with every value finite nothing is spent
+// but the check.
 //
 // Bound by the matrix and the vector units' turns: 46 % of the cycles have a
 // matrix instruction, the softmax's vector work takes about as many, and two
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
 
     // outputs: rows of the wave through LDS, 16-byte stores
     const int have = part != 0 ? 0 : rows > 32 ? 32 : rows;
-    auto put = [&](const int32_t* first_bad) {
+    auto put = [&](const int32_t* first) {
       char* st = lds + wave * (32 * D * 2);
 #pragma unroll
       for (int i = 0; i < DT; ++i)
@@ -305,15 +306,21 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
       for (int i = lane; i < 32 * CH; i += 64) {
         const int r = i / CH, ch = i % CH;
         if (r >= have) continue;
-        const i32x4 x = *reinterpret_cast<const i32x4*>(st + r * (D * 2) + ((ch ^ (r & (CH - 1))) * 16));
-        bf16* dst = o + (int64_t(q0 + r) * H + h) * D + ch * 8;
-        if (first_bad == nullptr) {
-          *reinterpret_cast<i32x4*>(dst) = x;
-        } else {
-          const bf16x8 y = __builtin_bit_cast(bf16x8, x);
-          for (int e = 0; e < 8; ++e)
-            if (q0 + r < first_bad[ch * 8 + e]) dst[e] = y[e];
+        i32x4 x = *reinterpret_cast<const i32x4*>(st + r * (D * 2) + ((ch ^ (r & (CH - 1))) * 16));
+        if (first != nullptr) {
+          // the infinities and NaN of the row's own past
+          bf16x8 y = __builtin_bit_cast(bf16x8, x);
+          for (int e = 0; e < 8; ++e) {
+            const int32_t* at = first + ch * 8 + e;
+            float z = to_f32(y[e]);
+            if (at[0] <= q0 + r) z += INFINITY;
+            if (at[D] <= q0 + r) z -= INFINITY;
+            if (at[2 * D] <= q0 + r) z = NAN;
+            y[e] = static_cast<bf16>(z);
+          }
+          x = __builtin_bit_cast(i32x4, y);
         }
+        *reinterpret_cast<i32x4*>(o + (int64_t(q0 + r) * H + h) * D + ch * 8) = x;
       }
     };
     const bool again = __syncthreads_or(bad);  // (also: every wave is done with the tiles)
@@ -323,15 +330,18 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
       continue;
     }
 
-    // Some output is not finite. first_bad[d]: the first token of the segment
-    // whose value d is not; the elements before it get outputs free of it.
-    __shared__ int32_t first_bad[D];
-    for (int d = tid; d < D; d += kThreads) first_bad[d] = 0x7fffffff;
+    // Some output is not finite. first[D x + d]: the first token of the segment
+    // whose value d is inf (x = 0), -inf (1), NaN (2).
+    __shared__ int32_t first[3 * D];
+    for (int i = tid; i < 3 * D; i += kThreads) first[i] = 0x7fffffff;
     __syncthreads();
-    for (int32_t s = t.a + tid / D; s < qend; s += kThreads / D)
-      if (!finite(to_f32(v[(int64_t(s) * Hkv + hk) * D + tid % D]))) {
-        atomicMin(&first_bad[tid % D], s);
-        break;
+    for (int kind = 0; kind < 3; ++kind)  // (one search each: a single one took the loop above its registers, 2.20 ms for 2.12)
+      for (int32_t s = t.a + tid / D; s < qend; s += kThreads / D) {
+        const float x = to_f32(v[(int64_t(s) * Hkv + hk) * D + tid % D]);
+        if (kind == 0 ? x == INFINITY : kind == 1 ? x == -INFINITY : x != x) {
+          atomicMin(&first[kind * D + tid % D], s);
+          break;
+        }
       }
     m = -FLT_MAX;
     l = 0.f;
@@ -347,7 +357,7 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
 #pragma unroll
       for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
     __syncthreads();
-    put(first_bad);
+    put(first);
     __syncthreads();
   }
 }

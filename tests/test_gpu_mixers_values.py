@@ -35,3 +35,34 @@ def test_attn_rows_go_by_their_own_scores(dtype, D, a):
             (q2 if t == "q" else k2)[0, a, :, ch] = x
             o, lse = pkv.attn_varlen(q2, k2, v, cu)
             assert torch.equal(o[0, :a], ref[0, :a]) and torch.equal(lse[:, :a], rl[:, :a]), (t, x, cu is None)
+
+
+def _with_special(ref, v, marks):
+    """Rows of o where values of v are not finite (marks: token, kv head, channel, value): ref, the rows with those
+    values finite, up to the first of them; from there on, since every weight of a token's own past is above 0, an
+    infinity of the one sign that came, or NaN."""
+    want = ref.clone()
+    rep = ref.shape[2] // v.shape[2]
+    for t, h, d, x in marks:
+        want[0, t:, h * rep:(h + 1) * rep, d] += x      # inf + -inf, and anything + NaN, is NaN
+    return want
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f32", 128), ("bf16", 32), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("s1,s2", [(70, 75), (70, 71), (64, 95), (3, 40), (40, 121), (500, 612), (1030, 1099), (0, 1)])
+def test_attn_infinity_beside_a_later_value(dtype, D, s1, s2):
+    """Row t attends to an infinity at s1 <= t and not to the value at s2 > t in its tile: it is that infinity."""
+    N = 1100
+    q, k, v, _ = attn_inputs(s1 + s2, N, 4, 2, D, dtype)
+    for cu in forms(N):
+        ref, rl = pkv.attn_varlen(q, k, v, cu)
+        for x1, x2 in ((INF, NAN), (INF, INF), (-INF, INF), (-INF, -INF), (NAN, INF)):
+            marks = [(s1, 0, 5, x1), (s2, 0, 5, x2), (s2, 1, 5, x1), (s1, 1, D - 1, x2), (s2, 0, 9, x2)]
+            v2 = v.clone()
+            for t, h, d, x in marks:
+                v2[0, t, h, d] = x
+            o, lse = pkv.attn_varlen(q, k, v2, cu)
+            want = _with_special(ref, v, marks)
+            same = (o == want) | (torch.isnan(o) & torch.isnan(want))
+            assert same.all(), (x1, x2, cu is None, torch.nonzero(~same)[:4].tolist())
+            assert torch.equal(lse, rl)
