@@ -12,9 +12,8 @@
 // head; a wave owns 32 columns of X, in fp32 registers, and of the output. The
 // in-chunk weights are formed in 16-token blocks, a block of columns per wave,
 // and shared through LDS as bf16. X is rounded to bf16 once, as the operand of
-// the readout; the update's decayed c is split into bf16 parts so that X itself
-// sees no bf16 rounding: three (24 bits) where final states, which are fp32
-// results, are asked for, two (2^-17) where X only feeds outputs.
+// the readout; the update's decayed c is split into three bf16 parts (24 bits) so
+// that X itself, an fp32 result, sees no bf16 rounding.
 //
 // Rows and columns of X are dealt to the registers so that 8 consecutive ones
 // are 8 consecutive registers of a lane (the transposing LDS reads take their
@@ -50,6 +49,7 @@ namespace pkv {
 namespace {
 
 constexpr int kC = 32;       // tokens per chunk of a walk
+constexpr int kParts = 3;    // bf16 parts of the update's c
 constexpr int kCState = 64;  // ... of a state walk
 
 template <int D>
@@ -190,7 +190,7 @@ __device__ __forceinline__ bool find_saved(const int32_t* __restrict__ cu, int32
 }
 
 // The update: X <- carry X + sum_s w_s b_s c_s^T from a chunk's tiles.
-template <int DA, int C, int kParts>
+template <int DA, int C>
 __device__ __forceinline__ void update(f32x16 (&X)[DA / 32], float carry, const bf16x8 (&cf)[C / 16], const float* w, int half,
                                        const Transposed<DA>& tb, const char* bt) {
   constexpr int TA = DA / 32;
@@ -248,7 +248,7 @@ __device__ __forceinline__ float update_weight(float scale, float g2, int s, int
 }
 
 // The state walk of one run: block blk of saved states x heads.
-template <int DA, int DB, bool kRev, int kParts>
+template <int DA, int DB, bool kRev>
 __device__ __forceinline__ void state_walk(const WalkArgs& x, const Role& R, int64_t blk, char* lds, float* upd) {
   constexpr int C = kCState, NT = 2 * DB, TA = DA / 32, SB = C * DA * 2, SC = C * DB * 2;
   const int32_t h = int32_t(blk % x.H), idx = int32_t(blk / x.H);
@@ -286,24 +286,24 @@ __device__ __forceinline__ void state_walk(const WalkArgs& x, const Role& R, int
     bf16x8 cf[C / 16];
 #pragma unroll
     for (int j = 0; j < C / 16; ++j) cf[j] = tc.read(bt + SB, wave, j);
-    update<DA, C, kParts>(X, ex2(g2 * run.len(run.chunk(it))), cf, upd + (it & 1) * C, lane >> 5, tb, bt);
+    update<DA, C>(X, ex2(g2 * run.len(run.chunk(it))), cf, upd + (it & 1) * C, lane >> 5, tb, bt);
   }
   StateAddr<DA, DB>(R.saved + (int64_t(idx) * x.H + h) * DA * DB, R.transposed, tid).store(X);
 }
 
 // Role 0 forward and, with kBoth, role 1 backward.
-template <int DA, int DB, int kParts, bool kBoth>
+template <int DA, int DB, bool kBoth>
 __global__ __launch_bounds__(2 * DB, 3) void linear_state_kernel(const WalkArgs x) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kCState * (DA + DB) * 2];
   __shared__ __attribute__((aligned(16))) float upd[2 * kCState];
   const int64_t n = x.N / x.run * x.H, blk = blockIdx.x;
   if (!kBoth || blk < n)
-    state_walk<DA, DB, false, kParts>(x, x.r[0], blk, lds, upd);
+    state_walk<DA, DB, false>(x, x.r[0], blk, lds, upd);
   else
-    state_walk<DA, DB, true, kParts>(x, x.r[1], blk - n, lds, upd);
+    state_walk<DA, DB, true>(x, x.r[1], blk - n, lds, upd);
 }
 
-template <int DA, int DB, bool kRev, int kParts, bool kPair>
+template <int DA, int DB, bool kRev, bool kPair>
 __global__ __launch_bounds__((kPair ? 4 : 2) * DB, kPair ? 2 : 3) void linear_walk_kernel(const WalkArgs x) {
   constexpr int NW = DB / 32, NT = (kPair ? 2 : 1) * 64 * NW, KA = DA / 16, TA = DA / 32;
   constexpr int SB = kC * DA * 2, SC = kC * DB * 2;
@@ -477,7 +477,7 @@ __global__ __launch_bounds__((kPair ? 4 : 2) * DB, kPair ? 2 : 3) void linear_wa
         store16(ro, uint32_t(col) * cs + 64 * wave + 16 * half + 32 * v, __builtin_bit_cast(i32x4, y));
       }
       __builtin_amdgcn_sched_barrier(0);
-      update<DA, kC, kParts>(X, ex2(g2 * n), cf, upd[(it & 1)], half, tb, bt);
+      update<DA, kC>(X, ex2(g2 * n), cf, upd[(it & 1)], half, tb, bt);
     }
 
     if (last && R.fin != nullptr)
@@ -585,19 +585,19 @@ Role role(const void* a, const void* b, const void* c, void* out, const float* i
 }
 
 // Own end states of the runs, then the states before them, of one or both roles.
-template <int DA, int DB, int kParts, bool kBoth>
+template <int DA, int DB, bool kBoth>
 void states(const WalkArgs& x, hipStream_t stream) {
   const int32_t count = int32_t(x.N / x.run), size = DA * DB;
-  linear_state_kernel<DA, DB, kParts, kBoth><<<dim3(uint32_t(int64_t(count) * x.H * (kBoth ? 2 : 1))), dim3(2 * DB), 0,
+  linear_state_kernel<DA, DB, kBoth><<<dim3(uint32_t(int64_t(count) * x.H * (kBoth ? 2 : 1))), dim3(2 * DB), 0,
                                                stream>>>(x);
   linear_scan_kernel<<<dim3(uint32_t(x.H * (size / (4 * kScan)) * (kBoth ? 2 : 1))), dim3(kScan), 0, stream>>>(x, size,
                                                                                                                count);
 }
 
-template <int DA, int DB, bool kRev, int kParts, bool kPair>
+template <int DA, int DB, bool kRev, bool kPair>
 void walk(const WalkArgs& x, hipStream_t stream) {
   const int64_t tail = x.N * x.H * DB * 2 + (x.r[0].fin ? int64_t(x.max_segs) * x.H * DA * DB * 4 : 0);
-  linear_walk_kernel<DA, DB, kRev, kParts, kPair>
+  linear_walk_kernel<DA, DB, kRev, kPair>
       <<<dim3(uint32_t(slot_blocks(x.grid, x.H) + tail_groups(tail))), dim3((kPair ? 4 : 2) * DB), 0, stream>>>(x);
 }
 
@@ -614,16 +614,16 @@ WalkArgs common(const LinearArgs& y) {
   return x;
 }
 
-template <int DK, int DV, int kParts>
+template <int DK, int DV>
 hipError_t fwd(const LinearArgs& y, hipStream_t s) {
   WalkArgs x = common(y);
   x.r[0] = role(y.q, y.k, y.v, y.o, y.initial_state, static_cast<float*>(y.workspace), y.final_state, 1.f, y.scale, false);
-  if (y.N > x.run) states<DK, DV, kParts, false>(x, s);
-  walk<DK, DV, false, kParts, false>(x, s);
+  if (y.N > x.run) states<DK, DV, false>(x, s);
+  walk<DK, DV, false, false>(x, s);
   return hipGetLastError();
 }
 
-template <int DK, int DV, int kParts>
+template <int DK, int DV>
 hipError_t bwd(const LinearArgs& y, const LinearGradArgs& z, hipStream_t s) {
   WalkArgs x = common(y);
   float* saved = static_cast<float*>(y.workspace);
@@ -631,32 +631,23 @@ hipError_t bwd(const LinearArgs& y, const LinearGradArgs& z, hipStream_t s) {
   if (y.N > x.run) {
     x.r[0] = role(nullptr, y.k, y.v, nullptr, y.initial_state, saved, nullptr, 1.f, 1.f, false);
     x.r[1] = role(nullptr, y.q, z.dout, nullptr, z.dfinal_state, adjoint, nullptr, y.scale, 1.f, false);
-    states<DK, DV, kParts, true>(x, s);
+    states<DK, DV, true>(x, s);
   }
   const Role dq = role(z.dout, y.v, y.k, z.dq, y.initial_state, saved, nullptr, 1.f, y.scale, true);
   const Role dv = role(y.k, y.q, z.dout, z.dv, z.dfinal_state, adjoint, z.d_initial_state, y.scale, 1.f, false);
   const Role dk = role(y.v, z.dout, y.q, z.dk, z.dfinal_state, adjoint, nullptr, y.scale, 1.f, true);
   x.r[0] = dq;
-  walk<DV, DK, false, 2, false>(x, s);
+  walk<DV, DK, false, false>(x, s);
   x.r[0] = dv;
   if constexpr (DK == DV) {
     x.r[1] = dk;
-    walk<DK, DV, true, kParts, true>(x, s);
+    walk<DK, DV, true, true>(x, s);
   } else {
-    walk<DK, DV, true, kParts, false>(x, s);
+    walk<DK, DV, true, false>(x, s);
     x.r[0] = dk;
-    walk<DV, DK, true, 2, false>(x, s);
+    walk<DV, DK, true, false>(x, s);
   }
   return hipGetLastError();
-}
-
-template <int DK, int DV>
-hipError_t fwd(const LinearArgs& y, hipStream_t s) {
-  return y.final_state ? fwd<DK, DV, 3>(y, s) : fwd<DK, DV, 2>(y, s);
-}
-template <int DK, int DV>
-hipError_t bwd(const LinearArgs& y, const LinearGradArgs& z, hipStream_t s) {
-  return z.d_initial_state ? bwd<DK, DV, 3>(y, z, s) : bwd<DK, DV, 2>(y, z, s);
 }
 
 }  // namespace

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import packed_varlen_gated_amd as pkv
-from test_gpu_mixers import attn_inputs, cu_gpu
+from test_gpu_mixers import attn_inputs, cu_gpu, lay, linear_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,21 @@ def test_attn_infinity_beside_a_later_value(dtype, D, s1, s2):
             same = (o == want) | (torch.isnan(o) & torch.isnan(want))
             assert same.all(), (x1, x2, cu is None, torch.nonzero(~same)[:4].tolist())
             assert torch.equal(lse, rl)
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv", [("f32", 32, 64), ("bf16", 32, 32), ("bf16", 64, 64), ("bf16", 128, 128),
+                                         ("bf16", 64, 128), ("bf16", 128, 64)])
+@pytest.mark.parametrize("states", [False, True])
+def test_linear_results_do_not_go_by_what_else_is_asked_for(dtype, Dk, Dv, states):
+    """The same o with and without the final state, the same gradients with and without the initial state's."""
+    N, cu = lay([700, 0, 33, 900], 7)
+    q, k, v, do, g, S0, dF = linear_inputs(7, N, 3, Dk, Dv, dtype, 4 if states else 0)
+    c = cu_gpu(cu)
+    a, fs = pkv.chunk_linear_attn_varlen(q, k, v, g, c, 0.5, initial_state=S0)
+    b, none = pkv.chunk_linear_attn_varlen(q, k, v, g, c, 0.5, initial_state=S0, output_final_state=False)
+    assert none is None and fs is not None and torch.equal(a, b)
+    x, y = (pkv.chunk_linear_attn_varlen_backward(q, k, v, g, do, c, 0.5, initial_state=S0, dfinal_state=dF,
+                                                  output_d_initial_state=w) for w in (True, False))
+    assert y.d_initial_state is None
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(getattr(x, n), getattr(y, n)), n
