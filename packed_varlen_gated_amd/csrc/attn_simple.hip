@@ -400,27 +400,20 @@ hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 
 }  // namespace
 
+// bf16: D = 32 alone (64 and 128 are attn_fwd.hip's and attn_bwd.hip's).
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream) {
-  if (dtype == 1) {
-    if (a.D == 32) return fwd<float, 32>(a, stream);
-    if (a.D == 64) return fwd<float, 64>(a, stream);
-    return fwd<float, 128>(a, stream);
-  }
-  if (a.D == 32) return fwd<bf16, 32>(a, stream);
-  if (a.D == 64) return fwd<bf16, 64>(a, stream);
-  return fwd<bf16, 128>(a, stream);
+  if (dtype == 0) return a.D == 32 ? fwd<bf16, 32>(a, stream) : hipErrorInvalidValue;
+  if (a.D == 32) return fwd<float, 32>(a, stream);
+  if (a.D == 64) return fwd<float, 64>(a, stream);
+  return fwd<float, 128>(a, stream);
 }
 
 hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g, int32_t dtype,
                                        hipStream_t stream) {
-  if (dtype == 1) {
-    if (a.D == 32) return bwd<float, 32>(a, g, stream);
-    if (a.D == 64) return bwd<float, 64>(a, g, stream);
-    return bwd<float, 128>(a, g, stream);
-  }
-  if (a.D == 32) return bwd<bf16, 32>(a, g, stream);
-  if (a.D == 64) return bwd<bf16, 64>(a, g, stream);
-  return bwd<bf16, 128>(a, g, stream);
+  if (dtype == 0) return a.D == 32 ? bwd<bf16, 32>(a, g, stream) : hipErrorInvalidValue;
+  if (a.D == 32) return bwd<float, 32>(a, g, stream);
+  if (a.D == 64) return bwd<float, 64>(a, g, stream);
+  return bwd<float, 128>(a, g, stream);
 }
 
 }  // namespace pkv

@@ -186,28 +186,41 @@ hipError_t bwd(const LinearArgs& x, const LinearGradArgs& y, hipStream_t s) {
   return hipGetLastError();
 }
 
-#define PKV_LINEAR_DISPATCH(fn, T, ...)                           \
+// The pairs with a dimension of 32, for either type, and the others, for fp32 alone
+// (with bf16 they are linear_chunk.hip's).
+#define PKV_LINEAR_32(fn, T, ...)                                     \
   if (x.Dk == 32 && x.Dv == 32) return fn<T, 32, 32>(__VA_ARGS__);    \
   if (x.Dk == 32 && x.Dv == 64) return fn<T, 32, 64>(__VA_ARGS__);    \
   if (x.Dk == 32 && x.Dv == 128) return fn<T, 32, 128>(__VA_ARGS__);  \
   if (x.Dk == 64 && x.Dv == 32) return fn<T, 64, 32>(__VA_ARGS__);    \
+  if (x.Dk == 128 && x.Dv == 32) return fn<T, 128, 32>(__VA_ARGS__)
+#define PKV_LINEAR_64(fn, T, ...)                                     \
   if (x.Dk == 64 && x.Dv == 64) return fn<T, 64, 64>(__VA_ARGS__);    \
   if (x.Dk == 64 && x.Dv == 128) return fn<T, 64, 128>(__VA_ARGS__);  \
-  if (x.Dk == 128 && x.Dv == 32) return fn<T, 128, 32>(__VA_ARGS__);  \
   if (x.Dk == 128 && x.Dv == 64) return fn<T, 128, 64>(__VA_ARGS__);  \
-  return fn<T, 128, 128>(__VA_ARGS__)
+  if (x.Dk == 128 && x.Dv == 128) return fn<T, 128, 128>(__VA_ARGS__)
 
 }  // namespace
 
 hipError_t launch_linear_serial(const LinearArgs& x, int32_t dtype, hipStream_t stream) {
-  if (dtype == 1) { PKV_LINEAR_DISPATCH(fwd, float, x, stream); }
-  PKV_LINEAR_DISPATCH(fwd, bf16, x, stream);
+  if (dtype == 0) {
+    PKV_LINEAR_32(fwd, bf16, x, stream);
+  } else {
+    PKV_LINEAR_32(fwd, float, x, stream);
+    PKV_LINEAR_64(fwd, float, x, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_linear_serial_backward(const LinearArgs& x, const LinearGradArgs& y, int32_t dtype,
                                          hipStream_t stream) {
-  if (dtype == 1) { PKV_LINEAR_DISPATCH(bwd, float, x, y, stream); }
-  PKV_LINEAR_DISPATCH(bwd, bf16, x, y, stream);
+  if (dtype == 0) {
+    PKV_LINEAR_32(bwd, bf16, x, y, stream);
+  } else {
+    PKV_LINEAR_32(bwd, float, x, y, stream);
+    PKV_LINEAR_64(bwd, float, x, y, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace pkv
