@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import packed_varlen_gated_amd as pkv
-from test_gpu_mixers import attn_inputs, cu_gpu, lay, linear_inputs
+from mixer_states import state_bound
+from test_gpu_mixers import attn_inputs, cu_gpu, host, lay, linear_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,25 @@ def test_linear_results_do_not_go_by_what_else_is_asked_for(dtype, Dk, Dv, state
     assert y.d_initial_state is None
     for n in ("dq", "dk", "dv"):
         assert torch.equal(getattr(x, n), getattr(y, n)), n
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+def test_linear_states_of_bf16_calls_are_fp32(Dk, Dv):
+    lens, g = [31, 300, 0, 700, 90, 32], [-0.01, -0.05, -0.3]
+    N, cu = lay(lens, 9)
+    q, k, v, do, _, _, _ = linear_inputs(9, N, 3, Dk, Dv, "bf16")
+    gd = torch.tensor(g, dtype=torch.float32, device=q.device)
+    _, fs = pkv.chunk_linear_attn_varlen(q, k, v, gd, cu_gpu(cu), 0.3)
+    gr = pkv.chunk_linear_attn_varlen_backward(q, k, v, gd, do, cu_gpu(cu), 0.3, output_d_initial_state=True)
+    hq, hk, hv, hdo = (host(t)[0] for t in (q, k, v, do))
+    gs = host(gd)
+    for i, n in enumerate(lens):
+        s = slice(int(cu[i]), int(cu[i]) + n)
+        for h in range(3):
+            w = np.exp(gs[h] * np.arange(n - 1, -1, -1))
+            want = {"final": (hk[s, h] * w[:, None]).T @ hv[s, h],
+                    "dinit": 0.3 * (hq[s, h] * np.exp(gs[h]) * w[::-1, None]).T @ hdo[s, h]}
+            for name, got in (("final", fs), ("dinit", gr.d_initial_state)):
+                x = host(got[i, h])
+                rel = np.linalg.norm(x - want[name]) / max(np.linalg.norm(want[name]), 1e-30)
+                assert rel <= state_bound(n, g[h]) if n else not x.any(), (name, n, g[h], rel)
