@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import packed_varlen_gated_amd as pkv
+from mixer_parity import check, linear_bounds
 from mixer_states import state_bound
-from test_gpu_mixers import attn_inputs, cu_gpu, host, lay, linear_inputs
+from test_gpu_mixers import attn_case, attn_inputs, cu_gpu, host, lay, linear_case, linear_inputs, linear_run
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,42 @@ def test_linear_states_of_bf16_calls_are_fp32(Dk, Dv):
                 x = host(got[i, h])
                 rel = np.linalg.norm(x - want[name]) / max(np.linalg.norm(want[name]), 1e-30)
                 assert rel <= state_bound(n, g[h]) if n else not x.any(), (name, n, g[h], rel)
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 32)])
+def test_attn_off_the_bf16_matrix_path_long(dtype, D):
+    attn_case([2100, 0, 300], 5, 2, 1, D, dtype, seed=D)
+    attn_case([1999], 0, 2, 2, D, dtype, seed=D + 1, none=True)
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv", [("f32", 64, 64), ("f32", 32, 128), ("bf16", 32, 32), ("bf16", 128, 32)])
+def test_linear_token_by_token_long(dtype, Dk, Dv):
+    linear_case([2500, 0, 41], 6, 2, Dk, Dv, dtype, True, seed=Dk)
+
+
+@pytest.mark.parametrize("states", [False, True])
+@pytest.mark.parametrize("dtype,Dk,Dv", [("f32", 64, 64), ("bf16", 32, 64), ("bf16", 64, 64), ("bf16", 128, 128),
+                                         ("bf16", 64, 128)])
+def test_linear_growing_states(dtype, Dk, Dv, states):
+    """Log decays above 0. A weight e^{g t} is off by 2 g t e for its argument, at most n e for g <= 0.5 and 2 n e for
+    0.8: the bound's gamma(4 (n + Dk + Dv) + 64) allows for 4 n roundings where the sums have 3 n, and 4 (Dk + Dv) + 64
+    more than n at these lengths.
+
+    Element by element only. The normwise bound of mixer_parity.py takes a result for many independent roundings of
+    like size; here 1 / (2 g) rows and, in each, 1 / (2 g) terms make the norm, one of each at g = 0.8, and a row with
+    one term s is (a_t.b_s) w rounded once times c_s, rounded again: off by up to 2^-8 as a whole and 2^-8 per element,
+    where the normwise bound allows for sqrt(3) times 2^-8 / sqrt(3). The element-wise bound has just these two."""
+    for lens, tail, g, scale in (([70, 33, 0, 64], 3, [0.01, 0.2, 0.8], 0.5), ([700, 5], 0, [0.02, 0.05], 1.0)):
+        N, cu = lay(lens, tail)
+        H, end = len(g), int(cu[-1])
+        q, k, v, do, _, S0, dF = linear_inputs(0, N, H, Dk, Dv, dtype, len(lens) if states else 0)
+        gd = torch.tensor(g, dtype=torch.float32, device=q.device)
+        got = linear_run(q, k, v, do, gd, S0, dF, cu_gpu(cu), scale)
+        want = linear_bounds(host(q)[0], host(k)[0], host(v)[0], host(gd), host(do)[0], cu, scale, host(S0), host(dF),
+                             dtype)
+        for name, (ref, bound) in want.items():
+            x = host(got[name])
+            if name not in ("final", "dinit"):
+                assert not x[0, end:].any(), name
+                x = x[0]
+            check(x, ref, bound, "f32", name)      # (no normwise bound)
