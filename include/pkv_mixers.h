@@ -27,7 +27,9 @@
  * cu_seqlens sets PKV_FLAG_BAD_CU_SEQLENS and leaves the outputs undefined;
  * nothing outside the tensors is read or written. No result of a segment
  * depends on the values of another segment, NaN and infinities included, and
- * equal calls give equal bits.
+ * equal calls give equal bits. The order of a sum may go by the call's sizes
+ * (N, max_segs, heads), so the same segment in another call may differ in its
+ * last bits.
  */
 #ifndef PKV_MIXERS_H
 #define PKV_MIXERS_H
@@ -53,7 +55,9 @@ extern "C" {
  * lse    float32 [Hq, N] or NULL (not written); the reverse pass needs it.
  * flags  int32 [1] or NULL; PKV_FLAG_BAD_CU_SEQLENS is OR-ed in.
  * Scores, softmax statistics and sums are fp32; with bf16 and D in {64, 128}
- * the weights are rounded to bf16 for the product with v.
+ * the weights are rounded to bf16 for the product with v. A row goes by the
+ * tokens up to its own alone: NaN, infinities and large values in later ones
+ * leave its bits as they are.
  * Supported: D in {32, 64, 128}. Errors: PKV_ERR_INVALID_ARGUMENT for a NULL
  * tensor, N < 1, N > INT32_MAX, Hq or Hkv < 1 or > 65536, Hq not a multiple of
  * Hkv, max_segs < 1 (with cu_seqlens), (N / 32 + max_segs) Hq >= 2^23, a
@@ -72,7 +76,8 @@ pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const in
  *   dq_t = scale sum_s dS_ts k_s
  *   dk_s = scale sum_t dS_ts q_t,  dv_s = sum_t P_ts do_t,
  * dk and dv summed over the query heads of their kv head, in an order that the
- * sizes and the segments' lengths fix.
+ * sizes and the segments' lengths fix. Sums, delta and dS are fp32; with bf16 and
+ * D in {64, 128} P and dS are rounded to bf16 for their products (dv; dq, dk).
  * A segment with NaN or infinities may have them anywhere in its gradients.
  * workspace  at least pkv_attn_varlen_backward_workspace_size() bytes, 256-byte
  *            aligned; scratch.
@@ -107,7 +112,8 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
  * With bf16 and Dk, Dv in {64, 128} the call works in chunks of 32 tokens:
  * states and sums are fp32, the in-chunk weights and, for the readout, the
  * state are rounded to bf16; NaN and infinities reach no other segment, but
- * may reach earlier tokens of their own chunk. Weights below 2^-150 are 0.
+ * may reach earlier tokens of their own chunk. Decay weights below 2^-126 are 0.
+ * Asking for the states or not changes no bit of the other results.
  * Supported: Dk, Dv in {32, 64, 128}. Errors: as pkv_attn_varlen with H in
  * place of the heads, max_segs * H > 2^22; PKV_ERR_WORKSPACE.
  */
@@ -128,6 +134,7 @@ pkv_status pkv_linear_attn_varlen(const void* q, const void* k, const void* v, c
  *   dq_t = scale * S_t do_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t
  *   d_initial_state = e^{g} dS_first (dfinal_state for an empty slot)
  * d_initial_state  float32 [max_segs, H, Dk, Dv] or NULL (not written).
+ * Roundings as in the forward call, the adjoint state dS like the state.
  */
 size_t pkv_linear_attn_varlen_backward_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv,
                                                       int32_t max_segs, int32_t dtype);

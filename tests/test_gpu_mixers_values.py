@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import packed_varlen_gated_amd as pkv
-from mixer_parity import check, linear_bounds
+from mixer_parity import check, gamma, half_step, linear_bounds
 from mixer_states import state_bound
 from test_gpu_mixers import attn_case, attn_inputs, cu_gpu, host, lay, linear_case, linear_inputs, linear_run
 
@@ -147,3 +147,20 @@ def test_linear_growing_states(dtype, Dk, Dv, states):
                 assert not x[0, end:].any(), name
                 x = x[0]
             check(x, ref, bound, "f32", name)      # (no normwise bound)
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 32), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("e", [60, 120, 125])
+def test_linear_small_decay_weights(dtype, D, e):
+    """A decay weight of 2^-e still counts: one token's large value, read by the next. The value 2^120 is exact, the
+    weight is off by 4 e32 for exp and 2 e32 of its argument (e ln 2 < 87: 174 e32), o by its rounding besides."""
+    q, k, v, _ = (torch.zeros_like(t) for t in attn_inputs(0, 2, 1, 1, D, dtype))
+    k[0, 0, 0, 0] = 1.0
+    q[0, 1, 0, 0] = 1.0
+    v[0, 0, 0, 3] = 2.0 ** 120
+    g = torch.tensor([-e * np.log(2)], dtype=torch.float32, device=q.device)
+    o, fs = pkv.chunk_linear_attn_varlen(q, k, v, g)
+    want = 2.0 ** 120 * np.exp(float(g[0]))
+    rel = gamma(180)
+    assert abs(float(fs[0, 0, 0, 3]) - want) <= rel * want
+    assert abs(float(o[0, 1, 0, 3]) - want) <= (rel + 2.01 * half_step(dtype)) * want
