@@ -36,10 +36,9 @@
 // matrix instruction, the softmax's vector work takes about as many, and two
 // work-groups per compute unit (the sums and Q take 192 registers at D 128) do not
 // hide all of one under the other. 65536 tokens in documents of up to 8192, H 32,
-// Hkv 8, D 128: 2.11-2.21 ms, 867-910 TFLOP/s of causal products (a large matrix
-// product reaches 1220 here, 1.57 ms); 16384 in one document 787 TFLOP/s forward and
-// reverse; 77 tokens, H 16: 8.8 us. A raised wave priority around the products made
-// the first 2.31 ms.
+// Hkv 8, D 128: 2.06-2.15 ms, 893-932 TFLOP/s of causal products (a large matrix
+// product reaches 1220 here, 1.57 ms); 77 tokens, H 16: 8.5-9.0 us. A raised wave
+// priority around the products made the first 2.31 ms.
 
 #include "mfma.h"
 #include "segments.h"
@@ -378,12 +377,14 @@ void run(const AttnArgs& a, hipStream_t stream) {
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
   // With few work-groups the longest walk over the keys sets the time, and waves that
   // share queries make it shorter; with many, or with many short walks, their joins
-  // cost more than they save. Only a single segment's length is known here. kS = 2 / 1,
-  // one segment, D 64: 1024 tokens, H 8 (64 tiles) 13.9 / 19.6 us; 4096, H 8 (256)
-  // 40.6 / 66.5; 8192, H 8 (512) 103 / 132; 8192, H 16 (1024) 190 / 176; 512, H 8
-  // 12.3 / 12.2. D 128 (one work-group per compute unit): 1024, H 8 (64) 21.4 / 26.3;
-  // 4096, H 4 (128) 62.7 / 86.1; 1024, H 32 (256) 31.4 / 28.9; 77 tokens 14.4 / 10.6.
-  // 4096 tokens in 20 segments, H 8, D 128: 27.8 / 15.1 us.
+  // cost more than they save. Only the length of a call's one slot is known here, and
+  // taken for N: a prompt with empty slots behind it takes kS = 1. kS = 2 / 1,
+  // one segment, D 64: 1024 tokens, H 8 (64 tiles) 12.9 / 19.7 us; 4096, H 8 (256)
+  // 40.0 / 65.1; 8192, H 8 (512) 98 / 129; 8192, H 16 (1024) 187 / 172; 512, H 8
+  // 10.4 / 12.2 (8 to 10 of them the host's). D 128 (one work-group per compute unit):
+  // 1024, H 8 (64) 19.8 / 25.0; 4096, H 4 (128) 58.5 / 82.5; 1024, H 32 (256)
+  // 28.8 / 26.9; 77 tokens 10.0 / 10.0. 4096 tokens in 20 segments, H 8, D 128:
+  // 27.6 / 14.3 us.
   const int64_t tiles = a.N / 128 * a.H;
   const bool share = a.max_segs == 1 && a.N >= 1024 && (a.D == 64 ? tiles <= 512 : tiles < 256);
   if (a.D == 64)

@@ -34,13 +34,14 @@
 // length depends on the call's sizes only.
 //
 // Bound by the chain of dependent steps of a chunk: the walk of 65536 tokens, H 32,
-// D 128 takes 548 us for 2.15 GB (413 us at a copy's rate), waiting 54 % of its
-// cycles, behind 123 us of run states and 19 us of their scan: 0.659 ms the call. With
-// 64-token chunks the walk took 682 us, with three stages and two work-groups per
+// D 128 takes 567 us for 2.15 GB (413 us at a copy's rate), waiting 52 % of its
+// cycles, behind 135 us of run states and 19 us of their scan: 0.680-0.688 ms the call
+// (with two parts in the update, 2^-17, 548 + 123 + 19 us and 0.660 ms). With 64-token
+// chunks the walk of two parts took 682 us, with three stages and two work-groups per
 // compute unit 622, with the update before the middle barrier 578 instead of 562.
-// 32768 tokens in one segment, H 16, with states: 73 + 23 + 130 us. 8192 tokens,
-// H 16, forward and reverse: 0.248 ms in seven launches. 32768 tokens in documents
-// of about 104, H 32, D 64: walks of 160, 160 and 205 us.
+// 32768 tokens in one segment, H 16, with states: 75 + 23 + 131 us. 8192 tokens,
+// H 16, forward and reverse: 0.264 ms in seven launches. 32768 tokens in documents
+// of about 104, H 32, D 64: walks of 167, 167 and 218 us.
 
 #include "mfma.h"
 #include "segments.h"
@@ -49,8 +50,8 @@ namespace pkv {
 namespace {
 
 constexpr int kC = 32;       // tokens per chunk of a walk
-constexpr int kParts = 3;    // bf16 parts of the update's c
 constexpr int kCState = 64;  // ... of a state walk
+constexpr int kParts = 3;    // bf16 parts of the update's c
 
 template <int D>
 struct Rows {  // an LDS tile of a chunk's rows of D channels
@@ -570,8 +571,8 @@ __global__ __launch_bounds__(kScan) void linear_scan_kernel(const WalkArgs x, in
 // [256, 4096]. Shorter runs keep more work-groups busy but save, scan and read
 // back more states (their number times their length is N H). Measured, us at
 // runs of 512 / 1024 / 2048: N H = 2^21 (65536 tokens, 39 segments, 32 heads of
-// 128): 867 / 721 / 661; 2^19 (one segment of 32768, 16 heads): 248 / 210 / 289;
-// 2^17 (8192 tokens, forward and reverse): 248 / 334 / 603 (256: 263).
+// 128): 883 / 742 / 680; 2^19 (one segment of 32768, 16 heads): 246 / 207 / 281;
+// 2^17 (8192 tokens, forward and reverse): 265 / 353 / 641 (256: 277).
 int32_t run_tokens(int64_t N, int32_t H) {
   int32_t r = 256;
   while (r < 4096 && int64_t(r) * r < N * H * 3 / 2) r *= 2;

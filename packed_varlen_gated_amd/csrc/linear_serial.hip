@@ -22,8 +22,8 @@
 // partial readouts are summed over the 16 row groups. The three walks of the reverse
 // pass are one launch where Dk = Dv. The chain of tokens bounds it, 80 to 180 ns each;
 // these are the shapes that models are debugged on. One segment of 4096 tokens, fp32,
-// forward / reverse: H 4, D 64 436 / 467 us, H 16, D 128 725 / 1114 us; 512 tokens,
-// H 4, D 32 41 / 41 us. With all columns in one work-group and three launches
+// forward / reverse: H 4, D 64 437 / 456 us, H 16, D 128 724 / 1108 us; bf16, H 16, D 32
+// 330 / 344 us; 512 tokens, H 4, D 32, fp32 41 / 41 us. With all columns in one work-group and three launches
 // 1482 / 4521, 5045 / 15007 and 73 / 221 us.
 
 #include "segments.h"
