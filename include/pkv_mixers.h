@@ -112,7 +112,8 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
  * With bf16 and Dk, Dv in {64, 128} the call works in chunks of 32 tokens:
  * states and sums are fp32, the in-chunk weights and, for the readout, the
  * state are rounded to bf16; NaN and infinities reach no other segment, but
- * may reach earlier tokens of their own chunk. Decay weights below 2^-126 are 0.
+ * may reach earlier tokens of their own chunk, and an infinity may become NaN.
+ * Decay weights below 2^-126 are 0.
  * Asking for the states or not changes no bit of the other results.
  * Supported: Dk, Dv in {32, 64, 128}. Errors: as pkv_attn_varlen with H in
  * place of the heads, max_segs * H > 2^22; PKV_ERR_WORKSPACE.

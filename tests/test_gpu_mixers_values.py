@@ -164,3 +164,52 @@ def test_linear_small_decay_weights(dtype, D, e):
     rel = gamma(180)
     assert abs(float(fs[0, 0, 0, 3]) - want) <= rel * want
     assert abs(float(o[0, 1, 0, 3]) - want) <= (rel + 2.01 * half_step(dtype)) * want
+
+
+@pytest.mark.parametrize("Hkv", [65536, 4096])
+def test_attn_most_heads(Hkv):
+    """65536 heads of 128: rows 16 MiB apart, so a tile of 128 spans almost 2^31 bytes. A few heads equal a call of
+    their own with as many per kv head; dk and dv as one of two sum orders (test_offsets_past_32_bits)."""
+    H, N, D, rep = 65536, 130, 128, 65536 // Hkv
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v, do = (torch.empty(1, N, h, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+                   for h in (H, Hkv, Hkv, H))
+    o, lse = pkv.attn_varlen(q, k, v)
+    gr = pkv.attn_varlen_backward(q, k, v, o, lse, do)
+    for a in (0, 777 % Hkv, Hkv - 1):
+        hs = slice(a * rep, (a + 1) * rep)
+        q1, do1 = (t[:, :, hs].contiguous() for t in (q, do))
+        k1, v1 = (t[:, :, a:a + 1].contiguous() for t in (k, v))
+        o1, lse1 = pkv.attn_varlen(q1, k1, v1)
+        gr1 = pkv.attn_varlen_backward(q1, k1, v1, o1, lse1, do1)
+        assert torch.equal(o[:, :, hs], o1) and torch.equal(lse[hs], lse1) and torch.equal(gr.dq[:, :, hs], gr1.dq)
+        hq, hdo = (t[0].double().transpose(0, 1) for t in (q1, do1))
+        hk, hv = k1[0, :, 0].double(), v1[0, :, 0].double()
+        P = torch.softmax((hq @ hk.T / D ** 0.5).masked_fill(torch.ones(N, N, device="cuda").triu(1).bool(), -INF), -1)
+        dP = hdo @ hv.T
+        dS = (P * (dP - (P * dP).sum(-1, keepdim=True))).abs() / D ** 0.5
+        for name, t in (("dk", (dS.transpose(1, 2) @ hq.abs()).sum(0)), ("dv", (P.transpose(1, 2) @ hdo.abs()).sum(0))):
+            x, y = getattr(gr, name)[0, :, a].double(), getattr(gr1, name)[0, :, 0].double()
+            # (1.02: P and dS are bf16 there)
+            bound = 2.0 ** -7 * torch.maximum(x.abs(), y.abs()) + 2 * gamma(rep * N) * 1.02 * t
+            assert ((x - y).abs() <= bound).all(), (name, a)
+
+
+def test_linear_most_heads():
+    H, N, D = 65536, 130, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v, do = (torch.empty(1, N, H, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(4))
+    g = torch.linspace(-2, 0, H, device="cuda")
+    cu = cu_gpu([0, 67, 67, 129])
+    S0 = torch.empty(3, H, D, D, device="cuda").normal_(generator=gen)
+    o, fs = pkv.chunk_linear_attn_varlen(q, k, v, g, cu, initial_state=S0)
+    gr = pkv.chunk_linear_attn_varlen_backward(q, k, v, g, do, cu, initial_state=S0, dfinal_state=S0)
+    hs = torch.tensor([0, 777, H - 1], device="cuda")
+    one = [t[:, :, hs].contiguous() for t in (q, k, v, do)]
+    o1, fs1 = pkv.chunk_linear_attn_varlen(*one[:3], g[hs], cu, initial_state=S0[:, hs].contiguous())
+    gr1 = pkv.chunk_linear_attn_varlen_backward(*one[:3], g[hs], one[3], cu, initial_state=S0[:, hs].contiguous(),
+                                                dfinal_state=S0[:, hs].contiguous())
+    assert torch.equal(o[:, :, hs], o1) and torch.equal(fs[:, hs], fs1)
+    for a, b in zip(gr[:3], gr1[:3]):
+        assert torch.equal(a[:, :, hs], b)
+    assert torch.equal(gr.d_initial_state[:, hs], gr1.d_initial_state)
