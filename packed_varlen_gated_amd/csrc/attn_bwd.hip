@@ -233,6 +233,27 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const float lse2 = rd.col < have ? lse[row] * kLog2e : 0.f;
 
     const float c = scale * kLog2e;
+    if (t.start == t.a) {
+      // A segment's first 32 queries have all their keys in the first block: delta is
+      // the sum of P dP there, without the rounding of o, which is as large as what
+      // is left of dq where a row has few keys.
+      wait_vm();
+      bar();
+      if (wave == 0) {
+        const uint32_t kt = lds_addr(lds), vt = kt + TB;
+        f32x16 s = {}, dp = {};
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          s = mfma32(rd.rows(kt, 0, i), qf[i], s);
+          dp = mfma32(rd.rows(vt, 0, i), df[i], dp);
+        }
+        delta = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          delta += 8 * (i / 4) + i % 4 <= rd.col - 4 * rd.half ? ex2(fmaf(s[i], c, -lse2)) * dp[i] : 0.f;
+        delta += other_half(delta);
+      }
+    }
     float rest = 0.f;  // sum_s dS_ts
     f32x16 acc[DT];
 #pragma unroll

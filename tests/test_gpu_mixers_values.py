@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import packed_varlen_gated_amd as pkv
-from mixer_parity import check, gamma, half_step, linear_bounds
+from mixer_parity import E32, check, gamma, half_step, linear_bounds
 from mixer_states import state_bound
 from test_gpu_mixers import attn_case, attn_inputs, cu_gpu, host, lay, linear_case, linear_inputs, linear_run
 
@@ -213,3 +213,49 @@ def test_linear_most_heads():
     for a, b in zip(gr[:3], gr1[:3]):
         assert torch.equal(a[:, :, hs], b)
     assert torch.equal(gr.d_initial_state[:, hs], gr1.d_initial_state)
+
+
+def _dq_bound(q, k, v, do, n, scale, u):
+    """dq of a segment's first n tokens, and the error it may have where delta = sum_s P_ts dP_ts is formed in fp32
+    (not from o, whose rounding is as large as what is left of a row that has few keys; the first row's dq is 0).
+    Weights as in mixer_parity.attn_bounds: a factor within exp(s_err + the error of lse + 8 e), lse within 2 s_err and
+    the sum's gamma_n; dP and delta are fp32 sums, dS is rounded once on its way into the product, dq once."""
+    Q, K, V, DO = (x[:n] for x in (q, k, v, do))
+    D = Q.shape[1]
+    mask = np.tril(np.ones((n, n), dtype=bool))
+    s = scale * (Q @ K.T)
+    top = np.where(mask, s, -np.inf).max(axis=1, keepdims=True)
+    P = np.where(mask, np.exp(s - top), 0)
+    P /= P.sum(1, keepdims=True)
+    s_err = gamma(D + 2) * abs(scale) * (abs(Q) @ abs(K).T) + 2 * E32 * abs(s)
+    s_top = np.where(mask, s_err, 0).max(axis=1, keepdims=True)
+    l_err = np.expm1(2 * s_top + 8 * E32) + gamma(n + 4)
+    lse_err = 2 * l_err + s_top + 8 * E32 * (1 + 2 * abs(s).max(axis=1, keepdims=True) + np.log(n))
+    p_err = np.expm1(s_err + lse_err + 8 * E32)
+    dP = DO @ V.T
+    p_abs = gamma(D + 2) * (abs(DO) @ abs(V).T)                                    # of dP
+    delta = (P * dP).sum(1, keepdims=True)
+    d_err = (P * ((p_err + gamma(n + 4)) * abs(dP) + (1 + p_err) * p_abs)).sum(1, keepdims=True)
+    dS = P * (dP - delta)
+    ds_err = P * (1 + p_err) * ((d_err + p_abs) * (1 + u) + (p_err + u + 2 * E32) * abs(dP - delta))
+    dq = scale * dS @ K
+    b = abs(scale) * (ds_err @ abs(K) + gamma(n + 8) * (abs(dS) @ abs(K)))
+    return dq, b + u * (abs(dq) + b) + 1e-37
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("none", [False, True])
+def test_attn_dq_of_a_segments_first_tokens(D, none):
+    lens = [300] if none else [1, 2, 5, 0, 17, 31, 32, 33, 64, 300]
+    N, cu = lay(lens, 0 if none else 6)
+    q, k, v, do = attn_inputs(D, N, 4, 2, D, "bf16")
+    c = None if none else cu_gpu(cu)
+    o, lse = pkv.attn_varlen(q, k, v, c)
+    gr = pkv.attn_varlen_backward(q, k, v, o, lse, do, c)
+    hq, hk, hv, hdo, got = (host(t)[0] for t in (q, k, v, do, gr.dq))
+    for i, n in enumerate(lens):
+        a, m = int(cu[i]), min(n, 32)
+        for h in range(4 if m else 0):
+            ref, bound = _dq_bound(hq[a:, h], hk[a:, h // 2], hv[a:, h // 2], hdo[a:, h], m, D ** -0.5, half_step("bf16"))
+            err = abs(got[a:a + m, h] - ref)
+            assert (err <= bound).all(), (n, h, float((err / bound).max()), int((err / bound).argmax()) // D)
