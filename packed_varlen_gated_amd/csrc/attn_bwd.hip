@@ -26,11 +26,11 @@
 // consecutive rows (transposing reads of 32 lanes) fall on distinct banks.
 //
 // 8192 tokens (documents of about 800, the longest 3409), H 16, Hkv 4, D 128:
-// forward 124, queries 175, keys 298 us, the longest document's walk; matrix
+// forward 120, queries 171, keys 308 us, the longest document's walk; matrix
 // instructions in 41 % and 30 % of the cycles. The keys pass holds k, v, dk and dv, 192
 // registers at D 128, so two waves a SIMD and no step starts before the last is done
-// with its registers. 32768 tokens in documents of about 104, H 32, D 64: 216 and
-// 219 us for 0.55 and 0.69 GB, latency of one or two tiles a work-group.
+// with its registers. 32768 tokens in documents of about 104, H 32, D 64: 210 and
+// 220 us for 0.55 and 0.69 GB, latency of one or two tiles a work-group.
 
 #include "mfma.h"
 #include "segments.h"

@@ -36,7 +36,7 @@
 // matrix instruction, the softmax's vector work takes about as many, and two
 // work-groups per compute unit (the sums and Q take 192 registers at D 128) do not
 // hide all of one under the other. 65536 tokens in documents of up to 8192, H 32,
-// Hkv 8, D 128: 2.06-2.15 ms, 893-932 TFLOP/s of causal products (a large matrix
+// Hkv 8, D 128: 2.06-2.16 ms, 888-932 TFLOP/s of causal products (a large matrix
 // product reaches 1220 here, 1.57 ms); 77 tokens, H 16: 8.5-9.0 us. A raised wave
 // priority around the products made the first 2.31 ms.
 

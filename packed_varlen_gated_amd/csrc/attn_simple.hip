@@ -25,7 +25,7 @@
 // product's result is the next one's operand as it stands.
 //
 // 512 tokens in documents of about 56, H 4, Hkv 2, D 32, fp32, forward and reverse:
-// 30 us, three dependent launches of 6.5, 7.5 and 13.8 us (one wave per 32 rows with
+// 30 us, three dependent launches of 6.5, 7.6 and 14.2 us (one wave per 32 rows with
 // scalar products: 73 us). One segment of 4096 tokens, forward / reverse: H 4, Hkv 2,
 // D 64, fp32 165 / 639 us; H 16, Hkv 4, D 128, fp32 1.02 / 2.83 ms (67 and 61 TFLOP/s
 // of causal products); D 32, bf16 0.31 / 1.16 ms.

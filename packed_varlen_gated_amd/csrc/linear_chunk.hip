@@ -34,14 +34,15 @@
 // length depends on the call's sizes only.
 //
 // Bound by the chain of dependent steps of a chunk: the walk of 65536 tokens, H 32,
-// D 128 takes 567 us for 2.15 GB (413 us at a copy's rate), waiting 52 % of its
-// cycles, behind 135 us of run states and 19 us of their scan: 0.680-0.688 ms the call
-// (with two parts in the update, 2^-17, 548 + 123 + 19 us and 0.660 ms). With 64-token
+// D 128 takes 585 us for 2.15 GB (413 us at a copy's rate), waiting 51 % of its
+// cycles, behind 159 us of run states and 20 us of their scan, over 8 calls under the
+// profiler; in a timed loop the call takes 0.680-0.688 ms (0.660 with two parts in the
+// update, 2^-17). With 64-token
 // chunks the walk of two parts took 682 us, with three stages and two work-groups per
 // compute unit 622, with the update before the middle barrier 578 instead of 562.
-// 32768 tokens in one segment, H 16, with states: 75 + 23 + 131 us. 8192 tokens,
+// 32768 tokens in one segment, H 16, with states: 75 + 23 + 130 us. 8192 tokens,
 // H 16, forward and reverse: 0.264 ms in seven launches. 32768 tokens in documents
-// of about 104, H 32, D 64: walks of 167, 167 and 218 us.
+// of about 104, H 32, D 64: walks of 164, 164 and 217 us.
 
 #include "mfma.h"
 #include "segments.h"
