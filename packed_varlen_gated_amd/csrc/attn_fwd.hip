@@ -334,14 +334,30 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
     __shared__ int32_t first[3 * D];
     for (int i = tid; i < 3 * D; i += kThreads) first[i] = 0x7fffffff;
     __syncthreads();
-    for (int kind = 0; kind < 3; ++kind)  // (one search each: a single one took the loop above its registers, 2.20 ms for 2.12)
-      for (int32_t s = t.a + tid / D; s < qend; s += kThreads / D) {
-        const float x = to_f32(v[(int64_t(s) * Hkv + hk) * D + tid % D]);
-        if (kind == 0 ? x == INFINITY : kind == 1 ? x == -INFINITY : x != x) {
-          atomicMin(&first[kind * D + tid % D], s);
-          break;
+    const int c8 = tid % CH * 8;
+    uint32_t seen = 0;  // by this thread: value e, kind x at bit 8 x + e
+    for (int32_t s = t.a + tid / CH; s < qend && seen >> 16 != 0xff; s += 4 * STEP) {
+      i32x4 y[4];  // (asked for together; a row past the end is the last one again)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int32_t su = s + u * STEP < qend ? s + u * STEP : qend - 1;
+        y[u] = *reinterpret_cast<const i32x4*>(v + (int64_t(su) * Hkv + hk) * D + c8);
+      }
+      // (loops as they are: unrolled, they changed the order of the first walk's LDS
+      // reads, which at D 128 then took 2.20 ms for 2.13 on attn_flat_microbatch)
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = uint32_t(y[u][e / 2]) >> (e % 2 * 16) & 0xffff;
+          if ((x & 0x7f80) != 0x7f80) continue;
+          const int kind = (x & 0x7f) != 0 ? 2 : int(x >> 15), bit = 8 * kind + e;
+          if (seen >> bit & 1) continue;
+          seen |= 1u << bit;
+          atomicMin(&first[kind * D + c8 + e], s + u * STEP < qend ? s + u * STEP : qend - 1);
         }
       }
+    }
     m = -FLT_MAX;
     l = 0.f;
 #pragma unroll
