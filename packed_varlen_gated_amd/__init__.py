@@ -16,7 +16,9 @@ Entry points (names follow RFC-0025 / RFC-0026):
 
 and, from ``mixers.py`` (include/pkv_mixers.h), the softmax and linear attention that stand next to
 KDA in a model and the recurrences' single-token steps: ``attn_varlen``, ``chunk_linear_attn_varlen``,
-their reverse passes, ``linear_attn_step`` and ``kda_step``.
+their reverse passes, ``linear_attn_step`` and ``kda_step``; from ``softmax.py``
+(include/pkv_softmax.h), what a softmax layer needs around it: ``qk_norm_rope``,
+``attn_window_varlen``, their reverse passes, ``paged_kv_append`` and ``attn_paged``.
 """
 
 import ctypes
@@ -94,6 +96,7 @@ def _load():
     lib.pkv_abi_version.argtypes = []
     lib.pkv_abi_version.restype = i32
     mixers.declare(lib)
+    softmax.declare(lib)
     _lib = lib
     return lib
 
@@ -420,8 +423,12 @@ def chunk_kda_varlen_backward(q, k, v, g, beta, do, cu_seqlens=None, scale=1.0, 
     return KdaGrads(dq, dk, dv, dg, dbeta, dinit)
 
 
-from . import mixers  # noqa: E402  (uses the helpers above)
+from . import mixers, softmax  # noqa: E402  (use the helpers above)
 from .mixers import (FLAG_BAD_SLOT, AttnGrads, LinearAttnGrads, attn_varlen,  # noqa: E402,F401
                      attn_varlen_backward, attn_varlen_backward_workspace_size, chunk_linear_attn_varlen,
                      chunk_linear_attn_varlen_backward, chunk_linear_attn_varlen_backward_workspace_size,
                      chunk_linear_attn_varlen_workspace_size, kda_step, linear_attn_step)
+from .softmax import (FLAG_BAD_LENGTH, FLAG_BAD_PAGE, QkNormRopeGrads, attn_paged,  # noqa: E402,F401
+                      attn_paged_workspace_size, attn_window_varlen, attn_window_varlen_backward,
+                      attn_window_varlen_backward_workspace_size, paged_kv_append, qk_norm_rope,
+                      qk_norm_rope_backward, qk_norm_rope_backward_workspace_size)

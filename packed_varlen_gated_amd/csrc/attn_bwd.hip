@@ -170,12 +170,12 @@ __device__ __forceinline__ void choose_form(const int32_t* __restrict__ cu, int3
   if (threadIdx.x == 0) *form = shared_form(sums[0], sums[1], H, Hkv) ? 4 : 1;
 }
 
-template <int D>
+template <int D, bool kWin>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
     int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dq, float* __restrict__ stats,
-    int32_t* __restrict__ flags, int32_t* __restrict__ form, SlotGrid grid) {
+    int32_t* __restrict__ flags, int32_t* __restrict__ form, SlotGrid grid, int32_t window, int32_t sinks) {
   constexpr int KS = D / 16, DT = D / 32, TB = Lds<D>::BYTES;
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
 
@@ -204,10 +204,12 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const int32_t q0 = t.start + wave * 32;
     const int32_t rows = t.e - q0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
     const int32_t qend = t.start + kB < t.e ? t.start + kB : t.e;
-    const int n_tiles = (qend - t.a + kT - 1) / kT;
+    const WindowWalk ww(kWin ? window : 0x7fffffff, kWin ? sinks : 0, kT, t.start, t.a);
+    const int n_tiles = kWin ? ww.count((qend - t.a + kT - 1) / kT) : (qend - t.a + kT - 1) / kT;
+    auto tile_start = [&](int it) { return t.a + (kWin ? ww.tile(it) : it) * kT; };
     const Loader<D, kT, kThreads> ld(kstride, tid);
     auto issue = [&](int it) {
-      const int32_t s0 = t.a + it * kT;
+      const int32_t s0 = tile_start(it);
       const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
       const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(n - 1) * kstride + D * 2;
       char* dst = lds + (it & 1) * 2 * TB;
@@ -249,8 +251,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
         }
         delta = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          delta += 8 * (i / 4) + i % 4 <= rd.col - 4 * rd.half ? ex2(fmaf(s[i], c, -lse2)) * dp[i] : 0.f;
+        for (int i = 0; i < 16; ++i) {
+          const int32_t key = 8 * (i / 4) + i % 4, at = rd.col - 4 * rd.half;
+          const bool sees = key <= at && (!kWin || key > at - window || key < sinks - 4 * rd.half);
+          delta += sees ? ex2(fmaf(s[i], c, -lse2)) * dp[i] : 0.f;
+        }
         delta += other_half(delta);
       }
     }
@@ -263,10 +268,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
       bar();
       if (it + 1 < n_tiles) issue(it + 1);
       const uint32_t kt = lds_addr(lds) + (it & 1) * 2 * TB, vt = kt + TB;
-      const int32_t s0 = t.a + it * kT;
+      const int32_t s0 = tile_start(it);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (have == 0 || s0 + 32 * j > q0 + 31) continue;
+        if (kWin && s0 + 32 * j + 31 <= q0 - window && s0 + 32 * j >= t.a + sinks) continue;
         f32x16 s = {}, dp = {};
 #pragma unroll
         for (int i = 0; i < KS; ++i) {  // independent products take turns
@@ -275,12 +281,26 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
         }
         bf16x8 ds[2];
         const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
+        if (kWin && s0 + 32 * j <= q0 + 31 - window) {
+          // keys 0 .. old of the block are behind the window, the first ones may be sinks
+          const int32_t old = q0 + rd.col - window - s0 - 32 * j - 4 * rd.half;
+          const int32_t sink = t.a + sinks - s0 - 32 * j - 4 * rd.half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = ex2(fmaf(s[i], c, -lse2));
-          const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
-          rest += x;
-          ds[i / 8][i % 8] = static_cast<bf16>(x);
+          for (int i = 0; i < 16; ++i) {
+            const int32_t key = 8 * (i / 4) + i % 4;
+            const float p = ex2(fmaf(s[i], c, -lse2));
+            const float x = key <= last && (key > old || key < sink) ? p * (dp[i] - delta) : 0.f;
+            rest += x;
+            ds[i / 8][i % 8] = static_cast<bf16>(x);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p = ex2(fmaf(s[i], c, -lse2));
+            const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
+            rest += x;
+            ds[i / 8][i % 8] = static_cast<bf16>(x);
+          }
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
@@ -312,12 +332,34 @@ struct DkvShape {
   static constexpr int T = kQ == 4 ? 128 : 64;    // queries per tile
 };
 
-template <int D, int kQ>
+// The keys pass under a window. A key's queries end `window` tokens behind it, except
+// a sink's, which go on to the segment's end: one work-group's walk over those would
+// outlast all others, so the queries behind the window ("far") have a launch of their
+// own before the keys pass. There a work-group takes the segment's sinks and kFar far
+// queries and leaves its sums in the workspace; the keys pass adds a segment's in order.
+// Far queries of segment i start at cu[i] + window; chunk c of them has slot
+// floor(cu[i] / chunk) + inc i + c. With chunk <= window and inc = 0 the slots of
+// different segments do not meet, since a segment of n tokens has at most
+// floor((cu[i] + n) / chunk) - floor(cu[i] / chunk) of them; a window below 64 would make
+// the chunks small and takes inc = 1 (one more slot per segment) instead.
+constexpr int kFar = 512;
+constexpr int kMaxSinks = 64;
+struct FarGrid {
+  int32_t chunk, inc;
+  __host__ __device__ explicit FarGrid(int32_t window)
+      : chunk(window < 64 || window > kFar ? kFar : window), inc(window < 64 ? 1 : 0) {}
+  __host__ __device__ int64_t slots(int64_t N, int64_t max_segs) const { return N / chunk + inc * max_segs; }
+};
+
+// kWin 0: no window; 1: the queries of a window; 2: the sinks' far queries.
+template <int D, int kQ, int kWin>
 __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void attn_dkv_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const bf16* __restrict__ dout, const float* __restrict__ stats, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dk,
-    bf16* __restrict__ dv, const int32_t* __restrict__ form, SlotGrid grid) {
+    bf16* __restrict__ dv, const int32_t* __restrict__ form, SlotGrid grid, int32_t window, int32_t sinks,
+    float* __restrict__ far) {
+  static_assert(kWin != 2 || DkvShape<kQ>::KEYS >= kMaxSinks, "a work-group has a segment's sinks");
   if (form != nullptr && *form != kQ) return;
   constexpr int KS = D / 16, DT = D / 32;
   constexpr int NT = DkvShape<kQ>::NT, T = DkvShape<kQ>::T, TB = T * D * 2;
@@ -325,18 +367,39 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB + 4 * T * 4];
 
   const int64_t b = blockIdx.x;
-  const int64_t blocks = slot_blocks(grid, Hkv);
-  if (b >= blocks) {
-    const int64_t j = b - blocks, groups = gridDim.x - blocks, cov = covered_tokens(cu, max_segs, N);
-    zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, groups);
-    zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, groups);
-    return;
+  const FarGrid fg(window);
+  int32_t slot, h0, h1;
+  SegTile t;
+  int32_t from = 0, to = 0;  // under a window: the queries [from, to)
+  if constexpr (kWin == 2) {
+    slot = int32_t(b / Hkv);
+    h0 = int32_t(b % Hkv);
+    h1 = h0 + 1;
+    t = {0, 0, 0, int32_t(N)};
+    if (cu != nullptr && (!find_segment(cu, max_segs, fg.chunk, fg.inc, slot, t.seg, t.a, t.e) ||
+                          !segment_ok(t.seg, t.a, t.e, N)))
+      return;
+    const int64_t c0 = int64_t(t.a) + window + (int64_t(slot) - t.a / fg.chunk - int64_t(fg.inc) * t.seg) * fg.chunk;
+    if (c0 >= t.e) return;
+    t.start = t.a;
+    from = int32_t(c0);
+    to = t.e - from < fg.chunk ? t.e : from + fg.chunk;
+  } else {
+    const int64_t blocks = slot_blocks(grid, Hkv);
+    if (b >= blocks) {
+      const int64_t j = b - blocks, groups = gridDim.x - blocks, cov = covered_tokens(cu, max_segs, N);
+      zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, groups);
+      zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, groups);
+      return;
+    }
+    slot_of(grid, b, Hkv, slot, h0, h1);
+    if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
+    from = t.start;
+    to = t.e - t.start > DkvShape<kQ>::KEYS - 1 + window ? t.start + DkvShape<kQ>::KEYS - 1 + window : t.e;
   }
   const int32_t rep = H / Hkv;
-  int32_t slot, h0, h1;
-  slot_of(grid, b, Hkv, slot, h0, h1);
-  SegTile t;
-  if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
+  auto q_from = [&] { return kWin ? from : t.start; };
+  auto q_to = [&] { return kWin ? to : t.e; };
 
   for (int32_t hk = h0; hk < h1; ++hk) {
     // (nothing that goes by the lane is kept from one head to the next)
@@ -344,14 +407,15 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
     const Reader<D> rd(tid);
     const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
     const int32_t k0 = t.start + wave / kQ * 32;  // the wave's first key
-    const int32_t rows = t.e - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-    const int per_head = (t.e - t.start + T - 1) / T, n_tiles = per_head * rep;
+    const int32_t kend = kWin == 2 && t.e - t.a > sinks ? t.a + sinks : t.e;
+    const int32_t rows = kend - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+    const int per_head = (q_to() - q_from() + T - 1) / T, n_tiles = per_head * rep;
     const Loader<D, T, NT> ld(qstride, tid);
     int ih = hk * rep, iq = 0;  // query head and tile of the next load
     // Q, dO and the statistics of the next tile
     auto issue = [&](int it) {
-      const int32_t s0 = t.start + iq * T, h = ih;
-      const int32_t n = t.e - s0 < T ? t.e - s0 : T;
+      const int32_t s0 = q_from() + iq * T, h = ih;
+      const int32_t n = q_to() - s0 < T ? q_to() - s0 : T;
       const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
       char* dst = lds + (it & 1) * 2 * TB;
       ld.issue(buffer(q + at, bytes), dst, wave);
@@ -388,14 +452,16 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
       const uint32_t qt0 = lds_addr(lds) + (it & 1) * 2 * TB;
       const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * T * 4);
       const f32x4* dl = ls + T / 4;
-      const int32_t s0 = t.start + cq * T;
+      const int32_t s0 = q_from() + cq * T;
       if (++cq == per_head) cq = 0;
 #pragma unroll 1
       for (int j = wave % kQ; j < T / 32; j += kQ) {
         const int32_t b0 = s0 + 32 * j;  // first query of the block
         // (addresses are formed per block: one register each instead of one per read)
         const uint32_t qt = fresh_uniform(qt0 + 32 * j * Lds<D>::ROW), ot = qt + TB;
-        if (have == 0 || b0 + 31 < k0 || b0 >= t.e) continue;
+        const int32_t kq = kWin == 2 ? k0 + window : k0;  // the first key's first query
+        if (have == 0 || b0 + 31 < kq || b0 >= q_to()) continue;
+        if (kWin == 1 && b0 >= k0 + 31 + window) continue;
         // Registers are full at D = 128 (k, v, dk and dv take 192): the weights are
         // done with before dP is begun, and nothing of a phase starts early. The
         // other wave of the SIMD fills the gaps.
@@ -405,9 +471,10 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
         for (int i = 0; i < KS; ++i) x = mfma32(rd.rows(qt, 0, i), kf[i], x);
         if (D == 128) __builtin_amdgcn_sched_barrier(0);
         // the lane's key takes part in the block's queries first .. end - 1
-        const bool edge = b0 < k0 + 31 || b0 + 32 > t.e;
-        const int32_t first = edge ? k0 + rd.col - b0 - 4 * rd.half : -64;
-        const int32_t end = edge ? t.e - b0 - 4 * rd.half : 64;
+        const bool edge = b0 < kq + 31 || b0 + 32 > q_to() || (kWin == 1 && b0 + 32 > k0 + window);
+        const int32_t first = edge ? kq + rd.col - b0 - 4 * rd.half : -64;
+        const int32_t qend = kWin == 1 && to - k0 > rd.col + window ? k0 + rd.col + window : q_to();
+        const int32_t end = edge ? qend - b0 - 4 * rd.half : 64;
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
           const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
@@ -475,6 +542,40 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
         join_sums(av, from);
       }
     }
+    if constexpr (kWin == 2) {
+      if (rd.col < have && wave % kQ == 0) {
+        float* out = far + ((int64_t(slot) * Hkv + hk) * 2 * sinks + (k0 - t.a) + rd.col) * D + 4 * rd.half;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float* x = out + 32 * i + 8 * j;
+            *reinterpret_cast<f32x4*>(x) = f32x4{ak[i][4 * j], ak[i][4 * j + 1], ak[i][4 * j + 2], ak[i][4 * j + 3]};
+            *reinterpret_cast<f32x4*>(x + int64_t(sinks) * D) =
+                f32x4{av[i][4 * j], av[i][4 * j + 1], av[i][4 * j + 2], av[i][4 * j + 3]};
+          }
+      }
+      return;
+    }
+    if (kWin == 1 && far != nullptr && k0 + rd.col - t.a < sinks && rd.col < have && wave % kQ == 0) {
+      const int32_t behind = t.e - t.a - window;
+      const int64_t first = int64_t(t.a) / fg.chunk + int64_t(fg.inc) * t.seg;
+      for (int32_t x = 0; x * int64_t(fg.chunk) < behind; ++x) {
+        const float* part = far + (((first + x) * Hkv + hk) * 2 * sinks + (k0 - t.a) + rd.col) * D + 4 * rd.half;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(part + 32 * i + 8 * j);
+            const f32x4 z = *reinterpret_cast<const f32x4*>(part + int64_t(sinks) * D + 32 * i + 8 * j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              ak[i][4 * j + e] += y[e];
+              av[i][4 * j + e] += z[e];
+            }
+          }
+      }
+    }
     if (have > 0 && wave % kQ == 0) {
       char* st = lds + wave / kQ * (32 * D * 2);
       const int64_t to = (int64_t(k0) * Hkv + hk) * D;
@@ -486,14 +587,33 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   }
 }
 
-template <int D, int kQ>
+template <int D, int kQ, int kWin = 0>
 void keys_pass(const AttnArgs& a, const AttnGradArgs& g, const int32_t* form, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
   const dim3 blocks(uint32_t(slot_blocks(grid, a.Hkv) + tail_groups(a.N * a.Hkv * D * 2)));
-  attn_dkv_kernel<D, kQ><<<blocks, dim3(DkvShape<kQ>::NT), 0, stream>>>(
+  attn_dkv_kernel<D, kQ, kWin><<<blocks, dim3(DkvShape<kQ>::NT), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), form, grid);
+      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), form, grid, a.window, a.sinks, g.far);
+}
+
+// The queries pass, the sinks' far queries, the keys pass.
+template <int D>
+hipError_t run_window(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
+  const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
+  const dim3 blocks(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2)));
+  attn_dq_kernel<D, true><<<blocks, dim3(kThreads), 0, stream>>>(
+      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
+      static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
+      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, nullptr, grid, a.window, a.sinks);
+  const int64_t far = a.sinks > 0 ? FarGrid(a.window).slots(a.N, a.max_segs) * a.Hkv : 0;
+  if (far > 0)
+    attn_dkv_kernel<D, 4, 2><<<dim3(uint32_t(far)), dim3(DkvShape<4>::NT), 0, stream>>>(
+        static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
+        static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, nullptr, nullptr,
+        nullptr, grid, a.window, a.sinks, g.far);
+  keys_pass<D, 1, 1>(a, g, nullptr, stream);
+  return hipGetLastError();
 }
 
 template <int D>
@@ -506,10 +626,10 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const bool may = shared_form(uint64_t(L), uint64_t(L * L), a.H, a.Hkv);
   int32_t* form = may && a.cu != nullptr ? reinterpret_cast<int32_t*>(g.stats + 2 * a.N * a.H) : nullptr;
   const dim3 blocks(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2)));
-  attn_dq_kernel<D><<<blocks, dim3(kThreads), 0, stream>>>(
+  attn_dq_kernel<D, false><<<blocks, dim3(kThreads), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
-      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, form, grid);
+      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, form, grid, 0, 0);
   // With cu the lengths are on the device: both forms are launched, and the one
   // that was not chosen ends at once.
   const bool share = a.cu == nullptr && shared_form(a.N, uint64_t(a.N) * a.N, a.H, a.Hkv);
@@ -520,7 +640,13 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 
 }  // namespace
 
+size_t attn_far_bytes(int64_t N, int64_t max_segs, int32_t Hkv, int32_t D, int32_t window, int32_t sinks) {
+  if (sinks == 0 || window >= N) return 0;
+  return size_t(FarGrid(window).slots(N, max_segs)) * Hkv * 2 * sinks * D * 4;
+}
+
 hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
+  if (a.window > 0 && a.window < a.N) return a.D == 64 ? run_window<64>(a, g, stream) : run_window<128>(a, g, stream);
   return a.D == 64 ? run<64>(a, g, stream) : run<128>(a, g, stream);
 }
 

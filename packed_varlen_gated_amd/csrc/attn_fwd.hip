@@ -69,11 +69,13 @@ struct Tile {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
-template <int D, int kS>
+template <int D, int kS, bool kWin>
 __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
-    bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, SlotGrid grid) {
+    bf16* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, SlotGrid grid, int32_t window,
+    int32_t sinks) {
+  static_assert(!kWin || kS == 1, "windowed walks are short");
   constexpr int kBM = Shape<kS>::BM, kBN = Shape<kS>::BN;
   using TileD = Tile<D, kBN>;
   constexpr int CH = TileD::CH, KS = D / 16, DT = D / 32, LD = kBN * CH / kThreads;
@@ -111,7 +113,9 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
     const int32_t q0 = t.start + wave / kS * 32;  // the wave's first query
     const int32_t rows = t.e - q0;           // its real queries (may be <= 0 or > 32)
     const int32_t qend = t.start + kBM < t.e ? t.start + kBM : t.e;
-    const int n_tiles = (qend - t.a + kBN - 1) / kBN;
+    const WindowWalk ww(kWin ? window : 0x7fffffff, kWin ? sinks : 0, kBN, t.start, t.a);
+    const int n_tiles = kWin ? ww.count((qend - t.a + kBN - 1) / kBN) : (qend - t.a + kBN - 1) / kBN;
+    auto tile_start = [&](int it) { return t.a + (kWin ? ww.tile(it) : it) * kBN; };
 
     // the lane's first chunk of a tile; the others are whole multiples of 16 rows
     // further (the swizzles' period)
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
     const uint32_t koff = uint32_t(lrow) * kstride + (lpos ^ TileD::k_swz(lrow)) * 16;
     const uint32_t voff = uint32_t(lrow) * kstride + (lpos ^ TileD::v_swz(lrow)) * 16;
     auto issue = [&](int it) {
-      const int32_t s0 = t.a + it * kBN;
+      const int32_t s0 = tile_start(it);
       const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
       const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(have - 1) * kstride + D * 2;
       const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);
@@ -181,8 +185,9 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
           }
           __syncthreads();
         }
-        const int32_t s0 = t.a + it * kBN + part * 64;  // the wave's first key
+        const int32_t s0 = tile_start(it) + part * 64;  // the wave's first key
         if (rows <= 0 || s0 > q0 + 31) continue;
+        if (kWin && s0 + 63 <= q0 - window && s0 >= t.a + sinks) continue;
         kt += part * (64 * D * 2);
         vt += part * (64 * D * 2);
 
@@ -204,6 +209,17 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               s[j][i] = 32 * j + 8 * (i / 4) + 4 * half + i % 4 <= last ? s[j][i] : -INFINITY;
+        }
+        if (kWin && s0 <= q0 + 31 - window) {
+          // keys 0 .. old of the tile are behind the window, the first ones may be sinks
+          const int32_t old = q0 + col - window - s0 - 4 * half, sink = t.a + sinks - s0 - 4 * half;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int32_t key = 32 * j + 8 * (i / 4) + i % 4;
+              s[j][i] = key > old || key < sink ? s[j][i] : -INFINITY;
+            }
         }
         float mx = s[0][0];
 #pragma unroll
@@ -329,6 +345,58 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
       continue;
     }
 
+    if constexpr (kWin) {
+      // Some output is not finite. What a row sees is no longer a prefix: after a walk
+      // with such values as 0, another one adds them to the rows that see them.
+      m = -FLT_MAX;
+      l = 0.f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+      __syncthreads();  // the outputs have left LDS
+      walk(true);
+      l += other_half(l);
+      const float inv2 = 1.f / l;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] *= inv2;
+      __shared__ uint32_t odd[kBN / 32];  // keys of the tile with such a value
+      for (int it = 0; it < n_tiles; ++it) {
+        __syncthreads();
+        if (tid < kBN / 32) odd[tid] = 0;
+        issue(it);
+        wait_vm();
+        __syncthreads();
+        const char* vt = lds + (it & 1) * 2 * TB + TB;
+        for (int i = tid; i < TB / 4; i += kThreads) {
+          const uint32_t x = reinterpret_cast<const uint32_t*>(vt)[i];
+          const int row = i / (D / 2);
+          if ((x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u) atomicOr(&odd[row / 32], 1u << (row % 32));
+        }
+        __syncthreads();
+        const int32_t s0 = tile_start(it);
+        for (int s = 0; s < kBN; ++s) {
+          if ((odd[s / 32] >> (s % 32) & 1) == 0) continue;
+          const int32_t at = s0 + s, t_ = q0 + col;
+          const bool sees = at <= t_ && (t_ - at < window || at - t.a < sinks);
+          // (a fixed register per value: acc is indexed by constants alone)
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int ch = 32 * i + 8 * (j / 4) + 4 * half + j % 4;
+              const float y = to_f32(*reinterpret_cast<const bf16*>(
+                  vt + s * (D * 2) + (((ch / 8) ^ TileD::v_swz(s)) * 16) + ch % 8 * 2));
+              if (sees && !finite(y)) acc[i][j] += y;
+            }
+        }
+      }
+      __syncthreads();
+      put(nullptr);
+      __syncthreads();
+      continue;
+    }
+
     // Some output is not finite. first[D x + d]: the first token of the segment
     // whose value d is inf (x = 0), -inf (1), NaN (2).
     __shared__ int32_t first[3 * D];
@@ -381,16 +449,21 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
 
 bool attn_mfma_supported(int32_t D, int32_t dtype) { return dtype == 0 && (D == 64 || D == 128); }
 
-template <int D, int kS>
+template <int D, int kS, bool kWin = false>
 void run(const AttnArgs& a, hipStream_t stream) {
   const SlotGrid g = slot_grid(a.N, a.max_segs, Shape<kS>::BM);
   const dim3 blocks(uint32_t(slot_blocks(g, a.H) + tail_groups(a.N * a.H * D * 2)));
-  attn_fwd_kernel<D, kS><<<blocks, dim3(kThreads), 0, stream>>>(
+  attn_fwd_kernel<D, kS, kWin><<<blocks, dim3(kThreads), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v), a.cu, a.max_segs,
-      a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g);
+      a.N, a.H, a.Hkv, a.scale, static_cast<bf16*>(a.o), a.lse, a.flags, g, a.window, a.sinks);
 }
 
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream) {
+  // (a window that no segment is longer than hides nothing)
+  if (a.window > 0 && a.window < a.N) {
+    a.D == 64 ? run<64, 1, true>(a, stream) : run<128, 1, true>(a, stream);
+    return hipGetLastError();
+  }
   // With few work-groups the longest walk over the keys sets the time, and waves that
   // share queries make it shorter; with many, or with many short walks, their joins
   // cost more than they save. Only the length of a call's one slot is known here, and

@@ -9,7 +9,8 @@
 //   dq_t = scale sum_s dS_ts k_s, dk_s = scale sum_t dS_ts q_t,
 //   dv_s = sum_t P_ts do_t, the last two also summed over the query heads that
 //   share the kv head, in a fixed order (no atomics).
-// Query head h reads kv head h / (Hq / Hkv).
+// Query head h reads kv head h / (Hq / Hkv). With a window, t attends to s only if
+// t - s < window or s is one of the segment's first `sinks` tokens.
 //
 // A work-group takes 32 rows (queries, or keys in the dk/dv pass) of one head. Its
 // four waves take the tiles of 32 of the other side in turn, each in LDS of its
@@ -65,6 +66,11 @@ __device__ __forceinline__ void store4(bf16* p, f32x4 x) {
 __device__ __forceinline__ void wave_fence() { asm volatile("" ::: "memory"); }
 
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// Whether token t of a segment from a on attends to token s of it.
+template <bool kWin>
+__device__ __forceinline__ bool attends(int64_t s, int64_t t, int64_t a, int32_t window, int32_t sinks) {
+  return s <= t && (!kWin || t - s < window || s - a < sinks);
+}
 __device__ __forceinline__ int row_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
 
 // 32 rows of a [N, H, D] tensor from `row` on into a wave's tile, zero past `end`;
@@ -145,11 +151,12 @@ __device__ __forceinline__ void store_sums(const Tile<D>* t, float f, T* out, in
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin>
 __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
-    T* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, int64_t slots) {
+    T* __restrict__ o, float* __restrict__ lse, int32_t* __restrict__ flags, int64_t slots, int32_t window,
+    int32_t sinks) {
   __shared__ Tile<D> tiles[2 * kWaves];
   __shared__ float sm[kWaves][kT], sl[kWaves][kT];
   const int64_t b = blockIdx.x;
@@ -174,7 +181,10 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
   load_row<T, D>(qf, q, row, row < t.e, H, h, half);
   float m = -INFINITY, l = 0.f;
   f32x16 acc[D / 32] = {};
-  for (int64_t s0 = t.a + wave * kT; s0 <= t.start; s0 += kWaves * kT) {
+  const WindowWalk ww(kWin ? window : 0x7fffffff, kWin ? sinks : 0, kT, t.start, t.a);
+  const int64_t walk_end = kWin ? t.a + int64_t(ww.count((t.start - t.a) / kT + 1) - 1) * kT : t.start;
+  for (int64_t w0 = t.a + wave * kT; w0 <= walk_end; w0 += kWaves * kT) {
+    const int64_t s0 = kWin ? t.a + int64_t(ww.tile(int32_t(w0 - t.a) / kT)) * kT : w0;
     wave_fence();
     fill<T, D>(tk, k, s0, t.e, Hkv, hk, lane);
     const bool ok = fill<T, D>(tv, v, s0, t.e, Hkv, hk, lane);
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     float mt = m;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      x[i] = s0 + row_of(i, half) <= row ? x[i] * scale : -INFINITY;
+      x[i] = attends<kWin>(s0 + row_of(i, half), row, t.a, window, sinks) ? x[i] * scale : -INFINITY;
       mt = fmaxf(mt, x[i]);
     }
     mt = fmaxf(mt, other_half(mt));
@@ -201,11 +211,11 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     for (int j = 0; j < D / 32; ++j)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[j][i] *= f;
-    if (s0 < t.start || __all(ok)) {
+    if ((s0 < t.start && (!kWin || s0 + window > t.start + 31)) || __all(ok)) {
       over_rows<D>(acc, tv, x, col, half);
     } else {
-      // The tile on the diagonal holds a value that is not finite: a weight of 0
-      // times it is NaN, so such values are 0 in the product and are added for the
+      // A tile on the diagonal (or at the end of a window) holds a value that is not
+      // finite: a weight of 0 times it is NaN, so such values are 0 in the product and are added for the
       // rows that attend to them alone. The other rows keep their bits.
       wave_fence();
       for (int i = lane; i < kT * D; i += 64) {
@@ -219,6 +229,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
       for (int i = 0; i < 16; ++i) tk.x[row_of(i, half)][col] = x[i];
       wave_fence();
       for (int s = 0; s < kT && s0 + s <= row && s0 + s < t.e; ++s) {
+        if (kWin && !attends<kWin>(s0 + s, row, t.a, window, sinks)) continue;
         const float p = tk.x[s][col];
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
@@ -250,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      if (t.a + w * kT > t.start) continue;  // (had no tile)
+      if (t.a + w * kT > walk_end) continue;  // (had no tile)
       const float f = expf(sm[w][r] - ms);
       sum += f * sl[w][r];
       x += f * tiles[2 * w].at(r, d);
@@ -260,12 +271,12 @@ __global__ __launch_bounds__(kThreads) void attn_simple_fwd(
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin>
 __global__ __launch_bounds__(kThreads) void attn_simple_dq(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ o,
     const T* __restrict__ dout, const float* __restrict__ lse, float* __restrict__ delta,
     const int32_t* __restrict__ cu, int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale,
-    T* __restrict__ dq, int32_t* __restrict__ flags, int64_t slots) {
+    T* __restrict__ dq, int32_t* __restrict__ flags, int64_t slots, int32_t window, int32_t sinks) {
   __shared__ Tile<D> tiles[2 * kWaves];
   const int64_t b = blockIdx.x;
   if (b >= slots * H) {
@@ -295,7 +306,10 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
   const float ls = real ? lse[int64_t(h) * N + row] : INFINITY;
   if (real && wave == 0 && half == 0) delta[int64_t(h) * N + row] = dl;  // for the keys pass
   f32x16 acc[D / 32] = {};
-  for (int64_t s0 = t.a + wave * kT; s0 <= t.start; s0 += kWaves * kT) {
+  const WindowWalk ww(kWin ? window : 0x7fffffff, kWin ? sinks : 0, kT, t.start, t.a);
+  const int64_t walk_end = kWin ? t.a + int64_t(ww.count((t.start - t.a) / kT + 1) - 1) * kT : t.start;
+  for (int64_t w0 = t.a + wave * kT; w0 <= walk_end; w0 += kWaves * kT) {
+    const int64_t s0 = kWin ? t.a + int64_t(ww.tile(int32_t(w0 - t.a) / kT)) * kT : w0;
     wave_fence();
     fill<T, D>(tk, k, s0, t.e, Hkv, hk, lane);
     fill<T, D>(tv, v, s0, t.e, Hkv, hk, lane);
@@ -304,7 +318,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
     const f32x16 y = over_channels<D>(tv, df, col, half);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      x[i] = s0 + row_of(i, half) <= row ? expf(x[i] * scale - ls) * (y[i] - dl) : 0.f;
+      x[i] = attends<kWin>(s0 + row_of(i, half), row, t.a, window, sinks) ? expf(x[i] * scale - ls) * (y[i] - dl) : 0.f;
     over_rows<D>(acc, tk, x, col, half);
   }
   wave_fence();
@@ -313,12 +327,12 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dq(
   store_sums<T, D>(tiles, scale, dq + (int64_t(t.start) * H + h) * D, int64_t(H) * D, t.e - t.start);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin>
 __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ dout,
     const float* __restrict__ lse, const float* __restrict__ delta, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, T* __restrict__ dk,
-    T* __restrict__ dv, int64_t slots) {
+    T* __restrict__ dv, int64_t slots, int32_t window, int32_t sinks) {
   __shared__ Tile<D> tiles[2 * kWaves];
   const int64_t b = blockIdx.x;
   if (b >= slots * Hkv) {
@@ -340,7 +354,9 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
   load_row<T, D>(vf, v, row, row < t.e, Hkv, hk, half);
   f32x16 ak[D / 32] = {}, av[D / 32] = {};
   // (query head, query tile) pairs, dealt to the waves in turn
-  const int64_t per = (int64_t(t.e) - t.start + kT - 1) / kT;
+  int64_t qe = t.e;
+  if (kWin && t.start - t.a >= sinks && t.e - t.start > kT - 1 + window) qe = t.start + kT - 1 + window;
+  const int64_t per = (qe - t.start + kT - 1) / kT;
   for (int64_t it = wave; it < per * rep; it += kWaves) {
     const int32_t h = hk * rep + int32_t(it / per);
     const int64_t s0 = t.start + it % per * kT;
@@ -360,7 +376,7 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int64_t s = s0 + row_of(i, half);
-      x[i] = s >= row && s < t.e ? expf(x[i] * scale - ls[i]) : 0.f;
+      x[i] = attends<kWin>(row, s, t.a, window, sinks) && s < t.e ? expf(x[i] * scale - ls[i]) : 0.f;
       y[i] = x[i] * (y[i] - dl[i]);
     }
     over_rows<D>(av, to, x, col, half);
@@ -377,45 +393,59 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
   store_sums<T, D>(tiles, 1.f, dv + to_, int64_t(Hkv) * D, t.e - t.start);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin>
 hipError_t fwd(const AttnArgs& a, hipStream_t stream) {
   const int64_t slots = tile_slots(a.N, a.max_segs, kT), grid = slots * a.H + tail_groups(a.N * a.H * D * sizeof(T));
-  attn_simple_fwd<T, D><<<dim3(uint32_t(grid)), dim3(kThreads), 0, stream>>>(
+  attn_simple_fwd<T, D, kWin><<<dim3(uint32_t(grid)), dim3(kThreads), 0, stream>>>(
       static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.cu, a.max_segs,
-      a.N, a.H, a.Hkv, a.scale, static_cast<T*>(a.o), a.lse, a.flags, slots);
+      a.N, a.H, a.Hkv, a.scale, static_cast<T*>(a.o), a.lse, a.flags, slots, a.window, a.sinks);
   return hipGetLastError();
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin>
 hipError_t bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
   const T* dout = static_cast<const T*>(g.dout);
   const int64_t slots = tile_slots(a.N, a.max_segs, kT);
-  attn_simple_dq<T, D><<<dim3(uint32_t(slots * a.H + tail_groups(a.N * a.H * D * sizeof(T)))), dim3(kThreads), 0, stream>>>(
+  attn_simple_dq<T, D, kWin><<<dim3(uint32_t(slots * a.H + tail_groups(a.N * a.H * D * sizeof(T)))), dim3(kThreads), 0, stream>>>(
       q, k, v, static_cast<const T*>(a.o), dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-      static_cast<T*>(g.dq), a.flags, slots);
-  attn_simple_dkv<T, D><<<dim3(uint32_t(slots * a.Hkv + tail_groups(a.N * a.Hkv * D * sizeof(T)))), dim3(kThreads), 0, stream>>>(
+      static_cast<T*>(g.dq), a.flags, slots, a.window, a.sinks);
+  attn_simple_dkv<T, D, kWin><<<dim3(uint32_t(slots * a.Hkv + tail_groups(a.N * a.Hkv * D * sizeof(T)))), dim3(kThreads), 0, stream>>>(
       q, k, v, dout, a.lse, g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, static_cast<T*>(g.dk),
-      static_cast<T*>(g.dv), slots);
+      static_cast<T*>(g.dv), slots, a.window, a.sinks);
   return hipGetLastError();
+}
+
+}  // namespace
+
+namespace {
+
+// (a window that no segment is longer than hides nothing)
+template <typename T, int D>
+hipError_t fwd_any(const AttnArgs& a, hipStream_t stream) {
+  return a.window > 0 && a.window < a.N ? fwd<T, D, true>(a, stream) : fwd<T, D, false>(a, stream);
+}
+template <typename T, int D>
+hipError_t bwd_any(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
+  return a.window > 0 && a.window < a.N ? bwd<T, D, true>(a, g, stream) : bwd<T, D, false>(a, g, stream);
 }
 
 }  // namespace
 
 // bf16: D = 32 alone (64 and 128 are attn_fwd.hip's and attn_bwd.hip's).
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream) {
-  if (dtype == 0) return a.D == 32 ? fwd<bf16, 32>(a, stream) : hipErrorInvalidValue;
-  if (a.D == 32) return fwd<float, 32>(a, stream);
-  if (a.D == 64) return fwd<float, 64>(a, stream);
-  return fwd<float, 128>(a, stream);
+  if (dtype == 0) return a.D == 32 ? fwd_any<bf16, 32>(a, stream) : hipErrorInvalidValue;
+  if (a.D == 32) return fwd_any<float, 32>(a, stream);
+  if (a.D == 64) return fwd_any<float, 64>(a, stream);
+  return fwd_any<float, 128>(a, stream);
 }
 
 hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g, int32_t dtype,
                                        hipStream_t stream) {
-  if (dtype == 0) return a.D == 32 ? bwd<bf16, 32>(a, g, stream) : hipErrorInvalidValue;
-  if (a.D == 32) return bwd<float, 32>(a, g, stream);
-  if (a.D == 64) return bwd<float, 64>(a, g, stream);
-  return bwd<float, 128>(a, g, stream);
+  if (dtype == 0) return a.D == 32 ? bwd_any<bf16, 32>(a, g, stream) : hipErrorInvalidValue;
+  if (a.D == 32) return bwd_any<float, 32>(a, g, stream);
+  if (a.D == 64) return bwd_any<float, 64>(a, g, stream);
+  return bwd_any<float, 128>(a, g, stream);
 }
 
 }  // namespace pkv

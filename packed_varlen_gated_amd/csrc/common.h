@@ -23,7 +23,9 @@ constexpr int32_t kFlagOverflow = 1;
 constexpr int32_t kFlagLeadingPad = 2;
 constexpr int32_t kFlagBadCuSeqlens = 4;
 constexpr int32_t kFlagGateRange = 8;
-constexpr int32_t kFlagBadSlot = 16;  // include/pkv_mixers.h
+constexpr int32_t kFlagBadSlot = 16;    // include/pkv_mixers.h
+constexpr int32_t kFlagBadPage = 32;    // include/pkv_softmax.h
+constexpr int32_t kFlagBadLength = 64;
 // The chunked bf16 paths split each 64-token chunk into 16-token sub-chunks
 // and put 2^{-(sum of a sub-chunk's log2 gates)} on one operand of its
 // diagonal block (the forward's query side, the reverse pass's key side).
@@ -142,6 +144,8 @@ struct AttnArgs {
   void* o;
   float* lse;
   int32_t* flags;
+  // window > 0: query t of a segment [a, e) attends to s with t - s < window or s - a < sinks
+  int32_t window = 0, sinks = 0;
 };
 struct AttnGradArgs {
   const void* dout;
@@ -149,6 +153,8 @@ struct AttnGradArgs {
   // behind it the form of the keys pass
   float* stats;
   void *dq, *dk, *dv;
+  // sums of the sinks' dk and dv over far queries (attn_bwd.hip), where there are sinks
+  float* far = nullptr;
 };
 hipError_t launch_attn_simple(const AttnArgs& a, int32_t dtype, hipStream_t stream);
 hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g, int32_t dtype,
@@ -158,6 +164,8 @@ hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g,
 bool attn_mfma_supported(int32_t D, int32_t dtype);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream);
+// Bytes of AttnGradArgs::far.
+size_t attn_far_bytes(int64_t N, int64_t max_segs, int32_t Hkv, int32_t D, int32_t window, int32_t sinks);
 
 // Linear attention with one decay per head.
 struct LinearArgs {
@@ -204,5 +212,54 @@ struct StepArgs {
   int32_t* flags;
 };
 hipError_t launch_step(const StepArgs& a, int32_t dtype, hipStream_t stream);
+
+// Norms of query and key heads with the rotation (see include/pkv_softmax.h);
+// weights and positions may be null. Strides in elements.
+struct NormRopeArgs {
+  const void *q, *k;
+  int64_t q_stride, k_stride;
+  const float *q_weight, *k_weight;
+  const int32_t* positions;
+  const float* inv_freq;
+  int64_t N;
+  int32_t Hq, Hkv, D, rot;
+  float eps;
+  bool interleaved;
+  void *q_out, *k_out;  // forward
+};
+struct NormRopeGradArgs {
+  const void *dq_out, *dk_out;
+  void *dq, *dk;
+  float *dq_weight, *dk_weight;  // may be null
+  float* partial;                // workspace
+};
+size_t norm_rope_workspace_bytes(int64_t N, int32_t D);
+hipError_t launch_norm_rope(const NormRopeArgs& x, int32_t dtype, hipStream_t stream);
+hipError_t launch_norm_rope_backward(const NormRopeArgs& x, const NormRopeGradArgs& y, int32_t dtype,
+                                     hipStream_t stream);
+
+// The paged cache and a call's new tokens; cu may be null (one each).
+struct PagedArgs {
+  const int32_t *table, *lens, *cu;
+  int64_t N;
+  int32_t R, Hkv, D, page_size, num_pages, max_pages;
+  int32_t* flags;
+};
+struct AppendArgs {
+  const void *k, *v;
+  int64_t k_stride, v_stride;
+  void *k_pages, *v_pages;
+};
+struct AttnPagedArgs {
+  const void *q, *k_pages, *v_pages;
+  int32_t Hq;
+  float scale;
+  int32_t window, sinks;  // window 0: none
+  void* o;
+  float* lse;
+  void* workspace;
+};
+hipError_t launch_paged_append(const PagedArgs& c, const AppendArgs& x, int32_t dtype, hipStream_t stream);
+hipError_t launch_attn_paged_simple(const PagedArgs& c, const AttnPagedArgs& x, int32_t dtype, hipStream_t stream);
 
 }  // namespace pkv

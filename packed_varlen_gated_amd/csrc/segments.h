@@ -138,6 +138,22 @@ __device__ __forceinline__ void check_cu(const int32_t* __restrict__ cu, int32_t
   if (bad) atomicOr(flags, kFlagBadCuSeqlens);
 }
 
+// What the queries of a tile attend to under a window: query t of segment [a, e) sees
+// key s <= t if t - s < window or s - a < sinks. `low` is the tile of `bn` keys (from a)
+// that holds the first key in the first query's window; `far` tiles in front of it hold
+// sinks. The walk is those, then tiles low, low + 1, ...
+struct WindowWalk {
+  int32_t low, far;
+  __device__ __forceinline__ WindowWalk(int32_t window, int32_t sinks, int32_t bn, int32_t start, int32_t a) {
+    const int32_t first = start - a - window + 1;
+    low = first > 0 ? first / bn : 0;
+    const int32_t s = (sinks + bn - 1) / bn;
+    far = s < low ? s : low;
+  }
+  __device__ __forceinline__ int32_t tile(int32_t it) const { return it < far ? it : it - far + low; }
+  __device__ __forceinline__ int32_t count(int32_t all) const { return all - low + far; }
+};
+
 // Zeroes rows [covered, N) of a [N, width]-byte tensor; part j of n of the
 // work (16-byte stores; width is a multiple of 16).
 __device__ __forceinline__ void zero_tail(void* base, int64_t covered, int64_t N, int64_t width,
