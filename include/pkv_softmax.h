@@ -63,7 +63,7 @@ extern "C" {
  * q_out, k_out  dense [N, Hq, D], [N, Hkv, D].
  * options    0 or PKV_OPT_ROPE_INTERLEAVED.
  * Supported: D in {32, 64, 128}, rot_dim a multiple of 16 in [0, D]. Errors:
- * PKV_ERR_INVALID_ARGUMENT for a NULL tensor, N < 1, N > INT32_MAX, heads < 1
+ * PKV_ERR_INVALID_ARGUMENT for a NULL tensor, N < 1, N > 2^25, heads < 1
  * or > 65536, a bad stride, eps < 0 or not finite, a misaligned or overlapping
  * tensor; PKV_ERR_UNSUPPORTED for another D, rot_dim, dtype or option.
  */
@@ -139,7 +139,7 @@ pkv_status pkv_attn_window_varlen_backward(const void* q, const void* k, const v
  *             the N packed ones; they are its last tokens. NULL: one new
  *             token for each request, N = R.
  * page_size   a multiple of 16, at most 65536; num_pages * page_size and
- *             max_pages * page_size at most INT32_MAX.
+ *             max_pages * page_size at most 2^30.
  *
  * pkv_paged_kv_append writes the new tokens' k and v [N, Hkv, D] (dense, or
  * with k_stride / v_stride elements from token to token as for
@@ -149,8 +149,8 @@ pkv_status pkv_attn_window_varlen_backward(const void* q, const void* k, const v
  * requests may share pages that no new token goes to; where two new tokens of
  * a call have one place, either's values may be there.
  * Supported: D in {32, 64, 128}. Errors: PKV_ERR_INVALID_ARGUMENT for a NULL
- * tensor, sizes out of range, R < 1, N < 1, N != R without cu_seqlens, a
- * misaligned or overlapping tensor; PKV_ERR_UNSUPPORTED for another D, dtype
+ * tensor, sizes out of range, R < 1, N < 1, (N / 16 + R) heads >= 2^23, N != R
+ * without cu_seqlens, a misaligned or overlapping tensor; PKV_ERR_UNSUPPORTED for another D, dtype
  * or page_size.
  */
 pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -177,9 +177,8 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
  * workspace  at least pkv_attn_paged_workspace_size() bytes, 256-byte aligned
  *            (NULL where that is 0).
  * Errors: as pkv_paged_kv_append; Hq not a multiple of Hkv, a scale that is
- * not finite, window < 0, sinks < 0, more than 2^30 tiles of work
- * (PKV_ERR_INVALID_ARGUMENT); sinks > 64 (PKV_ERR_UNSUPPORTED);
- * PKV_ERR_WORKSPACE.
+ * not finite, window < 0, sinks < 0 (PKV_ERR_INVALID_ARGUMENT); sinks > 64
+ * (PKV_ERR_UNSUPPORTED); PKV_ERR_WORKSPACE.
  */
 size_t pkv_attn_paged_workspace_size(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D,
                                      int32_t dtype);

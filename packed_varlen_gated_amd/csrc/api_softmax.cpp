@@ -10,6 +10,7 @@ namespace {
 using namespace pkv;
 
 constexpr int32_t kMaxSinks = 64;
+constexpr int64_t kMaxPlaces = int64_t(1) << 30;  // of a cache, and of a request
 
 Span f32_span(const float* p, int64_t n) { return {p, n * 4, 4}; }
 Span i32_span(const int32_t* p, int64_t n) { return {p, n * 4, 4}; }
@@ -49,7 +50,7 @@ pkv_status check_paged(const int32_t* cu, int64_t N, int32_t R, int32_t Hq, int3
     return PKV_ERR_INVALID_ARGUMENT;
   if (!known_dtype(dtype) || !supported_head_dim(D) || page_size < 16 || page_size > 65536 || page_size % 16 != 0)
     return PKV_ERR_UNSUPPORTED;
-  if (int64_t(num_pages) * page_size > kInt32Max || int64_t(max_pages) * page_size > kInt32Max ||
+  if (int64_t(num_pages) * page_size > kMaxPlaces || int64_t(max_pages) * page_size > kMaxPlaces ||
       (N / 16 + R) * Hq >= kMaxGroups)
     return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;
@@ -187,7 +188,9 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
 }
 
 size_t pkv_attn_paged_workspace_size(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype) {
-  return 0;
+  const int32_t one = 1;
+  if (check_paged(&one, N, R, Hq, Hkv, D, 16, 1, 1, dtype) != PKV_OK || !attn_mfma_supported(D, dtype)) return 0;
+  return attn_paged_workspace_bytes(D);
 }
 
 pkv_status pkv_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -210,6 +213,7 @@ pkv_status pkv_attn_paged(const void* q, const void* k_pages, const void* v_page
     return PKV_ERR_INVALID_ARGUMENT;
   const PagedArgs c{page_table, kv_lens, cu_seqlens, N, R, Hkv, D, page_size, num_pages, max_pages, flags};
   const AttnPagedArgs x{q, k_pages, v_pages, Hq, scale, window, window > 0 ? sinks : 0, o, lse, workspace};
+  if (attn_mfma_supported(D, dtype)) return from_hip(launch_attn_paged(c, x, static_cast<hipStream_t>(stream)));
   return from_hip(launch_attn_paged_simple(c, x, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -1,0 +1,692 @@
+// Attention of new tokens over the paged cache on the matrix cores (bf16, D in
+// {64, 128}).
+//
+//   o_t = sum_s softmax_s(scale q_t.k_s) v_s over the places s <= t of t's request,
+//   with a window those with t - s < window or s < sinks.
+//
+// Row i of a (request, kv head) is its new token i / rep under query head i % rep of
+// the group: the heads that share keys share their loads. Two forms:
+//   small  at most 32 rows (decoding): a work-group's four waves hold the same rows
+//          and take KW keys each of a block; every wave streams its keys through LDS
+//          of its own (no barrier in the walk), and the sums are joined at the end.
+//   big    tiles of 128 rows (chunks of prompts): a wave holds 32 rows, the four
+//          share blocks of 64 keys. A walk is that of the packed kernel (attn_fwd.hip):
+//          S^T = K Q^T, P = 2^(c S - m), O^T += V^T P^T, O rescaled only when a
+//          row's maximum grew by more than 2^8.
+//
+// Lengths are on the device and differ widely, so the work is dealt there: a tile's
+// blocks of keys are units, all units of the call are in one order (kv head, request,
+// tile, block), and work-group w takes units [w per, (w + 1) per) of it, the last
+// part of one tile, whole tiles, the first part of another. A tile that is cut leaves
+// its parts' sums in the workspace (two for each work-group at most) and a second
+// launch joins them. Every work-group finds its place by one scan over the requests.
+// In the big form a chunk's later tiles have more blocks than its earlier ones; tile i
+// and tile J - 1 - i together have nearly the same number for all i, so such a pair is
+// what a request has equal ones of.
+//
+// Pages are multiples of 16 places and a wave's loads go by 16 of them: one page and
+// one buffer descriptor for each 16 keys, whose size ends at the request's last token,
+// so that nothing else of a page is read.
+//
+// A weight of 0 times a value that is not finite is NaN. When a sum of a part is not
+// finite the part is walked again with such values as 0, and then they are added to
+// the rows that see them.
+
+#include "mfma.h"
+#include "paged.h"
+
+#include <float.h>
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kGrow = 8.f;  // log2 of what a row's maximum may grow by before O is rescaled
+
+template <int D, bool kBig>
+struct Form {
+  static constexpr int BM = kBig ? 128 : 32;                  // rows of a tile
+  static constexpr int KW = kBig ? 64 : D == 128 ? 32 : 64;   // keys of a wave in a block
+  static constexpr int BK = kBig ? 64 : 4 * KW;               // keys of a block
+  static constexpr int HALF = KW * D * 2;                     // bytes of a block's K (or V) in LDS, of a wave or of all
+  static constexpr int STAGE = 2 * HALF * (kBig ? 1 : 4);     // of a block
+  static constexpr int GROUPS = kBig ? 512 : 256;             // what the chip holds at a time
+  static constexpr int LEAST = kBig ? 4 : 2;                  // units of a work-group
+  static constexpr size_t PARTS = size_t(2) * GROUPS * BM * (D + 2) * 4;  // bytes of the parts' sums
+};
+
+template <int D>
+struct Swz {
+  static constexpr int CH = D / 8;  // 16-byte chunks of a row
+  static __device__ __forceinline__ int k(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
+  static __device__ __forceinline__ int v(int row) { return D == 128 ? (row & 3) << 2 : (row & 2) << 1; }
+};
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
+__device__ __forceinline__ int32_t uni(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uni(int64_t x) {
+  return int64_t(uint64_t(uint32_t(uni(int32_t(x)))) | uint64_t(uint32_t(uni(int32_t(x >> 32)))) << 32);
+}
+
+// What a tile's rows see.
+struct Span {
+  int32_t lo, hi;  // places of its first and last row
+  int32_t blocks;  // at least 1
+  WindowWalk ww;
+};
+template <int BM, int BK>
+__device__ __forceinline__ Span span_of(const Request& q, int32_t rep, int32_t window, int32_t sinks, int32_t j) {
+  const int32_t first = q.len - q.n;
+  const int64_t last = int64_t(BM) * (j + 1) - 1, rows = int64_t(q.n) * rep;
+  const int32_t lo = first + int32_t(int64_t(BM) * j / rep), hi = first + int32_t((last < rows ? last : rows - 1) / rep);
+  const WindowWalk ww(window > 0 ? window : 0x7fffffff, window > 0 ? sinks : 0, BK, lo > 0 ? lo : 0, 0);
+  return {lo, hi, hi < 0 ? 1 : ww.count(hi / BK + 1), ww};
+}
+
+// A request's part in the call: `pairs` (small form: its one tile) of `cost` units.
+struct Share {
+  Request q;
+  int32_t tiles, pairs, cost;
+  __device__ __forceinline__ int64_t units() const { return int64_t(pairs) * cost; }
+};
+template <int D, bool kBig>
+__device__ __forceinline__ Share share_of(const PagedArgs& c, const AttnPagedArgs& x, int32_t r) {
+  using F = Form<D, kBig>;
+  const int32_t rep = x.Hq / c.Hkv;
+  Share s{request(c, r), 0, 0, 0};
+  const int64_t rows = int64_t(s.q.n) * rep;
+  if (rows == 0 || (rows > 32) != kBig) return s;
+  if constexpr (!kBig) {
+    s.tiles = s.pairs = 1;
+    s.cost = span_of<F::BM, F::BK>(s.q, rep, x.window, x.sinks, 0).blocks;
+    return s;
+  }
+  s.tiles = int32_t((rows + F::BM - 1) / F::BM);
+  s.pairs = (s.tiles + 1) / 2;
+  // Without a window a tile's blocks are a rounded linear function of its number, at
+  // least 1 (and the last tile's are fewer where it is not full): the sum over a pair is
+  // at most that of the outermost one and 2 + 3. With one no tile has more than its
+  // window, its tokens and its sinks need.
+  const int32_t a = span_of<F::BM, F::BK>(s.q, rep, 0, 0, 0).blocks + span_of<F::BM, F::BK>(s.q, rep, 0, 0, s.tiles - 1).blocks;
+  s.cost = s.tiles == 1 ? a / 2 : a + 5;
+  if (x.window > 0) {
+    const int64_t most = (int64_t(x.window) + F::BM / rep + 1) / F::BK + 2 + (x.sinks + F::BK - 1) / F::BK;
+    const int64_t b = (s.tiles == 1 ? 1 : 2) * most;
+    s.cost = b < s.cost ? int32_t(b) : s.cost;
+  }
+  return s;
+}
+
+// The same in every lane: kept in scalar registers.
+__device__ __forceinline__ Share uniform(const Share& s) {
+  return {{uni(s.q.a), uni(s.q.n), uni(s.q.len), s.q.ok}, uni(s.tiles), uni(s.pairs), uni(s.cost)};
+}
+
+// The sum over the work-group's 256 threads, and over those before this one.
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t& before, int64_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t s = x;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t y = __shfl_up(s, d, 64);
+    if (lane >= d) s += y;
+  }
+  __syncthreads();  // the last scan's readers are done
+  if (lane == 63) lds[wave] = s;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    base += w < wave ? lds[w] : 0;
+    all += lds[w];
+  }
+  before = base + s - x;
+  return uni(all);
+}
+
+// The order of the call's units, and a place in it.
+template <int D, bool kBig>
+struct Place {
+  int64_t per_head;  // units of a kv head
+  int64_t per;       // units of a work-group
+  int32_t hk, r;     // the place's kv head and request
+  int64_t at;        // the request's first unit (of all)
+  Share s;           // the request
+
+  // All threads of the work-group; units of the call and the place of unit `per` w.
+  // False where there is none.
+  __device__ __forceinline__ bool find(const PagedArgs& c, const AttnPagedArgs& x, int64_t w, int64_t& unit) {
+    __shared__ int64_t lds[kThreads / 64 + 2];
+    int64_t mine = 0, before, total = 0;
+    for (int32_t r0 = 0; r0 < c.R; r0 += kThreads) {
+      const int32_t i = r0 + int32_t(threadIdx.x);
+      mine = i < c.R ? share_of<D, kBig>(c, x, i).units() : 0;
+      total += scan(mine, before, lds);
+    }
+    per_head = total;
+    const int64_t all = total * c.Hkv;
+    per = (all + Form<D, kBig>::GROUPS - 1) / Form<D, kBig>::GROUPS;
+    per = per < Form<D, kBig>::LEAST ? Form<D, kBig>::LEAST : per;
+    unit = per * w;
+    if (unit >= all) return false;
+    hk = int32_t(unit / total);
+    const int64_t y = unit - hk * total;
+    int64_t base = 0;
+    for (int32_t r0 = 0;; r0 += kThreads) {
+      if (c.R > kThreads) {  // (else the scan above is the one needed)
+        const int32_t i = r0 + int32_t(threadIdx.x);
+        mine = i < c.R ? share_of<D, kBig>(c, x, i).units() : 0;
+        total = scan(mine, before, lds);
+      }
+      if (y >= base + before && y < base + before + mine) {
+        lds[kThreads / 64] = r0 + int32_t(threadIdx.x);
+        lds[kThreads / 64 + 1] = base + before;
+      }
+      base += total;
+      if (y < base) break;
+    }
+    __syncthreads();
+    r = uni(int32_t(lds[kThreads / 64]));
+    at = int64_t(hk) * per_head + uni(lds[kThreads / 64 + 1]);
+    s = uniform(share_of<D, kBig>(c, x, r));
+    return true;
+  }
+
+  // The next request with units (the caller knows that there is one): 64 at a time.
+  __device__ __forceinline__ void next(const PagedArgs& c, const AttnPagedArgs& x) {
+    at += s.units();
+    ++r;
+    for (;;) {
+      if (r >= c.R) {
+        r = 0;
+        ++hk;
+      }
+      const int32_t i = r + int32_t(threadIdx.x & 63);
+      const uint64_t m = __builtin_amdgcn_ballot_w64(i < c.R && share_of<D, kBig>(c, x, i).pairs > 0);
+      if (m != 0) {
+        r = uni(r + int32_t(__builtin_ctzll(m)));
+        break;
+      }
+      r += 64;
+    }
+    s = uniform(share_of<D, kBig>(c, x, r));
+  }
+};
+
+// A part of a tile that begins at unit `unit`: its tile, and blocks [b0, b1) of it as
+// far as the tile goes; where the unit is one of the spare ones of a pair, b0 = b1.
+// `skip`: units from `unit` to the next tile.
+struct Part {
+  int32_t j;
+  Span sp;
+  int32_t b0;
+  int64_t skip;
+};
+template <int D, bool kBig>
+__device__ __forceinline__ Part part_at(const Place<D, kBig>& pl, const AttnPagedArgs& x, int32_t rep, int64_t unit) {
+  using F = Form<D, kBig>;
+  const Share& s = pl.s;
+  const int64_t off = unit - pl.at;
+  if constexpr (!kBig) {
+    const Span sp = span_of<F::BM, F::BK>(s.q, rep, x.window, x.sinks, 0);
+    return {0, sp, int32_t(off), sp.blocks - off};
+  }
+  const int32_t i = int32_t(off / s.cost), in = int32_t(off - int64_t(i) * s.cost);
+  const int32_t ja = s.tiles - 1 - i;
+  Span sp = span_of<F::BM, F::BK>(s.q, rep, x.window, x.sinks, ja);
+  if (in < sp.blocks) return {ja, sp, in, sp.blocks - in};
+  const int32_t past = sp.blocks;
+  if (ja != i) {
+    sp = span_of<F::BM, F::BK>(s.q, rep, x.window, x.sinks, i);
+    if (in < past + sp.blocks) return {i, sp, in - past, past + sp.blocks - in};
+  }
+  return {-1, sp, 0, s.cost - in};
+}
+
+template <int D, bool kBig>
+__global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(const PagedArgs c, const AttnPagedArgs x,
+                                                                            float* __restrict__ sums,
+                                                                            int64_t groups) {
+  using F = Form<D, kBig>;
+  constexpr int CH = Swz<D>::CH, KS = D / 16, DT = D / 32, NJ = F::KW / 32;
+  constexpr int GR = kBig ? 1 : F::KW / 16;  // granules of 16 keys that a wave loads of a block
+  constexpr int GL = 16 * CH / 64;           // loads of a granule of K (and of V)
+  constexpr int RL = 16 / GL;                // rows of a load
+  __shared__ __attribute__((aligned(1024))) char lds[2 * F::STAGE];
+  static_assert(kBig || 2 * F::STAGE >= 4 * 32 * (D + 6) * 4, "the waves' sums are joined in the stages");
+
+  const int64_t b = blockIdx.x;
+  if (b >= groups) {
+    const int64_t j = b - groups, n = gridDim.x - groups, end = covered_tokens(c.cu, c.R, c.N);
+    zero_tail(x.o, end, c.N, int64_t(x.Hq) * D * 2, j, n);
+    if (x.lse != nullptr)
+      for (int64_t i = j * kThreads + threadIdx.x; i < (c.N - end) * x.Hq; i += n * kThreads)
+        x.lse[(i / (c.N - end)) * c.N + end + i % (c.N - end)] = -INFINITY;
+    if (j == 0) check_requests(c);
+    return;
+  }
+  // Consecutive work-groups run on different XCDs: units that share keys go to one.
+  const int64_t w = kBig ? b % 8 * (F::GROUPS / 8) + b / 8 : b;
+  Place<D, kBig> pl;
+  int64_t unit;
+  if (!pl.find(c, x, w, unit)) return;
+  int64_t end = unit + pl.per;
+  {
+    const int64_t all = pl.per_head * c.Hkv;
+    end = end < all ? end : all;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int32_t rep = x.Hq / c.Hkv, ps = c.page_size;
+  const int32_t kstride = c.Hkv * D * 2;
+  const float cs = x.scale == 0.f ? 1.f : fabsf(x.scale) * kLog2e;  // (as in attn_fwd.hip)
+  const uint32_t flip = x.scale < 0.f ? 0x80008000u : 0u, keep = x.scale == 0.f ? 0u : ~0u;
+  const bf16 *kp = static_cast<const bf16*>(x.k_pages), *vp = static_cast<const bf16*>(x.v_pages);
+
+  // the lane's place in a load: row lrow of RL, chunk lpos
+  const int lrow = lane / CH, lpos = lane % CH;
+  const uint32_t koff = uint32_t(lrow) * kstride, kchunk = uint32_t(lpos ^ Swz<D>::k(lrow)) * 16;
+  const uint32_t voff = koff + uint32_t(lpos ^ Swz<D>::v(lrow)) * 16;
+  // LDS addresses of the lane's operand chunks
+  const int kx = Swz<D>::k(col);
+  const int vr = 4 * half + ((lane & 15) >> 2), vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vb = (lane & 1) * 8;
+  const int vx = Swz<D>::v(vr);
+
+  while (unit < end) {
+    if (unit >= pl.at + pl.s.units()) {
+      pl.next(c, x);
+      continue;
+    }
+    const Part pt = part_at<D, kBig>(pl, x, rep, unit);
+    if (pt.j < 0) {
+      unit += pt.skip;
+      continue;
+    }
+    const int32_t b0 = pt.b0, b1 = pt.skip < end - unit ? pt.sp.blocks : int32_t(b0 + (end - unit));
+    const bool whole = b0 == 0 && b1 == pt.sp.blocks;
+    const Request& rq = pl.s.q;
+    const int32_t r = pl.r, hk = pl.hk, window = x.window, sinks = window > 0 ? x.sinks : 0;
+    const int64_t rows_all = int64_t(rq.n) * rep, row0 = int64_t(pt.j) * F::BM;
+    const int32_t rows = rows_all - row0 < F::BM ? int32_t(rows_all - row0) : F::BM;  // the tile's
+    const int32_t wrow = kBig ? wave * 32 : 0;                                        // the wave's first
+    const int32_t mine = rows - wrow;
+    // the lane's row
+    const int64_t row = row0 + wrow + col;
+    const int32_t tok = int32_t((col < mine ? row : row0) / rep), head = hk * rep + int32_t((col < mine ? row : row0) % rep);
+    const int32_t place = col < mine ? rq.len - rq.n + tok : -1;
+    // places of the wave's first and last row
+    const int32_t wlo = uni(place), whi = __builtin_amdgcn_readlane(place, mine >= 32 ? 31 : (mine > 0 ? mine - 1 : 0));
+    const int64_t at = (int64_t(rq.a) + tok) * x.Hq + head;
+
+    bf16x8 qf[KS];
+    {
+      const bf16* q = static_cast<const bf16*>(x.q) + at * D + half * 8;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        i32x4 y = {0, 0, 0, 0};
+        if (col < mine) y = *reinterpret_cast<const i32x4*>(q + i * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = int((uint32_t(y[e]) ^ flip) & keep);
+        qf[i] = __builtin_bit_cast(bf16x8, y);
+      }
+    }
+    f32x16 acc[DT];
+    float m = -FLT_MAX, l = 0.f;
+
+    const int64_t trow = int64_t(r) * c.max_pages;
+    const int32_t wkey = kBig ? 16 * wave : F::KW * wave;  // the wave's first key to load of a block
+    // 64 entries of the request's row of the table from `ids0` on, one a lane: loads of
+    // entries would make every block wait for all loads before them
+    int32_t ids = 0, ids0 = -64;
+    auto issue = [&](int32_t blk, int st) {
+      const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? wave * (16 * D * 2) : wave * 2 * F::HALF);
+      const int32_t key = pt.sp.ww.tile(blk) * F::BK + wkey;
+      int32_t pg = key / ps, o = key - pg * ps;
+#pragma unroll
+      for (int g = 0; g < GR; ++g) {
+        const int32_t left = rq.len - key - 16 * g, have = left < 16 ? left : 16;
+        if (have > 0 && (pg < ids0 || pg >= ids0 + 64)) {
+          ids0 = pg;
+          // (waited for here, not at every use)
+          ids = fresh(c.table[trow + (pg + lane < c.max_pages ? pg + lane : c.max_pages - 1)]);
+        }
+        int32_t page = __builtin_amdgcn_readlane(ids, (pg - ids0) & 63);
+        if (have > 0 && (page < 0 || page >= c.num_pages)) {
+          if (c.flags != nullptr && lane == 0) atomicOr(c.flags, kFlagBadPage);
+          page = -1;
+        }
+        const bool ok = have > 0 && page >= 0;
+        const int64_t from = ok ? ((int64_t(page) * ps + o) * c.Hkv + hk) * D : 0;
+        const uint32_t bytes = ok ? (have - 1) * kstride + D * 2 : 0;
+        const u32x4 rk = descriptor(kp + from, bytes), rv = descriptor(vp + from, bytes);
+#pragma unroll
+        for (int u = 0; u < GL; ++u)  // rows RL u + lrow: the swizzle of K flips two or three bits of the chunk
+          load_lds16_async(rk, (koff + (kchunk ^ (Swz<D>::k(RL * u) * 16))) + u * RL * kstride, dst + g * (16 * D * 2) + u * 1024);
+#pragma unroll
+        for (int u = 0; u < GL; ++u)
+          load_lds16_async(rv, voff + u * RL * kstride, dst + F::HALF + g * (16 * D * 2) + u * 1024);
+        o += 16;
+        if (o == ps) {
+          o = 0;
+          ++pg;
+        }
+      }
+    };
+
+    // mode 0: the sums; 1: with values that are not finite as 0; 2: those values added
+    auto walk = [&](int mode) {
+      if (mode < 2) {
+        m = -FLT_MAX;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
+      }
+      issue(b0, 0);
+      for (int32_t blk = b0; blk < b1; ++blk) {
+        const int st = (blk - b0) & 1;
+        if constexpr (kBig) {
+          wait_vm();
+          bar();
+          if (blk + 1 < b1) issue(blk + 1, st ^ 1);
+        } else {
+          asm volatile("" ::: "memory");
+          if (blk + 1 < b1) {
+            issue(blk + 1, st ^ 1);
+            wait_loads<2 * GR * GL>();
+          } else {
+            wait_loads<0>();
+          }
+          asm volatile("" ::: "memory");
+        }
+        char* kt = lds + st * F::STAGE + (kBig ? 0 : wave * 2 * F::HALF);
+        char* vt = kt + F::HALF;
+        const int32_t s0 = pt.sp.ww.tile(blk) * F::BK + (kBig ? 0 : wkey);  // the wave's first key
+        if (mode > 0) {
+          // keys with a value that is not finite
+          __shared__ uint64_t odd_lds[kBig ? 1 : 4];
+          uint64_t odd = 0;
+          if constexpr (kBig) {
+            __syncthreads();
+            if (tid == 0) odd_lds[0] = 0;
+            __syncthreads();
+          }
+          for (int i = kBig ? tid : lane; i < F::HALF / 4; i += kBig ? kThreads : 64) {
+            uint32_t y = reinterpret_cast<uint32_t*>(vt)[i];
+            const bool a = (y & 0x7f80u) == 0x7f80u, e = (y & 0x7f800000u) == 0x7f800000u;
+            if (a || e) odd |= uint64_t(1) << (i / (D / 2));
+            if (mode == 1 && (a || e)) reinterpret_cast<uint32_t*>(vt)[i] = y & (a ? 0xffff0000u : ~0u) & (e ? 0xffffu : ~0u);
+          }
+          if constexpr (kBig) {
+            if (odd != 0) atomicOr(reinterpret_cast<unsigned long long*>(odd_lds), (unsigned long long)odd);
+            __syncthreads();
+            odd = odd_lds[0];
+          } else {
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) odd |= uint64_t(__shfl_xor((long long)odd, d, 64));
+            wait_all();
+            asm volatile("" ::: "memory");
+          }
+          if (mode == 2) {
+            for (int s = 0; s < F::KW; ++s) {
+              if ((odd >> s & 1) == 0) continue;
+              const int32_t p = s0 + s;
+              const bool sees = p <= place && (window == 0 || place - p < window || p < sinks);
+#pragma unroll
+              for (int i = 0; i < DT; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const int ch = 32 * i + 8 * (j / 4) + 4 * half + j % 4;
+                  const float y = to_f32(*reinterpret_cast<const bf16*>(
+                      vt + s * (D * 2) + (((ch / 8) ^ Swz<D>::v(s)) * 16) + ch % 8 * 2));
+                  if (sees && !finite(y)) acc[i][j] += y;
+                }
+            }
+            continue;
+          }
+        }
+        if (mine <= 0 || s0 > whi || (window > 0 && s0 + F::KW - 1 <= wlo - window && s0 >= sinks)) continue;
+
+        f32x16 s[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          s[j] = f32x16{};
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            const bf16x8 a = *reinterpret_cast<const bf16x8*>(kt + (32 * j + col) * (D * 2) + (((2 * i + half) ^ kx) * 16));
+            s[j] = mfma32(a, qf[i], s[j]);
+          }
+        }
+        // (a wave of less than 32 rows has lanes that see nothing: their sums are not used)
+        if (s0 + F::KW - 1 > wlo || (window > 0 && s0 <= whi - window)) {
+          const int32_t last = place - s0 - 4 * half, old = window > 0 ? last - window : -1;
+          const int32_t sink = sinks - s0 - 4 * half;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int32_t k = 32 * j + 8 * (i / 4) + i % 4;
+              s[j][i] = k <= last && (k > old || k < sink) ? s[j][i] : -INFINITY;
+            }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
+        mx = fmaxf(mx, other_half(mx)) * cs;
+        const bool grew = mx > m + kGrow;
+        if (__builtin_amdgcn_ballot_w64(grew) != 0) {
+          const float f = grew ? ex2(m - mx) : 1.f;
+          m = grew ? mx : m;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i][j] *= f;
+        }
+        bf16x8 p[2 * NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float y = ex2(fmaf(s[j][i], cs, -m));
+            l += y;
+            p[2 * j + i / 8][i % 8] = static_cast<bf16>(y);
+          }
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2 * NJ; ++j) {
+            const char* a = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
+            acc[i] = mfma32(join(read_tr(a), read_tr(a + 8 * (D * 2))), p[j], acc[i]);
+          }
+      }
+    };
+    walk(0);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) bad |= !finite(acc[i][j]);
+    bad = bad && col < mine;
+    const bool again = kBig ? __syncthreads_or(bad) != 0 : __builtin_amdgcn_ballot_w64(bad) != 0;
+    if (again) {
+      walk(1);
+      if constexpr (kBig) __syncthreads();
+      walk(2);
+    }
+    l += other_half(l);
+    __syncthreads();  // every wave is done with the stages
+
+    // The tile's outputs, or the part's sums (a part with the tile's first block is the
+    // work-group's last one, any other its first).
+    const int64_t slot = 2 * w + (b0 == 0 ? 1 : 0);
+    float* ps_ = sums + slot * F::BM * D;
+    float* pst = sums + int64_t(2) * F::GROUPS * F::BM * D + slot * F::BM * 2;
+    bf16* o = static_cast<bf16*>(x.o);
+    if constexpr (kBig) {
+      if (col < mine) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int ch = 32 * i + 8 * j + 4 * half;
+            if (whole) {
+              bf16x4 y;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = static_cast<bf16>(acc[i][4 * j + e] * inv);
+              *reinterpret_cast<bf16x4*>(o + at * D + ch) = y;
+            } else {
+              *reinterpret_cast<f32x4*>(ps_ + (wrow + col) * D + ch) =
+                  f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+            }
+          }
+        if (half == 0) {
+          if (!whole) {
+            pst[2 * (wrow + col)] = m;
+            pst[2 * (wrow + col) + 1] = l;
+          } else if (x.lse != nullptr) {
+            x.lse[int64_t(head) * c.N + rq.a + tok] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+          }
+        }
+      }
+    } else {
+      // [wave][row][D + 4] and then [wave][row] m, l
+      float* js = reinterpret_cast<float*>(lds);
+      float* jst = js + 4 * 32 * (D + 4);
+      if (col < mine) {
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4*>(js + (wave * 32 + col) * (D + 4) + 32 * i + 8 * j + 4 * half) =
+                f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+        if (half == 0) {
+          jst[2 * (wave * 32 + col)] = m;
+          jst[2 * (wave * 32 + col) + 1] = l;
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int q = i / (D / 4), d = i % (D / 4) * 4;
+        float top = jst[2 * q], sum = 0.f;
+#pragma unroll
+        for (int v = 1; v < 4; ++v) top = fmaxf(top, jst[2 * (v * 32 + q)]);
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float f = ex2(jst[2 * (v * 32 + q)] - top);
+          sum += f * jst[2 * (v * 32 + q) + 1];
+          const f32x4 z = *reinterpret_cast<const f32x4*>(js + (v * 32 + q) * (D + 4) + d);
+          // (an infinity stays one, however small its wave's share)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] += finite(z[e]) ? f * z[e] : z[e];
+        }
+        if (!whole) {
+          *reinterpret_cast<f32x4*>(ps_ + q * D + d) = y;
+          if (d == 0) {
+            pst[2 * q] = top;
+            pst[2 * q + 1] = sum;
+          }
+          continue;
+        }
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        const int32_t t = q / rep, hh = hk * rep + q % rep;
+        bf16x4 z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = static_cast<bf16>(y[e] * inv);
+        *reinterpret_cast<bf16x4*>(o + ((int64_t(rq.a) + t) * x.Hq + hh) * D + d) = z;
+        if (x.lse != nullptr && d == 0)
+          x.lse[int64_t(hh) * c.N + rq.a + t] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+      }
+      __syncthreads();  // the sums have left LDS
+    }
+    unit += b1 - b0;
+  }
+}
+
+// Joins the parts of cut tiles: work-group w has the tile that is cut where the share
+// of the main launch's work-group w + 1 begins, if that is the tile's first cut. Its
+// outputs are dealt to gridDim.y work-groups.
+template <int D, bool kBig>
+__device__ __forceinline__ void join_parts(const PagedArgs& c, const AttnPagedArgs& x, const float* __restrict__ sums,
+                                           int64_t w) {
+  using F = Form<D, kBig>;
+  Place<D, kBig> pl;
+  int64_t unit;
+  if (!pl.find(c, x, w + 1, unit)) return;
+  const int32_t rep = x.Hq / c.Hkv;
+  const Part pt = part_at<D, kBig>(pl, x, rep, unit);
+  if (pt.j < 0 || pt.b0 == 0 || unit - pt.b0 < w * pl.per) return;
+  const int64_t last = (unit - pt.b0 + pt.sp.blocks - 1) / pl.per;  // the last work-group with a part
+  const Request& rq = pl.s.q;
+  const int64_t row0 = int64_t(pt.j) * F::BM, left = int64_t(rq.n) * rep - row0;
+  const int rows = left < F::BM ? int(left) : F::BM;
+  const float* st = sums + int64_t(2) * F::GROUPS * F::BM * D;
+  auto slot = [&](int64_t v) { return 2 * v + (v == w ? 1 : 0); };
+  for (int i = blockIdx.y * kThreads + threadIdx.x; i < rows * (D / 4); i += gridDim.y * kThreads) {
+    const int q = i / (D / 4), d = i % (D / 4) * 4;
+    float top = -FLT_MAX, sum = 0.f;
+    for (int64_t v = w; v <= last; ++v) top = fmaxf(top, st[(slot(v) * F::BM + q) * 2]);
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t v = w; v <= last; ++v) {
+      const int64_t at = slot(v) * F::BM + q;
+      const float f = ex2(st[at * 2] - top);
+      sum += f * st[at * 2 + 1];
+      const f32x4 z = *reinterpret_cast<const f32x4*>(sums + at * D + d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] += finite(z[e]) ? f * z[e] : z[e];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    const int64_t row = row0 + q;
+    const int32_t t = int32_t(row / rep), hh = pl.hk * rep + int32_t(row % rep);
+    bf16x4 z;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = static_cast<bf16>(y[e] * inv);
+    *reinterpret_cast<bf16x4*>(static_cast<bf16*>(x.o) + ((int64_t(rq.a) + t) * x.Hq + hh) * D + d) = z;
+    if (x.lse != nullptr && d == 0)
+      x.lse[int64_t(hh) * c.N + rq.a + t] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(const PagedArgs c, const AttnPagedArgs x,
+                                                                   const float* __restrict__ small,
+                                                                   const float* __restrict__ big, int small_groups) {
+  if (int(blockIdx.x) < small_groups)
+    join_parts<D, false>(c, x, small, blockIdx.x);
+  else
+    join_parts<D, true>(c, x, big, int64_t(blockIdx.x) - small_groups);
+}
+
+// Which forms a call's requests can have.
+bool any_small(const PagedArgs& c, int32_t Hq) { return Hq / c.Hkv <= 32; }
+bool any_big(const PagedArgs& c, int32_t Hq) { return c.cu != nullptr || Hq / c.Hkv > 32; }
+
+template <int D>
+hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
+  const bool s = any_small(c, x.Hq), b = any_big(c, x.Hq);
+  float* small = static_cast<float*>(x.workspace);
+  float* big = reinterpret_cast<float*>(static_cast<char*>(x.workspace) + Form<D, false>::PARTS);
+  // (the first launch also zeroes the rows that no request has)
+  const int64_t tail = c.cu == nullptr ? 1 : tail_groups(c.N * x.Hq * D * 2);
+  constexpr int64_t gs = Form<D, false>::GROUPS, gb = Form<D, true>::GROUPS;
+  if (b) attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(kThreads), 0, stream>>>(c, x, big, gb);
+  if (s) attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(kThreads), 0, stream>>>(c, x, small, gs);
+  const int js = s ? int(gs) - 1 : 0, jb = b ? int(gb) - 1 : 0;
+  attn_paged_join_kernel<D><<<dim3(js + jb, b ? 4 : 1), dim3(kThreads), 0, stream>>>(c, x, small, big, js);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_paged_workspace_bytes(int32_t D) {
+  return D == 64 ? Form<64, false>::PARTS + Form<64, true>::PARTS : Form<128, false>::PARTS + Form<128, true>::PARTS;
+}
+
+hipError_t launch_attn_paged(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
+  return c.D == 64 ? run<64>(c, x, stream) : run<128>(c, x, stream);
+}
+
+}  // namespace pkv

@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
       qf[p] = row < rows ? load4(static_cast<const T*>(x.q) + out * D + 8 * p + 4 * half) : f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
     f32x16 acc[D / 32] = {};
-    const WindowWalk ww(win ? x.window : 0x7fffffff, win ? x.sinks : 0, kT, lo, 0);
+    const WindowWalk ww(win ? x.window : 0x7fffffff, win ? x.sinks : 0, kT, lo > 0 ? lo : 0, 0);
     const int32_t n_tiles = hi < 0 ? 0 : ww.count(hi / kT + 1);
     for (int32_t it = wave; it < n_tiles; it += kWaves) {
       const int32_t s0 = ww.tile(it) * kT;
@@ -219,7 +219,7 @@ hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attn_paged_simple(const PagedArgs& c, const AttnPagedArgs& x, int32_t dtype, hipStream_t stream) {
-  if (dtype == 0) return c.D == 32 ? run<bf16, 32>(c, x, stream) : c.D == 64 ? run<bf16, 64>(c, x, stream) : run<bf16, 128>(c, x, stream);
+  if (dtype == 0) return c.D == 32 ? run<bf16, 32>(c, x, stream) : hipErrorInvalidValue;
   if (c.D == 32) return run<float, 32>(c, x, stream);
   if (c.D == 64) return run<float, 64>(c, x, stream);
   return run<float, 128>(c, x, stream);

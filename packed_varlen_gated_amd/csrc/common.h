@@ -260,6 +260,10 @@ struct AttnPagedArgs {
   void* workspace;
 };
 hipError_t launch_paged_append(const PagedArgs& c, const AppendArgs& x, int32_t dtype, hipStream_t stream);
+// Off the matrix-core path: fp32, and bf16 at D = 32.
 hipError_t launch_attn_paged_simple(const PagedArgs& c, const AttnPagedArgs& x, int32_t dtype, hipStream_t stream);
+// The matrix-core kernels (where attn_mfma_supported).
+size_t attn_paged_workspace_bytes(int32_t D);
+hipError_t launch_attn_paged(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream);
 
 }  // namespace pkv

@@ -47,6 +47,28 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t of
   // (a scalar offset would not take part in the range check)
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
 }
+// The same, with the waits left to the caller. Behind the builtin the compiler waits for
+// all loads before the next read of LDS that it cannot tell apart, that is, for those of
+// the next tile before this one is used. `lds` is a byte address (lds_addr). The loads
+// count for wait_vm and wait_loads; no register is written. The descriptor is that of
+// buffer(), the same in every lane.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uintptr_t>(base);
+  return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b))),
+               uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32) & 0xffffu)),
+               uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+}
+__device__ __forceinline__ void load_lds16_async(u32x4 r, uint32_t off, uint32_t lds) {
+  // (an instruction that reads m0 right behind its change would need a wait state)
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(lds), "v"(off), "s"(r)
+      : "memory", "m0");
+}
 // x, recomputed from here on: what is derived from it in a loop is not kept in
 // registers across the loop.
 __device__ __forceinline__ uint32_t fresh(uint32_t x) {

@@ -341,6 +341,13 @@ def test_paged_chunks(dtype, D, window, sinks):
     paged_case([900], [310], 2, 1, D, dtype, 64, window, sinks, seed=window + 1)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (9, 2)])
+@pytest.mark.parametrize("dtype,D", PAGED_TYPES)
+def test_paged_rows_before_the_first_place(dtype, D, window, sinks):
+    """More new tokens than kv_lens: those before the first place see nothing."""
+    paged_case([3, 0, 10, 200, 1, 0], [7, 4, 30, 300, 2, 150], 4, 2, D, dtype, 16, window, sinks, tail=2, seed=window)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (6, 1), (8, 2), (5, 5), (40, 1), (16, 2), (140, 1)])
 @pytest.mark.parametrize("dtype,D", [("f32", 32), ("bf16", 64), ("bf16", 128)])
 def test_paged_heads(Hq, Hkv, dtype, D):
