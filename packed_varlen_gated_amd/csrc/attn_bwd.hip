@@ -64,6 +64,11 @@ struct Loader {
     off = uint32_t(row) * stride + (pos ^ Lds<D>::swz(row)) * 16;
     step = uint32_t(STEP) * stride;
   }
+  __device__ __forceinline__ void issue_async(u32x4 r, char* dst, int wave) const {
+    const uint32_t o = fresh(off);
+#pragma unroll
+    for (int i = 0; i < LD; ++i) load_lds16_async(r, o + i * step, lds_addr(dst) + wave * 1024 + i * NT * 16);
+  }
   __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, char* dst, int wave) const {
     const uint32_t o = fresh(off);
 #pragma unroll
@@ -213,8 +218,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
       const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
       const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(n - 1) * kstride + D * 2;
       char* dst = lds + (it & 1) * 2 * TB;
-      ld.issue(buffer(k + at, bytes), dst, wave);
-      ld.issue(buffer(v + at, bytes), dst + TB, wave);
+      if constexpr (kWin) {
+        ld.issue_async(descriptor(k + at, bytes), dst, wave);
+        ld.issue_async(descriptor(v + at, bytes), dst + TB, wave);
+      } else {
+        ld.issue(buffer(k + at, bytes), dst, wave);
+        ld.issue(buffer(v + at, bytes), dst + TB, wave);
+      }
     };
     issue(0);
 
@@ -418,11 +428,20 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
       const int32_t n = q_to() - s0 < T ? q_to() - s0 : T;
       const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
       char* dst = lds + (it & 1) * 2 * TB;
-      ld.issue(buffer(q + at, bytes), dst, wave);
-      ld.issue(buffer(dout + at, bytes), dst + TB, wave);
+      if constexpr (kWin) {
+        ld.issue_async(descriptor(q + at, bytes), dst, wave);
+        ld.issue_async(descriptor(dout + at, bytes), dst + TB, wave);
+      } else {
+        ld.issue(buffer(q + at, bytes), dst, wave);
+        ld.issue(buffer(dout + at, bytes), dst + TB, wave);
+      }
       if (wave < T / 32) {  // lse log2 e and delta, 64 queries a wave
         const int w = wave / (T / 64), part = wave % (T / 64) * 64;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        if constexpr (kWin)
+          load_lds4_async(descriptor(stats + (int64_t(w) * H + h) * N + s0, n * 4), uint32_t(part + lane) * 4,
+                          lds_addr(lds) + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4);
+        else
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
             buffer(stats + (int64_t(w) * H + h) * N + s0, int64_t(n) * 4),
             (__attribute__((address_space(3))) void*)(lds + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4), 4,
             uint32_t(part + lane) * 4, 0, 0, 0);

@@ -128,9 +128,18 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
       const int32_t s0 = tile_start(it);
       const int32_t have = t.e - s0 < kBN ? t.e - s0 : kBN;
       const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(have - 1) * kstride + D * 2;
+      const uint32_t ko = fresh(koff), vo = fresh(voff);
+      if constexpr (kWin) {
+        const u32x4 rk = descriptor(k + at, bytes), rv = descriptor(v + at, bytes);
+        const uint32_t dst = lds_addr(lds) + (it & 1) * 2 * TB + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) load_lds16_async(rk, ko + i * STEP * kstride, dst + i * kThreads * 16);
+#pragma unroll
+        for (int i = 0; i < LD; ++i) load_lds16_async(rv, vo + i * STEP * kstride, dst + TB + i * kThreads * 16);
+        return;
+      }
       const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);
       char* dst = lds + (it & 1) * 2 * TB + wave * 1024;
-      const uint32_t ko = fresh(koff), vo = fresh(voff);
 #pragma unroll
       for (int i = 0; i < LD; ++i) load_lds16(rk, ko + i * STEP * kstride, dst + i * kThreads * 16);
 #pragma unroll

@@ -59,16 +59,25 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
                uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32) & 0xffffu)),
                uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 }
+// (an instruction that reads m0 right behind its change needs a wait state; m0 is the
+// compiler's own and put back)
+#define PKV_LOAD_LDS_ASYNC(op)               \
+  uint32_t m0;                               \
+  asm volatile(                              \
+      "s_mov_b32 %0, m0\n\t"                 \
+      "s_mov_b32 m0, %1\n\t"                 \
+      "s_nop 0\n\t" op " %2, %3, 0 offen lds\n\t" \
+      "s_mov_b32 m0, %0"                     \
+      : "=&s"(m0)                            \
+      : "s"(lds), "v"(off), "s"(r)           \
+      : "memory")
 __device__ __forceinline__ void load_lds16_async(u32x4 r, uint32_t off, uint32_t lds) {
-  // (an instruction that reads m0 right behind its change would need a wait state)
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, 0 offen lds"
-      :
-      : "s"(lds), "v"(off), "s"(r)
-      : "memory", "m0");
+  PKV_LOAD_LDS_ASYNC("buffer_load_dwordx4");
 }
+__device__ __forceinline__ void load_lds4_async(u32x4 r, uint32_t off, uint32_t lds) {
+  PKV_LOAD_LDS_ASYNC("buffer_load_dword");
+}
+#undef PKV_LOAD_LDS_ASYNC
 // x, recomputed from here on: what is derived from it in a loop is not kept in
 // registers across the loop.
 __device__ __forceinline__ uint32_t fresh(uint32_t x) {
