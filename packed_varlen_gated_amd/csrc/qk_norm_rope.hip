@@ -8,9 +8,9 @@
 //
 // D / 16 lanes share a head's row of one token: a lane holds the two 16-byte
 // chunks (bf16) whose channels are each other's partners, so the rotation needs no
-// exchange and the norm D / 32 steps of one. A wave takes one token: it forms
-// the token's 8 angles per lane once and walks the heads 1024 / D rows at a time,
-// the loads of several steps going out together.
+// exchange and the norm log2(D / 16) steps of one. A wave takes one token: its lanes
+// form an angle each, once, and it walks the heads 1024 / D rows at a time, the loads
+// of several steps going out together, the first ones before the angles.
 //
 // An angle is p f / 2 pi turns, formed in fp64 and reduced to half a turn before it
 // is rounded to fp32: at position 10^6 an fp32 product is off by 0.03 rad.
@@ -18,17 +18,18 @@
 // Bound by memory: nothing is read twice, and the arithmetic is a third of the
 // vector units' time at the copy's rate.
 
-#include "common.h"
+#include "mfma.h"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kAhead = 4;  // row groups of a wave that are loaded together
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// Steps (1024 / D rows) of a wave that are loaded together, and in the reverse pass.
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+template <typename T>
+constexpr int kBack = 1;
 
 struct Chunk {  // 8 channels
   float x[8];
@@ -86,15 +87,20 @@ struct Lane {
     at0 = split ? 8 * j : 16 * j;
     at1 = split ? 8 * j + rot / 2 : 16 * j + 8;
   }
-  __device__ __forceinline__ void turn(const float* __restrict__ freq, int32_t p) {
+  // The angles of position p: lane i of the wave forms that of pair i (there are at most
+  // 64), and every lane fetches its 8.
+  __device__ __forceinline__ void turn(const float* __restrict__ freq, int32_t p, int rot) {
+    const int lane = threadIdx.x & 63;
+    float c = 1.f, s = 0.f;
+    if (2 * lane < rot) {
+      const double t = double(p) * (double(freq[lane]) * 0.15915494309189533577);
+      sincospif(2.f * float(t - rint(t)), &s, &c);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      cs[i] = 1.f;
-      sn[i] = 0.f;
-      if (pair >= 0) {
-        const double t = double(p) * (double(freq[pair + i]) * 0.15915494309189533577);
-        sincospif(2.f * float(t - rint(t)), &sn[i], &cs[i]);
-      }
+      const float x = __shfl(c, pair + i, 64), y = __shfl(s, pair + i, 64);
+      cs[i] = pair < 0 ? 1.f : x;
+      sn[i] = pair < 0 ? 0.f : y;
     }
   }
   // The rotation by the angles (dir 1) or back (dir -1).
@@ -136,33 +142,39 @@ __device__ __forceinline__ float inv_rms(const Chunk& a, const Chunk& b, float e
   return 1.f / sqrtf(Lane<D, kInter>::sum(s) * (1.f / D) + eps);
 }
 
-// Steps [g0, g1) of one tensor's heads at one token; x, y: the token's rows.
-template <typename T, int D, bool kInter>
-__device__ __forceinline__ void forward_rows(const Lane<D, kInter>& ln, const Weight& w, const T* __restrict__ x,
-                                             T* __restrict__ y, int heads, int g0, int g1, float eps) {
-  for (int g = g0; g < g1; g += kAhead) {
-    Raw<T> ra[kAhead], rb[kAhead];
+// kU steps of one tensor's heads at one token, from step g on. Rows past the last head
+// are the last one again (a load under a condition costs registers), and not stored.
+template <typename T, int D, bool kInter, int kU>
+struct Batch {
+  Raw<T> a[kU], b[kU];
+  __device__ __forceinline__ void load(const Lane<D, kInter>& ln, const T* __restrict__ x, int heads, int g) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = (g + u) * ln.ROWS + ln.row;
-      if (g + u < g1 && h < heads) {
-        ra[u].load(x + h * D + ln.at0);
-        rb[u].load(x + h * D + ln.at1);
-      }
+    for (int u = 0; u < kU; ++u) {
+      const int i = (g + u) * ln.ROWS + ln.row, h = i < heads ? i : heads - 1;
+      a[u].load(x + h * D + ln.at0);
+      b[u].load(x + h * D + ln.at1);
     }
+  }
+};
+
+// y of a batch's rows.
+template <typename T, int D, bool kInter, int kU>
+__device__ __forceinline__ void forward_batch(const Lane<D, kInter>& ln, const Weight& w,
+                                              const Batch<T, D, kInter, kU>& x, T* __restrict__ y, int heads, int g,
+                                              int g1, float eps) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = (g + u) * ln.ROWS + ln.row;
-      if (g + u >= g1) break;
-      if (h >= heads) continue;
-      Chunk a = ra[u].get(), b = rb[u].get();
-      const float r = inv_rms<T, D, kInter>(a, b, eps);
+  for (int u = 0; u < kU; ++u) {
+    const int h = (g + u) * ln.ROWS + ln.row;
+    if (g + u >= g1) break;
+    Chunk a = x.a[u].get(), b = x.b[u].get();
+    const float r = inv_rms<T, D, kInter>(a, b, eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a.x[i] *= r * w.a.x[i];
-        b.x[i] *= r * w.b.x[i];
-      }
-      ln.template rotate<1>(a, b);
+    for (int i = 0; i < 8; ++i) {
+      a.x[i] *= r * w.a.x[i];
+      b.x[i] *= r * w.b.x[i];
+    }
+    ln.template rotate<1>(a, b);
+    if (h < heads) {
       store_chunk(y + h * D + ln.at0, a);
       store_chunk(y + h * D + ln.at1, b);
     }
@@ -192,67 +204,72 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const NormRopeAr
   const int q1 = g1 < gq ? g1 : gq, k0 = g0 > gq ? g0 - gq : 0, k1 = g1 - gq;
   const T *q = static_cast<const T*>(x.q) + n * x.q_stride, *k = static_cast<const T*>(x.k) + n * x.k_stride;
   T *qo = static_cast<T*>(x.q_out) + n * x.Hq * D, *ko = static_cast<T*>(x.k_out) + n * x.Hkv * D;
+  // the first rows' loads go out before the position is used
+  L ln(lane, x.rot);
+  Batch<T, D, kInter, kAhead<T>> bq;
+  Batch<T, D, kInter, kBack<T>> bk;
+  if (g0 < q1) bq.load(ln, q, x.Hq, g0);
+  if (k0 < k1) bk.load(ln, k, x.Hkv, k0);
+  Weight w;
+  w.load(g0 < q1 ? x.q_weight : x.k_weight, ln.at0, ln.at1);
   if (p < 0) {
     if (g0 < q1) zero_rows<T, D>(qo, x.Hq, g0, q1, lane);
     if (k0 < k1) zero_rows<T, D>(ko, x.Hkv, k0, k1, lane);
     return;
   }
-  L ln(lane, x.rot);
-  ln.turn(x.inv_freq, p);
-  Weight w;
+  ln.turn(x.inv_freq, p, x.rot);
   if (g0 < q1) {
-    w.load(x.q_weight, ln.at0, ln.at1);
-    forward_rows<T, D, kInter>(ln, w, q, qo, x.Hq, g0, q1, x.eps);
+    for (int g = g0;;) {
+      forward_batch<T, D, kInter, kAhead<T>>(ln, w, bq, qo, x.Hq, g, q1, x.eps);
+      if ((g += kAhead<T>) >= q1) break;
+      bq.load(ln, q, x.Hq, g);
+    }
   }
   if (k0 < k1) {
-    w.load(x.k_weight, ln.at0, ln.at1);
-    forward_rows<T, D, kInter>(ln, w, k, ko, x.Hkv, k0, k1, x.eps);
+    if (g0 < q1) w.load(x.k_weight, ln.at0, ln.at1);
+    for (int g = k0;;) {
+      forward_batch<T, D, kInter, kBack<T>>(ln, w, bk, ko, x.Hkv, g, k1, x.eps);
+      if ((g += kBack<T>) >= k1) break;
+      bk.load(ln, k, x.Hkv, g);
+    }
   }
 }
 
-// All heads of one tensor at one token; the row's part of dw is added to `dw`.
-template <typename T, int D, bool kInter>
-__device__ __forceinline__ void backward_rows(const Lane<D, kInter>& ln, const Weight& w, Weight& dw,
-                                              const T* __restrict__ x, const T* __restrict__ dy, T* __restrict__ dx,
-                                              int heads, float eps) {
-  constexpr int kU = 2;
-  const int groups = (heads + ln.ROWS - 1) / ln.ROWS;
-  for (int g = 0; g < groups; g += kU) {
-    Raw<T> ra[kU], rb[kU], rc[kU], rd[kU];
+// dx of a batch's rows; their part of dw is added to `dw`.
+template <typename T, int D, bool kInter, int kU>
+__device__ __forceinline__ void backward_batch(const Lane<D, kInter>& ln, const float* w, Weight& dw,
+                                               const Batch<T, D, kInter, kU>& x, const Batch<T, D, kInter, kU>& dy,
+                                               T* __restrict__ dx, int heads, int g, float eps) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int h = (g + u) * ln.ROWS + ln.row;
-      if (h < heads) {
-        ra[u].load(x + h * D + ln.at0);
-        rb[u].load(x + h * D + ln.at1);
-        rc[u].load(dy + h * D + ln.at0);
-        rd[u].load(dy + h * D + ln.at1);
-      }
+  for (int u = 0; u < kU; ++u) {
+    const int h = (g + u) * ln.ROWS + ln.row;
+    Chunk a = x.a[u].get(), b = x.b[u].get(), c = dy.a[u].get(), d = dy.b[u].get();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c.x[i] = h < heads ? c.x[i] : 0.f;
+      d.x[i] = h < heads ? d.x[i] : 0.f;
     }
+    const float r = inv_rms<T, D, kInter>(a, b, eps);
+    ln.template rotate<-1>(c, d);
+    const Chunk wa = load_chunk(w + fresh(ln.at0)), wb = load_chunk(w + fresh(ln.at1));
+    float s = 0.f;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int h = (g + u) * ln.ROWS + ln.row;
-      if (h >= heads) continue;
-      Chunk a = ra[u].get(), b = rb[u].get(), c = rc[u].get(), d = rd[u].get();
-      const float r = inv_rms<T, D, kInter>(a, b, eps);
-      ln.template rotate<-1>(c, d);
-      float s = 0.f;
+    for (int i = 0; i < 8; ++i) {
+      a.x[i] *= r;  // z
+      b.x[i] *= r;
+      dw.a.x[i] += c.x[i] * a.x[i];
+      dw.b.x[i] += d.x[i] * b.x[i];
+      c.x[i] *= wa.x[i];
+      d.x[i] *= wb.x[i];
+      s += c.x[i] * a.x[i] + d.x[i] * b.x[i];
+    }
+    s = Lane<D, kInter>::sum(s) * (1.f / D);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a.x[i] *= r;  // z
-        b.x[i] *= r;
-        dw.a.x[i] += c.x[i] * a.x[i];
-        dw.b.x[i] += d.x[i] * b.x[i];
-        c.x[i] *= w.a.x[i];
-        d.x[i] *= w.b.x[i];
-        s += c.x[i] * a.x[i] + d.x[i] * b.x[i];
-      }
-      s = Lane<D, kInter>::sum(s) * (1.f / D);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c.x[i] = r * (c.x[i] - a.x[i] * s);
-        d.x[i] = r * (d.x[i] - b.x[i] * s);
-      }
+    for (int i = 0; i < 8; ++i) {
+      c.x[i] = r * (c.x[i] - a.x[i] * s);
+      d.x[i] = r * (d.x[i] - b.x[i] * s);
+    }
+    if (h < heads) {
       store_chunk(dx + h * D + ln.at0, c);
       store_chunk(dx + h * D + ln.at1, d);
     }
@@ -285,59 +302,85 @@ __device__ __forceinline__ void join_weight(const Lane<D, kInter>& ln, Weight& d
   __syncthreads();
 }
 
-// Work-group b takes every gridDim.x-th group of kWaves tokens, a wave one token at
-// a time; partial: [gridDim.x, 2, D] sums of dw, or null.
+// How the reverse pass's work-groups and their partial sums are shared out: by the steps
+// of a token, at most one wave a token, four waves a SIMD in all.
+struct Split {
+  int q, k;
+  Split(const NormRopeArgs& x) {
+    const int64_t rows = 1024 / x.D, sq = (x.Hq + rows - 1) / rows, sk = (x.Hkv + rows - 1) / rows;
+    const int64_t most = (x.N + kWaves - 1) / kWaves, k0 = kGroups * sk / (sq + sk);
+    const int64_t k1 = k0 < 1 ? 1 : k0;
+    k = int(k1 < most ? k1 : most);
+    q = int(kGroups - k1 < most ? kGroups - k1 : most);
+  }
+  static constexpr int64_t kGroups = 1024;
+};
+
+// Work-groups [0, groups_q) have q, the others k: a tensor's work-group i takes every
+// n-th group of kWaves tokens of its n, a wave one token at a time. partial: D sums of dw
+// for each work-group, or null.
 template <typename T, int D, bool kInter>
-__global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(const NormRopeArgs x, const NormRopeGradArgs y,
-                                                                    float* __restrict__ partial) {
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) void qk_norm_rope_bwd_kernel(
+    const NormRopeArgs x, const NormRopeGradArgs y, float* __restrict__ partial, int groups_q) {
   __shared__ float lds[kWaves][D];
+  __shared__ __attribute__((aligned(16))) float weight[D];  // (registers are for the sums)
   using L = Lane<D, kInter>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool isq = int(blockIdx.x) < groups_q;
+  const int group = isq ? blockIdx.x : blockIdx.x - groups_q, groups = isq ? groups_q : gridDim.x - groups_q;
+  const int heads = isq ? x.Hq : x.Hkv, steps = (heads + L::ROWS - 1) / L::ROWS;
+  const int64_t stride = isq ? x.q_stride : x.k_stride, dense = int64_t(heads) * D;
+  const T *xs = static_cast<const T*>(isq ? x.q : x.k), *dys = static_cast<const T*>(isq ? y.dq_out : y.dk_out);
+  T* dxs = static_cast<T*>(isq ? y.dq : y.dk);
+  const float* w = isq ? x.q_weight : x.k_weight;
+  for (int d = threadIdx.x; d < D; d += kThreads) weight[d] = w == nullptr ? 1.f : w[d];
+  __syncthreads();
   L ln(lane, x.rot);
-  Weight wq, wk, dwq = {}, dwk = {};
-  wq.load(x.q_weight, ln.at0, ln.at1);
-  wk.load(x.k_weight, ln.at0, ln.at1);
-  for (int64_t n = int64_t(blockIdx.x) * kWaves + wave; n < x.N; n += int64_t(gridDim.x) * kWaves) {
+  Weight dw = {};
+  for (int64_t n = int64_t(group) * kWaves + wave; n < x.N; n += int64_t(groups) * kWaves) {
     const int32_t p = x.positions == nullptr ? int32_t(n) : x.positions[n];
-    const int64_t qd = n * x.Hq * D, kd = n * x.Hkv * D;
-    T *dq = static_cast<T*>(y.dq) + qd, *dk = static_cast<T*>(y.dk) + kd;
+    // the first rows' loads go out before the position is used
+    Batch<T, D, kInter, kBack<T>> bx, by;
+    bx.load(ln, xs + n * stride, heads, 0);
+    by.load(ln, dys + n * dense, heads, 0);
     if (p < 0) {
-      zero_rows<T, D>(dq, x.Hq, 0, x.Hq, lane);
-      zero_rows<T, D>(dk, x.Hkv, 0, x.Hkv, lane);
+      zero_rows<T, D>(dxs + n * dense, heads, 0, steps, lane);
       continue;
     }
-    ln.turn(x.inv_freq, p);
-    backward_rows<T, D, kInter>(ln, wq, dwq, static_cast<const T*>(x.q) + n * x.q_stride,
-                                static_cast<const T*>(y.dq_out) + qd, dq, x.Hq, x.eps);
-    backward_rows<T, D, kInter>(ln, wk, dwk, static_cast<const T*>(x.k) + n * x.k_stride,
-                                static_cast<const T*>(y.dk_out) + kd, dk, x.Hkv, x.eps);
+    ln.turn(x.inv_freq, p, x.rot);
+    for (int g = 0;;) {
+      backward_batch<T, D, kInter, kBack<T>>(ln, weight, dw, bx, by, dxs + n * dense, heads, g, x.eps);
+      if ((g += kBack<T>) >= steps) break;
+      bx.load(ln, xs + n * stride, heads, g);
+      by.load(ln, dys + n * dense, heads, g);
+    }
   }
-  if (partial == nullptr) return;
-  join_weight<D, kInter>(ln, dwq, lds, partial + int64_t(blockIdx.x) * 2 * D);
-  join_weight<D, kInter>(ln, dwk, lds, partial + int64_t(blockIdx.x) * 2 * D + D);
+  if (partial != nullptr) join_weight<D, kInter>(ln, dw, lds, partial + int64_t(blockIdx.x) * D);
 }
 
-// Column sums of partial [groups, 2 D]: 32 columns a work-group, 8 slices of rows,
-// joined in order.
+// Column sums of the partial sums [groups_q + groups_k, D]: 4 columns of one tensor a
+// work-group, every 256th row a thread, joined in order.
 template <int D>
-__global__ __launch_bounds__(kThreads) void qk_norm_rope_dw_kernel(const float* __restrict__ partial, int groups,
-                                                                   float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ float lds[8][32];
-  const int c = threadIdx.x % 32, s = threadIdx.x / 32, col = blockIdx.x * 32 + c;
-  float x = 0.f;
-  for (int g = s; g < groups; g += 8) x += partial[int64_t(g) * 2 * D + col];
-  lds[s][c] = x;
-  __syncthreads();
-  if (s != 0) return;
-  for (int i = 1; i < 8; ++i) x += lds[i][c];
-  float* out = col < D ? dwq : dwk;
-  if (out != nullptr) out[col % D] = x;
-}
-
-// Work-groups of the reverse pass: four waves a SIMD, and their partial sums stay few.
-int64_t bwd_groups(int64_t N) {
-  const int64_t g = (N + kWaves - 1) / kWaves;
-  return g < 1024 ? g : 1024;
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_dw_kernel(const float* __restrict__ partial, int groups_q,
+                                                                   int groups_k, float* __restrict__ dwq,
+                                                                   float* __restrict__ dwk) {
+  __shared__ f32x4 lds[kThreads];
+  const bool isq = blockIdx.x < D / 4;
+  const int col = blockIdx.x % (D / 4) * 4, end = isq ? groups_q : groups_q + groups_k;
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int g = (isq ? 0 : groups_q) + threadIdx.x; g < end; g += kThreads)
+    x += *reinterpret_cast<const f32x4*>(partial + int64_t(g) * D + col);
+  lds[threadIdx.x] = x;
+  for (int n = kThreads / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (int(threadIdx.x) < n) lds[threadIdx.x] += lds[threadIdx.x + n];
+  }
+  float* out = isq ? dwq : dwk;
+  if (threadIdx.x == 0 && out != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[col + e] = lds[0][e];
+  }
 }
 
 template <typename T, int D, bool kInter>
@@ -354,12 +397,12 @@ hipError_t forward(const NormRopeArgs& x, hipStream_t stream) {
 
 template <typename T, int D, bool kInter>
 hipError_t backward(const NormRopeArgs& x, const NormRopeGradArgs& y, hipStream_t stream) {
-  const int64_t groups = bwd_groups(x.N);
+  const Split g(x);
   float* partial = y.dq_weight != nullptr || y.dk_weight != nullptr ? y.partial : nullptr;
-  qk_norm_rope_bwd_kernel<T, D, kInter><<<dim3(uint32_t(groups)), dim3(kThreads), 0, stream>>>(x, y, partial);
+  qk_norm_rope_bwd_kernel<T, D, kInter><<<dim3(g.q + g.k), dim3(kThreads), 0, stream>>>(x, y, partial, g.q);
   if (partial != nullptr)
-    qk_norm_rope_dw_kernel<D><<<dim3(2 * D / 32), dim3(kThreads), 0, stream>>>(partial, int(groups), y.dq_weight,
-                                                                             y.dk_weight);
+    qk_norm_rope_dw_kernel<D><<<dim3(2 * D / 4), dim3(kThreads), 0, stream>>>(partial, g.q, g.k, y.dq_weight,
+                                                                            y.dk_weight);
   return hipGetLastError();
 }
 
@@ -374,7 +417,10 @@ hipError_t backward(const NormRopeArgs& x, const NormRopeGradArgs& y, hipStream_
 
 }  // namespace
 
-size_t norm_rope_workspace_bytes(int64_t N, int32_t D) { return size_t(bwd_groups(N)) * 2 * D * 4; }
+size_t norm_rope_workspace_bytes(int64_t N, int32_t D) {
+  const int64_t most = 2 * ((N + kWaves - 1) / kWaves);
+  return size_t(most < Split::kGroups ? most : Split::kGroups) * D * 4;
+}
 
 hipError_t launch_norm_rope(const NormRopeArgs& x, int32_t dtype, hipStream_t stream) {
   return PKV_NORM_ROPE_DISPATCH(forward, x, stream);
