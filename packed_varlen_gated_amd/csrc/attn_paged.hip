@@ -46,13 +46,22 @@ constexpr float kGrow = 8.f;  // log2 of what a row's maximum may grow by before
 template <int D, bool kBig>
 struct Form {
   static constexpr int BM = kBig ? 128 : 32;                  // rows of a tile
-  static constexpr int KW = kBig ? 64 : D == 128 ? 32 : 64;   // keys of a wave in a block
+  static constexpr int KW = kBig ? 64 : 32;                   // keys of a wave in a block
   static constexpr int BK = kBig ? 64 : 4 * KW;               // keys of a block
   static constexpr int HALF = KW * D * 2;                     // bytes of a block's K (or V) in LDS, of a wave or of all
   static constexpr int STAGE = 2 * HALF * (kBig ? 1 : 4);     // of a block
-  static constexpr int GROUPS = kBig ? 512 : 256;             // what the chip holds at a time
+  static constexpr int PER_CU = kBig || D == 64 ? 2 : 1;      // work-groups of a compute unit (by LDS)
+  static constexpr int GROUPS = 256 * PER_CU;                 // what the chip holds at a time
   static constexpr int LEAST = kBig ? 4 : 2;                  // units of a work-group
-  static constexpr size_t PARTS = size_t(2) * GROUPS * BM * (D + 2) * 4;  // bytes of the parts' sums
+  // the parts' sums in the workspace: two of a work-group, [BM, D] and [BM, 2] m, l
+  static constexpr size_t STATS = size_t(2) * GROUPS * BM * D;
+  static constexpr size_t PARTS = (STATS + size_t(2) * GROUPS * BM * 2) * 4;
+};
+
+// A cut tile, written by the work-group where its second part lies.
+struct Cut {
+  int32_t last;  // work-group of the last part; -1: there is no tile whose second part is here
+  int32_t rows, hk, rep_first, a, rep_mod;  // its rows, from row rep_first * rep + rep_mod of the request on
 };
 
 template <int D>
@@ -244,9 +253,11 @@ __device__ __forceinline__ Part part_at(const Place<D, kBig>& pl, const AttnPage
 }
 
 template <int D, bool kBig>
-__global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(const PagedArgs c, const AttnPagedArgs x,
-                                                                            float* __restrict__ sums,
-                                                                            int64_t groups) {
+__global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_kernel(const PagedArgs c,
+                                                                                     const AttnPagedArgs x,
+                                                                                     float* __restrict__ sums,
+                                                                                     Cut* __restrict__ cuts,
+                                                                                     int64_t groups) {
   using F = Form<D, kBig>;
   constexpr int CH = Swz<D>::CH, KS = D / 16, DT = D / 32, NJ = F::KW / 32;
   constexpr int GR = kBig ? 1 : F::KW / 16;  // granules of 16 keys that a wave loads of a block
@@ -269,7 +280,9 @@ __global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(cons
   const int64_t w = kBig ? b % 8 * (F::GROUPS / 8) + b / 8 : b;
   Place<D, kBig> pl;
   int64_t unit;
+  if (threadIdx.x == 0) cuts[w].last = -1;
   if (!pl.find(c, x, w, unit)) return;
+  const int64_t begin = unit;
   int64_t end = unit + pl.per;
   {
     const int64_t all = pl.per_head * c.Hkv;
@@ -304,6 +317,11 @@ __global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(cons
     }
     const int32_t b0 = pt.b0, b1 = pt.skip < end - unit ? pt.sp.blocks : int32_t(b0 + (end - unit));
     const bool whole = b0 == 0 && b1 == pt.sp.blocks;
+    if (unit == begin && b0 > 0 && unit - b0 >= begin - pl.per && threadIdx.x == 0) {
+      const int64_t row0 = int64_t(pt.j) * F::BM, left = int64_t(pl.s.q.n) * rep - row0;
+      cuts[w] = {int32_t((unit - b0 + pt.sp.blocks - 1) / pl.per), left < F::BM ? int32_t(left) : F::BM, pl.hk,
+                 int32_t(row0 / rep), pl.s.q.a, int32_t(row0 % rep)};
+    }
     const Request& rq = pl.s.q;
     const int32_t r = pl.r, hk = pl.hk, window = x.window, sinks = window > 0 ? x.sinks : 0;
     const int64_t rows_all = int64_t(rq.n) * rep, row0 = int64_t(pt.j) * F::BM;
@@ -344,7 +362,10 @@ __global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(cons
       int32_t pg = key / ps, o = key - pg * ps;
 #pragma unroll
       for (int g = 0; g < GR; ++g) {
-        const int32_t left = rq.len - key - 16 * g, have = left < 16 ? left : 16;
+        const int32_t first = key + 16 * g, left = rq.len - first;
+        // (what no row of the tile sees is not loaded)
+        const bool seen = first <= pt.sp.hi && (window == 0 || first + 15 > pt.sp.lo - window || first < sinks);
+        const int32_t have = !seen ? 0 : left < 16 ? left : 16;
         if (have > 0 && (pg < ids0 || pg >= ids0 + 64)) {
           ids0 = pg;
           // (waited for here, not at every use)
@@ -522,7 +543,7 @@ __global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(cons
     // work-group's last one, any other its first).
     const int64_t slot = 2 * w + (b0 == 0 ? 1 : 0);
     float* ps_ = sums + slot * F::BM * D;
-    float* pst = sums + int64_t(2) * F::GROUPS * F::BM * D + slot * F::BM * 2;
+    float* pst = sums + F::STATS + slot * F::BM * 2;
     bf16* o = static_cast<bf16*>(x.o);
     if constexpr (kBig) {
       if (col < mine) {
@@ -606,58 +627,107 @@ __global__ __launch_bounds__(kThreads, kBig ? 2 : 1) void attn_paged_kernel(cons
   }
 }
 
-// Joins the parts of cut tiles: work-group w has the tile that is cut where the share
-// of the main launch's work-group w + 1 begins, if that is the tile's first cut. Its
-// outputs are dealt to gridDim.y work-groups.
+// Joins the parts of cut tiles: work-group w the tile whose second part was in the main
+// launch's work-group w. A thread sums 4 channels of a row over every n-th part, the
+// loads of 8 parts going out together, and the n threads of a row's channels are joined
+// at the end: many parts (one long request) and few rows, or few parts and many rows.
 template <int D, bool kBig>
 __device__ __forceinline__ void join_parts(const PagedArgs& c, const AttnPagedArgs& x, const float* __restrict__ sums,
-                                           int64_t w) {
+                                           const Cut* __restrict__ cuts, int64_t w) {
   using F = Form<D, kBig>;
-  Place<D, kBig> pl;
-  int64_t unit;
-  if (!pl.find(c, x, w + 1, unit)) return;
-  const int32_t rep = x.Hq / c.Hkv;
-  const Part pt = part_at<D, kBig>(pl, x, rep, unit);
-  if (pt.j < 0 || pt.b0 == 0 || unit - pt.b0 < w * pl.per) return;
-  const int64_t last = (unit - pt.b0 + pt.sp.blocks - 1) / pl.per;  // the last work-group with a part
-  const Request& rq = pl.s.q;
-  const int64_t row0 = int64_t(pt.j) * F::BM, left = int64_t(rq.n) * rep - row0;
-  const int rows = left < F::BM ? int(left) : F::BM;
-  const float* st = sums + int64_t(2) * F::GROUPS * F::BM * D;
-  auto slot = [&](int64_t v) { return 2 * v + (v == w ? 1 : 0); };
-  for (int i = blockIdx.y * kThreads + threadIdx.x; i < rows * (D / 4); i += gridDim.y * kThreads) {
-    const int q = i / (D / 4), d = i % (D / 4) * 4;
-    float top = -FLT_MAX, sum = 0.f;
-    for (int64_t v = w; v <= last; ++v) top = fmaxf(top, st[(slot(v) * F::BM + q) * 2]);
+  constexpr int kQ = D / 4, kAtOnce = 8;
+  __shared__ f32x4 ly[kThreads];
+  __shared__ float lm[kThreads], ll[kThreads];
+  const Cut t = cuts[w];
+  if (t.last < 0) return;
+  const int parts = t.last - int(w) + 2, n = parts > 2 * kAtOnce ? 8 : parts > kAtOnce ? 2 : 1;
+  const int rep = x.Hq / c.Hkv, d = threadIdx.x % kQ * 4, i = threadIdx.x / kQ, mine = i % n;
+  const int block = kThreads / kQ / n;  // rows at a time
+  const float* st = sums + F::STATS;
+  for (int q0 = blockIdx.y * block; q0 < t.rows; q0 += gridDim.y * block) {
+    const int q = q0 + i / n < t.rows ? q0 + i / n : t.rows - 1;
+    float m = -FLT_MAX, l = 0.f;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t v = w; v <= last; ++v) {
-      const int64_t at = slot(v) * F::BM + q;
-      const float f = ex2(st[at * 2] - top);
-      sum += f * st[at * 2 + 1];
-      const f32x4 z = *reinterpret_cast<const f32x4*>(sums + at * D + d);
+    for (int p0 = mine; p0 < parts; p0 += n * kAtOnce) {
+      float pm[kAtOnce], pl[kAtOnce];
+      f32x4 z[kAtOnce];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] += finite(z[e]) ? f * z[e] : z[e];
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int p = p0 + u * n < parts ? p0 + u * n : mine;
+        const int64_t at = (2 * (w - 1 + p) + (p == 0 ? 1 : 0)) * F::BM + q;
+        pm[u] = st[2 * at];
+        pl[u] = st[2 * at + 1];
+        z[u] = *reinterpret_cast<const f32x4*>(sums + at * D + d);
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) top = p0 + u * n < parts ? fmaxf(top, pm[u]) : top;
+      const float f = ex2(m - top);
+      m = top;
+      l *= f;
+      // (an infinity stays one, however small its part's share)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = finite(y[e]) ? f * y[e] : y[e];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (p0 + u * n >= parts) break;
+        const float g = ex2(pm[u] - top);
+        l += g * pl[u];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += finite(z[u][e]) ? g * z[u][e] : z[u][e];
+      }
+    }
+    __syncthreads();  // the last rows are read
+    ly[threadIdx.x] = y;
+    lm[threadIdx.x] = m;
+    ll[threadIdx.x] = l;
+    __syncthreads();
+    if (mine != 0 || q0 + i / n >= t.rows) continue;
+    float top = m, sum = 0.f;
+    for (int v = 1; v < n; ++v) top = fmaxf(top, lm[threadIdx.x + v * kQ]);
+    y = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int v = 0; v < n; ++v) {
+      const int at = threadIdx.x + v * kQ;
+      const float g = ex2(lm[at] - top);
+      sum += g * ll[at];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] += finite(ly[at][e]) ? g * ly[at][e] : ly[at][e];
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    const int64_t row = row0 + q;
-    const int32_t t = int32_t(row / rep), hh = pl.hk * rep + int32_t(row % rep);
+    const int row = t.rep_mod + q, tok = t.a + t.rep_first + row / rep, hh = t.hk * rep + row % rep;
     bf16x4 z;
 #pragma unroll
     for (int e = 0; e < 4; ++e) z[e] = static_cast<bf16>(y[e] * inv);
-    *reinterpret_cast<bf16x4*>(static_cast<bf16*>(x.o) + ((int64_t(rq.a) + t) * x.Hq + hh) * D + d) = z;
-    if (x.lse != nullptr && d == 0)
-      x.lse[int64_t(hh) * c.N + rq.a + t] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+    *reinterpret_cast<bf16x4*>(static_cast<bf16*>(x.o) + (int64_t(tok) * x.Hq + hh) * D + d) = z;
+    if (x.lse != nullptr && d == 0) x.lse[int64_t(hh) * c.N + tok] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
   }
 }
 
+// The workspace: the small form's parts, the big form's, the cuts of both.
+template <int D>
+struct Workspace {
+  using S = Form<D, false>;
+  using B = Form<D, true>;
+  static constexpr size_t BYTES = S::PARTS + B::PARTS + (S::GROUPS + B::GROUPS) * sizeof(Cut);
+  float *small, *big;
+  Cut *small_cuts, *big_cuts;
+  explicit Workspace(void* ws) {
+    char* p = static_cast<char*>(ws);
+    small = reinterpret_cast<float*>(p);
+    big = reinterpret_cast<float*>(p + S::PARTS);
+    small_cuts = reinterpret_cast<Cut*>(p + S::PARTS + B::PARTS);
+    big_cuts = small_cuts + S::GROUPS;
+  }
+};
+
+// Work-groups [0, small) join what the small form's work-groups 1 .. small cut.
 template <int D>
 __global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(const PagedArgs c, const AttnPagedArgs x,
-                                                                   const float* __restrict__ small,
-                                                                   const float* __restrict__ big, int small_groups) {
-  if (int(blockIdx.x) < small_groups)
-    join_parts<D, false>(c, x, small, blockIdx.x);
+                                                                   const Workspace<D> ws, int small) {
+  if (int(blockIdx.x) < small)
+    join_parts<D, false>(c, x, ws.small, ws.small_cuts, int64_t(blockIdx.x) + 1);
   else
-    join_parts<D, true>(c, x, big, int64_t(blockIdx.x) - small_groups);
+    join_parts<D, true>(c, x, ws.big, ws.big_cuts, int64_t(blockIdx.x) - small + 1);
 }
 
 // Which forms a call's requests can have.
@@ -667,23 +737,21 @@ bool any_big(const PagedArgs& c, int32_t Hq) { return c.cu != nullptr || Hq / c.
 template <int D>
 hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   const bool s = any_small(c, x.Hq), b = any_big(c, x.Hq);
-  float* small = static_cast<float*>(x.workspace);
-  float* big = reinterpret_cast<float*>(static_cast<char*>(x.workspace) + Form<D, false>::PARTS);
+  const Workspace<D> ws(x.workspace);
   // (the first launch also zeroes the rows that no request has)
   const int64_t tail = c.cu == nullptr ? 1 : tail_groups(c.N * x.Hq * D * 2);
   constexpr int64_t gs = Form<D, false>::GROUPS, gb = Form<D, true>::GROUPS;
-  if (b) attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(kThreads), 0, stream>>>(c, x, big, gb);
-  if (s) attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(kThreads), 0, stream>>>(c, x, small, gs);
+  if (b) attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(kThreads), 0, stream>>>(c, x, ws.big, ws.big_cuts, gb);
+  if (s) attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(kThreads), 0, stream>>>(c, x, ws.small,
+                                                                                                     ws.small_cuts, gs);
   const int js = s ? int(gs) - 1 : 0, jb = b ? int(gb) - 1 : 0;
-  attn_paged_join_kernel<D><<<dim3(js + jb, b ? 4 : 1), dim3(kThreads), 0, stream>>>(c, x, small, big, js);
+  attn_paged_join_kernel<D><<<dim3(js + jb, 4), dim3(kThreads), 0, stream>>>(c, x, ws, js);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attn_paged_workspace_bytes(int32_t D) {
-  return D == 64 ? Form<64, false>::PARTS + Form<64, true>::PARTS : Form<128, false>::PARTS + Form<128, true>::PARTS;
-}
+size_t attn_paged_workspace_bytes(int32_t D) { return D == 64 ? Workspace<64>::BYTES : Workspace<128>::BYTES; }
 
 hipError_t launch_attn_paged(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   return c.D == 64 ? run<64>(c, x, stream) : run<128>(c, x, stream);
