@@ -138,8 +138,8 @@ pkv_status pkv_attn_window_varlen_backward(const void* q, const void* k, const v
  * cu_seqlens  int32 [R + 1]: request r's new tokens are [cu[r], cu[r + 1]) of
  *             the N packed ones; they are its last tokens. NULL: one new
  *             token for each request, N = R.
- * page_size   a multiple of 16, at most 65536; num_pages * page_size and
- *             max_pages * page_size at most 2^30.
+ * page_size   a multiple of 16, at most 65536; num_pages * page_size at
+ *             most 2^30, max_pages * page_size at most 2^29.
  *
  * pkv_paged_kv_append writes the new tokens' k and v [N, Hkv, D] (dense, or
  * with k_stride / v_stride elements from token to token as for

@@ -10,7 +10,7 @@ namespace {
 using namespace pkv;
 
 constexpr int32_t kMaxSinks = 64;
-constexpr int64_t kMaxPlaces = int64_t(1) << 30;  // of a cache, and of a request
+constexpr int64_t kMaxPlaces = int64_t(1) << 30;  // of a cache; of a request half of it
 
 Span f32_span(const float* p, int64_t n) { return {p, n * 4, 4}; }
 Span i32_span(const int32_t* p, int64_t n) { return {p, n * 4, 4}; }
@@ -50,7 +50,7 @@ pkv_status check_paged(const int32_t* cu, int64_t N, int32_t R, int32_t Hq, int3
     return PKV_ERR_INVALID_ARGUMENT;
   if (!known_dtype(dtype) || !supported_head_dim(D) || page_size < 16 || page_size > 65536 || page_size % 16 != 0)
     return PKV_ERR_UNSUPPORTED;
-  if (int64_t(num_pages) * page_size > kMaxPlaces || int64_t(max_pages) * page_size > kMaxPlaces ||
+  if (int64_t(num_pages) * page_size > kMaxPlaces || int64_t(max_pages) * page_size > kMaxPlaces / 2 ||
       (N / 16 + R) * Hq >= kMaxGroups)
     return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;

@@ -41,6 +41,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int32_t kPlaces = 1 << 29;  // of a request
 constexpr float kGrow = 8.f;  // log2 of what a row's maximum may grow by before O is rescaled
 
 template <int D, bool kBig>
@@ -252,12 +253,23 @@ __device__ __forceinline__ Part part_at(const Place<D, kBig>& pl, const AttnPage
   return {-1, sp, 0, s.cost - in};
 }
 
+// A launch's arguments. They are read again (scalar loads) for each part of the work:
+// held in registers over a walk, they would push what the walk needs out of them.
+struct Launch {
+  PagedArgs c;
+  AttnPagedArgs x;
+  float* sums;
+  Cut* cuts;
+  int64_t groups;
+};
+typedef __attribute__((address_space(4))) void* KernelArgs;
+__device__ __forceinline__ Launch reload(KernelArgs& p) {
+  asm volatile("" : "+s"(p));
+  return *(const Launch*)p;
+}
+
 template <int D, bool kBig>
-__global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_kernel(const PagedArgs c,
-                                                                                     const AttnPagedArgs x,
-                                                                                     float* __restrict__ sums,
-                                                                                     Cut* __restrict__ cuts,
-                                                                                     int64_t groups) {
+__global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch launch) {
   using F = Form<D, kBig>;
   constexpr int CH = Swz<D>::CH, KS = D / 16, DT = D / 32, NJ = F::KW / 32;
   constexpr int GR = kBig ? 1 : F::KW / 16;  // granules of 16 keys that a wave loads of a block
@@ -265,10 +277,13 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
   constexpr int RL = 16 / GL;                // rows of a load
   __shared__ __attribute__((aligned(1024))) char lds[2 * F::STAGE];
   static_assert(kBig || 2 * F::STAGE >= 4 * 32 * (D + 6) * 4, "the waves' sums are joined in the stages");
+  __shared__ Share shares[kThreads / 64];  // the request, of every wave
 
   const int64_t b = blockIdx.x;
-  if (b >= groups) {
-    const int64_t j = b - groups, n = gridDim.x - groups, end = covered_tokens(c.cu, c.R, c.N);
+  if (b >= launch.groups) {
+    const PagedArgs& c = launch.c;
+    const AttnPagedArgs& x = launch.x;
+    const int64_t j = b - launch.groups, n = gridDim.x - launch.groups, end = covered_tokens(c.cu, c.R, c.N);
     zero_tail(x.o, end, c.N, int64_t(x.Hq) * D * 2, j, n);
     if (x.lse != nullptr)
       for (int64_t i = j * kThreads + threadIdx.x; i < (c.N - end) * x.Hq; i += n * kThreads)
@@ -277,68 +292,102 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
     return;
   }
   // Consecutive work-groups run on different XCDs: units that share keys go to one.
-  const int64_t w = kBig ? b % 8 * (F::GROUPS / 8) + b / 8 : b;
+  const int32_t w = kBig ? int32_t(b) % 8 * (F::GROUPS / 8) + int32_t(b) / 8 : int32_t(b);
+  KernelArgs args = (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr();
   Place<D, kBig> pl;
-  int64_t unit;
-  if (threadIdx.x == 0) cuts[w].last = -1;
-  if (!pl.find(c, x, w, unit)) return;
-  const int64_t begin = unit;
-  int64_t end = unit + pl.per;
+  int64_t unit, end;
+  if (threadIdx.x == 0) launch.cuts[w].last = -1;
+  if (!pl.find(launch.c, launch.x, w, unit)) return;
   {
-    const int64_t all = pl.per_head * c.Hkv;
-    end = end < all ? end : all;
+    const int64_t all = pl.per_head * launch.c.Hkv;
+    end = unit + pl.per < all ? unit + pl.per : all;
+    // the tile whose second part is here
+    const int32_t rep = launch.x.Hq / launch.c.Hkv;
+    const Part pt = part_at<D, kBig>(pl, launch.x, rep, unit);
+    if (pt.j >= 0 && pt.b0 > 0 && unit - pt.b0 >= unit - pl.per && threadIdx.x == 0) {
+      const int64_t row0 = int64_t(pt.j) * F::BM, left = int64_t(pl.s.q.n) * rep - row0;
+      launch.cuts[w] = {int32_t((unit - pt.b0 + pt.sp.blocks - 1) / pl.per), left < F::BM ? int32_t(left) : F::BM, pl.hk,
+                        int32_t(row0 / rep), pl.s.q.a, int32_t(row0 % rep)};
+    }
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int32_t rep = x.Hq / c.Hkv, ps = c.page_size;
-  const int32_t kstride = c.Hkv * D * 2;
-  const float cs = x.scale == 0.f ? 1.f : fabsf(x.scale) * kLog2e;  // (as in attn_fwd.hip)
-  const uint32_t flip = x.scale < 0.f ? 0x80008000u : 0u, keep = x.scale == 0.f ? 0u : ~0u;
-  const bf16 *kp = static_cast<const bf16*>(x.k_pages), *vp = static_cast<const bf16*>(x.v_pages);
+  shares[wave] = pl.s;
 
   // the lane's place in a load: row lrow of RL, chunk lpos
   const int lrow = lane / CH, lpos = lane % CH;
-  const uint32_t koff = uint32_t(lrow) * kstride, kchunk = uint32_t(lpos ^ Swz<D>::k(lrow)) * 16;
-  const uint32_t voff = koff + uint32_t(lpos ^ Swz<D>::v(lrow)) * 16;
+  const uint32_t kchunk = uint32_t(lpos ^ Swz<D>::k(lrow)) * 16, vchunk = uint32_t(lpos ^ Swz<D>::v(lrow)) * 16;
   // LDS addresses of the lane's operand chunks
   const int kx = Swz<D>::k(col);
   const int vr = 4 * half + ((lane & 15) >> 2), vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vb = (lane & 1) * 8;
   const int vx = Swz<D>::v(vr);
 
+  const int32_t wrow = kBig ? wave * 32 : 0;  // the wave's first row in a tile
+  // The part at `unit`, the wave's rows of its tile and the lane's row: its token and head
+  // (of the tile's first row where there is none). Formed where they are needed: a walk,
+  // another one and the outputs each have their own and hold nothing for one another.
+  struct Piece {
+    Launch a;
+    Share s;
+    Part pt;
+    int32_t rep, b1, mine, tok, head;
+  };
+  auto piece = [&] {
+    Piece p;
+    p.a = reload(args);
+    asm volatile("" ::: "memory");
+    p.rep = p.a.x.Hq / p.a.c.Hkv;
+    pl.s = p.s = uniform(shares[wave]);
+    p.pt = part_at<D, kBig>(pl, p.a.x, p.rep, unit);
+    p.b1 = p.pt.skip < end - unit ? p.pt.sp.blocks : int32_t(p.pt.b0 + (end - unit));
+    const int64_t row0 = int64_t(p.pt.j) * F::BM, left = int64_t(p.s.q.n) * p.rep - row0;
+    p.mine = (left < F::BM ? int32_t(left) : F::BM) - wrow;
+    const int64_t row = col < p.mine ? row0 + wrow + col : row0;
+    p.tok = int32_t(row / p.rep);
+    p.head = pl.hk * p.rep + int32_t(row % p.rep);
+    return p;
+  };
+
   while (unit < end) {
-    if (unit >= pl.at + pl.s.units()) {
-      pl.next(c, x);
-      continue;
+    {
+      const Launch a = reload(args);
+      asm volatile("" ::: "memory");
+      pl.s = uniform(shares[wave]);
+      if (unit >= pl.at + pl.s.units()) {
+        pl.next(a.c, a.x);
+        shares[wave] = pl.s;
+        continue;
+      }
+      const Part pt = part_at<D, kBig>(pl, a.x, a.x.Hq / a.c.Hkv, unit);
+      if (pt.j < 0) {
+        unit += pt.skip;
+        continue;
+      }
     }
-    const Part pt = part_at<D, kBig>(pl, x, rep, unit);
-    if (pt.j < 0) {
-      unit += pt.skip;
-      continue;
-    }
-    const int32_t b0 = pt.b0, b1 = pt.skip < end - unit ? pt.sp.blocks : int32_t(b0 + (end - unit));
-    const bool whole = b0 == 0 && b1 == pt.sp.blocks;
-    if (unit == begin && b0 > 0 && unit - b0 >= begin - pl.per && threadIdx.x == 0) {
-      const int64_t row0 = int64_t(pt.j) * F::BM, left = int64_t(pl.s.q.n) * rep - row0;
-      cuts[w] = {int32_t((unit - b0 + pt.sp.blocks - 1) / pl.per), left < F::BM ? int32_t(left) : F::BM, pl.hk,
-                 int32_t(row0 / rep), pl.s.q.a, int32_t(row0 % rep)};
-    }
-    const Request& rq = pl.s.q;
-    const int32_t r = pl.r, hk = pl.hk, window = x.window, sinks = window > 0 ? x.sinks : 0;
-    const int64_t rows_all = int64_t(rq.n) * rep, row0 = int64_t(pt.j) * F::BM;
-    const int32_t rows = rows_all - row0 < F::BM ? int32_t(rows_all - row0) : F::BM;  // the tile's
-    const int32_t wrow = kBig ? wave * 32 : 0;                                        // the wave's first
-    const int32_t mine = rows - wrow;
-    // the lane's row
-    const int64_t row = row0 + wrow + col;
-    const int32_t tok = int32_t((col < mine ? row : row0) / rep), head = hk * rep + int32_t((col < mine ? row : row0) % rep);
-    const int32_t place = col < mine ? rq.len - rq.n + tok : -1;
+    f32x16 acc[DT];
+    float m = -FLT_MAX, l = 0.f;
+
+    // mode 0: the sums; 1: with values that are not finite as 0; 2: those values added.
+    // Whether some sum of the lane's row is not finite.
+    auto walk = [&](int mode) {
+    const Piece pc = piece();
+    const Launch& a = pc.a;
+    const Part& pt = pc.pt;
+    const int32_t mine = pc.mine, tok = pc.tok, head = pc.head, b0 = pt.b0, b1 = pc.b1;
+    pl.s = pc.s;
+    // (a place is below kPlaces: no window is one of that many)
+    const int32_t window = a.x.window > 0 && a.x.window < kPlaces ? a.x.window : kPlaces;
+    const int32_t sinks = a.x.window > 0 ? a.x.sinks : 0;
+    const int32_t place = col < mine ? pl.s.q.len - pl.s.q.n + tok : -1;
     // places of the wave's first and last row
     const int32_t wlo = uni(place), whi = __builtin_amdgcn_readlane(place, mine >= 32 ? 31 : (mine > 0 ? mine - 1 : 0));
-    const int64_t at = (int64_t(rq.a) + tok) * x.Hq + head;
+    const bool rows_here = mine > 0;
+    const float cs = a.x.scale == 0.f ? 1.f : fabsf(a.x.scale) * kLog2e;  // (as in attn_fwd.hip)
 
     bf16x8 qf[KS];
     {
-      const bf16* q = static_cast<const bf16*>(x.q) + at * D + half * 8;
+      const uint32_t flip = a.x.scale < 0.f ? 0x80008000u : 0u, keep = a.x.scale == 0.f ? 0u : ~0u;
+      const bf16* q = static_cast<const bf16*>(a.x.q) + ((int64_t(pl.s.q.a) + tok) * a.x.Hq + head) * D + half * 8;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         i32x4 y = {0, 0, 0, 0};
@@ -348,38 +397,48 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
         qf[i] = __builtin_bit_cast(bf16x8, y);
       }
     }
-    f32x16 acc[DT];
-    float m = -FLT_MAX, l = 0.f;
-
-    const int64_t trow = int64_t(r) * c.max_pages;
+    const int32_t ps = a.c.page_size, num_pages = a.c.num_pages, kstride = a.c.Hkv * D * 2;
+    const char* kbase = static_cast<const char*>(a.x.k_pages) + int64_t(pl.hk) * D * 2;
+    const char* vbase = static_cast<const char*>(a.x.v_pages) + int64_t(pl.hk) * D * 2;
+    const uint32_t koff = uint32_t(lrow) * kstride, voff = koff + vchunk;
     const int32_t wkey = kBig ? 16 * wave : F::KW * wave;  // the wave's first key to load of a block
+    const int32_t far = pt.sp.ww.far, low = pt.sp.ww.low - far;
+    const int32_t limit = pt.sp.hi + 1, oldest = pt.sp.lo - window - 15;  // (a granule past `oldest` is in the window)
+    auto first_key = [&](int32_t blk) { return (blk < far ? blk : blk + low) * F::BK; };
     // 64 entries of the request's row of the table from `ids0` on, one a lane: loads of
     // entries would make every block wait for all loads before them
     int32_t ids = 0, ids0 = -64;
-    auto issue = [&](int32_t blk, int st) {
+    // page and place in it of the wave's first key of the block to load next
+    int32_t npg = 0, no = 0;
+    const int32_t step_pg = F::BK / ps, step_o = F::BK % ps;
+    auto issue = [&](int32_t blk, int st, bool start) {
       const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? wave * (16 * D * 2) : wave * 2 * F::HALF);
-      const int32_t key = pt.sp.ww.tile(blk) * F::BK + wkey;
-      int32_t pg = key / ps, o = key - pg * ps;
+      const int32_t key = first_key(blk) + wkey;
+      if (start || blk == far) {
+        npg = key / ps;
+        no = key - npg * ps;
+      }
+      int32_t pg = npg, o = no;
 #pragma unroll
       for (int g = 0; g < GR; ++g) {
-        const int32_t first = key + 16 * g, left = rq.len - first;
+        const int32_t first = key + 16 * g, left = limit - first;
         // (what no row of the tile sees is not loaded)
-        const bool seen = first <= pt.sp.hi && (window == 0 || first + 15 > pt.sp.lo - window || first < sinks);
-        const int32_t have = !seen ? 0 : left < 16 ? left : 16;
-        if (have > 0 && (pg < ids0 || pg >= ids0 + 64)) {
+        const bool seen = left > 0 && (first > oldest || first < sinks);
+        if (seen && (pg < ids0 || pg >= ids0 + 64)) {
+          const Launch a = reload(args);
           ids0 = pg;
           // (waited for here, not at every use)
-          ids = fresh(c.table[trow + (pg + lane < c.max_pages ? pg + lane : c.max_pages - 1)]);
+          ids = fresh(a.c.table[int64_t(pl.r) * a.c.max_pages + (pg + lane < a.c.max_pages ? pg + lane : a.c.max_pages - 1)]);
         }
-        int32_t page = __builtin_amdgcn_readlane(ids, (pg - ids0) & 63);
-        if (have > 0 && (page < 0 || page >= c.num_pages)) {
-          if (c.flags != nullptr && lane == 0) atomicOr(c.flags, kFlagBadPage);
-          page = -1;
+        const int32_t page = __builtin_amdgcn_readlane(ids, (pg - ids0) & 63);
+        const bool ok = seen && page >= 0 && page < num_pages;
+        if (seen && !ok) {
+          const Launch a = reload(args);
+          if (a.c.flags != nullptr && lane == 0) atomicOr(a.c.flags, kFlagBadPage);
         }
-        const bool ok = have > 0 && page >= 0;
-        const int64_t from = ok ? ((int64_t(page) * ps + o) * c.Hkv + hk) * D : 0;
-        const uint32_t bytes = ok ? (have - 1) * kstride + D * 2 : 0;
-        const u32x4 rk = descriptor(kp + from, bytes), rv = descriptor(vp + from, bytes);
+        const int64_t from = ok ? int64_t(page * ps + o) * kstride : 0;
+        const uint32_t bytes = ok ? ((left < 16 ? left : 16) - 1) * kstride + D * 2 : 0;
+        const u32x4 rk = descriptor(kbase + from, bytes), rv = descriptor(vbase + from, bytes);
 #pragma unroll
         for (int u = 0; u < GL; ++u)  // rows RL u + lrow: the swizzle of K flips two or three bits of the chunk
           load_lds16_async(rk, (koff + (kchunk ^ (Swz<D>::k(RL * u) * 16))) + u * RL * kstride, dst + g * (16 * D * 2) + u * 1024);
@@ -392,27 +451,31 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
           ++pg;
         }
       }
+      npg += step_pg;
+      no += step_o;
+      if (no >= ps) {
+        no -= ps;
+        ++npg;
+      }
     };
 
-    // mode 0: the sums; 1: with values that are not finite as 0; 2: those values added
-    auto walk = [&](int mode) {
       if (mode < 2) {
         m = -FLT_MAX;
         l = 0.f;
 #pragma unroll
         for (int i = 0; i < DT; ++i) acc[i] = f32x16{};
       }
-      issue(b0, 0);
+      issue(b0, 0, true);
       for (int32_t blk = b0; blk < b1; ++blk) {
         const int st = (blk - b0) & 1;
         if constexpr (kBig) {
           wait_vm();
           bar();
-          if (blk + 1 < b1) issue(blk + 1, st ^ 1);
+          if (blk + 1 < b1) issue(blk + 1, st ^ 1, false);
         } else {
           asm volatile("" ::: "memory");
           if (blk + 1 < b1) {
-            issue(blk + 1, st ^ 1);
+            issue(blk + 1, st ^ 1, false);
             wait_loads<2 * GR * GL>();
           } else {
             wait_loads<0>();
@@ -421,10 +484,10 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
         }
         char* kt = lds + st * F::STAGE + (kBig ? 0 : wave * 2 * F::HALF);
         char* vt = kt + F::HALF;
-        const int32_t s0 = pt.sp.ww.tile(blk) * F::BK + (kBig ? 0 : wkey);  // the wave's first key
+        const int32_t s0 = first_key(blk) + (kBig ? 0 : wkey);  // the wave's first key
         if (mode > 0) {
           // keys with a value that is not finite
-          __shared__ uint64_t odd_lds[kBig ? 1 : 4];
+          __shared__ uint64_t odd_lds[1];
           uint64_t odd = 0;
           if constexpr (kBig) {
             __syncthreads();
@@ -433,9 +496,9 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
           }
           for (int i = kBig ? tid : lane; i < F::HALF / 4; i += kBig ? kThreads : 64) {
             uint32_t y = reinterpret_cast<uint32_t*>(vt)[i];
-            const bool a = (y & 0x7f80u) == 0x7f80u, e = (y & 0x7f800000u) == 0x7f800000u;
-            if (a || e) odd |= uint64_t(1) << (i / (D / 2));
-            if (mode == 1 && (a || e)) reinterpret_cast<uint32_t*>(vt)[i] = y & (a ? 0xffff0000u : ~0u) & (e ? 0xffffu : ~0u);
+            const bool p = (y & 0x7f80u) == 0x7f80u, e = (y & 0x7f800000u) == 0x7f800000u;
+            if (p || e) odd |= uint64_t(1) << (i / (D / 2));
+            if (mode == 1 && (p || e)) reinterpret_cast<uint32_t*>(vt)[i] = y & (p ? 0xffff0000u : ~0u) & (e ? 0xffffu : ~0u);
           }
           if constexpr (kBig) {
             if (odd != 0) atomicOr(reinterpret_cast<unsigned long long*>(odd_lds), (unsigned long long)odd);
@@ -451,7 +514,7 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
             for (int s = 0; s < F::KW; ++s) {
               if ((odd >> s & 1) == 0) continue;
               const int32_t p = s0 + s;
-              const bool sees = p <= place && (window == 0 || place - p < window || p < sinks);
+              const bool sees = p <= place && (place - p < window || p < sinks);
 #pragma unroll
               for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -465,7 +528,7 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
             continue;
           }
         }
-        if (mine <= 0 || s0 > whi || (window > 0 && s0 + F::KW - 1 <= wlo - window && s0 >= sinks)) continue;
+        if (!rows_here || s0 > whi || (s0 + F::KW - 1 <= wlo - window && s0 >= sinks)) continue;
 
         f32x16 s[NJ];
 #pragma unroll
@@ -473,14 +536,13 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
           s[j] = f32x16{};
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
-            const bf16x8 a = *reinterpret_cast<const bf16x8*>(kt + (32 * j + col) * (D * 2) + (((2 * i + half) ^ kx) * 16));
-            s[j] = mfma32(a, qf[i], s[j]);
+            const bf16x8 y = *reinterpret_cast<const bf16x8*>(kt + (32 * j + col) * (D * 2) + (((2 * i + half) ^ kx) * 16));
+            s[j] = mfma32(y, qf[i], s[j]);
           }
         }
         // (a wave of less than 32 rows has lanes that see nothing: their sums are not used)
-        if (s0 + F::KW - 1 > wlo || (window > 0 && s0 <= whi - window)) {
-          const int32_t last = place - s0 - 4 * half, old = window > 0 ? last - window : -1;
-          const int32_t sink = sinks - s0 - 4 * half;
+        if (s0 + F::KW - 1 > wlo || s0 <= whi - window) {
+          const int32_t last = place - s0 - 4 * half, old = last - window, sink = sinks - s0 - 4 * half;
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -518,36 +580,45 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
         for (int i = 0; i < DT; ++i)
 #pragma unroll
           for (int j = 0; j < 2 * NJ; ++j) {
-            const char* a = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
-            acc[i] = mfma32(join(read_tr(a), read_tr(a + 8 * (D * 2))), p[j], acc[i]);
+            const char* y = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
+            acc[i] = mfma32(join(read_tr(y), read_tr(y + 8 * (D * 2))), p[j], acc[i]);
           }
       }
+      bool bad = false;
+      if (mode == 0) {
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) bad |= !finite(acc[i][j]);
+      }
+      return bad && place >= 0;
     };
-    walk(0);
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) bad |= !finite(acc[i][j]);
-    bad = bad && col < mine;
-    const bool again = kBig ? __syncthreads_or(bad) != 0 : __builtin_amdgcn_ballot_w64(bad) != 0;
-    if (again) {
+    const bool bad = walk(0);
+    // (in the big form also: every wave is done with the stages)
+    if (kBig ? __syncthreads_or(bad) != 0 : __builtin_amdgcn_ballot_w64(bad) != 0) {
       walk(1);
       if constexpr (kBig) __syncthreads();
       walk(2);
+      if constexpr (kBig) __syncthreads();
     }
     l += other_half(l);
-    __syncthreads();  // every wave is done with the stages
+    if constexpr (!kBig) __syncthreads();  // every wave is done with the stages
 
     // The tile's outputs, or the part's sums (a part with the tile's first block is the
     // work-group's last one, any other its first).
-    const int64_t slot = 2 * w + (b0 == 0 ? 1 : 0);
-    float* ps_ = sums + slot * F::BM * D;
-    float* pst = sums + F::STATS + slot * F::BM * 2;
-    bf16* o = static_cast<bf16*>(x.o);
+    const Piece pc = piece();
+    const Launch& a = pc.a;
+    const Share& sh = pc.s;
+    const int32_t rep = pc.rep, mine = pc.mine, tok = pc.tok, head = pc.head, b0 = pc.pt.b0;
+    const bool whole = b0 == 0 && pc.b1 == pc.pt.sp.blocks;
+    const int64_t slot = 2 * int64_t(w) + (b0 == 0 ? 1 : 0);
+    float* psum = a.sums + slot * F::BM * D;
+    float* pst = a.sums + F::STATS + slot * F::BM * 2;
+    bf16* o = static_cast<bf16*>(a.x.o);
     if constexpr (kBig) {
       if (col < mine) {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+        bf16* to = o + ((int64_t(sh.q.a) + tok) * a.x.Hq + head) * D;
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -557,9 +628,9 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
               bf16x4 y;
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[e] = static_cast<bf16>(acc[i][4 * j + e] * inv);
-              *reinterpret_cast<bf16x4*>(o + at * D + ch) = y;
+              *reinterpret_cast<bf16x4*>(to + ch) = y;
             } else {
-              *reinterpret_cast<f32x4*>(ps_ + (wrow + col) * D + ch) =
+              *reinterpret_cast<f32x4*>(psum + (wrow + col) * D + ch) =
                   f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
             }
           }
@@ -567,8 +638,8 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
           if (!whole) {
             pst[2 * (wrow + col)] = m;
             pst[2 * (wrow + col) + 1] = l;
-          } else if (x.lse != nullptr) {
-            x.lse[int64_t(head) * c.N + rq.a + tok] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+          } else if (a.x.lse != nullptr) {
+            a.x.lse[int64_t(head) * a.c.N + sh.q.a + tok] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
           }
         }
       }
@@ -589,7 +660,7 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
         }
       }
       __syncthreads();
-      for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      for (int i = tid; i < mine * (D / 4); i += kThreads) {
         const int q = i / (D / 4), d = i % (D / 4) * 4;
         float top = jst[2 * q], sum = 0.f;
 #pragma unroll
@@ -605,7 +676,7 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
           for (int e = 0; e < 4; ++e) y[e] += finite(z[e]) ? f * z[e] : z[e];
         }
         if (!whole) {
-          *reinterpret_cast<f32x4*>(ps_ + q * D + d) = y;
+          *reinterpret_cast<f32x4*>(psum + q * D + d) = y;
           if (d == 0) {
             pst[2 * q] = top;
             pst[2 * q + 1] = sum;
@@ -613,17 +684,17 @@ __global__ __launch_bounds__(kThreads, (Form<D, kBig>::PER_CU)) void attn_paged_
           continue;
         }
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        const int32_t t = q / rep, hh = hk * rep + q % rep;
+        const int32_t t = q / rep, hh = pl.hk * rep + q % rep;
         bf16x4 z;
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[e] = static_cast<bf16>(y[e] * inv);
-        *reinterpret_cast<bf16x4*>(o + ((int64_t(rq.a) + t) * x.Hq + hh) * D + d) = z;
-        if (x.lse != nullptr && d == 0)
-          x.lse[int64_t(hh) * c.N + rq.a + t] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+        *reinterpret_cast<bf16x4*>(o + ((int64_t(sh.q.a) + t) * a.x.Hq + hh) * D + d) = z;
+        if (a.x.lse != nullptr && d == 0)
+          a.x.lse[int64_t(hh) * a.c.N + sh.q.a + t] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
       }
       __syncthreads();  // the sums have left LDS
     }
-    unit += b1 - b0;
+    unit += pc.b1 - b0;
   }
 }
 
@@ -741,9 +812,10 @@ hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   // (the first launch also zeroes the rows that no request has)
   const int64_t tail = c.cu == nullptr ? 1 : tail_groups(c.N * x.Hq * D * 2);
   constexpr int64_t gs = Form<D, false>::GROUPS, gb = Form<D, true>::GROUPS;
-  if (b) attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(kThreads), 0, stream>>>(c, x, ws.big, ws.big_cuts, gb);
-  if (s) attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(kThreads), 0, stream>>>(c, x, ws.small,
-                                                                                                     ws.small_cuts, gs);
+  if (b) attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(kThreads), 0, stream>>>(Launch{c, x, ws.big, ws.big_cuts, gb});
+  if (s)
+    attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(kThreads), 0, stream>>>(
+        Launch{c, x, ws.small, ws.small_cuts, gs});
   const int js = s ? int(gs) - 1 : 0, jb = b ? int(gb) - 1 : 0;
   attn_paged_join_kernel<D><<<dim3(js + jb, 4), dim3(kThreads), 0, stream>>>(c, x, ws, js);
   return hipGetLastError();

@@ -144,6 +144,7 @@ __device__ __forceinline__ void check_cu(const int32_t* __restrict__ cu, int32_t
 // sinks. The walk is those, then tiles low, low + 1, ...
 struct WindowWalk {
   int32_t low, far;
+  WindowWalk() = default;
   __device__ __forceinline__ WindowWalk(int32_t window, int32_t sinks, int32_t bn, int32_t start, int32_t a) {
     const int32_t first = start - a - window + 1;
     low = first > 0 ? first / bn : 0;
