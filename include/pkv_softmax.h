@@ -113,8 +113,8 @@ pkv_status pkv_attn_window_varlen(const void* q, const void* k, const void* v,
 /*
  * Reverse pass, as pkv_attn_varlen_backward with the window's pairs. The
  * workspace also holds partial sums of the sinks' gradients: 8 sinks D Hkv
- * bytes for every min(window, 512) tokens (windows below 64: for every 512
- * tokens and every segment slot).
+ * bytes for every chunk of 128 to 512 tokens (of `window` tokens if that is
+ * less; windows below 64: for every chunk and every segment slot).
  */
 size_t pkv_attn_window_varlen_backward_workspace_size(int64_t N, int32_t Hq, int32_t Hkv, int32_t D,
                                                       int32_t max_segs, int32_t dtype, int32_t window,

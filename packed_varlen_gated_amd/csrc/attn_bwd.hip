@@ -333,8 +333,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
 }
 
 // kQ waves share 32 keys and take the 32-query blocks of a tile in turn, their
-// sums added at the end: kQ = 1, four waves hold 128 keys; kQ = 4, eight waves
-// hold 64.
+// sums added at the end: kQ = 1, four waves hold 128 keys; kQ = 2, four hold 64 (under
+// a window); kQ = 4, eight waves hold 64.
 template <int kQ>
 struct DkvShape {
   static constexpr int NT = kQ == 4 ? 512 : 256;  // threads
@@ -351,13 +351,19 @@ struct DkvShape {
 // floor(cu[i] / chunk) + inc i + c. With chunk <= window and inc = 0 the slots of
 // different segments do not meet, since a segment of n tokens has at most
 // floor((cu[i] + n) / chunk) - floor(cu[i] / chunk) of them; a window below 64 would make
-// the chunks small and takes inc = 1 (one more slot per segment) instead.
-constexpr int kFar = 512;
+// the chunks small and takes inc = 1 (one more slot per segment) instead. The chunks are
+// 128 to 512 tokens, so that there are 512 work-groups if the call has that many: 8192
+// tokens, H 16, Hkv 4, D 128, window 512, 4 sinks: 221 us the reverse pass in chunks of
+// 512, FIGA in chunks of 128; 16384 tokens: 388 and FIGB.
 constexpr int kMaxSinks = 64;
 struct FarGrid {
   int32_t chunk, inc;
-  __host__ __device__ explicit FarGrid(int32_t window)
-      : chunk(window < 64 || window > kFar ? kFar : window), inc(window < 64 ? 1 : 0) {}
+  __host__ __device__ FarGrid(int64_t N, int32_t Hkv, int32_t window) {
+    const int64_t want = N * Hkv / 512 / 128 * 128 + 128;
+    chunk = want > 512 ? 512 : int32_t(want);
+    inc = window < 64 ? 1 : 0;
+    if (inc == 0 && chunk > window) chunk = window;
+  }
   __host__ __device__ int64_t slots(int64_t N, int64_t max_segs) const { return N / chunk + inc * max_segs; }
 };
 
@@ -377,7 +383,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB + 4 * T * 4];
 
   const int64_t b = blockIdx.x;
-  const FarGrid fg(window);
+  const FarGrid fg(N, Hkv, window);
   int32_t slot, h0, h1;
   SegTile t;
   int32_t from = 0, to = 0;  // under a window: the queries [from, to)
@@ -576,17 +582,36 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
       }
       return;
     }
-    if (kWin == 1 && far != nullptr && k0 + rd.col - t.a < sinks && rd.col < have && wave % kQ == 0) {
-      const int32_t behind = t.e - t.a - window;
+    if (kWin == 1 && far != nullptr && t.start == t.a && t.e - t.a > window) {
+      // The sinks' sums over the far queries: every thread sums 4 channels of a sink over
+      // the chunks, the loads of 8 going out together.
+      static_assert(4 * TB >= 2 * kMaxSinks * D * 4 || kWin != 1, "the far sums fit the tiles' buffers");
+      f32x4* fs = reinterpret_cast<f32x4*>(lds);  // dk, dv of [sink][D / 4]
       const int64_t first = int64_t(t.a) / fg.chunk + int64_t(fg.inc) * t.seg;
-      for (int32_t x = 0; x * int64_t(fg.chunk) < behind; ++x) {
-        const float* part = far + (((first + x) * Hkv + hk) * 2 * sinks + (k0 - t.a) + rd.col) * D + 4 * rd.half;
+      const int32_t chunks = (t.e - t.a - window + fg.chunk - 1) / fg.chunk;
+      const int64_t step = int64_t(Hkv) * 2 * sinks * (D / 4);
+      if (kQ == 1) __syncthreads();  // every wave is done with the tiles
+      for (int i = tid; i < 2 * sinks * (D / 4); i += NT) {
+        const f32x4* part = reinterpret_cast<const f32x4*>(far) + (first * Hkv + hk) * 2 * sinks * (D / 4) + i;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        for (int32_t c0 = 0; c0 < chunks; c0 += 8) {
+          f32x4 y[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) y[u] = part[(c0 + u < chunks ? c0 + u : c0) * step];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) x += c0 + u < chunks ? y[u] : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        fs[i] = x;
+      }
+      __syncthreads();
+      const int key = k0 - t.a + rd.col;
+      if (key < sinks && wave % kQ == 0) {
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const f32x4 y = *reinterpret_cast<const f32x4*>(part + 32 * i + 8 * j);
-            const f32x4 z = *reinterpret_cast<const f32x4*>(part + int64_t(sinks) * D + 32 * i + 8 * j);
+            const f32x4 y = fs[key * (D / 4) + 8 * i + 2 * j + rd.half];
+            const f32x4 z = fs[(sinks + key) * (D / 4) + 8 * i + 2 * j + rd.half];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               ak[i][4 * j + e] += y[e];
@@ -594,6 +619,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
             }
           }
       }
+      __syncthreads();
     }
     if (have > 0 && wave % kQ == 0) {
       char* st = lds + wave / kQ * (32 * D * 2);
@@ -625,13 +651,28 @@ hipError_t run_window(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stre
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
       a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, nullptr, grid, a.window, a.sinks);
-  const int64_t far = a.sinks > 0 ? FarGrid(a.window).slots(a.N, a.max_segs) * a.Hkv : 0;
+  const int64_t far = a.sinks > 0 ? FarGrid(a.N, a.Hkv, a.window).slots(a.N, a.max_segs) * a.Hkv : 0;
   if (far > 0)
     attn_dkv_kernel<D, 4, 2><<<dim3(uint32_t(far)), dim3(DkvShape<4>::NT), 0, stream>>>(
         static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
         static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, nullptr, nullptr,
         nullptr, grid, a.window, a.sinks, g.far);
-  keys_pass<D, 1, 1>(a, g, nullptr, stream);
+  // Few keys leave most of the chip without work unless waves share them. kQ = 1 / 2 / 4,
+  // the whole reverse pass, window 512, H 16, Hkv 4 but where said:
+  //   65536 tokens, H 32, Hkv 8, D 128, window 1024 (4096 work-groups of 128 keys)  3686 / 3713 / 4127 us
+  //   16384, Hkv 16, D 64, window 256 (2048)                                         181 / 187 / 294
+  //   16384, D 128, window 1024 (512)                                                638 / 610 / 675
+  //   16384, D 64 (512)                                                              208 / 208 / 246
+  //   8192, D 128 (256)                                                              217 / 172 / 191
+  //   2048, H 8, Hkv 8, D 64, window 256 (128)                                        36 / 29 / 30
+  //   4096, H 8, Hkv 1, D 128, window 2048 (32)                                      952 / 563 / 384
+  const int64_t keys = (a.N + 127) / 128 * a.Hkv;
+  if (keys > 512)
+    keys_pass<D, 1, 1>(a, g, nullptr, stream);
+  else if (keys > 64)
+    keys_pass<D, 2, 1>(a, g, nullptr, stream);
+  else
+    keys_pass<D, 4, 1>(a, g, nullptr, stream);
   return hipGetLastError();
 }
 
@@ -661,7 +702,7 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 
 size_t attn_far_bytes(int64_t N, int64_t max_segs, int32_t Hkv, int32_t D, int32_t window, int32_t sinks) {
   if (sinks == 0 || window >= N) return 0;
-  return size_t(FarGrid(window).slots(N, max_segs)) * Hkv * 2 * sinks * D * 4;
+  return size_t(FarGrid(N, Hkv, window).slots(N, max_segs)) * Hkv * 2 * sinks * D * 4;
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {

@@ -82,13 +82,14 @@ def test_window_backward_refusals(lib, kw, code):  # noqa: F811
     assert _call(lib.pkv_attn_window_varlen_backward, _window(ATTN_BWD), kw) == code
 
 
-@pytest.mark.parametrize("window,sinks", [(1, 1), (63, 4), (64, 4), (300, 64), (5000, 1)])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (63, 4), (64, 4), (127, 2), (300, 64), (5000, 1)])
 def test_window_workspace_holds_every_far_chunk(lib, window, sinks):  # noqa: F811
     """8 sinks D Hkv bytes for every chunk of queries behind a segment's window, wherever the segments lie."""
     base = dict(N=20000, Hq=4, Hkv=2, D=64, max_segs=30, dtype=0)
     size = lambda s: lib.pkv_attn_window_varlen_backward_workspace_size(*base.values(), window, s)
     per = 8 * sinks * 64 * 2
-    chunk = 512 if window < 64 or window > 512 else window
+    chunk = min(512, base["N"] * 2 // 512 // 128 * 128 + 128)
+    chunk = chunk if window < 64 else min(chunk, window)
     most = base["N"] // chunk + (base["max_segs"] if window < 64 else 0)
     assert size(sinks) - size(0) == most * per
 
