@@ -65,9 +65,11 @@ struct Loader {
     step = uint32_t(STEP) * stride;
   }
   __device__ __forceinline__ void issue_async(u32x4 r, char* dst, int wave) const {
-    const uint32_t o = fresh(off);
+    uint32_t o[LD];
+    o[0] = fresh(off);
 #pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16_async(r, o + i * step, lds_addr(dst) + wave * 1024 + i * NT * 16);
+    for (int i = 1; i < LD; ++i) o[i] = o[0] + i * step;
+    load_lds16_async<LD, NT * 16>(r, o, lds_addr(dst) + wave * 1024);
   }
   __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, char* dst, int wave) const {
     const uint32_t o = fresh(off);

@@ -132,10 +132,13 @@ __global__ __launch_bounds__(kThreads, D == 64 && kS == 1 ? 3 : 2) void attn_fwd
       if constexpr (kWin) {
         const u32x4 rk = descriptor(k + at, bytes), rv = descriptor(v + at, bytes);
         const uint32_t dst = lds_addr(lds) + (it & 1) * 2 * TB + wave * 1024;
+        uint32_t off[LD];
 #pragma unroll
-        for (int i = 0; i < LD; ++i) load_lds16_async(rk, ko + i * STEP * kstride, dst + i * kThreads * 16);
+        for (int i = 0; i < LD; ++i) off[i] = ko + i * STEP * kstride;
+        load_lds16_async<LD, kThreads * 16>(rk, off, dst);
 #pragma unroll
-        for (int i = 0; i < LD; ++i) load_lds16_async(rv, vo + i * STEP * kstride, dst + TB + i * kThreads * 16);
+        for (int i = 0; i < LD; ++i) off[i] = vo + i * STEP * kstride;
+        load_lds16_async<LD, kThreads * 16>(rv, off, dst + TB);
         return;
       }
       const auto rk = buffer(k + at, bytes), rv = buffer(v + at, bytes);

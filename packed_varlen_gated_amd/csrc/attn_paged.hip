@@ -40,18 +40,19 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the join
 constexpr int32_t kPlaces = 1 << 29;  // of a request
 constexpr float kGrow = 8.f;  // log2 of what a row's maximum may grow by before O is rescaled
 
 template <int D, bool kBig>
 struct Form {
-  static constexpr int BM = kBig ? 128 : 32;                  // rows of a tile
+  static constexpr int NT = kBig ? 512 : 256;                 // threads
+  static constexpr int BM = kBig ? 256 : 32;                  // rows of a tile
   static constexpr int KW = kBig ? 64 : 32;                   // keys of a wave in a block
   static constexpr int BK = kBig ? 64 : 4 * KW;               // keys of a block
   static constexpr int HALF = KW * D * 2;                     // bytes of a block's K (or V) in LDS, of a wave or of all
   static constexpr int STAGE = 2 * HALF * (kBig ? 1 : 4);     // of a block
-  static constexpr int PER_CU = kBig || D == 64 ? 2 : 1;      // work-groups of a compute unit (by LDS)
+  static constexpr int PER_CU = !kBig && D == 64 ? 2 : 1;     // work-groups of a compute unit (by LDS; by registers)
   static constexpr int GROUPS = 256 * PER_CU;                 // what the chip holds at a time
   static constexpr int LEAST = kBig ? 4 : 2;                  // units of a work-group
   // the parts' sums in the workspace: two of a work-group, [BM, D] and [BM, 2] m, l
@@ -114,11 +115,11 @@ __device__ __forceinline__ Share share_of(const PagedArgs& c, const AttnPagedArg
   s.tiles = int32_t((rows + F::BM - 1) / F::BM);
   s.pairs = (s.tiles + 1) / 2;
   // Without a window a tile's blocks are a rounded linear function of its number, at
-  // least 1 (and the last tile's are fewer where it is not full): the sum over a pair is
-  // at most that of the outermost one and 2 + 3. With one no tile has more than its
-  // window, its tokens and its sinks need.
+  // least 1 (the last tile's are fewer, where it is not full, by BM / BK at most): the sum
+  // over a pair is at most that of the outermost one, 2 and what the last tile lacks. With
+  // one no tile has more than its window, its tokens and its sinks need.
   const int32_t a = span_of<F::BM, F::BK>(s.q, rep, 0, 0, 0).blocks + span_of<F::BM, F::BK>(s.q, rep, 0, 0, s.tiles - 1).blocks;
-  s.cost = s.tiles == 1 ? a / 2 : a + 5;
+  s.cost = s.tiles == 1 ? a / 2 : a + 3 + F::BM / F::BK;
   if (x.window > 0) {
     const int64_t most = (int64_t(x.window) + F::BM / rep + 1) / F::BK + 2 + (x.sinks + F::BK - 1) / F::BK;
     const int64_t b = (s.tiles == 1 ? 1 : 2) * most;
@@ -132,7 +133,8 @@ __device__ __forceinline__ Share uniform(const Share& s) {
   return {{uni(s.q.a), uni(s.q.n), uni(s.q.len), s.q.ok}, uni(s.tiles), uni(s.pairs), uni(s.cost)};
 }
 
-// The sum over the work-group's 256 threads, and over those before this one.
+// The sum over the work-group's threads, and over those before this one.
+template <int NT>
 __device__ __forceinline__ int64_t scan(int64_t x, int64_t& before, int64_t* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t s = x;
@@ -146,7 +148,7 @@ __device__ __forceinline__ int64_t scan(int64_t x, int64_t& before, int64_t* lds
   __syncthreads();
   int64_t base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) {
+  for (int w = 0; w < NT / 64; ++w) {
     base += w < wave ? lds[w] : 0;
     all += lds[w];
   }
@@ -166,12 +168,13 @@ struct Place {
   // All threads of the work-group; units of the call and the place of unit `per` w.
   // False where there is none.
   __device__ __forceinline__ bool find(const PagedArgs& c, const AttnPagedArgs& x, int64_t w, int64_t& unit) {
-    __shared__ int64_t lds[kThreads / 64 + 2];
+    constexpr int NT = Form<D, kBig>::NT;
+    __shared__ int64_t lds[NT / 64 + 2];
     int64_t mine = 0, before, total = 0;
-    for (int32_t r0 = 0; r0 < c.R; r0 += kThreads) {
+    for (int32_t r0 = 0; r0 < c.R; r0 += NT) {
       const int32_t i = r0 + int32_t(threadIdx.x);
       mine = i < c.R ? share_of<D, kBig>(c, x, i).units() : 0;
-      total += scan(mine, before, lds);
+      total += scan<NT>(mine, before, lds);
     }
     per_head = total;
     const int64_t all = total * c.Hkv;
@@ -182,22 +185,22 @@ struct Place {
     hk = int32_t(unit / total);
     const int64_t y = unit - hk * total;
     int64_t base = 0;
-    for (int32_t r0 = 0;; r0 += kThreads) {
-      if (c.R > kThreads) {  // (else the scan above is the one needed)
+    for (int32_t r0 = 0;; r0 += NT) {
+      if (c.R > NT) {  // (else the scan above is the one needed)
         const int32_t i = r0 + int32_t(threadIdx.x);
         mine = i < c.R ? share_of<D, kBig>(c, x, i).units() : 0;
-        total = scan(mine, before, lds);
+        total = scan<NT>(mine, before, lds);
       }
       if (y >= base + before && y < base + before + mine) {
-        lds[kThreads / 64] = r0 + int32_t(threadIdx.x);
-        lds[kThreads / 64 + 1] = base + before;
+        lds[NT / 64] = r0 + int32_t(threadIdx.x);
+        lds[NT / 64 + 1] = base + before;
       }
       base += total;
       if (y < base) break;
     }
     __syncthreads();
-    r = uni(int32_t(lds[kThreads / 64]));
-    at = int64_t(hk) * per_head + uni(lds[kThreads / 64 + 1]);
+    r = uni(int32_t(lds[NT / 64]));
+    at = int64_t(hk) * per_head + uni(lds[NT / 64 + 1]);
     s = uniform(share_of<D, kBig>(c, x, r));
     return true;
   }
@@ -269,15 +272,16 @@ __device__ __forceinline__ Launch reload(KernelArgs& p) {
 }
 
 template <int D, bool kBig>
-__global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch launch) {
+__global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(const Launch launch) {
   using F = Form<D, kBig>;
   constexpr int CH = Swz<D>::CH, KS = D / 16, DT = D / 32, NJ = F::KW / 32;
+  constexpr int NT = F::NT;
   constexpr int GR = kBig ? 1 : F::KW / 16;  // granules of 16 keys that a wave loads of a block
   constexpr int GL = 16 * CH / 64;           // loads of a granule of K (and of V)
   constexpr int RL = 16 / GL;                // rows of a load
   __shared__ __attribute__((aligned(1024))) char lds[2 * F::STAGE];
   static_assert(kBig || 2 * F::STAGE >= 4 * 32 * (D + 6) * 4, "the waves' sums are joined in the stages");
-  __shared__ Share shares[kThreads / 64];  // the request, of every wave
+  __shared__ Share shares[NT / 64];  // the request, of every wave
 
   const int64_t b = blockIdx.x;
   if (b >= launch.groups) {
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
     const int64_t j = b - launch.groups, n = gridDim.x - launch.groups, end = covered_tokens(c.cu, c.R, c.N);
     zero_tail(x.o, end, c.N, int64_t(x.Hq) * D * 2, j, n);
     if (x.lse != nullptr)
-      for (int64_t i = j * kThreads + threadIdx.x; i < (c.N - end) * x.Hq; i += n * kThreads)
+      for (int64_t i = j * NT + threadIdx.x; i < (c.N - end) * x.Hq; i += n * NT)
         x.lse[(i / (c.N - end)) * c.N + end + i % (c.N - end)] = -INFINITY;
     if (j == 0) check_requests(c);
     return;
@@ -316,7 +320,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
 
   // the lane's place in a load: row lrow of RL, chunk lpos
   const int lrow = lane / CH, lpos = lane % CH;
-  const uint32_t kchunk = uint32_t(lpos ^ Swz<D>::k(lrow)) * 16, vchunk = uint32_t(lpos ^ Swz<D>::v(lrow)) * 16;
+  // (in the big form waves 0 to 3 load K, the others V)
+  const bool loads_v = kBig && wave >= 4;
   // LDS addresses of the lane's operand chunks
   const int kx = Swz<D>::k(col);
   const int vr = 4 * half + ((lane & 15) >> 2), vc = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vb = (lane & 1) * 8;
@@ -400,8 +405,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
     const int32_t ps = a.c.page_size, num_pages = a.c.num_pages, kstride = a.c.Hkv * D * 2;
     const char* kbase = static_cast<const char*>(a.x.k_pages) + int64_t(pl.hk) * D * 2;
     const char* vbase = static_cast<const char*>(a.x.v_pages) + int64_t(pl.hk) * D * 2;
-    const uint32_t koff = uint32_t(lrow) * kstride, voff = koff + vchunk;
-    const int32_t wkey = kBig ? 16 * wave : F::KW * wave;  // the wave's first key to load of a block
+    const int32_t wkey = kBig ? 16 * (wave & 3) : F::KW * wave;  // the wave's first key to load of a block
+    uint32_t koff[GL], voff[GL];
+#pragma unroll
+    for (int u = 0; u < GL; ++u) {
+      const int row = RL * u + lrow;
+      koff[u] = row * kstride + uint32_t(lpos ^ (loads_v ? Swz<D>::v(row) : Swz<D>::k(row))) * 16;
+      voff[u] = row * kstride + uint32_t(lpos ^ Swz<D>::v(row)) * 16;
+    }
     const int32_t far = pt.sp.ww.far, low = pt.sp.ww.low - far;
     const int32_t limit = pt.sp.hi + 1, oldest = pt.sp.lo - window - 15;  // (a granule past `oldest` is in the window)
     auto first_key = [&](int32_t blk) { return (blk < far ? blk : blk + low) * F::BK; };
@@ -412,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
     int32_t npg = 0, no = 0;
     const int32_t step_pg = F::BK / ps, step_o = F::BK % ps;
     auto issue = [&](int32_t blk, int st, bool start) {
-      const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? wave * (16 * D * 2) : wave * 2 * F::HALF);
+      const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? (wave & 3) * (16 * D * 2) + (loads_v ? F::HALF : 0) : wave * 2 * F::HALF);
       const int32_t key = first_key(blk) + wkey;
       if (start || blk == far) {
         npg = key / ps;
@@ -438,13 +449,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
         }
         const int64_t from = ok ? int64_t(page * ps + o) * kstride : 0;
         const uint32_t bytes = ok ? ((left < 16 ? left : 16) - 1) * kstride + D * 2 : 0;
-        const u32x4 rk = descriptor(kbase + from, bytes), rv = descriptor(vbase + from, bytes);
-#pragma unroll
-        for (int u = 0; u < GL; ++u)  // rows RL u + lrow: the swizzle of K flips two or three bits of the chunk
-          load_lds16_async(rk, (koff + (kchunk ^ (Swz<D>::k(RL * u) * 16))) + u * RL * kstride, dst + g * (16 * D * 2) + u * 1024);
-#pragma unroll
-        for (int u = 0; u < GL; ++u)
-          load_lds16_async(rv, voff + u * RL * kstride, dst + F::HALF + g * (16 * D * 2) + u * 1024);
+        load_lds16_async<GL, 1024>(descriptor((loads_v ? vbase : kbase) + from, bytes), koff, dst + g * (16 * D * 2));
+        if constexpr (!kBig)
+          load_lds16_async<GL, 1024>(descriptor(vbase + from, bytes), voff, dst + F::HALF + g * (16 * D * 2));
         o += 16;
         if (o == ps) {
           o = 0;
@@ -494,7 +501,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
             if (tid == 0) odd_lds[0] = 0;
             __syncthreads();
           }
-          for (int i = kBig ? tid : lane; i < F::HALF / 4; i += kBig ? kThreads : 64) {
+          for (int i = kBig ? tid : lane; i < F::HALF / 4; i += kBig ? NT : 64) {
             uint32_t y = reinterpret_cast<uint32_t*>(vt)[i];
             const bool p = (y & 0x7f80u) == 0x7f80u, e = (y & 0x7f800000u) == 0x7f800000u;
             if (p || e) odd |= uint64_t(1) << (i / (D / 2));
@@ -660,7 +667,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_paged_kernel(const Launch la
         }
       }
       __syncthreads();
-      for (int i = tid; i < mine * (D / 4); i += kThreads) {
+      for (int i = tid; i < mine * (D / 4); i += NT) {
         const int q = i / (D / 4), d = i % (D / 4) * 4;
         float top = jst[2 * q], sum = 0.f;
 #pragma unroll
@@ -812,9 +819,11 @@ hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   // (the first launch also zeroes the rows that no request has)
   const int64_t tail = c.cu == nullptr ? 1 : tail_groups(c.N * x.Hq * D * 2);
   constexpr int64_t gs = Form<D, false>::GROUPS, gb = Form<D, true>::GROUPS;
-  if (b) attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(kThreads), 0, stream>>>(Launch{c, x, ws.big, ws.big_cuts, gb});
+  if (b)
+    attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(Form<D, true>::NT), 0, stream>>>(
+        Launch{c, x, ws.big, ws.big_cuts, gb});
   if (s)
-    attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(kThreads), 0, stream>>>(
+    attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(Form<D, false>::NT), 0, stream>>>(
         Launch{c, x, ws.small, ws.small_cuts, gs});
   const int js = s ? int(gs) - 1 : 0, jb = b ? int(gb) - 1 : 0;
   attn_paged_join_kernel<D><<<dim3(js + jb, 4), dim3(kThreads), 0, stream>>>(c, x, ws, js);

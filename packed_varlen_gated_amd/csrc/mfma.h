@@ -59,25 +59,35 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
                uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32) & 0xffffu)),
                uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 }
-// (an instruction that reads m0 right behind its change needs a wait state; m0 is the
-// compiler's own and put back)
-#define PKV_LOAD_LDS_ASYNC(op)               \
-  uint32_t m0;                               \
-  asm volatile(                              \
-      "s_mov_b32 %0, m0\n\t"                 \
-      "s_mov_b32 m0, %1\n\t"                 \
-      "s_nop 0\n\t" op " %2, %3, 0 offen lds\n\t" \
-      "s_mov_b32 m0, %0"                     \
-      : "=&s"(m0)                            \
-      : "s"(lds), "v"(off), "s"(r)           \
-      : "memory")
-__device__ __forceinline__ void load_lds16_async(u32x4 r, uint32_t off, uint32_t lds) {
-  PKV_LOAD_LDS_ASYNC("buffer_load_dwordx4");
+// Load u of N goes to lds + u kStep, from off[u]. (An instruction that reads m0 right
+// behind its change needs a wait state; m0 is the compiler's own and put back.)
+template <int N, int kStep>
+__device__ __forceinline__ void load_lds16_async(u32x4 r, const uint32_t (&off)[N], uint32_t lds) {
+  static_assert(N == 2 || N == 4, "the loads of a tile or of a granule");
+  uint32_t m0;
+#define PKV_FIRST(x) "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 " x ", %2, 0 offen lds\n\t"
+#define PKV_NEXT(x) "s_add_u32 m0, m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 " x ", %2, 0 offen lds\n\t"
+  if constexpr (N == 2)
+    asm volatile(PKV_FIRST("%4") PKV_NEXT("%5") "s_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(lds), "s"(r), "i"(kStep), "v"(off[0]), "v"(off[1])
+                 : "memory", "scc");
+  else
+    asm volatile(PKV_FIRST("%4") PKV_NEXT("%5") PKV_NEXT("%6") PKV_NEXT("%7") "s_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(lds), "s"(r), "i"(kStep), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3])
+                 : "memory", "scc");
+#undef PKV_FIRST
+#undef PKV_NEXT
 }
+// 4 bytes per lane.
 __device__ __forceinline__ void load_lds4_async(u32x4 r, uint32_t off, uint32_t lds) {
-  PKV_LOAD_LDS_ASYNC("buffer_load_dword");
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(lds), "v"(off), "s"(r)
+               : "memory");
 }
-#undef PKV_LOAD_LDS_ASYNC
 // x, recomputed from here on: what is derived from it in a loop is not kept in
 // registers across the loop.
 __device__ __forceinline__ uint32_t fresh(uint32_t x) {
