@@ -292,20 +292,28 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
           dp = mfma32(rd.rows(vt, j, i), df[i], dp);
         }
         bf16x8 ds[2];
-        const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
-        if (kWin && s0 + 32 * j <= q0 + 31 - window) {
-          // keys 0 .. old of the block are behind the window, the first ones may be sinks
-          const int32_t old = q0 + rd.col - window - s0 - 32 * j - 4 * rd.half;
-          const int32_t sink = t.a + sinks - s0 - 32 * j - 4 * rd.half;
+        // (blocks that every row sees whole, most of a window's, have no comparisons)
+        auto weights = [&](auto sees) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int32_t key = 8 * (i / 4) + i % 4;
             const float p = ex2(fmaf(s[i], c, -lse2));
-            const float x = key <= last && (key > old || key < sink) ? p * (dp[i] - delta) : 0.f;
+            const float x = sees(8 * (i / 4) + i % 4) ? p * (dp[i] - delta) : 0.f;
             rest += x;
             ds[i / 8][i % 8] = static_cast<bf16>(x);
           }
+        };
+        const int32_t b0 = s0 + 32 * j;
+        if constexpr (kWin) {
+          if (b0 + 31 <= q0 && b0 > q0 + 31 - window) {
+            weights([](int32_t) { return true; });
+          } else {
+            // keys last + 1 .. are ahead, keys 0 .. old are behind the window, the first ones may be sinks
+            const int32_t last = q0 + rd.col - b0 - 4 * rd.half, old = last - window;
+            const int32_t sink = t.a + sinks - b0 - 4 * rd.half;
+            weights([&](int32_t key) { return (key <= last) & ((key > old) | (key < sink)); });
+          }
         } else {
+          const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float p = ex2(fmaf(s[i], c, -lse2));
@@ -323,9 +331,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     // The sum of a row's dS is 0; what it is short of that is delta's error, which
     // stems from the rounding of o. The keys pass gets delta without it.
     rest += other_half(rest);
+    // (Under a window with its sign turned: the keys pass begins dP from it.)
     if (rd.half == 0 && rd.col < have) {
       stats[row] = lse2;
-      stats[int64_t(H) * N + row] = delta + rest;
+      stats[int64_t(H) * N + row] = kWin ? -delta - rest : delta + rest;
     }
     __syncthreads();
     if (have > 0)
@@ -356,7 +365,7 @@ struct DkvShape {
 // the chunks small and takes inc = 1 (one more slot per segment) instead. The chunks are
 // 128 to 512 tokens, so that there are 512 work-groups if the call has that many: 8192
 // tokens, H 16, Hkv 4, D 128, window 512, 4 sinks: 221 us the reverse pass in chunks of
-// 512, FIGA in chunks of 128; 16384 tokens: 388 and FIGB.
+// 512, 196 in chunks of 128; 16384 tokens: 388 and 371.
 constexpr int kMaxSinks = 64;
 struct FarGrid {
   int32_t chunk, inc;
@@ -502,19 +511,33 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
         const int32_t first = edge ? kq + rd.col - b0 - 4 * rd.half : -64;
         const int32_t qend = kWin == 1 && to - k0 > rd.col + window ? k0 + rd.col + window : q_to();
         const int32_t end = edge ? qend - b0 - 4 * rd.half : 64;
+        auto weights = [&](auto sees) {
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 4 * i4 + e, r = 8 * i4 + e;
-            const float y = ex2(fmaf(x[i], c, -l4[e]));
-            x[i] = r >= first && r < end ? y : 0.f;
-            p[i / 8][i % 8] = static_cast<bf16>(x[i]);
+            for (int e = 0; e < 4; ++e) {
+              const int i = 4 * i4 + e;
+              const float y = ex2(fmaf(x[i], c, -l4[e]));
+              x[i] = sees(8 * i4 + e) ? y : 0.f;
+              p[i / 8][i % 8] = static_cast<bf16>(x[i]);
+            }
           }
-        }
+        };
+        if (kWin != 0 && !edge)
+          weights([](int32_t) { return true; });
+        else
+          weights([&](int32_t r) { return (r >= first) & (r < end); });
         if (D == 128) __builtin_amdgcn_sched_barrier(0);
         f32x16 dp = {};
+        if constexpr (kWin != 0) {
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const f32x4 d4 = dl[8 * j + 2 * i4 + rd.half];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dp[4 * i4 + e] = d4[e];
+          }
+        }
 #pragma unroll
         for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(ot, 0, i), vf[i], dp);
         if (D == 128) __builtin_amdgcn_sched_barrier(0);
@@ -524,7 +547,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 4 * i4 + e;
-            ds[i / 8][i % 8] = static_cast<bf16>(x[i] * (dp[i] - d4[e]));
+            ds[i / 8][i % 8] = static_cast<bf16>(kWin ? x[i] * dp[i] : x[i] * (dp[i] - d4[e]));
           }
         }
 #pragma unroll
