@@ -7,12 +7,25 @@
 // Row i of a (request, kv head) is its new token i / rep under query head i % rep of
 // the group: the heads that share keys share their loads. Two forms:
 //   small  at most 32 rows (decoding): a work-group's four waves hold the same rows
-//          and take KW keys each of a block; every wave streams its keys through LDS
-//          of its own (no barrier in the walk), and the sums are joined at the end.
-//   big    tiles of 128 rows (chunks of prompts): a wave holds 32 rows, the four
-//          share blocks of 64 keys. A walk is that of the packed kernel (attn_fwd.hip):
-//          S^T = K Q^T, P = 2^(c S - m), O^T += V^T P^T, O rescaled only when a
-//          row's maximum grew by more than 2^8.
+//          and take 32 keys each of a block of 128; every wave streams its keys through
+//          LDS of its own (no barrier in the walk), and the sums are joined at the end.
+//   big    tiles of 256 rows (chunks of prompts): a wave holds 32 rows, the eight
+//          share blocks of 64 keys, four waves loading K and four V. A walk is that of the
+//          packed kernel (attn_fwd.hip): S^T = K Q^T, P = 2^(c S - m), O^T += V^T P^T, O
+//          rescaled only when a row's maximum grew by more than 2^8.
+//
+// The small form is bound by the bytes of the cache that are seen, read once. Every wave
+// has two blocks in flight (the waits are written here: the compiler's own, before a read
+// of LDS behind a load into LDS, would wait for both). One request of 131072 tokens, H 32,
+// Hkv 8, D 128: 108 us for 0.54 GB, 5.0 TB/s of the 5.13 that a large copy reaches. 64 requests
+// of about 2000 tokens, the longest 16384: 145 us for 0.69 GB, 4.8 TB/s. 128 requests with
+// a window of 1024, H 16, Hkv 4, D 64: 38 us for 0.13 GB; a work-group has about 9 blocks
+// there, and its start (the scan over the requests), the parts' sums and the join are the rest.
+// The big form is bound by matrix instructions and what feeds them: 2048 new tokens behind
+// 27953 others, H 32, Hkv 8, D 128: 984 us, 989 TFLOP/s, where a product of 8192^3 reaches
+// 1233. With tiles of 128 rows and four waves, each key was loaded twice as often: 1080 us.
+// Loads into LDS take about a fifth of it, reads of LDS a tenth, 2^x nothing (each left out
+// in turn).
 //
 // Lengths are on the device and differ widely, so the work is dealt there: a tile's
 // blocks of keys are units, all units of the call are in one order (kv head, request,
@@ -375,96 +388,96 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
     // mode 0: the sums; 1: with values that are not finite as 0; 2: those values added.
     // Whether some sum of the lane's row is not finite.
     auto walk = [&](int mode) {
-    const Piece pc = piece();
-    const Launch& a = pc.a;
-    const Part& pt = pc.pt;
-    const int32_t mine = pc.mine, tok = pc.tok, head = pc.head, b0 = pt.b0, b1 = pc.b1;
-    pl.s = pc.s;
-    // (a place is below kPlaces: no window is one of that many)
-    const int32_t window = a.x.window > 0 && a.x.window < kPlaces ? a.x.window : kPlaces;
-    const int32_t sinks = a.x.window > 0 ? a.x.sinks : 0;
-    const int32_t place = col < mine ? pl.s.q.len - pl.s.q.n + tok : -1;
-    // places of the wave's first and last row
-    const int32_t wlo = uni(place), whi = __builtin_amdgcn_readlane(place, mine >= 32 ? 31 : (mine > 0 ? mine - 1 : 0));
-    const bool rows_here = mine > 0;
-    const float cs = a.x.scale == 0.f ? 1.f : fabsf(a.x.scale) * kLog2e;  // (as in attn_fwd.hip)
+      const Piece pc = piece();
+      const Launch& a = pc.a;
+      const Part& pt = pc.pt;
+      const int32_t mine = pc.mine, tok = pc.tok, head = pc.head, b0 = pt.b0, b1 = pc.b1;
+      pl.s = pc.s;
+      // (a place is below kPlaces: no window is one of that many)
+      const int32_t window = a.x.window > 0 && a.x.window < kPlaces ? a.x.window : kPlaces;
+      const int32_t sinks = a.x.window > 0 ? a.x.sinks : 0;
+      const int32_t place = col < mine ? pl.s.q.len - pl.s.q.n + tok : -1;
+      // places of the wave's first and last row
+      const int32_t wlo = uni(place), whi = __builtin_amdgcn_readlane(place, mine >= 32 ? 31 : (mine > 0 ? mine - 1 : 0));
+      const bool rows_here = mine > 0;
+      const float cs = a.x.scale == 0.f ? 1.f : fabsf(a.x.scale) * kLog2e;  // (as in attn_fwd.hip)
 
-    bf16x8 qf[KS];
-    {
-      const uint32_t flip = a.x.scale < 0.f ? 0x80008000u : 0u, keep = a.x.scale == 0.f ? 0u : ~0u;
-      const bf16* q = static_cast<const bf16*>(a.x.q) + ((int64_t(pl.s.q.a) + tok) * a.x.Hq + head) * D + half * 8;
+      bf16x8 qf[KS];
+      {
+        const uint32_t flip = a.x.scale < 0.f ? 0x80008000u : 0u, keep = a.x.scale == 0.f ? 0u : ~0u;
+        const bf16* q = static_cast<const bf16*>(a.x.q) + ((int64_t(pl.s.q.a) + tok) * a.x.Hq + head) * D + half * 8;
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        i32x4 y = {0, 0, 0, 0};
-        if (col < mine) y = *reinterpret_cast<const i32x4*>(q + i * 16);
+        for (int i = 0; i < KS; ++i) {
+          i32x4 y = {0, 0, 0, 0};
+          if (col < mine) y = *reinterpret_cast<const i32x4*>(q + i * 16);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = int((uint32_t(y[e]) ^ flip) & keep);
-        qf[i] = __builtin_bit_cast(bf16x8, y);
-      }
-    }
-    const int32_t ps = a.c.page_size, num_pages = a.c.num_pages, kstride = a.c.Hkv * D * 2;
-    const char* kbase = static_cast<const char*>(a.x.k_pages) + int64_t(pl.hk) * D * 2;
-    const char* vbase = static_cast<const char*>(a.x.v_pages) + int64_t(pl.hk) * D * 2;
-    const int32_t wkey = kBig ? 16 * (wave & 3) : F::KW * wave;  // the wave's first key to load of a block
-    uint32_t koff[GL], voff[GL];
-#pragma unroll
-    for (int u = 0; u < GL; ++u) {
-      const int row = RL * u + lrow;
-      koff[u] = row * kstride + uint32_t(lpos ^ (loads_v ? Swz<D>::v(row) : Swz<D>::k(row))) * 16;
-      voff[u] = row * kstride + uint32_t(lpos ^ Swz<D>::v(row)) * 16;
-    }
-    const int32_t far = pt.sp.ww.far, low = pt.sp.ww.low - far;
-    const int32_t limit = pt.sp.hi + 1, oldest = pt.sp.lo - window - 15;  // (a granule past `oldest` is in the window)
-    auto first_key = [&](int32_t blk) { return (blk < far ? blk : blk + low) * F::BK; };
-    // 64 entries of the request's row of the table from `ids0` on, one a lane: loads of
-    // entries would make every block wait for all loads before them
-    int32_t ids = 0, ids0 = -64;
-    // page and place in it of the wave's first key of the block to load next
-    int32_t npg = 0, no = 0;
-    const int32_t step_pg = F::BK / ps, step_o = F::BK % ps;
-    auto issue = [&](int32_t blk, int st, bool start) {
-      const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? (wave & 3) * (16 * D * 2) + (loads_v ? F::HALF : 0) : wave * 2 * F::HALF);
-      const int32_t key = first_key(blk) + wkey;
-      if (start || blk == far) {
-        npg = key / ps;
-        no = key - npg * ps;
-      }
-      int32_t pg = npg, o = no;
-#pragma unroll
-      for (int g = 0; g < GR; ++g) {
-        const int32_t first = key + 16 * g, left = limit - first;
-        // (what no row of the tile sees is not loaded)
-        const bool seen = left > 0 && (first > oldest || first < sinks);
-        if (seen && (pg < ids0 || pg >= ids0 + 64)) {
-          const Launch a = reload(args);
-          ids0 = pg;
-          // (waited for here, not at every use)
-          ids = fresh(a.c.table[int64_t(pl.r) * a.c.max_pages + (pg + lane < a.c.max_pages ? pg + lane : a.c.max_pages - 1)]);
-        }
-        const int32_t page = __builtin_amdgcn_readlane(ids, (pg - ids0) & 63);
-        const bool ok = seen && page >= 0 && page < num_pages;
-        if (seen && !ok) {
-          const Launch a = reload(args);
-          if (a.c.flags != nullptr && lane == 0) atomicOr(a.c.flags, kFlagBadPage);
-        }
-        const int64_t from = ok ? int64_t(page * ps + o) * kstride : 0;
-        const uint32_t bytes = ok ? ((left < 16 ? left : 16) - 1) * kstride + D * 2 : 0;
-        load_lds16_async<GL, 1024>(descriptor((loads_v ? vbase : kbase) + from, bytes), koff, dst + g * (16 * D * 2));
-        if constexpr (!kBig)
-          load_lds16_async<GL, 1024>(descriptor(vbase + from, bytes), voff, dst + F::HALF + g * (16 * D * 2));
-        o += 16;
-        if (o == ps) {
-          o = 0;
-          ++pg;
+          for (int e = 0; e < 4; ++e) y[e] = int((uint32_t(y[e]) ^ flip) & keep);
+          qf[i] = __builtin_bit_cast(bf16x8, y);
         }
       }
-      npg += step_pg;
-      no += step_o;
-      if (no >= ps) {
-        no -= ps;
-        ++npg;
+      const int32_t ps = a.c.page_size, num_pages = a.c.num_pages, kstride = a.c.Hkv * D * 2;
+      const char* kbase = static_cast<const char*>(a.x.k_pages) + int64_t(pl.hk) * D * 2;
+      const char* vbase = static_cast<const char*>(a.x.v_pages) + int64_t(pl.hk) * D * 2;
+      const int32_t wkey = kBig ? 16 * (wave & 3) : F::KW * wave;  // the wave's first key to load of a block
+      uint32_t koff[GL], voff[GL];
+#pragma unroll
+      for (int u = 0; u < GL; ++u) {
+        const int row = RL * u + lrow;
+        koff[u] = row * kstride + uint32_t(lpos ^ (loads_v ? Swz<D>::v(row) : Swz<D>::k(row))) * 16;
+        voff[u] = row * kstride + uint32_t(lpos ^ Swz<D>::v(row)) * 16;
       }
-    };
+      const int32_t far = pt.sp.ww.far, low = pt.sp.ww.low - far;
+      const int32_t limit = pt.sp.hi + 1, oldest = pt.sp.lo - window - 15;  // (a granule past `oldest` is in the window)
+      auto first_key = [&](int32_t blk) { return (blk < far ? blk : blk + low) * F::BK; };
+      // 64 entries of the request's row of the table from `ids0` on, one a lane: loads of
+      // entries would make every block wait for all loads before them
+      int32_t ids = 0, ids0 = -64;
+      // page and place in it of the wave's first key of the block to load next
+      int32_t npg = 0, no = 0;
+      const int32_t step_pg = F::BK / ps, step_o = F::BK % ps;
+      auto issue = [&](int32_t blk, int st, bool start) {
+        const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? (wave & 3) * (16 * D * 2) + (loads_v ? F::HALF : 0) : wave * 2 * F::HALF);
+        const int32_t key = first_key(blk) + wkey;
+        if (start || blk == far) {
+          npg = key / ps;
+          no = key - npg * ps;
+        }
+        int32_t pg = npg, o = no;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+          const int32_t first = key + 16 * g, left = limit - first;
+          // (what no row of the tile sees is not loaded)
+          const bool seen = left > 0 && (first > oldest || first < sinks);
+          if (seen && (pg < ids0 || pg >= ids0 + 64)) {
+            const Launch a = reload(args);
+            ids0 = pg;
+            // (waited for here, not at every use)
+            ids = fresh(a.c.table[int64_t(pl.r) * a.c.max_pages + (pg + lane < a.c.max_pages ? pg + lane : a.c.max_pages - 1)]);
+          }
+          const int32_t page = __builtin_amdgcn_readlane(ids, (pg - ids0) & 63);
+          const bool ok = seen && page >= 0 && page < num_pages;
+          if (seen && !ok) {
+            const Launch a = reload(args);
+            if (a.c.flags != nullptr && lane == 0) atomicOr(a.c.flags, kFlagBadPage);
+          }
+          const int64_t from = ok ? int64_t(page * ps + o) * kstride : 0;
+          const uint32_t bytes = ok ? ((left < 16 ? left : 16) - 1) * kstride + D * 2 : 0;
+          load_lds16_async<GL, 1024>(descriptor((loads_v ? vbase : kbase) + from, bytes), koff, dst + g * (16 * D * 2));
+          if constexpr (!kBig)
+            load_lds16_async<GL, 1024>(descriptor(vbase + from, bytes), voff, dst + F::HALF + g * (16 * D * 2));
+          o += 16;
+          if (o == ps) {
+            o = 0;
+            ++pg;
+          }
+        }
+        npg += step_pg;
+        no += step_o;
+        if (no >= ps) {
+          no -= ps;
+          ++npg;
+        }
+      };
 
       if (mode < 2) {
         m = -FLT_MAX;
