@@ -189,8 +189,9 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
 
 size_t pkv_attn_paged_workspace_size(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype) {
   const int32_t one = 1;
-  if (check_paged(&one, N, R, Hq, Hkv, D, 16, 1, 1, dtype) != PKV_OK || !attn_mfma_supported(D, dtype)) return 0;
-  return attn_paged_workspace_bytes(D);
+  if (check_paged(&one, N, R, Hq, Hkv, D, 16, 1, 1, dtype) != PKV_OK) return 0;
+  return attn_mfma_supported(D, dtype) ? attn_paged_workspace_bytes(D)
+                                       : attn_paged_simple_workspace_bytes(N, R, Hq, Hkv, D);
 }
 
 pkv_status pkv_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,

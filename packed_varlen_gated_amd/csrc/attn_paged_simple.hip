@@ -8,8 +8,14 @@
 // i / rep, query head i % rep of the group, so that a group's heads share the keys.
 // Its four waves take the tiles of 32 places in turn, each in LDS of its own, and
 // their sums are joined at the end. The products' layouts are those of the packed
-// kernels in attn_simple.hip. These shapes serve the small fp32 batches that models
-// are debugged on: a walk is not split over work-groups.
+// kernels in attn_simple.hip. Where the call has fewer row tiles than the chip holds
+// work-groups, a walk is split over several, and a second launch joins their sums.
+//
+// These shapes serve the small fp32 batches that models are debugged on. Bound by the
+// latency of a tile's loads: a wave has one tile at a time, and its fp32 products take 32
+// rows where a decoding request has H / Hkv. fp32, one token each: one request of 131072
+// tokens, H 32, Hkv 8, D 128: 0.80 ms (unsplit 25), 1.35 TB/s; 8 of 8000, H 8, Hkv 4, D 64:
+// 63 us, 2.1 TB/s; 4 of 300, D 32: 18 us.
 
 #include "paged.h"
 
@@ -64,9 +70,20 @@ __device__ __forceinline__ void fill(Tile<D>& tk, Tile<D>& tv, const PagedArgs& 
   }
 }
 
+// The parts' sums in the workspace, a record of [32, D] and [32, 2] (m, l) for each row
+// tile, kv head and split. Tile i of request r has slot floor(cu[r] rep / 32) + r + i: those
+// of different requests do not meet.
+int64_t tile_slots(int64_t N, int64_t R, int32_t rep) { return N * rep / kT + R; }
+template <int D>
+__device__ __forceinline__ float* record(const AttnPagedArgs& x, const PagedArgs& c, const Request& rq, int32_t r,
+                                         int64_t row0, int32_t hk, int splits, int split) {
+  const int64_t slot = int64_t(rq.a) * (x.Hq / c.Hkv) / kT + r + row0 / kT;
+  return static_cast<float*>(x.workspace) + ((slot * c.Hkv + hk) * splits + split) * (kT * (D + 2));
+}
+
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const PagedArgs c, const AttnPagedArgs x, int parts,
-                                                                     int64_t groups) {
+                                                                     int splits, int64_t groups) {
   __shared__ Tile<D> tiles[2 * kWaves];
   __shared__ float sm[kWaves][kT], sl[kWaves][kT];
   const int64_t b = blockIdx.x;
@@ -80,7 +97,8 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
     if (j == 0) check_requests(c);
     return;
   }
-  const int32_t part = int32_t(b % parts), hk = int32_t(b / parts % c.Hkv), r = int32_t(b / parts / c.Hkv);
+  const int32_t split = int32_t(b % splits), part = int32_t(b / splits % parts);
+  const int32_t hk = int32_t(b / splits / parts % c.Hkv), r = int32_t(b / splits / parts / c.Hkv);
   const Request rq = request(c, r);
   if (!rq.ok) return;
   const int32_t rep = x.Hq / c.Hkv, first = rq.len - rq.n;  // the first new token's place
@@ -105,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
     f32x16 acc[D / 32] = {};
     const WindowWalk ww(win ? x.window : 0x7fffffff, win ? x.sinks : 0, kT, lo > 0 ? lo : 0, 0);
     const int32_t n_tiles = hi < 0 ? 0 : ww.count(hi / kT + 1);
-    for (int32_t it = wave; it < n_tiles; it += kWaves) {
+    for (int32_t it = split * kWaves + wave; it < n_tiles; it += splits * kWaves) {
       const int32_t s0 = ww.tile(it) * kT;
       wave_fence();
       fill<T, D>(tk, tv, c, kp, vp, r, rq.len, s0, hk, lane);
@@ -196,6 +214,15 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += fabsf(z[e]) <= kFinite ? f * z[e] : z[e];
       }
+      if (splits > 1) {
+        float* rec = record<D>(x, c, rq, r, row0, hk, splits, split);
+        store4(rec + q * D + d, y);
+        if (d == 0) {
+          rec[kT * D + 2 * q] = top;
+          rec[kT * D + 2 * q + 1] = sum;
+        }
+        continue;
+      }
       const int64_t to = (rq.a + (row0 + q) / rep) * x.Hq + hk * rep + (row0 + q) % rep;
       store4(o + to * D + d, sum == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : y * (1.f / sum));
       if (x.lse != nullptr && d == 0)
@@ -205,18 +232,74 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
   }
 }
 
+// Joins the splits' sums in their order, a thread 4 channels of a row.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_paged_simple_join_kernel(const PagedArgs c, const AttnPagedArgs x,
+                                                                          int parts, int splits) {
+  const int64_t b = blockIdx.x;
+  const int32_t part = int32_t(b % parts), hk = int32_t(b / parts % c.Hkv), r = int32_t(b / parts / c.Hkv);
+  const Request rq = request(c, r);
+  const int32_t rep = x.Hq / c.Hkv;
+  const int64_t rows = int64_t(rq.n) * rep;
+  for (int64_t row0 = int64_t(part) * kT; row0 < rows; row0 += int64_t(parts) * kT) {
+    const float* rec = record<D>(x, c, rq, r, row0, hk, splits, 0);
+    for (int i = threadIdx.x; i < kT * D / 4; i += kThreads) {
+      const int q = i / (D / 4), d = i % (D / 4) * 4;
+      if (row0 + q >= rows) continue;
+      float top = -INFINITY, sum = 0.f;
+      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int u = 0; u < splits; ++u) top = fmaxf(top, rec[u * (kT * (D + 2)) + kT * D + 2 * q]);
+      const float ms = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+      for (int u = 0; u < splits; ++u) {
+        const float* __restrict__ at = rec + u * (kT * (D + 2));
+        const float f = expf(at[kT * D + 2 * q] - ms);
+        sum += f * at[kT * D + 2 * q + 1];
+        const f32x4 z = load4(at + q * D + d);
+        // (an infinity stays one, however small its split's share)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += fabsf(z[e]) <= kFinite ? f * z[e] : z[e];
+      }
+      const int64_t to = (rq.a + (row0 + q) / rep) * x.Hq + hk * rep + (row0 + q) % rep;
+      store4(static_cast<T*>(x.o) + to * D + d, sum == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : y * (1.f / sum));
+      if (x.lse != nullptr && d == 0)
+        x.lse[(hk * rep + (row0 + q) % rep) * c.N + rq.a + (row0 + q) / rep] = sum == 0.f ? -INFINITY : top + logf(sum);
+    }
+  }
+}
+
+// A walk is split where the call's row tiles are fewer than the work-groups that the chip
+// holds (by LDS, two tiles for each wave), so that it does.
+int64_t most_splits(int64_t N, int64_t R, int32_t Hq, int32_t Hkv, int32_t D) {
+  const int64_t chip = 256 * (D == 128 ? 1 : D == 64 ? 2 : 4), n = chip / (tile_slots(N, R, Hq / Hkv) * Hkv);
+  return n < 1 ? 1 : n < 64 ? n : 64;
+}
+
 template <typename T, int D>
 hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   // a request's tiles of rows are dealt to as many work-groups as the call's rows could fill
   const int64_t pairs = int64_t(c.R) * c.Hkv, most = (c.N * (x.Hq / c.Hkv) + kT - 1) / kT, room = (1 << 16) / pairs;
   const int64_t parts = c.cu == nullptr ? (x.Hq / c.Hkv + kT - 1) / kT : (room < 1 ? 1 : (room < most ? room : most));
-  const int64_t groups = pairs * parts;
+  // (a split has two tiles for each wave of the longest walk that the table allows)
+  const int64_t worth = int64_t(c.max_pages) * c.page_size / (2 * kWaves * kT);
+  int64_t splits = most_splits(c.N, c.R, x.Hq, c.Hkv, D);
+  splits = worth < splits ? (worth < 1 ? 1 : worth) : splits;
+  const int64_t groups = pairs * parts * splits;
   attn_paged_simple_kernel<T, D><<<dim3(uint32_t(groups + tail_groups(c.N * x.Hq * D * sizeof(T)))), dim3(kThreads), 0,
-                                   stream>>>(c, x, int(parts), groups);
+                                   stream>>>(c, x, int(parts), int(splits), groups);
+  if (splits > 1)
+    attn_paged_simple_join_kernel<T, D><<<dim3(uint32_t(pairs * parts)), dim3(kThreads), 0, stream>>>(c, x, int(parts),
+                                                                                                     int(splits));
   return hipGetLastError();
 }
 
 }  // namespace
+
+size_t attn_paged_simple_workspace_bytes(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D) {
+  const int64_t n = most_splits(N, R, Hq, Hkv, D);
+  return n == 1 ? 0 : size_t(tile_slots(N, R, Hq / Hkv)) * Hkv * n * kT * (D + 2) * 4;
+}
 
 hipError_t launch_attn_paged_simple(const PagedArgs& c, const AttnPagedArgs& x, int32_t dtype, hipStream_t stream) {
   if (dtype == 0) return c.D == 32 ? run<bf16, 32>(c, x, stream) : hipErrorInvalidValue;

@@ -377,6 +377,36 @@ def test_paged_long_and_short_requests(D):
     paged_case(lens.tolist(), news.tolist(), 4, 2, D, "bf16", 32, 50, 4, tail=3, seed=5)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1700, 40)])
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 32)])
+def test_paged_long_walks_in_parts(dtype, D, window, sinks):
+    """Few requests with long walks: many work-groups to each; a table far wider than its requests."""
+    paged_case([9001], [1], 8, 2, D, dtype, 64, window, sinks, seed=1, one_each=True)
+    paged_case([0, 4500, 3, 2049], [1, 1, 1, 1], 3, 1, D, dtype, 16, window, sinks, seed=2, one_each=True)
+    paged_case([2600, 0, 40, 3100], [37, 1, 0, 9], 4, 2, D, dtype, 32, window, sinks, tail=3, seed=3)
+    rng = np.random.default_rng(4)
+    lens, cu = [2500, 900], np.array([0, 5, 6])
+    table, kp, vp = cache_of(rng, lens, 16, 2, D, dtype)
+    q = on_gpu(rng.standard_normal((6, 4, D)), dtype)
+    wide = i32(np.concatenate([table, np.full((2, 4000), -1)], 1))
+    b = paged_bounds(host(q), host(kp), host(vp), table, lens, cu, window, sinks, None, dtype)
+    for t in (i32(table), wide):
+        o, lse = pkv.attn_paged(q, kp, vp, t, i32(lens), i32(cu), window or None, sinks, output_lse=True)
+        check(host(o), *b["o"], dtype, "o")
+        check(host(lse), *b["lse"], "f32", "lse")
+    # a value that is not finite reaches the rows that see it, whichever part has it
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for at in (0, 39, 41, 700, 1500, 2495, 2497, 2499):
+            v2 = vp.clone()
+            v2[int(table[0, at // 16]), at % 16] = bad
+            got, l2 = pkv.attn_paged(q, kp, v2, wide, i32(lens), i32(cu), window or None, sinks, output_lse=True)
+            see = softmax.visible(np.arange(2495, 2500), np.array([at]), window, sinks)[:, 0]
+            sees = torch.from_numpy(np.append(see, False)).to(dev())
+            assert torch.equal(got[~sees], o[~sees]) and torch.equal(l2, lse)
+            want = torch.full_like(got[sees], bad).float()
+            assert torch.equal(torch.nan_to_num(got[sees].float(), 7.0, 8.0, 9.0), torch.nan_to_num(want, 7.0, 8.0, 9.0))
+
+
 @pytest.mark.parametrize("dtype,D", [("f32", 32), ("bf16", 64), ("bf16", 128)])
 def test_paged_equals_packed(dtype, D):
     """A prompt's only chunk over the cache is the packed call's segment (up to the order of sums)."""
