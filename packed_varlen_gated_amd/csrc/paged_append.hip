@@ -3,7 +3,9 @@
 // A work-group takes 16 tokens of one request (a tile aligned to the request's first
 // new token, found as in segments.h), a wave one token at a time: the token's row of
 // all kv heads, 16 bytes a lane. With one token per request a work-group takes 4.
-// A copy: bound by memory, in small calls by the chain request, page, row.
+// A copy: bound by memory, in small calls by the chain request, page, row. 6236 tokens of
+// four prompts, Hkv 8, D 128: 11.7 us for 51 MB; 64 requests' single tokens: 3 us, in a call
+// of 9 us from Python.
 
 #include "paged.h"
 

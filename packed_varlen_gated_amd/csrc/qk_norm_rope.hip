@@ -16,7 +16,11 @@
 // is rounded to fp32: at position 10^6 an fp32 product is off by 0.03 rad.
 //
 // Bound by memory: nothing is read twice, and the arithmetic is a third of the
-// vector units' time at the copy's rate.
+// vector units' time at the copy's rate. 65536 tokens of a fused projection, H 32, Hkv 8,
+// D 128, all channels rotated: 252 us for 1.34 GB, 5.3 TB/s (a large copy 5.13). 8192 tokens,
+// H 16, Hkv 4, D 128, 64 channels rotated, forward and reverse pass: 61 us for 0.21 GB,
+// three launches (the last sums the weights' gradients of the work-groups). With the angles
+// formed by every lane for itself and before the loads: 307 and 110 us.
 
 #include "mfma.h"
 
