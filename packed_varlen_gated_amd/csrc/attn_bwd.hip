@@ -31,122 +31,13 @@
 // registers at D 128, so two waves a SIMD and no step starts before the last is done
 // with its registers. 32768 tokens in documents of about 104, H 32, D 64: 210 and
 // 220 us for 0.55 and 0.69 GB, latency of one or two tiles a work-group.
-//
-// Through a window (kWin) the queries pass walks the tiles of WindowWalk (segments.h), the
-// keys pass the queries up to `window` behind its keys, and a launch of its own takes the
-// queries further behind that see the sinks (at FarGrid). Blocks that every row sees whole
-// have no comparisons, and dP begins from -delta in the keys pass. 8192 tokens (documents as
-// above), H 16, Hkv 4, D 128, window 512: queries 85, keys 95 us, matrix instructions in
-// 22 and 26 % of the cycles, vector ones in as many, LDS reads in 17 %: a block's phases
-// (products, weights, products) wait for one another, and registers allow two waves a
-// SIMD. 16384 tokens in one document, H 16, Hkv 16, D 64, window 256, 4 sinks: queries 77,
-// far queries 32, keys 75 us, where 0.2, 0.07 and 0.2 GB take 39, 13 and 39 at a copy's rate.
 
-#include "mfma.h"
-#include "segments.h"
+#include "attn_grad.h"
 
 #include <cmath>
 
 namespace pkv {
 namespace {
-
-constexpr int kB = 128;   // queries, or keys, that a work-group owns
-constexpr int kT = 64;    // tokens of a tile of the other side
-constexpr int kThreads = 256;
-
-template <int D>
-struct Lds {
-  static constexpr int CH = D / 8, ROW = D * 2, BYTES = kT * ROW;
-  static __device__ __forceinline__ int swz(int row) {
-    return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
-  }
-};
-
-// The lane's part in loading a tile of T rows: its first chunk; the others are
-// whole multiples of 16 rows further (the swizzle's period).
-template <int D, int T, int NT>
-struct Loader {
-  static constexpr int LD = T * Lds<D>::CH / NT, STEP = NT / Lds<D>::CH;
-  static_assert(STEP % 16 == 0, "the swizzle repeats");
-  uint32_t off, step;
-  __device__ __forceinline__ Loader(int32_t stride, int tid) {
-    const int row = tid / Lds<D>::CH, pos = tid % Lds<D>::CH;
-    off = uint32_t(row) * stride + (pos ^ Lds<D>::swz(row)) * 16;
-    step = uint32_t(STEP) * stride;
-  }
-  __device__ __forceinline__ void issue_async(u32x4 r, char* dst, int wave) const {
-    uint32_t o[LD];
-    o[0] = fresh(off);
-#pragma unroll
-    for (int i = 1; i < LD; ++i) o[i] = o[0] + i * step;
-    load_lds16_async<LD, NT * 16>(r, o, lds_addr(dst) + wave * 1024);
-  }
-  __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, char* dst, int wave) const {
-    const uint32_t o = fresh(off);
-#pragma unroll
-    for (int i = 0; i < LD; ++i) load_lds16(r, o + i * step, dst + wave * 1024 + i * NT * 16);
-  }
-};
-
-// Operand reads from a tile (of 1024-byte alignment): rows 32 j + lane % 32
-// (contraction over channels, step i of 16), and transposed: channels
-// 32 i + lane % 32 (contraction over the rows of 16-row step j, in the order of
-// a product's result registers). The swizzle is an XOR of address bits that the
-// step only flips: an address register per read kind, not one per step.
-template <int D>
-struct Reader {
-  int col, half;
-  uint32_t row0, tr0, tr1;
-  __device__ __forceinline__ Reader(int tid) {
-    const int lane = tid & 63;
-    half = lane >> 5;
-    col = lane & 31;
-    row0 = col * Lds<D>::ROW + (half ^ Lds<D>::swz(col)) * 16;
-    const int r = 4 * half + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-    tr0 = r * Lds<D>::ROW + (lane & 1) * 8 + (c ^ Lds<D>::swz(r)) * 16;
-    tr1 = (r + 8) * Lds<D>::ROW + (lane & 1) * 8 + (c ^ Lds<D>::swz(r + 8)) * 16;
-  }
-  __device__ __forceinline__ bf16x8 rows(uint32_t t, int j, int i) const {
-    return read_lds8(((t + row0) ^ (32 * i)) + 32 * j * Lds<D>::ROW);
-  }
-  __device__ __forceinline__ bf16x8 channels(uint32_t t, int i, int j) const {
-    return join(read_tr(((t + tr0) ^ (64 * i)) + 16 * j * Lds<D>::ROW),
-                read_tr(((t + tr1) ^ (64 * i)) + 16 * j * Lds<D>::ROW));
-  }
-};
-
-// `have` (<= 32) rows of one head as operand fragments: lane's row lane % 32.
-template <int D>
-__device__ __forceinline__ void load_rows(bf16x8 (&f)[D / 16], const bf16* base, int32_t have, int32_t stride,
-                                          const Reader<D>& rd) {
-  const auto r = buffer(base, have > 0 ? int64_t(have - 1) * stride + D * 2 : 0);
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) f[i] = load8(r, uint32_t(rd.col) * stride + (2 * i + rd.half) * 16);
-}
-
-// 32 rows of a wave's transposed sums times f, through LDS, to `dst` (stride in
-// elements); st: 32 rows of the wave's own.
-template <int D>
-__device__ __forceinline__ void store_rows(const f32x16 (&acc)[D / 32], float f, char* st, bf16* dst, int64_t stride,
-                                           int32_t have, const Reader<D>& rd) {
-  constexpr int CH = Lds<D>::CH, ROW = Lds<D>::ROW;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bf16x4 x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = static_cast<bf16>(acc[i][4 * j + e] * f);
-      *reinterpret_cast<bf16x4*>(st + rd.col * ROW + (((4 * i + j) ^ (rd.col & (CH - 1))) * 16) + rd.half * 8) = x;
-    }
-  asm volatile("" ::: "memory");  // the wave's own rows: its LDS accesses are in order
-  for (int i = rd.half * 32 + rd.col; i < 32 * CH; i += 64) {
-    const int r = i / CH, ch = i % CH;
-    if (r < have)
-      *reinterpret_cast<i32x4*>(dst + r * stride + ch * 8) =
-          *reinterpret_cast<const i32x4*>(st + r * ROW + ((ch ^ (r & (CH - 1))) * 16));
-  }
-}
 
 // A work-group of the keys pass is a serial walk over the queries of the group's
 // heads. If the walk of the longest segment outlasts what all walks come to when
@@ -187,12 +78,12 @@ __device__ __forceinline__ void choose_form(const int32_t* __restrict__ cu, int3
   if (threadIdx.x == 0) *form = shared_form(sums[0], sums[1], H, Hkv) ? 4 : 1;
 }
 
-template <int D, bool kWin>
+template <int D>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
     int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dq, float* __restrict__ stats,
-    int32_t* __restrict__ flags, int32_t* __restrict__ form, SlotGrid grid, int32_t window, int32_t sinks) {
+    int32_t* __restrict__ flags, int32_t* __restrict__ form, SlotGrid grid) {
   constexpr int KS = D / 16, DT = D / 32, TB = Lds<D>::BYTES;
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB];  // K, V of the even tiles, K, V of the odd ones
 
@@ -221,22 +112,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     const int32_t q0 = t.start + wave * 32;
     const int32_t rows = t.e - q0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
     const int32_t qend = t.start + kB < t.e ? t.start + kB : t.e;
-    const WindowWalk ww(kWin ? window : 0x7fffffff, kWin ? sinks : 0, kT, t.start, t.a);
-    const int n_tiles = kWin ? ww.count((qend - t.a + kT - 1) / kT) : (qend - t.a + kT - 1) / kT;
-    auto tile_start = [&](int it) { return t.a + (kWin ? ww.tile(it) : it) * kT; };
+    const int n_tiles = (qend - t.a + kT - 1) / kT;
     const Loader<D, kT, kThreads> ld(kstride, tid);
     auto issue = [&](int it) {
-      const int32_t s0 = tile_start(it);
+      const int32_t s0 = t.a + it * kT;
       const int32_t n = t.e - s0 < kT ? t.e - s0 : kT;
       const int64_t at = (int64_t(s0) * Hkv + hk) * D, bytes = int64_t(n - 1) * kstride + D * 2;
       char* dst = lds + (it & 1) * 2 * TB;
-      if constexpr (kWin) {
-        ld.issue_async(descriptor(k + at, bytes), dst, wave);
-        ld.issue_async(descriptor(v + at, bytes), dst + TB, wave);
-      } else {
-        ld.issue(buffer(k + at, bytes), dst, wave);
-        ld.issue(buffer(v + at, bytes), dst + TB, wave);
-      }
+      ld.issue(buffer(k + at, bytes), dst, wave);
+      ld.issue(buffer(v + at, bytes), dst + TB, wave);
     };
     issue(0);
 
@@ -273,11 +157,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
         }
         delta = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int32_t key = 8 * (i / 4) + i % 4, at = rd.col - 4 * rd.half;
-          const bool sees = key <= at && (!kWin || key > at - window || key < sinks - 4 * rd.half);
-          delta += sees ? ex2(fmaf(s[i], c, -lse2)) * dp[i] : 0.f;
-        }
+        for (int i = 0; i < 16; ++i)
+          delta += 8 * (i / 4) + i % 4 <= rd.col - 4 * rd.half ? ex2(fmaf(s[i], c, -lse2)) * dp[i] : 0.f;
         delta += other_half(delta);
       }
     }
@@ -290,11 +171,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
       bar();
       if (it + 1 < n_tiles) issue(it + 1);
       const uint32_t kt = lds_addr(lds) + (it & 1) * 2 * TB, vt = kt + TB;
-      const int32_t s0 = tile_start(it);
+      const int32_t s0 = t.a + it * kT;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (have == 0 || s0 + 32 * j > q0 + 31) continue;
-        if (kWin && s0 + 32 * j + 31 <= q0 - window && s0 + 32 * j >= t.a + sinks) continue;
         f32x16 s = {}, dp = {};
 #pragma unroll
         for (int i = 0; i < KS; ++i) {  // independent products take turns
@@ -302,35 +182,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
           dp = mfma32(rd.rows(vt, j, i), df[i], dp);
         }
         bf16x8 ds[2];
-        // (blocks that every row sees whole, most of a window's, have no comparisons)
-        auto weights = [&](auto sees) {
+        const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p = ex2(fmaf(s[i], c, -lse2));
-            const float x = sees(8 * (i / 4) + i % 4) ? p * (dp[i] - delta) : 0.f;
-            rest += x;
-            ds[i / 8][i % 8] = static_cast<bf16>(x);
-          }
-        };
-        const int32_t b0 = s0 + 32 * j;
-        if constexpr (kWin) {
-          if (b0 + 31 <= q0 && b0 > q0 + 31 - window) {
-            weights([](int32_t) { return true; });
-          } else {
-            // keys last + 1 .. are ahead, keys 0 .. old are behind the window, the first ones may be sinks
-            const int32_t last = q0 + rd.col - b0 - 4 * rd.half, old = last - window;
-            const int32_t sink = t.a + sinks - b0 - 4 * rd.half;
-            weights([&](int32_t key) { return (key <= last) & ((key > old) | (key < sink)); });
-          }
-        } else {
-          const int32_t last = s0 + 32 * j + 31 > q0 ? q0 + rd.col - s0 - 32 * j - 4 * rd.half : 32;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p = ex2(fmaf(s[i], c, -lse2));
-            const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
-            rest += x;
-            ds[i / 8][i % 8] = static_cast<bf16>(x);
-          }
+        for (int i = 0; i < 16; ++i) {
+          const float p = ex2(fmaf(s[i], c, -lse2));
+          const float x = 8 * (i / 4) + i % 4 <= last ? p * (dp[i] - delta) : 0.f;
+          rest += x;
+          ds[i / 8][i % 8] = static_cast<bf16>(x);
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
@@ -341,10 +199,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
     // The sum of a row's dS is 0; what it is short of that is delta's error, which
     // stems from the rounding of o. The keys pass gets delta without it.
     rest += other_half(rest);
-    // (Under a window with its sign turned: the keys pass begins dP from it.)
     if (rd.half == 0 && rd.col < have) {
       stats[row] = lse2;
-      stats[int64_t(H) * N + row] = kWin ? -delta - rest : delta + rest;
+      stats[int64_t(H) * N + row] = delta + rest;
     }
     __syncthreads();
     if (have > 0)
@@ -354,8 +211,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_dq_kernel(
 }
 
 // kQ waves share 32 keys and take the 32-query blocks of a tile in turn, their
-// sums added at the end: kQ = 1, four waves hold 128 keys; kQ = 2, four hold 64 (under
-// a window); kQ = 4, eight waves hold 64.
+// sums added at the end: kQ = 1, four waves hold 128 keys; kQ = 4, eight waves
+// hold 64.
 template <int kQ>
 struct DkvShape {
   static constexpr int NT = kQ == 4 ? 512 : 256;  // threads
@@ -363,40 +220,12 @@ struct DkvShape {
   static constexpr int T = kQ == 4 ? 128 : 64;    // queries per tile
 };
 
-// The keys pass under a window. A key's queries end `window` tokens behind it, except
-// a sink's, which go on to the segment's end: one work-group's walk over those would
-// outlast all others, so the queries behind the window ("far") have a launch of their
-// own before the keys pass. There a work-group takes the segment's sinks and kFar far
-// queries and leaves its sums in the workspace; the keys pass adds a segment's in order.
-// Far queries of segment i start at cu[i] + window; chunk c of them has slot
-// floor(cu[i] / chunk) + inc i + c. With chunk <= window and inc = 0 the slots of
-// different segments do not meet, since a segment of n tokens has at most
-// floor((cu[i] + n) / chunk) - floor(cu[i] / chunk) of them; a window below 64 would make
-// the chunks small and takes inc = 1 (one more slot per segment) instead. The chunks are
-// 128 to 512 tokens, so that there are 512 work-groups if the call has that many: 8192
-// tokens, H 16, Hkv 4, D 128, window 512, 4 sinks: 221 us the reverse pass in chunks of
-// 512, 196 in chunks of 128; 16384 tokens: 388 and 371.
-constexpr int kMaxSinks = 64;
-struct FarGrid {
-  int32_t chunk, inc;
-  __host__ __device__ FarGrid(int64_t N, int32_t Hkv, int32_t window) {
-    const int64_t want = N * Hkv / 512 / 128 * 128 + 128;
-    chunk = want > 512 ? 512 : int32_t(want);
-    inc = window < 64 ? 1 : 0;
-    if (inc == 0 && chunk > window) chunk = window;
-  }
-  __host__ __device__ int64_t slots(int64_t N, int64_t max_segs) const { return N / chunk + inc * max_segs; }
-};
-
-// kWin 0: no window; 1: the queries of a window; 2: the sinks' far queries.
-template <int D, int kQ, int kWin>
+template <int D, int kQ>
 __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void attn_dkv_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
     const bf16* __restrict__ dout, const float* __restrict__ stats, const int32_t* __restrict__ cu,
     int32_t max_segs, int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dk,
-    bf16* __restrict__ dv, const int32_t* __restrict__ form, SlotGrid grid, int32_t window, int32_t sinks,
-    float* __restrict__ far) {
-  static_assert(kWin != 2 || DkvShape<kQ>::KEYS >= kMaxSinks, "a work-group has a segment's sinks");
+    bf16* __restrict__ dv, const int32_t* __restrict__ form, SlotGrid grid) {
   if (form != nullptr && *form != kQ) return;
   constexpr int KS = D / 16, DT = D / 32;
   constexpr int NT = DkvShape<kQ>::NT, T = DkvShape<kQ>::T, TB = T * D * 2;
@@ -404,39 +233,18 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   __shared__ __attribute__((aligned(1024))) char lds[4 * TB + 4 * T * 4];
 
   const int64_t b = blockIdx.x;
-  const FarGrid fg(N, Hkv, window);
-  int32_t slot, h0, h1;
-  SegTile t;
-  int32_t from = 0, to = 0;  // under a window: the queries [from, to)
-  if constexpr (kWin == 2) {
-    slot = int32_t(b / Hkv);
-    h0 = int32_t(b % Hkv);
-    h1 = h0 + 1;
-    t = {0, 0, 0, int32_t(N)};
-    if (cu != nullptr && (!find_segment(cu, max_segs, fg.chunk, fg.inc, slot, t.seg, t.a, t.e) ||
-                          !segment_ok(t.seg, t.a, t.e, N)))
-      return;
-    const int64_t c0 = int64_t(t.a) + window + (int64_t(slot) - t.a / fg.chunk - int64_t(fg.inc) * t.seg) * fg.chunk;
-    if (c0 >= t.e) return;
-    t.start = t.a;
-    from = int32_t(c0);
-    to = t.e - from < fg.chunk ? t.e : from + fg.chunk;
-  } else {
-    const int64_t blocks = slot_blocks(grid, Hkv);
-    if (b >= blocks) {
-      const int64_t j = b - blocks, groups = gridDim.x - blocks, cov = covered_tokens(cu, max_segs, N);
-      zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, groups);
-      zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, groups);
-      return;
-    }
-    slot_of(grid, b, Hkv, slot, h0, h1);
-    if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
-    from = t.start;
-    to = t.e - t.start > DkvShape<kQ>::KEYS - 1 + window ? t.start + DkvShape<kQ>::KEYS - 1 + window : t.e;
+  const int64_t blocks = slot_blocks(grid, Hkv);
+  if (b >= blocks) {
+    const int64_t j = b - blocks, groups = gridDim.x - blocks, cov = covered_tokens(cu, max_segs, N);
+    zero_tail(dk, cov, N, int64_t(Hkv) * D * 2, j, groups);
+    zero_tail(dv, cov, N, int64_t(Hkv) * D * 2, j, groups);
+    return;
   }
   const int32_t rep = H / Hkv;
-  auto q_from = [&] { return kWin ? from : t.start; };
-  auto q_to = [&] { return kWin ? to : t.e; };
+  int32_t slot, h0, h1;
+  slot_of(grid, b, Hkv, slot, h0, h1);
+  SegTile t;
+  if (!find_tile(cu, max_segs, N, DkvShape<kQ>::KEYS, slot, t)) return;
 
   for (int32_t hk = h0; hk < h1; ++hk) {
     // (nothing that goes by the lane is kept from one head to the next)
@@ -444,31 +252,21 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
     const Reader<D> rd(tid);
     const int32_t kstride = Hkv * D * 2, qstride = H * D * 2;
     const int32_t k0 = t.start + wave / kQ * 32;  // the wave's first key
-    const int32_t kend = kWin == 2 && t.e - t.a > sinks ? t.a + sinks : t.e;
-    const int32_t rows = kend - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
-    const int per_head = (q_to() - q_from() + T - 1) / T, n_tiles = per_head * rep;
+    const int32_t rows = t.e - k0, have = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+    const int per_head = (t.e - t.start + T - 1) / T, n_tiles = per_head * rep;
     const Loader<D, T, NT> ld(qstride, tid);
     int ih = hk * rep, iq = 0;  // query head and tile of the next load
     // Q, dO and the statistics of the next tile
     auto issue = [&](int it) {
-      const int32_t s0 = q_from() + iq * T, h = ih;
-      const int32_t n = q_to() - s0 < T ? q_to() - s0 : T;
+      const int32_t s0 = t.start + iq * T, h = ih;
+      const int32_t n = t.e - s0 < T ? t.e - s0 : T;
       const int64_t at = (int64_t(s0) * H + h) * D, bytes = int64_t(n - 1) * qstride + D * 2;
       char* dst = lds + (it & 1) * 2 * TB;
-      if constexpr (kWin) {
-        ld.issue_async(descriptor(q + at, bytes), dst, wave);
-        ld.issue_async(descriptor(dout + at, bytes), dst + TB, wave);
-      } else {
-        ld.issue(buffer(q + at, bytes), dst, wave);
-        ld.issue(buffer(dout + at, bytes), dst + TB, wave);
-      }
+      ld.issue(buffer(q + at, bytes), dst, wave);
+      ld.issue(buffer(dout + at, bytes), dst + TB, wave);
       if (wave < T / 32) {  // lse log2 e and delta, 64 queries a wave
         const int w = wave / (T / 64), part = wave % (T / 64) * 64;
-        if constexpr (kWin)
-          load_lds4_async(descriptor(stats + (int64_t(w) * H + h) * N + s0, n * 4), uint32_t(part + lane) * 4,
-                          lds_addr(lds) + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4);
-        else
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
             buffer(stats + (int64_t(w) * H + h) * N + s0, int64_t(n) * 4),
             (__attribute__((address_space(3))) void*)(lds + 4 * TB + (((it & 1) * 2 + w) * T + part) * 4), 4,
             uint32_t(part + lane) * 4, 0, 0, 0);
@@ -498,16 +296,14 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
       const uint32_t qt0 = lds_addr(lds) + (it & 1) * 2 * TB;
       const f32x4* ls = reinterpret_cast<const f32x4*>(lds + 4 * TB + (it & 1) * 2 * T * 4);
       const f32x4* dl = ls + T / 4;
-      const int32_t s0 = q_from() + cq * T;
+      const int32_t s0 = t.start + cq * T;
       if (++cq == per_head) cq = 0;
 #pragma unroll 1
       for (int j = wave % kQ; j < T / 32; j += kQ) {
         const int32_t b0 = s0 + 32 * j;  // first query of the block
         // (addresses are formed per block: one register each instead of one per read)
         const uint32_t qt = fresh_uniform(qt0 + 32 * j * Lds<D>::ROW), ot = qt + TB;
-        const int32_t kq = kWin == 2 ? k0 + window : k0;  // the first key's first query
-        if (have == 0 || b0 + 31 < kq || b0 >= q_to()) continue;
-        if (kWin == 1 && b0 >= k0 + 31 + window) continue;
+        if (have == 0 || b0 + 31 < k0 || b0 >= t.e) continue;
         // Registers are full at D = 128 (k, v, dk and dv take 192): the weights are
         // done with before dP is begun, and nothing of a phase starts early. The
         // other wave of the SIMD fills the gaps.
@@ -517,37 +313,22 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
         for (int i = 0; i < KS; ++i) x = mfma32(rd.rows(qt, 0, i), kf[i], x);
         if (D == 128) __builtin_amdgcn_sched_barrier(0);
         // the lane's key takes part in the block's queries first .. end - 1
-        const bool edge = b0 < kq + 31 || b0 + 32 > q_to() || (kWin == 1 && b0 + 32 > k0 + window);
-        const int32_t first = edge ? kq + rd.col - b0 - 4 * rd.half : -64;
-        const int32_t qend = kWin == 1 && to - k0 > rd.col + window ? k0 + rd.col + window : q_to();
-        const int32_t end = edge ? qend - b0 - 4 * rd.half : 64;
-        auto weights = [&](auto sees) {
+        const bool edge = b0 < k0 + 31 || b0 + 32 > t.e;
+        const int32_t first = edge ? k0 + rd.col - b0 - 4 * rd.half : -64;
+        const int32_t end = edge ? t.e - b0 - 4 * rd.half : 64;
 #pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const f32x4 l4 = ls[8 * j + 2 * i4 + rd.half];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 4 * i4 + e;
-              const float y = ex2(fmaf(x[i], c, -l4[e]));
-              x[i] = sees(8 * i4 + e) ? y : 0.f;
-              p[i / 8][i % 8] = static_cast<bf16>(x[i]);
-            }
-          }
-        };
-        if (kWin != 0 && !edge)
-          weights([](int32_t) { return true; });
-        else
-          weights([&](int32_t r) { return (r >= first) & (r < end); });
-        if (D == 128) __builtin_amdgcn_sched_barrier(0);
-        f32x16 dp = {};
-        if constexpr (kWin != 0) {
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 d4 = dl[8 * j + 2 * i4 + rd.half];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dp[4 * i4 + e] = d4[e];
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * i4 + e, r = 8 * i4 + e;
+            const float y = ex2(fmaf(x[i], c, -l4[e]));
+            x[i] = r >= first && r < end ? y : 0.f;
+            p[i / 8][i % 8] = static_cast<bf16>(x[i]);
           }
         }
+        if (D == 128) __builtin_amdgcn_sched_barrier(0);
+        f32x16 dp = {};
 #pragma unroll
         for (int i = 0; i < KS; ++i) dp = mfma32(rd.rows(ot, 0, i), vf[i], dp);
         if (D == 128) __builtin_amdgcn_sched_barrier(0);
@@ -557,7 +338,7 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 4 * i4 + e;
-            ds[i / 8][i % 8] = static_cast<bf16>(kWin ? x[i] * dp[i] : x[i] * (dp[i] - d4[e]));
+            ds[i / 8][i % 8] = static_cast<bf16>(x[i] * (dp[i] - d4[e]));
           }
         }
 #pragma unroll
@@ -602,60 +383,6 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
         join_sums(av, from);
       }
     }
-    if constexpr (kWin == 2) {
-      if (rd.col < have && wave % kQ == 0) {
-        float* out = far + ((int64_t(slot) * Hkv + hk) * 2 * sinks + (k0 - t.a) + rd.col) * D + 4 * rd.half;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float* x = out + 32 * i + 8 * j;
-            *reinterpret_cast<f32x4*>(x) = f32x4{ak[i][4 * j], ak[i][4 * j + 1], ak[i][4 * j + 2], ak[i][4 * j + 3]};
-            *reinterpret_cast<f32x4*>(x + int64_t(sinks) * D) =
-                f32x4{av[i][4 * j], av[i][4 * j + 1], av[i][4 * j + 2], av[i][4 * j + 3]};
-          }
-      }
-      return;
-    }
-    if (kWin == 1 && far != nullptr && t.start == t.a && t.e - t.a > window) {
-      // The sinks' sums over the far queries: every thread sums 4 channels of a sink over
-      // the chunks, the loads of 8 going out together.
-      static_assert(4 * TB >= 2 * kMaxSinks * D * 4 || kWin != 1, "the far sums fit the tiles' buffers");
-      f32x4* fs = reinterpret_cast<f32x4*>(lds);  // dk, dv of [sink][D / 4]
-      const int64_t first = int64_t(t.a) / fg.chunk + int64_t(fg.inc) * t.seg;
-      const int32_t chunks = (t.e - t.a - window + fg.chunk - 1) / fg.chunk;
-      const int64_t step = int64_t(Hkv) * 2 * sinks * (D / 4);
-      if (kQ == 1) __syncthreads();  // every wave is done with the tiles
-      for (int i = tid; i < 2 * sinks * (D / 4); i += NT) {
-        const f32x4* part = reinterpret_cast<const f32x4*>(far) + (first * Hkv + hk) * 2 * sinks * (D / 4) + i;
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-        for (int32_t c0 = 0; c0 < chunks; c0 += 8) {
-          f32x4 y[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) y[u] = part[(c0 + u < chunks ? c0 + u : c0) * step];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) x += c0 + u < chunks ? y[u] : f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        fs[i] = x;
-      }
-      __syncthreads();
-      const int key = k0 - t.a + rd.col;
-      if (key < sinks && wave % kQ == 0) {
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 y = fs[key * (D / 4) + 8 * i + 2 * j + rd.half];
-            const f32x4 z = fs[(sinks + key) * (D / 4) + 8 * i + 2 * j + rd.half];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              ak[i][4 * j + e] += y[e];
-              av[i][4 * j + e] += z[e];
-            }
-          }
-      }
-      __syncthreads();
-    }
     if (have > 0 && wave % kQ == 0) {
       char* st = lds + wave / kQ * (32 * D * 2);
       const int64_t to = (int64_t(k0) * Hkv + hk) * D;
@@ -667,48 +394,14 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
   }
 }
 
-template <int D, int kQ, int kWin = 0>
+template <int D, int kQ>
 void keys_pass(const AttnArgs& a, const AttnGradArgs& g, const int32_t* form, hipStream_t stream) {
   const SlotGrid grid = slot_grid(a.N, a.max_segs, DkvShape<kQ>::KEYS);
   const dim3 blocks(uint32_t(slot_blocks(grid, a.Hkv) + tail_groups(a.N * a.Hkv * D * 2)));
-  attn_dkv_kernel<D, kQ, kWin><<<blocks, dim3(DkvShape<kQ>::NT), 0, stream>>>(
+  attn_dkv_kernel<D, kQ><<<blocks, dim3(DkvShape<kQ>::NT), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale,
-      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), form, grid, a.window, a.sinks, g.far);
-}
-
-// The queries pass, the sinks' far queries, the keys pass.
-template <int D>
-hipError_t run_window(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
-  const SlotGrid grid = slot_grid(a.N, a.max_segs, kB);
-  const dim3 blocks(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2)));
-  attn_dq_kernel<D, true><<<blocks, dim3(kThreads), 0, stream>>>(
-      static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
-      static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
-      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, nullptr, grid, a.window, a.sinks);
-  const int64_t far = a.sinks > 0 ? FarGrid(a.N, a.Hkv, a.window).slots(a.N, a.max_segs) * a.Hkv : 0;
-  if (far > 0)
-    attn_dkv_kernel<D, 4, 2><<<dim3(uint32_t(far)), dim3(DkvShape<4>::NT), 0, stream>>>(
-        static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
-        static_cast<const bf16*>(g.dout), g.stats, a.cu, a.max_segs, a.N, a.H, a.Hkv, a.scale, nullptr, nullptr,
-        nullptr, grid, a.window, a.sinks, g.far);
-  // Few keys leave most of the chip without work unless waves share them. kQ = 1 / 2 / 4,
-  // the whole reverse pass, window 512, H 16, Hkv 4 but where said:
-  //   65536 tokens, H 32, Hkv 8, D 128, window 1024 (4096 work-groups of 128 keys)  3686 / 3713 / 4127 us
-  //   16384, Hkv 16, D 64, window 256 (2048)                                         181 / 187 / 294
-  //   16384, D 128, window 1024 (512)                                                638 / 610 / 675
-  //   16384, D 64 (512)                                                              208 / 208 / 246
-  //   8192, D 128 (256)                                                              217 / 172 / 191
-  //   2048, H 8, Hkv 8, D 64, window 256 (128)                                        36 / 29 / 30
-  //   4096, H 8, Hkv 1, D 128, window 2048 (32)                                      952 / 563 / 384
-  const int64_t keys = (a.N + 127) / 128 * a.Hkv;
-  if (keys > 512)
-    keys_pass<D, 1, 1>(a, g, nullptr, stream);
-  else if (keys > 64)
-    keys_pass<D, 2, 1>(a, g, nullptr, stream);
-  else
-    keys_pass<D, 4, 1>(a, g, nullptr, stream);
-  return hipGetLastError();
+      static_cast<bf16*>(g.dk), static_cast<bf16*>(g.dv), form, grid);
 }
 
 template <int D>
@@ -721,10 +414,10 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
   const bool may = shared_form(uint64_t(L), uint64_t(L * L), a.H, a.Hkv);
   int32_t* form = may && a.cu != nullptr ? reinterpret_cast<int32_t*>(g.stats + 2 * a.N * a.H) : nullptr;
   const dim3 blocks(uint32_t(slot_blocks(grid, a.H) + tail_groups(a.N * a.H * D * 2)));
-  attn_dq_kernel<D, false><<<blocks, dim3(kThreads), 0, stream>>>(
+  attn_dq_kernel<D><<<blocks, dim3(kThreads), 0, stream>>>(
       static_cast<const bf16*>(a.q), static_cast<const bf16*>(a.k), static_cast<const bf16*>(a.v),
       static_cast<const bf16*>(a.o), static_cast<const bf16*>(g.dout), a.lse, a.cu, a.max_segs, a.N, a.H, a.Hkv,
-      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, form, grid, 0, 0);
+      a.scale, static_cast<bf16*>(g.dq), g.stats, a.flags, form, grid);
   // With cu the lengths are on the device: both forms are launched, and the one
   // that was not chosen ends at once.
   const bool share = a.cu == nullptr && shared_form(a.N, uint64_t(a.N) * a.N, a.H, a.Hkv);
@@ -735,13 +428,8 @@ hipError_t run(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
 
 }  // namespace
 
-size_t attn_far_bytes(int64_t N, int64_t max_segs, int32_t Hkv, int32_t D, int32_t window, int32_t sinks) {
-  if (sinks == 0 || window >= N) return 0;
-  return size_t(FarGrid(N, Hkv, window).slots(N, max_segs)) * Hkv * 2 * sinks * D * 4;
-}
-
 hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream) {
-  if (a.window > 0 && a.window < a.N) return a.D == 64 ? run_window<64>(a, g, stream) : run_window<128>(a, g, stream);
+  if (a.window > 0 && a.window < a.N) return launch_attn_window_bwd(a, g, stream);
   return a.D == 64 ? run<64>(a, g, stream) : run<128>(a, g, stream);
 }
 

@@ -355,9 +355,9 @@ __global__ __launch_bounds__(kThreads) void attn_simple_dkv(
   load_row<T, D>(vf, v, row, row < t.e, Hkv, hk, half);
   f32x16 ak[D / 32] = {}, av[D / 32] = {};
   // (query head, query tile) pairs, dealt to the waves in turn
-  int64_t qe = t.e;
-  if (kWin && t.start - t.a >= sinks && t.e - t.start > kT - 1 + window) qe = t.start + kT - 1 + window;
-  const int64_t per = (qe - t.start + kT - 1) / kT;
+  int64_t per = (int64_t(t.e) - t.start + kT - 1) / kT;
+  if constexpr (kWin)
+    if (t.start - t.a >= sinks && t.e - t.start > kT - 1 + window) per = (kT - 1 + window + kT - 1) / kT;
   for (int64_t it = wave; it < per * rep; it += kWaves) {
     const int32_t h = hk * rep + int32_t(it / per);
     const int64_t s0 = t.start + it % per * kT;

@@ -164,6 +164,7 @@ hipError_t launch_attn_simple_backward(const AttnArgs& a, const AttnGradArgs& g,
 bool attn_mfma_supported(int32_t D, int32_t dtype);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream);
+hipError_t launch_attn_window_bwd(const AttnArgs& a, const AttnGradArgs& g, hipStream_t stream);
 // Bytes of AttnGradArgs::far.
 size_t attn_far_bytes(int64_t N, int64_t max_segs, int32_t Hkv, int32_t D, int32_t window, int32_t sinks);
 
