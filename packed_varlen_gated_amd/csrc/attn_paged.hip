@@ -839,7 +839,9 @@ hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
     attn_paged_kernel<D, false><<<dim3(uint32_t(gs + (b ? 0 : tail))), dim3(Form<D, false>::NT), 0, stream>>>(
         Launch{c, x, ws.small, ws.small_cuts, gs});
   const int js = s ? int(gs) - 1 : 0, jb = b ? int(gb) - 1 : 0;
-  attn_paged_join_kernel<D><<<dim3(js + jb, 4), dim3(kThreads), 0, stream>>>(c, x, ws, js);
+  // (the big form's tiles have 8 times the rows: 4 and 16 work-groups to a tile, 27 and 23 us
+  // of 1007 us of a long prompt's chunk)
+  attn_paged_join_kernel<D><<<dim3(js + jb, b ? 16 : 4), dim3(kThreads), 0, stream>>>(c, x, ws, js);
   return hipGetLastError();
 }
 

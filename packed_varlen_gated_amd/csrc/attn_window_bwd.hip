@@ -8,10 +8,12 @@
 // Blocks that every row sees whole, most of a window's, have no comparisons, and dP begins
 // from -delta in the keys pass. The loads' waits are written here (load_lds16_async).
 //
-// 8192 tokens (documents of about 800, the longest 3409), H 16, Hkv 4, D 128, window 512: queries 85, keys 95 us, matrix instructions in
-// 22 and 26 % of the cycles, vector ones in as many, LDS reads in 17 %: a block's phases
-// (products, weights, products) wait for one another, and registers allow two waves a
-// SIMD. 16384 tokens in one document, H 16, Hkv 16, D 64, window 256, 4 sinks: queries 77,
+// 8192 tokens (documents of about 800, the longest 3409), H 16, Hkv 4, D 128, window 512:
+// queries 75, keys 86 us, of which 24 and 18 are the rows' own loads and stores (work-groups
+// start and end together); matrix instructions in 22 and 26 % of the cycles, vector ones in as
+// many, LDS reads in 17 %: a block's phases (products, weights, products) wait for one another,
+// and registers allow two waves a SIMD. Left out in turn, the tiles' loads took 6 and 14 us,
+// row-wise LDS reads 7 and 4, transposing ones 2 and 4, 2^x 3 and 4. 16384 tokens in one document, H 16, Hkv 16, D 64, window 256, 4 sinks: queries 77,
 // far queries 32, keys 75 us, where 0.2, 0.07 and 0.2 GB take 39, 13 and 39 at a copy's rate.
 
 #include "attn_grad.h"
@@ -39,7 +41,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_window_dq_kern
   int32_t slot, h0, h1;
   slot_of(grid, b, H, slot, h0, h1);
   SegTile t;
-  // late tiles have the most keys: they start first
+  // late tiles have the most keys, up to a window of them: they start first
   if (slot < grid.near) slot = grid.near - 1 - slot;
   if (!find_tile(cu, max_segs, N, kB, slot, t)) return;
 
