@@ -10,19 +10,22 @@
 //
 // 8192 tokens (documents of about 800, the longest 3409), H 16, Hkv 4, D 128, window 512:
 // queries 75, keys 86 us, of which 24 and 18 are the rows' own loads and stores (work-groups
-// start and end together); matrix instructions in 22 and 26 % of the cycles, vector ones in as
-// many, LDS reads in 17 %: a block's phases (products, weights, products) wait for one another,
-// and registers allow two waves a SIMD. Left out in turn, the tiles' loads took 6 and 14 us,
-// row-wise LDS reads 7 and 4, transposing ones 2 and 4, 2^x 3 and 4. 16384 tokens in one document, H 16, Hkv 16, D 64, window 256, 4 sinks: queries 77,
-// far queries 32, keys 75 us, where 0.2, 0.07 and 0.2 GB take 39, 13 and 39 at a copy's rate.
+// start and end together); matrix instructions in 28 and 33 % of the cycles, vector ones in
+// as many, LDS reads in 15 and 22 %: a block's phases (products, weights, products) wait for
+// one another, and registers allow two waves a SIMD. Left out in turn, the tiles' loads took
+// 6 and 14 us, row-wise LDS reads 7 and 4, transposing ones 2 and 4, 2^x 3 and 4. 16384 tokens
+// in one document, H 16, Hkv 16, D 64, window 256, 4 sinks: queries 64, far queries 29, keys
+// 70 us, where 0.2, 0.07 and 0.2 GB take 39, 13 and 39 at a copy's rate.
 
 #include "attn_grad.h"
 
 namespace pkv {
 namespace {
 
+// (At D 64 the edges' comparisons do not fit the 128 registers of four waves a SIMD: 220 us
+// the call with 13 of them in memory, 212 with three waves.)
 template <int D>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_window_dq_kernel(
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_window_dq_kernel(
     const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v, const bf16* __restrict__ o,
     const bf16* __restrict__ dout, const float* __restrict__ lse, const int32_t* __restrict__ cu, int32_t max_segs,
     int64_t N, int32_t H, int32_t Hkv, float scale, bf16* __restrict__ dq, float* __restrict__ stats,
