@@ -21,7 +21,8 @@
  * data-dependent ones go to the device `flags` word. Tensors in `dtype` are
  * 16-byte aligned; fp32 and int32 ones are aligned to their element size. No
  * output overlaps an input or another output (but see pkv_paged_kv_append).
- * Equal calls give equal bits; the order of a sum may go by the call's sizes.
+ * Equal calls give equal bits; the order of a sum may go by the call's sizes,
+ * over a paged cache also by the lengths of the call's requests.
  * Workspaces are scratch: calls that share one must be ordered on one stream.
  */
 #ifndef PKV_SOFTMAX_H

@@ -7,7 +7,7 @@
 // Row i of a (request, kv head) is its new token i / rep under query head i % rep of
 // the group: the heads that share keys share their loads. Two forms:
 //   small  at most 32 rows (decoding): a work-group's four waves hold the same rows
-//          and take 32 keys each of a block of 128; every wave streams its keys through
+//          and take 16 (D 64: 32) keys each of a block; every wave streams its keys through
 //          LDS of its own (no barrier in the walk), and the sums are joined at the end.
 //   big    tiles of 256 rows (chunks of prompts): a wave holds 32 rows, the eight
 //          share blocks of 64 keys, four waves loading K and four V. A walk is that of the
@@ -61,12 +61,11 @@ template <int D, bool kBig>
 struct Form {
   static constexpr int NT = kBig ? 512 : 256;                 // threads
   static constexpr int BM = kBig ? 256 : 32;                  // rows of a tile
-  static constexpr int KW = kBig ? 64 : 32;                   // keys of a wave in a block
+  static constexpr int KW = kBig ? 64 : D == 128 ? 16 : 32;   // keys of a wave in a block
   static constexpr int BK = kBig ? 64 : 4 * KW;               // keys of a block
   static constexpr int HALF = KW * D * 2;                     // bytes of a block's K (or V) in LDS, of a wave or of all
   static constexpr int STAGE = 2 * HALF * (kBig ? 1 : 4);     // of a block
-  static constexpr int PER_CU = !kBig && D == 64 ? 2 : 1;     // work-groups of a compute unit (by LDS; by registers)
-  static constexpr int GROUPS = 256 * PER_CU;                 // what the chip holds at a time
+  static constexpr int GROUPS = kBig ? 256 : 512;             // at most: what the chip holds at a time
   static constexpr int LEAST = kBig ? 4 : 2;                  // units of a work-group
   // the parts' sums in the workspace: two of a work-group, [BM, D] and [BM, 2] m, l
   static constexpr size_t STATS = size_t(2) * GROUPS * BM * D;
@@ -180,7 +179,8 @@ struct Place {
 
   // All threads of the work-group; units of the call and the place of unit `per` w.
   // False where there is none.
-  __device__ __forceinline__ bool find(const PagedArgs& c, const AttnPagedArgs& x, int64_t w, int64_t& unit) {
+  __device__ __forceinline__ bool find(const PagedArgs& c, const AttnPagedArgs& x, int64_t w, int64_t groups,
+                                       int64_t& unit) {
     constexpr int NT = Form<D, kBig>::NT;
     __shared__ int64_t lds[NT / 64 + 2];
     int64_t mine = 0, before, total = 0;
@@ -191,7 +191,7 @@ struct Place {
     }
     per_head = total;
     const int64_t all = total * c.Hkv;
-    per = (all + Form<D, kBig>::GROUPS - 1) / Form<D, kBig>::GROUPS;
+    per = (all + groups - 1) / groups;
     per = per < Form<D, kBig>::LEAST ? Form<D, kBig>::LEAST : per;
     unit = per * w;
     if (unit >= all) return false;
@@ -287,13 +287,14 @@ __device__ __forceinline__ Launch reload(KernelArgs& p) {
 template <int D, bool kBig>
 __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(const Launch launch) {
   using F = Form<D, kBig>;
-  constexpr int CH = Swz<D>::CH, KS = D / 16, DT = D / 32, NJ = F::KW / 32;
+  constexpr int CH = Swz<D>::CH, KS = D / 16, DT = D / 32, NJ = (F::KW + 31) / 32;
+  constexpr int NR = F::KW == 16 ? 8 : 16;  // registers of a product of 32 keys (8: of its first 16) that are used
   constexpr int NT = F::NT;
   constexpr int GR = kBig ? 1 : F::KW / 16;  // granules of 16 keys that a wave loads of a block
   constexpr int GL = 16 * CH / 64;           // loads of a granule of K (and of V)
   constexpr int RL = 16 / GL;                // rows of a load
-  __shared__ __attribute__((aligned(1024))) char lds[2 * F::STAGE];
-  static_assert(kBig || 2 * F::STAGE >= 4 * 32 * (D + 6) * 4, "the waves' sums are joined in the stages");
+  constexpr int JOIN = kBig ? 0 : 4 * 32 * (D + 6) * 4;  // the waves' sums are joined in the stages
+  __shared__ __attribute__((aligned(1024))) char lds[2 * F::STAGE > JOIN ? 2 * F::STAGE : JOIN];
   __shared__ Share shares[NT / 64];  // the request, of every wave
 
   const int64_t b = blockIdx.x;
@@ -314,7 +315,7 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
   Place<D, kBig> pl;
   int64_t unit, end;
   if (threadIdx.x == 0) launch.cuts[w].last = -1;
-  if (!pl.find(launch.c, launch.x, w, unit)) return;
+  if (!pl.find(launch.c, launch.x, w, launch.groups, unit)) return;
   {
     const int64_t all = pl.per_head * launch.c.Hkv;
     end = unit + pl.per < all ? unit + pl.per : all;
@@ -566,7 +567,7 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < NR; ++i) {
               const int32_t k = 32 * j + 8 * (i / 4) + i % 4;
               s[j][i] = k <= last && (k > old || k < sink) ? s[j][i] : -INFINITY;
             }
@@ -575,7 +576,7 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
+          for (int i = 0; i < NR; ++i) mx = fmaxf(mx, s[j][i]);
         mx = fmaxf(mx, other_half(mx)) * cs;
         const bool grew = mx > m + kGrow;
         if (__builtin_amdgcn_ballot_w64(grew) != 0) {
@@ -587,11 +588,11 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[i][j] *= f;
         }
-        bf16x8 p[2 * NJ];
+        bf16x8 p[F::KW / 16];
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < NR; ++i) {
             const float y = ex2(fmaf(s[j][i], cs, -m));
             l += y;
             p[2 * j + i / 8][i % 8] = static_cast<bf16>(y);
@@ -599,7 +600,7 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2 * NJ; ++j) {
+          for (int j = 0; j < F::KW / 16; ++j) {
             const char* y = vt + (16 * j + vr) * (D * 2) + (((4 * i + vc) ^ vx) * 16) + vb;
             acc[i] = mfma32(join(read_tr(y), read_tr(y + 8 * (D * 2))), p[j], acc[i]);
           }
@@ -831,7 +832,17 @@ hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   const Workspace<D> ws(x.workspace);
   // (the first launch also zeroes the rows that no request has)
   const int64_t tail = c.cu == nullptr ? 1 : tail_groups(c.N * x.Hq * D * 2);
-  constexpr int64_t gs = Form<D, false>::GROUPS, gb = Form<D, true>::GROUPS;
+  // Two work-groups of the small form fit a compute unit: one hides the other's start and
+  // end, which counts where walks are many and short, and costs a longer join and parts of
+  // half the length. One token each, H 32, Hkv 8, D 128, 256 / 512 work-groups:
+  //   1 request of 131072 tokens (8 walks)      108 / 112 us
+  //   64 of about 2000 (512)                    146 / 149
+  //   128 of 300, of 2000 (1024)                 47 / 36, 194 / 202
+  //   256 of 300, of 1500 (2048)                 90 / 66, 290 / 294
+  //   1024 of 130, of 600 (8192)                269 / 171, 518 / 481
+  // D 64, the same, 512 the better nearly everywhere: 64 of 4096 117 / 110, 256 of 300 60 / 41.
+  constexpr int64_t gb = Form<D, true>::GROUPS;
+  const int64_t gs = D == 128 && int64_t(c.R) * c.Hkv < 1024 ? Form<D, false>::GROUPS / 2 : Form<D, false>::GROUPS;
   if (b)
     attn_paged_kernel<D, true><<<dim3(uint32_t(gb + tail)), dim3(Form<D, true>::NT), 0, stream>>>(
         Launch{c, x, ws.big, ws.big_cuts, gb});

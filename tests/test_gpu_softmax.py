@@ -458,12 +458,16 @@ def test_paged_hidden_values_reach_nothing(dtype, D, window, sinks):
 
 @pytest.mark.parametrize("dtype,D", [("f32", 32), ("bf16", 64), ("bf16", 128)])
 def test_paged_bad_numbers_set_their_flags(dtype, D):
-    """A bad length, page or cu_seqlens sets its flag; the other requests keep their bits, nothing else is written."""
+    """A bad length, page or cu_seqlens sets its flag; the other requests have their results, nothing else is written."""
     rng = np.random.default_rng(6)
     lens = [70, 40, 100]
     table, kp, vp = cache_of(rng, lens, 16, 2, D, dtype)
     q, k, v = (on_gpu(rng.standard_normal((3, h, D)), dtype) for h in (4, 2, 2))
     ref, _ = pkv.attn_paged(q, kp, vp, i32(table), i32(lens))
+    # where a request's keys are cut goes by the lengths of the call's requests, and with it the order of its sums:
+    # both results are within the bounds of the same value, so within twice that of each other
+    bound = 2 * paged_bounds(host(q), host(kp), host(vp), table, lens, np.arange(4), 0, 0, None, dtype)["o"][1]
+    same = lambda o: (np.abs(host(o) - host(ref)) <= bound)[[0, 2]].all()
     flags = torch.zeros(1, dtype=torch.int32, device=dev())
 
     def both(table, lens, cu=None):
@@ -476,7 +480,7 @@ def test_paged_bad_numbers_set_their_flags(dtype, D):
         return o, f, int(flags), k2, v2
     for bad in (-1, 16 * table.shape[1] + 1, 2 ** 31 - 1):
         o, f, g, k2, v2 = both(table, [70, bad, 100])
-        assert f == g == pkv.FLAG_BAD_LENGTH and torch.equal(o[[0, 2]], ref[[0, 2]])
+        assert f == g == pkv.FLAG_BAD_LENGTH and same(o)
         changed = (k2 != kp).flatten(1).any(1).sum()
         assert int(changed) == 2
     for bad in (-1, len(kp), 2 ** 31 - 1, -(2 ** 31)):
