@@ -66,7 +66,7 @@ struct Form {
   static constexpr int HALF = KW * D * 2;                     // bytes of a block's K (or V) in LDS, of a wave or of all
   static constexpr int STAGE = 2 * HALF * (kBig ? 1 : 4);     // of a block
   static constexpr int GROUPS = kBig ? 256 : 512;             // at most: what the chip holds at a time
-  static constexpr int LEAST = kBig ? 4 : 2;                  // units of a work-group
+  static constexpr int LEAST = 2;  // units of a work-group (4: a prompt of 128 tokens 38 us instead of 27)
   // the parts' sums in the workspace: two of a work-group, [BM, D] and [BM, 2] m, l
   static constexpr size_t STATS = size_t(2) * GROUPS * BM * D;
   static constexpr size_t PARTS = (STATS + size_t(2) * GROUPS * BM * 2) * 4;
@@ -101,7 +101,8 @@ template <int BM, int BK>
 __device__ __forceinline__ Span span_of(const Request& q, int32_t rep, int32_t window, int32_t sinks, int32_t j) {
   const int32_t first = q.len - q.n;
   const int64_t last = int64_t(BM) * (j + 1) - 1, rows = int64_t(q.n) * rep;
-  const int32_t lo = first + int32_t(int64_t(BM) * j / rep), hi = first + int32_t((last < rows ? last : rows - 1) / rep);
+  const int32_t lo = first + int32_t(int64_t(BM) * j / rep);
+  const int32_t hi = first + int32_t((last < rows ? last : rows - 1) / rep);
   const WindowWalk ww(window > 0 ? window : 0x7fffffff, window > 0 ? sinks : 0, BK, lo > 0 ? lo : 0, 0);
   return {lo, hi, hi < 0 ? 1 : ww.count(hi / BK + 1), ww};
 }
@@ -130,7 +131,8 @@ __device__ __forceinline__ Share share_of(const PagedArgs& c, const AttnPagedArg
   // least 1 (the last tile's are fewer, where it is not full, by BM / BK at most): the sum
   // over a pair is at most that of the outermost one, 2 and what the last tile lacks. With
   // one no tile has more than its window, its tokens and its sinks need.
-  const int32_t a = span_of<F::BM, F::BK>(s.q, rep, 0, 0, 0).blocks + span_of<F::BM, F::BK>(s.q, rep, 0, 0, s.tiles - 1).blocks;
+  const int32_t a = span_of<F::BM, F::BK>(s.q, rep, 0, 0, 0).blocks +
+                    span_of<F::BM, F::BK>(s.q, rep, 0, 0, s.tiles - 1).blocks;
   s.cost = s.tiles == 1 ? a / 2 : a + 3 + F::BM / F::BK;
   if (x.window > 0) {
     const int64_t most = (int64_t(x.window) + F::BM / rep + 1) / F::BK + 2 + (x.sinks + F::BK - 1) / F::BK;
@@ -324,8 +326,12 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
     const Part pt = part_at<D, kBig>(pl, launch.x, rep, unit);
     if (pt.j >= 0 && pt.b0 > 0 && unit - pt.b0 >= unit - pl.per && threadIdx.x == 0) {
       const int64_t row0 = int64_t(pt.j) * F::BM, left = int64_t(pl.s.q.n) * rep - row0;
-      launch.cuts[w] = {int32_t((unit - pt.b0 + pt.sp.blocks - 1) / pl.per), left < F::BM ? int32_t(left) : F::BM, pl.hk,
-                        int32_t(row0 / rep), pl.s.q.a, int32_t(row0 % rep)};
+      launch.cuts[w] = {int32_t((unit - pt.b0 + pt.sp.blocks - 1) / pl.per),
+                        left < F::BM ? int32_t(left) : F::BM,
+                        pl.hk,
+                        int32_t(row0 / rep),
+                        pl.s.q.a,
+                        int32_t(row0 % rep)};
     }
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -399,7 +405,8 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
       const int32_t sinks = a.x.window > 0 ? a.x.sinks : 0;
       const int32_t place = col < mine ? pl.s.q.len - pl.s.q.n + tok : -1;
       // places of the wave's first and last row
-      const int32_t wlo = uni(place), whi = __builtin_amdgcn_readlane(place, mine >= 32 ? 31 : (mine > 0 ? mine - 1 : 0));
+      const int32_t wlo = uni(place);
+      const int32_t whi = __builtin_amdgcn_readlane(place, mine >= 32 ? 31 : (mine > 0 ? mine - 1 : 0));
       const bool rows_here = mine > 0;
       const float cs = a.x.scale == 0.f ? 1.f : fabsf(a.x.scale) * kLog2e;  // (as in attn_fwd.hip)
 
@@ -428,7 +435,8 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
         voff[u] = row * kstride + uint32_t(lpos ^ Swz<D>::v(row)) * 16;
       }
       const int32_t far = pt.sp.ww.far, low = pt.sp.ww.low - far;
-      const int32_t limit = pt.sp.hi + 1, oldest = pt.sp.lo - window - 15;  // (a granule past `oldest` is in the window)
+      // (a granule past `oldest` is in the window)
+      const int32_t limit = pt.sp.hi + 1, oldest = pt.sp.lo - window - 15;
       auto first_key = [&](int32_t blk) { return (blk < far ? blk : blk + low) * F::BK; };
       // 64 entries of the request's row of the table from `ids0` on, one a lane: loads of
       // entries would make every block wait for all loads before them
@@ -437,7 +445,8 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
       int32_t npg = 0, no = 0;
       const int32_t step_pg = F::BK / ps, step_o = F::BK % ps;
       auto issue = [&](int32_t blk, int st, bool start) {
-        const uint32_t dst = lds_addr(lds) + st * F::STAGE + (kBig ? (wave & 3) * (16 * D * 2) + (loads_v ? F::HALF : 0) : wave * 2 * F::HALF);
+        const uint32_t dst = lds_addr(lds) + st * F::STAGE +
+                             (kBig ? (wave & 3) * (16 * D * 2) + (loads_v ? F::HALF : 0) : wave * 2 * F::HALF);
         const int32_t key = first_key(blk) + wkey;
         if (start || blk == far) {
           npg = key / ps;
@@ -453,7 +462,8 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
             const Launch a = reload(args);
             ids0 = pg;
             // (waited for here, not at every use)
-            ids = fresh(a.c.table[int64_t(pl.r) * a.c.max_pages + (pg + lane < a.c.max_pages ? pg + lane : a.c.max_pages - 1)]);
+            const int32_t at = pg + lane < a.c.max_pages ? pg + lane : a.c.max_pages - 1;
+            ids = fresh(a.c.table[int64_t(pl.r) * a.c.max_pages + at]);
           }
           const int32_t page = __builtin_amdgcn_readlane(ids, (pg - ids0) & 63);
           const bool ok = seen && page >= 0 && page < num_pages;
@@ -519,7 +529,8 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
             uint32_t y = reinterpret_cast<uint32_t*>(vt)[i];
             const bool p = (y & 0x7f80u) == 0x7f80u, e = (y & 0x7f800000u) == 0x7f800000u;
             if (p || e) odd |= uint64_t(1) << (i / (D / 2));
-            if (mode == 1 && (p || e)) reinterpret_cast<uint32_t*>(vt)[i] = y & (p ? 0xffff0000u : ~0u) & (e ? 0xffffu : ~0u);
+            if (mode == 1 && (p || e))
+              reinterpret_cast<uint32_t*>(vt)[i] = y & (p ? 0xffff0000u : ~0u) & (e ? 0xffffu : ~0u);
           }
           if constexpr (kBig) {
             if (odd != 0) atomicOr(reinterpret_cast<unsigned long long*>(odd_lds), (unsigned long long)odd);
@@ -557,7 +568,8 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
           s[j] = f32x16{};
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
-            const bf16x8 y = *reinterpret_cast<const bf16x8*>(kt + (32 * j + col) * (D * 2) + (((2 * i + half) ^ kx) * 16));
+            const char* at = kt + (32 * j + col) * (D * 2) + (((2 * i + half) ^ kx) * 16);
+            const bf16x8 y = *reinterpret_cast<const bf16x8*>(at);
             s[j] = mfma32(y, qf[i], s[j]);
           }
         }
