@@ -186,6 +186,7 @@ struct Place {
     constexpr int NT = Form<D, kBig>::NT;
     __shared__ int64_t lds[NT / 64 + 2];
     int64_t mine = 0, before, total = 0;
+    if (threadIdx.x == 0) lds[NT / 64] = -1;
     for (int32_t r0 = 0; r0 < c.R; r0 += NT) {
       const int32_t i = r0 + int32_t(threadIdx.x);
       mine = i < c.R ? share_of<D, kBig>(c, x, i).units() : 0;
@@ -200,7 +201,7 @@ struct Place {
     hk = int32_t(unit / total);
     const int64_t y = unit - hk * total;
     int64_t base = 0;
-    for (int32_t r0 = 0;; r0 += NT) {
+    for (int32_t r0 = 0; r0 < c.R; r0 += NT) {
       if (c.R > NT) {  // (else the scan above is the one needed)
         const int32_t i = r0 + int32_t(threadIdx.x);
         mine = i < c.R ? share_of<D, kBig>(c, x, i).units() : 0;
@@ -215,19 +216,21 @@ struct Place {
     }
     __syncthreads();
     r = uni(int32_t(lds[NT / 64]));
+    if (r < 0) return false;  // (as in `next`)
     at = int64_t(hk) * per_head + uni(lds[NT / 64 + 1]);
     s = uniform(share_of<D, kBig>(c, x, r));
     return true;
   }
 
-  // The next request with units (the caller knows that there is one): 64 at a time.
-  __device__ __forceinline__ void next(const PagedArgs& c, const AttnPagedArgs& x) {
+  // The next request with units, 64 at a time. False where there is none, which only a
+  // caller sees that changes the lengths under a running call: it ends all the same.
+  __device__ __forceinline__ bool next(const PagedArgs& c, const AttnPagedArgs& x) {
     at += s.units();
     ++r;
     for (;;) {
       if (r >= c.R) {
         r = 0;
-        ++hk;
+        if (++hk >= c.Hkv) return false;
       }
       const int32_t i = r + int32_t(threadIdx.x & 63);
       const uint64_t m = __builtin_amdgcn_ballot_w64(i < c.R && share_of<D, kBig>(c, x, i).pairs > 0);
@@ -238,6 +241,7 @@ struct Place {
       r += 64;
     }
     s = uniform(share_of<D, kBig>(c, x, r));
+    return s.pairs > 0;
   }
 };
 
@@ -379,7 +383,7 @@ __global__ __launch_bounds__((Form<D, kBig>::NT), 2) void attn_paged_kernel(cons
       asm volatile("" ::: "memory");
       pl.s = uniform(shares[wave]);
       if (unit >= pl.at + pl.s.units()) {
-        pl.next(a.c, a.x);
+        if (!pl.next(a.c, a.x)) return;
         shares[wave] = pl.s;
         continue;
       }
