@@ -624,12 +624,13 @@ def test_captured_and_replayed(dtype, D):
             assert torch.equal(a, b), (i, j)
 
 
-def test_paged_captured_with_changing_lengths():
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_paged_captured_with_changing_lengths(dtype, D):
     """A captured call goes by the lengths, pages and chunks that the tensors hold at the replay."""
     rng = np.random.default_rng(5)
-    D, lens = 128, [900, 500, 1200, 64]
-    table, kp, vp = cache_of(rng, lens, 16, 2, D, "bf16")
-    q = on_gpu(rng.standard_normal((160, 8, D)), "bf16")
+    lens = [900, 500, 1200, 64]
+    table, kp, vp = cache_of(rng, lens, 16, 2, D, dtype)
+    q = on_gpu(rng.standard_normal((160, 8, D)), dtype)
     lays = [([900, 500, 1200, 64], [0, 1, 2, 3, 4]), ([300, 2, 1100, 0], [0, 100, 102, 160, 160]),
             ([16, 17, 1200, 1], [0, 1, 17, 150, 151])]
     t, n, c = i32(table), i32(lays[0][0]), i32(lays[0][1])
@@ -650,6 +651,40 @@ def test_paged_captured_with_changing_lengths():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), i
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 128)])
+def test_decoding_step_captured(dtype, D):
+    """A step's append and attention, captured once: the caller's lengths grow by one between replays, over a page's end."""
+    rng = np.random.default_rng(9)
+    lens, steps = [300, 15, 1, 2000, 63], 5
+    table, kp, vp = cache_of(rng, [n + steps + 1 for n in lens], 16, 2, D, dtype)
+    q = on_gpu(rng.standard_normal((steps, 5, 8, D)), dtype)
+    k, v = (on_gpu(rng.standard_normal((steps, 5, 2, D)), dtype) for _ in range(2))
+    t, n = i32(table), i32(lens)
+
+    def step(q, k, v, kp, vp):
+        pkv.paged_kv_append(k, v, kp, vp, t, n)
+        return pkv.attn_paged(q, kp, vp, t, n, output_lse=True)
+    now = [x[0].clone() for x in (q, k, v)]
+    pages = [kp.clone(), vp.clone()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*now, kp.clone(), vp.clone())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = step(*now, kp, vp)
+    for i in range(steps):
+        n += 1
+        for x, y in zip(now, (q, k, v)):
+            x.copy_(y[i])
+        g.replay()
+        want = step(q[i], k[i], v[i], *pages)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), i
+        assert torch.equal(kp.nan_to_num(7.0), pages[0].nan_to_num(7.0)), i
+
+
 def test_on_another_stream():
     x = _layer_inputs("bf16", 64, 40)
     y = {n: t.clone() for n, t in x.items()}
@@ -662,9 +697,10 @@ def test_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
-def test_two_calls_at_once():
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 32)])
+def test_two_calls_at_once(dtype, D):
     """Calls of two streams, each with its own workspace, do not disturb each other."""
-    x, y = _layer_inputs("bf16", 128, 41), _layer_inputs("bf16", 128, 42)
+    x, y = _layer_inputs(dtype, D, 41), _layer_inputs(dtype, D, 42)
     again = [{n: t.clone() for n, t in z.items()} for z in (x, y)]
     want = [_layer(x), _layer(y)]
     streams = [torch.cuda.Stream() for _ in range(2)]
