@@ -59,13 +59,17 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
                uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32) & 0xffffu)),
                uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 }
-// Load u of N goes to lds + u kStep, from off[u]. (An instruction that reads m0 right
-// behind its change needs a wait state; m0 is the compiler's own and put back.)
+// Load u of N goes to lds + u kStep, from off[u]. What the hardware does not check has its
+// wait states here, where no schedule can take them away: a load reads a scalar register
+// that a vector instruction wrote (readfirstlane in descriptor(), or readlane where the
+// compiler had spilled it) five states after the write at the earliest, which the compiler
+// keeps for its own loads but not for those in a text: two moves and s_nop 2. And a load
+// into LDS reads m0 one state after its change. (m0 is the compiler's own and put back.)
 template <int N, int kStep>
 __device__ __forceinline__ void load_lds16_async(u32x4 r, const uint32_t (&off)[N], uint32_t lds) {
   static_assert(N == 2 || N == 4, "the loads of a tile or of a granule");
   uint32_t m0;
-#define PKV_FIRST(x) "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 " x ", %2, 0 offen lds\n\t"
+#define PKV_FIRST(x) "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\tbuffer_load_dwordx4 " x ", %2, 0 offen lds\n\t"
 #define PKV_NEXT(x) "s_add_u32 m0, m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 " x ", %2, 0 offen lds\n\t"
   if constexpr (N == 2)
     asm volatile(PKV_FIRST("%4") PKV_NEXT("%5") "s_mov_b32 m0, %0"
@@ -80,10 +84,10 @@ __device__ __forceinline__ void load_lds16_async(u32x4 r, const uint32_t (&off)[
 #undef PKV_FIRST
 #undef PKV_NEXT
 }
-// 4 bytes per lane.
+// 4 bytes per lane, with the same wait states.
 __device__ __forceinline__ void load_lds4_async(u32x4 r, uint32_t off, uint32_t lds) {
   uint32_t m0;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\tbuffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
                : "=&s"(m0)
                : "s"(lds), "v"(off), "s"(r)
                : "memory");
