@@ -51,14 +51,29 @@ __device__ __forceinline__ void wave_fence() { asm volatile("" ::: "memory"); }
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
 __device__ __forceinline__ int row_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
 
-// 32 places of a request from p0 on, zero past its end and in a missing page.
+// What a tile's rows see, by the 16 places of a granule (pages are multiples of them): some
+// row sees a granule whose first place is at most `hi` and past `oldest` or one of the sinks.
+struct Seen {
+  int32_t hi, sinks;
+  int64_t oldest;
+  // rows at places lo .. hi; window 0: none
+  __device__ __forceinline__ Seen(int32_t lo, int32_t hi, int32_t window, int32_t sinks)
+      : hi(hi), sinks(sinks), oldest(window > 0 ? int64_t(lo) - window - 15 : -16) {}
+  __device__ __forceinline__ bool granule(int32_t p) const {
+    const int32_t first = p & ~15;
+    return first <= hi && (first > oldest || first < sinks);
+  }
+};
+
+// 32 places of a request from p0 on, zero past its end, in a missing page and where no row
+// sees the granule: its page may be gone, so the table is not asked for it.
 template <typename T, int D>
 __device__ __forceinline__ void fill(Tile<D>& tk, Tile<D>& tv, const PagedArgs& c, const T* __restrict__ kp,
-                                     const T* __restrict__ vp, int32_t r, int32_t len, int32_t p0, int32_t hk,
-                                     int lane) {
-  // pages are multiples of 16 places: lane l looks up the row of place l % 32
+                                     const T* __restrict__ vp, int32_t r, int32_t len, int32_t p0, const Seen& seen,
+                                     int32_t hk, int lane) {
+  // lane l looks up the row of place l % 32
   const int32_t p = p0 + (lane & 31);
-  const int32_t page = p < len ? page_of(c, r, p) : -1;
+  const int32_t page = p < len && seen.granule(p) ? page_of(c, r, p) : -1;
   const int64_t row = page < 0 ? -1 : page_row(c, page, p) * c.Hkv + hk;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
@@ -123,10 +138,11 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
     f32x16 acc[D / 32] = {};
     const WindowWalk ww(win ? x.window : 0x7fffffff, win ? x.sinks : 0, kT, lo > 0 ? lo : 0, 0);
     const int32_t n_tiles = hi < 0 ? 0 : ww.count(hi / kT + 1);
+    const Seen seen(lo, hi, x.window, x.sinks);
     for (int32_t it = split * kWaves + wave; it < n_tiles; it += splits * kWaves) {
       const int32_t s0 = ww.tile(it) * kT;
       wave_fence();
-      fill<T, D>(tk, tv, c, kp, vp, r, rq.len, s0, hk, lane);
+      fill<T, D>(tk, tv, c, kp, vp, r, rq.len, s0, seen, hk, lane);
       wave_fence();
       f32x16 s = {};
 #pragma unroll
