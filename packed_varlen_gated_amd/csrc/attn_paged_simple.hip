@@ -14,8 +14,8 @@
 // These shapes serve the small fp32 batches that models are debugged on. Bound by the
 // latency of a tile's loads: a wave has one tile at a time, and its fp32 products take 32
 // rows where a decoding request has H / Hkv. fp32, one token each: one request of 131072
-// tokens, H 32, Hkv 8, D 128: 0.80 ms (unsplit 25), 1.35 TB/s; 8 of 8000, H 8, Hkv 4, D 64:
-// 63 us, 2.1 TB/s; 4 of 300, D 32: 18 us.
+// tokens, H 32, Hkv 8, D 128: 0.81 ms (unsplit 25), 1.33 TB/s; 8 of 8000, H 8, Hkv 4, D 64:
+// 62 us, 2.1 TB/s; 4 of 300, D 32: 18 us.
 
 #include "paged.h"
 
@@ -160,7 +160,9 @@ __global__ __launch_bounds__(kThreads) void attn_paged_simple_kernel(const Paged
       mt = fmaxf(mt, other_half(mt));
       // a row whose scores so far are all -inf has no maximum to subtract
       const float ms = mt == -INFINITY ? 0.f : mt;
-      const float f = expf(m - ms);
+      // (more than 0, as it is without its rounding: an infinity in a sum stays one, however
+      // much larger a later score)
+      const float f = fmaxf(expf(m - ms), 0x1p-149f);
       m = mt;
       l *= f;
 #pragma unroll

@@ -47,3 +47,31 @@ def test_paged_entries_that_no_token_needs_may_hold_anything(dtype, D, window, s
             call(t)
             assert int(flags) == pkv.FLAG_BAD_PAGE
             flags.zero_()
+
+
+@pytest.mark.parametrize("dtype,D", PAGED_TYPES)
+def test_paged_an_infinity_stays_one_under_larger_scores(dtype, D):
+    """A weight of e^-300 is none in fp32, but more than 0: an infinite value that it stands at is the sum, whether its
+    key is walked before or after the larger scores."""
+    rng = np.random.default_rng(D)
+    n = 1000
+    for news, at in ((1, 5), (1, 990), (40, 5)):
+        table, kp, vp = cache_of(rng, [n], 16, 1, D, dtype)
+        q = on_gpu(rng.standard_normal((1, 1, D)), dtype)
+        for p in [*range(39, 960, 32)] + [at]:       # in every tile of keys
+            x = q[0, 0].float()
+            kp[int(table[0, p // 16]), p % 16, 0] = (x * ((0.0 if p == at else 300.0) / float(x @ x))).to(kp.dtype)
+        args = (i32(table), i32([n]), i32([0, news]))
+        q = q.expand(news, 2, D).contiguous()
+        want, wl = pkv.attn_paged(q, kp, vp, *args, scale=1.0, output_lse=True)
+        assert float(wl.min()) > 290
+        bad = torch.tensor([float("inf"), -float("inf"), float("nan")])
+        v2 = vp.clone()
+        v2[int(table[0, at // 16]), at % 16, 0, 3:6] = bad.to(v2)
+        o, lse = pkv.attn_paged(q, kp, v2, *args, scale=1.0, output_lse=True)
+        assert torch.equal(lse, wl)
+        hit = torch.zeros(D, dtype=torch.bool, device=dev())
+        hit[3:6] = True
+        assert torch.equal(o[..., ~hit], want[..., ~hit])
+        got = torch.nan_to_num(o[..., hit].float().cpu(), 7.0, 8.0, 9.0)
+        assert torch.equal(got, torch.nan_to_num(bad, 7.0, 8.0, 9.0).expand_as(got)), (news, at, o[..., hit])
