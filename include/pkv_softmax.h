@@ -167,7 +167,7 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
  *
  * q, o   [N, Hq, D] in `dtype`; query head h reads kv head h / (Hq / Hkv).
  * lse    float32 [Hq, N] or NULL (not written).
- * window 0 (no window, sinks ignored) or more.
+ * window 0 (no window; sinks, 0 or more, are ignored) or more.
  * A row that sees nothing (an idle request, a place before the first) and the
  * rows behind cu_seqlens[R] get o = 0, lse = -inf. A bad length or a malformed
  * cu_seqlens sets its flag and leaves its requests' rows undefined; so does a
@@ -179,8 +179,8 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
  *            (NULL where that is 0): in bf16 85 MB at D 128 and 43 at D 64,
  *            whatever the sizes, else at most 5 MB.
  * Errors: as pkv_paged_kv_append; Hq not a multiple of Hkv, a scale that is
- * not finite, window < 0, sinks < 0 (PKV_ERR_INVALID_ARGUMENT); sinks > 64
- * (PKV_ERR_UNSUPPORTED); PKV_ERR_WORKSPACE.
+ * not finite, window < 0, sinks < 0 (PKV_ERR_INVALID_ARGUMENT); with a window
+ * sinks > 64 (PKV_ERR_UNSUPPORTED); PKV_ERR_WORKSPACE.
  */
 size_t pkv_attn_paged_workspace_size(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D,
                                      int32_t dtype);

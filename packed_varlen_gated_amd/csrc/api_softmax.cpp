@@ -203,7 +203,7 @@ pkv_status pkv_attn_paged(const void* q, const void* k_pages, const void* v_page
   if (!std::isfinite(scale) || window < 0 || sinks < 0) return PKV_ERR_INVALID_ARGUMENT;
   const pkv_status st = check_paged(cu_seqlens, N, R, Hq, Hkv, D, page_size, num_pages, max_pages, dtype);
   if (st != PKV_OK) return st;
-  if (sinks > kMaxSinks) return PKV_ERR_UNSUPPORTED;
+  if (window > 0 && sinks > kMaxSinks) return PKV_ERR_UNSUPPORTED;
   const size_t need = pkv_attn_paged_workspace_size(N, R, Hq, Hkv, D, dtype);
   if (!workspace_ok(workspace, workspace_bytes, need)) return PKV_ERR_WORKSPACE;
   const int64_t es = elem_size(dtype), qb = N * Hq * D * es, pb = int64_t(num_pages) * page_size * Hkv * D * es;
