@@ -55,7 +55,8 @@ extern "C" {
  * q, k       [N, Hq, D], [N, Hkv, D] in `dtype`, heads dense, consecutive
  *            tokens q_stride / k_stride elements apart (views of one
  *            projection's result): at least the heads' size, multiples of 16
- *            bytes. k's tokens may lie between q's.
+ *            bytes, N of them at most 2^46 bytes. k's tokens may lie between
+ *            q's.
  * q_weight, k_weight  float32 [D] or NULL (1).
  * positions  int32 [N] or NULL (0 .. N - 1). A negative one marks a row to
  *            leave out (padding): its outputs and gradients are 0, and its

@@ -64,9 +64,10 @@ inline bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 inline int64_t strided_bytes(int64_t N, int64_t stride, int64_t heads, int64_t D, int64_t es) {
   return ((N - 1) * stride + heads * D) * es;
 }
-// Tokens of `heads` dense heads, 16-byte aligned and not on each other.
-inline bool stride_ok(int64_t stride, int64_t heads, int64_t D, int64_t es) {
-  return stride >= heads * D && stride <= (int64_t(1) << 40) && stride * es % 16 == 0;
+// N tokens of `heads` dense heads, 16-byte aligned and not on each other, whose bytes (at
+// most 2^46, more than an address space has) do not overflow.
+inline bool stride_ok(int64_t N, int64_t stride, int64_t heads, int64_t D, int64_t es) {
+  return stride >= heads * D && stride <= (int64_t(1) << 46) / es / N && stride * es % 16 == 0;
 }
 
 }  // namespace pkv

@@ -24,7 +24,7 @@ pkv_status check_norm_rope(int64_t q_stride, int64_t k_stride, const float* inv_
       (options & ~PKV_OPT_ROPE_INTERLEAVED) != 0)
     return PKV_ERR_UNSUPPORTED;
   const int64_t es = elem_size(dtype);
-  if (!stride_ok(q_stride, Hq, D, es) || !stride_ok(k_stride, Hkv, D, es) || (rot > 0 && inv_freq == nullptr))
+  if (!stride_ok(N, q_stride, Hq, D, es) || !stride_ok(N, k_stride, Hkv, D, es) || (rot > 0 && inv_freq == nullptr))
     return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;
 }
@@ -176,7 +176,7 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
   const pkv_status st = check_paged(cu_seqlens, N, R, Hkv, Hkv, D, page_size, num_pages, max_pages, dtype);
   if (st != PKV_OK) return st;
   const int64_t es = elem_size(dtype), pb = int64_t(num_pages) * page_size * Hkv * D * es;
-  if (!stride_ok(k_stride, Hkv, D, es) || !stride_ok(v_stride, Hkv, D, es)) return PKV_ERR_INVALID_ARGUMENT;
+  if (!stride_ok(N, k_stride, Hkv, D, es) || !stride_ok(N, v_stride, Hkv, D, es)) return PKV_ERR_INVALID_ARGUMENT;
   if (!spans_ok({{k, strided_bytes(N, k_stride, Hkv, D, es), 16}, {v, strided_bytes(N, v_stride, Hkv, D, es), 16},
                  i32_span(page_table, int64_t(R) * max_pages), i32_span(kv_lens, R),
                  i32_span(cu_seqlens, int64_t(R) + 1)},
