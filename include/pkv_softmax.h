@@ -177,8 +177,11 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
  * statistics and sums are fp32; with bf16 and D in {64, 128} the weights are
  * rounded to bf16 for the product with v.
  * workspace  at least pkv_attn_paged_workspace_size() bytes, 256-byte aligned
- *            (NULL where that is 0): in bf16 85 MB at D 128 and 43 at D 64,
- *            whatever the sizes, else at most 5 MB.
+ *            (NULL where that is 0): in bf16 85 MB at D 128 and 43 at D 64 if
+ *            a request can have more than 32 rows (N Hq / Hkv > 32), 17 and 9
+ *            if not, else at most 5 MB. Without cu_seqlens a request has one
+ *            token: those bf16 calls need what the function says for
+ *            N = R = 1.
  * Errors: as pkv_paged_kv_append; Hq not a multiple of Hkv, a scale that is
  * not finite, window < 0, sinks < 0 (PKV_ERR_INVALID_ARGUMENT); with a window
  * sinks > 64 (PKV_ERR_UNSUPPORTED); PKV_ERR_WORKSPACE.

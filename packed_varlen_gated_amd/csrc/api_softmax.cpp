@@ -56,6 +56,12 @@ pkv_status check_paged(const int32_t* cu, int64_t N, int32_t R, int32_t Hq, int3
   return PKV_OK;
 }
 
+// chunks: with cu_seqlens.
+size_t paged_workspace(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, bool chunks) {
+  return attn_mfma_supported(D, dtype) ? attn_paged_workspace_bytes(N, Hq, Hkv, D, chunks)
+                                       : attn_paged_simple_workspace_bytes(N, R, Hq, Hkv, D);
+}
+
 }  // namespace
 
 extern "C" {
@@ -190,8 +196,7 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int64_t k_stride, i
 size_t pkv_attn_paged_workspace_size(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype) {
   const int32_t one = 1;
   if (check_paged(&one, N, R, Hq, Hkv, D, 16, 1, 1, dtype) != PKV_OK) return 0;
-  return attn_mfma_supported(D, dtype) ? attn_paged_workspace_bytes(D)
-                                       : attn_paged_simple_workspace_bytes(N, R, Hq, Hkv, D);
+  return paged_workspace(N, R, Hq, Hkv, D, dtype, true);
 }
 
 pkv_status pkv_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -204,7 +209,7 @@ pkv_status pkv_attn_paged(const void* q, const void* k_pages, const void* v_page
   const pkv_status st = check_paged(cu_seqlens, N, R, Hq, Hkv, D, page_size, num_pages, max_pages, dtype);
   if (st != PKV_OK) return st;
   if (window > 0 && sinks > kMaxSinks) return PKV_ERR_UNSUPPORTED;
-  const size_t need = pkv_attn_paged_workspace_size(N, R, Hq, Hkv, D, dtype);
+  const size_t need = paged_workspace(N, R, Hq, Hkv, D, dtype, cu_seqlens != nullptr);
   if (!workspace_ok(workspace, workspace_bytes, need)) return PKV_ERR_WORKSPACE;
   const int64_t es = elem_size(dtype), qb = N * Hq * D * es, pb = int64_t(num_pages) * page_size * Hkv * D * es;
   const Span ws{need > 0 ? workspace : nullptr, int64_t(need), 256};

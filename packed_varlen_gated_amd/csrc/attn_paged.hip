@@ -811,20 +811,22 @@ __device__ __forceinline__ void join_parts(const PagedArgs& c, const AttnPagedAr
   }
 }
 
-// The workspace: the small form's parts, the big form's, the cuts of both.
+// The workspace: the small form's parts and cuts, and those of the big form where a call can
+// have it.
 template <int D>
 struct Workspace {
   using S = Form<D, false>;
   using B = Form<D, true>;
-  static constexpr size_t BYTES = S::PARTS + B::PARTS + (S::GROUPS + B::GROUPS) * sizeof(Cut);
+  static constexpr size_t SMALL = S::PARTS + S::GROUPS * sizeof(Cut), BIG = B::PARTS + B::GROUPS * sizeof(Cut);
+  static_assert(S::PARTS % 16 == 0 && SMALL % 16 == 0 && B::PARTS % 16 == 0, "16-byte stores");
   float *small, *big;
   Cut *small_cuts, *big_cuts;
   explicit Workspace(void* ws) {
     char* p = static_cast<char*>(ws);
     small = reinterpret_cast<float*>(p);
-    big = reinterpret_cast<float*>(p + S::PARTS);
-    small_cuts = reinterpret_cast<Cut*>(p + S::PARTS + B::PARTS);
-    big_cuts = small_cuts + S::GROUPS;
+    small_cuts = reinterpret_cast<Cut*>(p + S::PARTS);
+    big = reinterpret_cast<float*>(p + SMALL);
+    big_cuts = reinterpret_cast<Cut*>(p + SMALL + B::PARTS);
   }
 };
 
@@ -838,13 +840,14 @@ __global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(const PagedAr
     join_parts<D, true>(c, x, ws.big, ws.big_cuts, int64_t(blockIdx.x) - small + 1);
 }
 
-// Which forms a call's requests can have.
-bool any_small(const PagedArgs& c, int32_t Hq) { return Hq / c.Hkv <= 32; }
-bool any_big(const PagedArgs& c, int32_t Hq) { return c.cu != nullptr || Hq / c.Hkv > 32; }
+// Which forms a call's requests can have: at most 32 rows of one, and more (all N tokens may
+// be one request's, but without cu_seqlens each has its own).
+bool any_small(int32_t rep) { return rep <= 32; }
+bool any_big(int64_t N, int32_t rep, bool chunks) { return (chunks ? N : 1) * rep > 32; }
 
 template <int D>
 hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
-  const bool s = any_small(c, x.Hq), b = any_big(c, x.Hq);
+  const bool s = any_small(x.Hq / c.Hkv), b = any_big(c.N, x.Hq / c.Hkv, c.cu != nullptr);
   const Workspace<D> ws(x.workspace);
   // (the first launch also zeroes the rows that no request has)
   const int64_t tail = c.cu == nullptr ? 1 : tail_groups(c.N * x.Hq * D * 2);
@@ -874,7 +877,10 @@ hipError_t run(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
 
 }  // namespace
 
-size_t attn_paged_workspace_bytes(int32_t D) { return D == 64 ? Workspace<64>::BYTES : Workspace<128>::BYTES; }
+size_t attn_paged_workspace_bytes(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, bool chunks) {
+  const size_t big = any_big(N, Hq / Hkv, chunks) ? (D == 64 ? Workspace<64>::BIG : Workspace<128>::BIG) : 0;
+  return (D == 64 ? Workspace<64>::SMALL : Workspace<128>::SMALL) + big;
+}
 
 hipError_t launch_attn_paged(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream) {
   return c.D == 64 ? run<64>(c, x, stream) : run<128>(c, x, stream);

@@ -264,8 +264,8 @@ hipError_t launch_paged_append(const PagedArgs& c, const AppendArgs& x, int32_t 
 // Off the matrix-core path: fp32, and bf16 at D = 32.
 size_t attn_paged_simple_workspace_bytes(int64_t N, int32_t R, int32_t Hq, int32_t Hkv, int32_t D);
 hipError_t launch_attn_paged_simple(const PagedArgs& c, const AttnPagedArgs& x, int32_t dtype, hipStream_t stream);
-// The matrix-core kernels (where attn_mfma_supported).
-size_t attn_paged_workspace_bytes(int32_t D);
+// The matrix-core kernels (where attn_mfma_supported). chunks: with cu_seqlens.
+size_t attn_paged_workspace_bytes(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, bool chunks);
 hipError_t launch_attn_paged(const PagedArgs& c, const AttnPagedArgs& x, hipStream_t stream);
 
 }  // namespace pkv

@@ -17,6 +17,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
+from . import PKV_BF16
 from .mixers import (AttnGrads, _attn_shapes, _code, _dtype_code, _flags_of, _load, _need, _need_shape, _ptr, _run,
                      _scratch, _shape, _tensors)
 
@@ -251,8 +252,15 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None
          _ptr(cu_seqlens), N, R, Hkv, D, size, pages, width, code, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(flags))
 
 
-def attn_paged_workspace_size(N, R, Hq, Hkv, D, dtype):
-    return int(_load().pkv_attn_paged_workspace_size(N, R, Hq, Hkv, D, _dtype_code(dtype)))
+def attn_paged_workspace_size(N, R, Hq, Hkv, D, dtype, chunks=True):
+    """chunks: whether the call has cu_seqlens (without it bf16 calls at D 64 and 128 need a fifth)."""
+    return int(_paged_workspace_size(_load(), N, R, Hq, Hkv, D, _dtype_code(dtype), chunks))
+
+
+def _paged_workspace_size(lib, N, R, Hq, Hkv, D, code, chunks):
+    if not chunks and code == PKV_BF16 and D > 32:
+        N = R = 1
+    return lib.pkv_attn_paged_workspace_size(N, R, Hq, Hkv, D, code)
 
 
 def attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, window=None, sinks=0, scale=None,
@@ -285,7 +293,8 @@ def attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, window
         _tensors(dev, dt, 3, out=out)
         _shape(out, "out", q.shape)
     lse = torch.empty(Hq, N, dtype=torch.float32, device=q.device) if output_lse else None
-    workspace, ws_bytes = _scratch(workspace, lib.pkv_attn_paged_workspace_size(N, R, Hq, Hkv, D, code), q)
+    workspace, ws_bytes = _scratch(
+        workspace, _paged_workspace_size(lib, N, R, Hq, Hkv, D, code, cu_seqlens is not None), q)
     _run(lib.pkv_attn_paged, dev, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
          kv_lens.data_ptr(), _ptr(cu_seqlens), N, R, Hq, Hkv, D, size, pages, width,
          1.0 / math.sqrt(D) if scale is None else float(scale), code, _int32(window, "window"), _int32(sinks, "sinks"),

@@ -75,3 +75,25 @@ def test_paged_an_infinity_stays_one_under_larger_scores(dtype, D):
         assert torch.equal(o[..., ~hit], want[..., ~hit])
         got = torch.nan_to_num(o[..., hit].float().cpu(), 7.0, 8.0, 9.0)
         assert torch.equal(got, torch.nan_to_num(bad, 7.0, 8.0, 9.0).expand_as(got)), (news, at, o[..., hit])
+
+
+@pytest.mark.parametrize("dtype,D", PAGED_TYPES)
+@pytest.mark.parametrize("Hq,Hkv,news", [(8, 2, None), (40, 1, None), (8, 2, [1, 0, 4, 3]), (8, 2, [1, 0, 40, 3])])
+def test_paged_takes_no_more_than_its_workspace(dtype, D, Hq, Hkv, news):
+    """A workspace of just the size that the call asks for: the same bits as with its own, and nothing behind it changes."""
+    rng = np.random.default_rng(D)
+    lens = [3000, 17, 900, 2100]
+    cu = None if news is None else i32(np.concatenate([[0], np.cumsum(news)]))
+    N = sum(news or [1] * 4)
+    table, kp, vp = cache_of(rng, lens, 16, Hkv, D, dtype)
+    q = on_gpu(rng.standard_normal((N, Hq, D)), dtype)
+    need = pkv.attn_paged_workspace_size(N, 4, Hq, Hkv, D, q.dtype, chunks=news is not None)
+    args = (q, kp, vp, i32(table), i32(lens), cu)
+    want, wl = pkv.attn_paged(*args, output_lse=True)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device=dev())
+    for _ in range(2):
+        o, lse = pkv.attn_paged(*args, output_lse=True, workspace=ws[:need]) if need else (want, wl)
+        assert torch.equal(o, want) and torch.equal(lse, wl) and bool((ws[need:] == 255).all())
+    if need:
+        with pytest.raises(ValueError, match="workspace holds"):
+            pkv.attn_paged(*args, workspace=ws[:need - 1])
