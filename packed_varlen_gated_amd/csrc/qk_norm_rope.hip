@@ -29,9 +29,19 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-// Steps (1024 / D rows) of a wave that are loaded together, and in the reverse pass.
+// Steps (1024 / D rows) of a wave that are loaded together, and in the reverse pass. Other
+// waves hide most of a load. Forward, 1 / 2 / 4 steps, D 128 but where said:
+//   bf16  65536 tokens, H 32, Hkv 8        254 / 258 / 254 us
+//         8192, H 16, Hkv 4                23.7 / 24.8 / 24.9
+//         16384, H 128, Hkv 8              223 / 222 / 220
+//         16384, H 16, Hkv 16, D 64        27.5 / 29.6 / 30.3 (a token is one step)
+//   fp32  32768, H 32, Hkv 8               259 / 256 / 249
+//         16384, H 32, Hkv 8, D 64         71.5 / 69.1 / 72.6
+//         2048, H 32, Hkv 8                17.0 / 17.8 / 17.6
+// Reverse, 1 / 2 steps (2 do not fit the registers): bf16, 65536 tokens 432 / 1192, fp32,
+// 32768 386 / 682.
 template <typename T>
-constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+constexpr int kAhead = sizeof(T) == 2 ? 1 : 2;
 template <typename T>
 constexpr int kBack = 1;
 
@@ -391,8 +401,18 @@ template <typename T, int D, bool kInter>
 hipError_t forward(const NormRopeArgs& x, hipStream_t stream) {
   constexpr int ROWS = Lane<D, kInter>::ROWS;
   const int64_t steps = (x.Hq + ROWS - 1) / ROWS + (x.Hkv + ROWS - 1) / ROWS;
-  // A few tokens: a token's steps go to waves of their own.
-  int64_t split = 8192 / x.N;
+  // A few tokens: a token's steps go to waves of their own, up to 2048 waves in all; with
+  // more, forming a token's angles again costs what it saves. bf16, D 128, H 32, Hkv 8 (5
+  // steps), no split / up to 1024, 2048, 4096, 8192 waves:
+  //   1 token                     5.3 / -, 4.0, 4.0, 4.0 us
+  //   256 tokens                  7.4 / 4.9, 5.4, 5.4, 5.5
+  //   768                            - / 8.3, 7.6, 8.0, 8.6
+  //   1024                        8.5 / 8.7, 8.0, 9.0, 10.1
+  //   1500                       10.8 / 10.8, 10.8, 9.8, 13.8
+  //   2048                       12.3 / 12.3, 12.3, 12.3, 15.2
+  //   4096                       18.4 / 18.4, 18.4, 18.4, 21.3
+  // H 128, Hkv 8 (17 steps): 256 tokens 7.5, 7.6, 9.9, 9.9; 1024 19.1, 16.0, 15.8, 19.1.
+  int64_t split = 2048 / x.N;
   split = split < 1 ? 1 : (split < steps ? split : steps);
   const int64_t groups = (x.N * split + kWaves - 1) / kWaves;
   qk_norm_rope_kernel<T, D, kInter><<<dim3(uint32_t(groups)), dim3(kThreads), 0, stream>>>(x, int(split));
