@@ -24,6 +24,7 @@
  * Equal calls give equal bits; the order of a sum may go by the call's sizes,
  * over a paged cache also by the lengths of the call's requests.
  * Workspaces are scratch: calls that share one must be ordered on one stream.
+ * What a call reads, lengths and tables among it, must not change while it runs.
  */
 #ifndef PKV_SOFTMAX_H
 #define PKV_SOFTMAX_H

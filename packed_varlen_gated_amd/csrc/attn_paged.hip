@@ -275,8 +275,10 @@ __device__ __forceinline__ Part part_at(const Place<D, kBig>& pl, const AttnPage
   return {-1, sp, 0, s.cost - in};
 }
 
-// A launch's arguments. They are read again (scalar loads) for each part of the work:
-// held in registers over a walk, they would push what the walk needs out of them.
+// A launch's arguments. They are read again (scalar loads) for each part of the work: held in
+// registers over a walk, they would push more of what the walk needs out of them. At D 128 its
+// own are still too many: 106 (small form) and 117 (big) scalar registers are kept in vector
+// lanes, some of them read back for every block (D 64: 11 and 4).
 struct Launch {
   PagedArgs c;
   AttnPagedArgs x;

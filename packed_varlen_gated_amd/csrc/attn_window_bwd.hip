@@ -313,9 +313,9 @@ __global__ __launch_bounds__(DkvShape<kQ>::NT, D == 64 && kQ == 1 ? 3 : 2) void 
         const int32_t kq = kFar ? k0 + window : k0;  // the first key's first query
         if (have == 0 || b0 + 31 < kq || b0 >= to) continue;
         if (!kFar && b0 >= k0 + 31 + window) continue;
-        // Registers are full at D = 128 (k, v, dk and dv take 192): the weights are
-        // done with before dP is begun, and nothing of a phase starts early. The
-        // other wave of the SIMD fills the gaps.
+        // Registers are full at D = 128 (k, v, dk and dv take 192; 5 to 8 of the others
+        // are in memory): the weights are done with before dP is begun, and nothing of a
+        // phase starts early. The other wave of the SIMD fills the gaps.
         bf16x8 p[2], ds[2];
         f32x16 x = {};
 #pragma unroll

@@ -15,11 +15,13 @@
 // An angle is p f / 2 pi turns, formed in fp64 and reduced to half a turn before it
 // is rounded to fp32: at position 10^6 an fp32 product is off by 0.03 rad.
 //
-// Bound by memory: nothing is read twice, and the arithmetic is a third of the
-// vector units' time at the copy's rate. 65536 tokens of a fused projection, H 32, Hkv 8,
-// D 128, all channels rotated: 252 us for 1.34 GB, 5.3 TB/s (a large copy 5.13). 8192 tokens,
-// H 16, Hkv 4, D 128, 64 channels rotated, forward and reverse pass: 61 us for 0.21 GB,
-// three launches (the last sums the weights' gradients of the work-groups). With the angles
+// Bound by memory where tokens are many: nothing is read twice. 65536 tokens of a fused
+// projection, H 32, Hkv 8, D 128, all channels rotated: 253 us for 1.34 GB, 5.3 TB/s (a large
+// copy 5.13), with vector instructions in 51 % of the cycles. 8192 tokens, H 16, Hkv 4, D 128,
+// 64 channels rotated, forward and reverse pass: 61 us for 0.21 GB (41 at the copy's rate),
+// three launches of 21, 29 and 4 us (the last sums the weights' gradients of the
+// work-groups); vector instructions take 64 and 68 % of the first two: a token is two steps
+// there, behind its position, fp64 product, sine and cosine and 16 exchanges. With the angles
 // formed by every lane for itself and before the loads: 307 and 110 us.
 
 #include "mfma.h"
