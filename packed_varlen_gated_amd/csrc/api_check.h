@@ -1,6 +1,6 @@
-// Argument checks shared by the entry points of include/pkv_softmax.h. Every check
-// runs before any HIP call, so invalid arguments are reported synchronously and
-// nothing is enqueued.
+// Argument checks shared by the entry points of include/pkv_mixers.h and
+// include/pkv_softmax.h. Every check runs before any HIP call, so invalid arguments are
+// reported synchronously and nothing is enqueued.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -4,56 +4,12 @@
 
 #include "pkv_mixers.h"
 
-#include <hip/hip_runtime.h>
-
-#include <cmath>
-#include <initializer_list>
-
+#include "api_check.h"
 #include "common.h"
 
 namespace {
 
-constexpr int64_t kInt32Max = 2147483647;
-// Work-groups of a launch: a grid holds less than 2^32 work-items, of at most 512
-// a group.
-constexpr int64_t kMaxGroups = int64_t(1) << 23;
-
-bool supported_head_dim(int32_t d) { return d == 32 || d == 64 || d == 128; }
-bool known_dtype(int32_t dt) { return dt == PKV_BF16 || dt == PKV_F32; }
-int64_t elem_size(int32_t dt) { return dt == PKV_BF16 ? 2 : 4; }
-pkv_status from_hip(hipError_t e) { return e == hipSuccess ? PKV_OK : PKV_ERR_HIP; }
-
-struct Span {
-  const void* p;
-  int64_t bytes;
-  int64_t align;
-};
-
-bool overlap(const Span& a, const Span& b) {
-  if (a.p == nullptr || b.p == nullptr) return false;
-  const char *x = static_cast<const char*>(a.p), *y = static_cast<const char*>(b.p);
-  return x < y + b.bytes && y < x + a.bytes;
-}
-
-// Alignment of every span, and no output on an input or another output.
-bool spans_ok(std::initializer_list<Span> ins, std::initializer_list<Span> outs) {
-  for (const Span& s : ins)
-    if (reinterpret_cast<uintptr_t>(s.p) % s.align != 0) return false;
-  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-    if (reinterpret_cast<uintptr_t>(o->p) % o->align != 0) return false;
-    for (const Span& s : ins)
-      if (overlap(*o, s)) return false;
-    for (const Span* p = outs.begin(); p != o; ++p)
-      if (overlap(*o, *p)) return false;
-  }
-  return true;
-}
-
-bool any_null(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (p == nullptr) return true;
-  return false;
-}
+using namespace pkv;
 
 // N, max_segs (set to 1 without cu) and scale of a packed call.
 bool packed_sizes_ok(const int32_t* cu, int32_t& max_segs, int64_t N, float scale) {
