@@ -36,18 +36,14 @@ pkv_status check_linear(const int32_t* cu, int32_t& max_segs, int64_t N, int32_t
       int64_t(max_segs) * H > (int64_t(1) << 22))
     return PKV_ERR_INVALID_ARGUMENT;
   if (!known_dtype(dtype) || !supported_head_dim(Dk) || !supported_head_dim(Dv)) return PKV_ERR_UNSUPPORTED;
-  if (pkv::linear_chunk_supported(Dk, Dv, dtype) && pkv::linear_chunk_grid(N, max_segs, H) >= kMaxGroups)
+  if (linear_chunk_supported(Dk, Dv, dtype) && linear_chunk_grid(N, max_segs, H) >= kMaxGroups)
     return PKV_ERR_INVALID_ARGUMENT;
   return PKV_OK;
 }
 
 size_t linear_workspace(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t dtype, bool reverse) {
-  if (N < 1 || N > kInt32Max || H < 1 || H > 65536 || !pkv::linear_chunk_supported(Dk, Dv, dtype)) return 0;
-  return pkv::linear_chunk_workspace_bytes(N, H, Dk, Dv, reverse);
-}
-
-bool workspace_ok(const void* ws, size_t bytes, size_t need) {
-  return need == 0 || (ws != nullptr && bytes >= need && reinterpret_cast<uintptr_t>(ws) % 256 == 0);
+  if (N < 1 || N > kInt32Max || H < 1 || H > 65536 || !linear_chunk_supported(Dk, Dv, dtype)) return 0;
+  return linear_chunk_workspace_bytes(N, H, Dk, Dv, reverse);
 }
 
 }  // namespace
@@ -64,10 +60,10 @@ pkv_status pkv_attn_varlen(const void* q, const void* k, const void* v, const in
   if (!spans_ok({{q, qb, 16}, {k, kb, 16}, {v, kb, 16}, cu_span(cu_seqlens, max_segs)},
                 {{o, qb, 16}, {lse, N * Hq * 4, 4}, {flags, 4, 4}}))
     return PKV_ERR_INVALID_ARGUMENT;
-  const pkv::AttnArgs a{q, k, v, cu_seqlens, max_segs, N, Hq, Hkv, D, scale, o, lse, flags};
-  if (pkv::attn_mfma_supported(D, dtype))
-    return from_hip(pkv::launch_attn_fwd(a, static_cast<hipStream_t>(stream)));
-  return from_hip(pkv::launch_attn_simple(a, dtype, static_cast<hipStream_t>(stream)));
+  const AttnArgs a{q, k, v, cu_seqlens, max_segs, N, Hq, Hkv, D, scale, o, lse, flags};
+  if (attn_mfma_supported(D, dtype))
+    return from_hip(launch_attn_fwd(a, static_cast<hipStream_t>(stream)));
+  return from_hip(launch_attn_simple(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
 size_t pkv_attn_varlen_backward_workspace_size(int64_t N, int32_t Hq, int32_t Hkv, int32_t D,
@@ -95,12 +91,12 @@ pkv_status pkv_attn_varlen_backward(const void* q, const void* k, const void* v,
                  cu_span(cu_seqlens, max_segs), {dq, qb, 16}, {dk, kb, 16}, {dv, kb, 16}, {flags, 4, 4}},
                 {{workspace, int64_t(need), 256}}))
     return PKV_ERR_WORKSPACE;
-  const pkv::AttnArgs a{q,   k,   v, cu_seqlens, max_segs, N, Hq, Hkv, D, scale, const_cast<void*>(o),
+  const AttnArgs a{q,   k,   v, cu_seqlens, max_segs, N, Hq, Hkv, D, scale, const_cast<void*>(o),
                         const_cast<float*>(lse), flags};
-  const pkv::AttnGradArgs g{dout, static_cast<float*>(workspace), dq, dk, dv};
-  if (pkv::attn_mfma_supported(D, dtype))
-    return from_hip(pkv::launch_attn_bwd(a, g, static_cast<hipStream_t>(stream)));
-  return from_hip(pkv::launch_attn_simple_backward(a, g, dtype, static_cast<hipStream_t>(stream)));
+  const AttnGradArgs g{dout, static_cast<float*>(workspace), dq, dk, dv};
+  if (attn_mfma_supported(D, dtype))
+    return from_hip(launch_attn_bwd(a, g, static_cast<hipStream_t>(stream)));
+  return from_hip(launch_attn_simple_backward(a, g, dtype, static_cast<hipStream_t>(stream)));
 }
 
 size_t pkv_linear_attn_varlen_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv, int32_t max_segs,
@@ -125,11 +121,11 @@ pkv_status pkv_linear_attn_varlen(const void* q, const void* k, const void* v, c
                 {{o, vb, 16}, {final_state, sb, 16}, {flags, 4, 4},
                  {need > 0 ? workspace : nullptr, int64_t(need), 16}}))
     return PKV_ERR_INVALID_ARGUMENT;
-  const pkv::LinearArgs x{q,  k,  v,     g,             cu_seqlens, max_segs,    N,     H,
+  const LinearArgs x{q,  k,  v,     g,             cu_seqlens, max_segs,    N,     H,
                           Dk, Dv, scale, initial_state, o,          final_state, flags, workspace};
-  if (pkv::linear_chunk_supported(Dk, Dv, dtype))
-    return from_hip(pkv::launch_linear_chunk(x, static_cast<hipStream_t>(stream)));
-  return from_hip(pkv::launch_linear_serial(x, dtype, static_cast<hipStream_t>(stream)));
+  if (linear_chunk_supported(Dk, Dv, dtype))
+    return from_hip(launch_linear_chunk(x, static_cast<hipStream_t>(stream)));
+  return from_hip(launch_linear_serial(x, dtype, static_cast<hipStream_t>(stream)));
 }
 
 size_t pkv_linear_attn_varlen_backward_workspace_size(int64_t N, int32_t H, int32_t Dk, int32_t Dv,
@@ -156,12 +152,12 @@ pkv_status pkv_linear_attn_varlen_backward(const void* q, const void* k, const v
                 {{dq, kb, 16}, {dk, kb, 16}, {dv, vb, 16}, {d_initial_state, sb, 16}, {flags, 4, 4},
                  {need > 0 ? workspace : nullptr, int64_t(need), 16}}))
     return PKV_ERR_INVALID_ARGUMENT;
-  const pkv::LinearArgs x{q,  k,  v,     g,             cu_seqlens, max_segs, N,     H,
+  const LinearArgs x{q,  k,  v,     g,             cu_seqlens, max_segs, N,     H,
                           Dk, Dv, scale, initial_state, nullptr,    nullptr,  flags, workspace};
-  const pkv::LinearGradArgs y{dout, dfinal_state, dq, dk, dv, d_initial_state};
-  if (pkv::linear_chunk_supported(Dk, Dv, dtype))
-    return from_hip(pkv::launch_linear_chunk_backward(x, y, static_cast<hipStream_t>(stream)));
-  return from_hip(pkv::launch_linear_serial_backward(x, y, dtype, static_cast<hipStream_t>(stream)));
+  const LinearGradArgs y{dout, dfinal_state, dq, dk, dv, d_initial_state};
+  if (linear_chunk_supported(Dk, Dv, dtype))
+    return from_hip(launch_linear_chunk_backward(x, y, static_cast<hipStream_t>(stream)));
+  return from_hip(launch_linear_serial_backward(x, y, dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -181,8 +177,8 @@ pkv_status step(const void* q, const void* k, const void* v, const void* g, int6
                  {slots, R * 4, 4}},
                 {{state, int64_t(S) * H * Dk * Dv * 4, 16}, {o, vb, 16}, {flags, 4, 4}}))
     return PKV_ERR_INVALID_ARGUMENT;
-  const pkv::StepArgs a{q, k, v, g, beta, slots, R, S, H, Dk, Dv, scale, l2, state, o, flags};
-  return from_hip(pkv::launch_step(a, dtype, static_cast<hipStream_t>(stream)));
+  const StepArgs a{q, k, v, g, beta, slots, R, S, H, Dk, Dv, scale, l2, state, o, flags};
+  return from_hip(launch_step(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
