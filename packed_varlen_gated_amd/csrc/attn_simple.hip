@@ -32,47 +32,17 @@
 // of causal products); D 32, bf16 0.31 / 1.16 ms. The first of these through a window of
 // 24 with 2 sinks: 28 us, launches of 6.6, 7.8 and 13.6 us.
 
+#include "attn_f32.h"
 #include "segments.h"
 
 namespace pkv {
 namespace {
 
-constexpr int kT = 32;        // tokens per tile, both sides
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr float kFinite = 3.4028234663852886e38f;
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-template <int D>
-struct alignas(16) Tile {  // of one wave
-  float x[kT][D + 4];      // (rows 4 banks apart)
-  __device__ __forceinline__ f32x4 at(int r, int d) const { return *reinterpret_cast<const f32x4*>(&x[r][d]); }
-};
-
-__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-__device__ __forceinline__ f32x4 load4(const bf16* p) {
-  typedef bf16 b16x4 __attribute__((ext_vector_type(4)));
-  const b16x4 x = *reinterpret_cast<const b16x4*>(p);
-  return f32x4{to_f32(x[0]), to_f32(x[1]), to_f32(x[2]), to_f32(x[3])};
-}
-__device__ __forceinline__ void store4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
-__device__ __forceinline__ void store4(bf16* p, f32x4 x) {
-  typedef bf16 b16x4 __attribute__((ext_vector_type(4)));
-  *reinterpret_cast<b16x4*>(p) = b16x4{from_f32<bf16>(x[0]), from_f32<bf16>(x[1]), from_f32<bf16>(x[2]), from_f32<bf16>(x[3])};
-}
-
-// The wave's LDS accesses are in order; nothing is moved across.
-__device__ __forceinline__ void wave_fence() { asm volatile("" ::: "memory"); }
-
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
 // Whether token t of a segment from a on attends to token s of it.
 template <bool kWin>
 __device__ __forceinline__ bool attends(int64_t s, int64_t t, int64_t a, int32_t window, int32_t sinks) {
   return s <= t && (!kWin || t - s < window || s - a < sinks);
 }
-__device__ __forceinline__ int row_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
 
 // 32 rows of a [N, H, D] tensor from `row` on into a wave's tile, zero past `end`;
 // whether the lane's values are all finite.
